@@ -486,6 +486,144 @@ MOE_API moe_status moe_route_noalloc(const int32_t* d_topk_idx, const float* d_t
                                      int32_t* d_perm, int32_t* d_inv, uint32_t* d_status,
                                      struct CUstream_st* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the layer for few tokens.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * moe_add_rms_norm -- residual addition, root-mean-square norm, and the
+ * norm's output in 8 bits, one pass:
+ *   r = bf16(x + residual)   (r = x when d_residual is NULL)
+ *   y = r * rsqrt(mean(r^2) + eps) * weight      (float)
+ * and of y: BF16 (d_y), E4M3 codes with scales (d_q, d_q_scale), or both.
+ *   d_x            BF16 [num_tokens, hidden], rows x_stride elements apart.
+ *   d_residual     BF16 likewise (residual_stride), or NULL.
+ *   d_weight       BF16 [hidden].
+ *   d_residual_out BF16 [num_tokens, hidden]: r; given exactly when
+ *                  d_residual is.  May be d_residual itself (dense rows).
+ *   d_y            BF16 [num_tokens, hidden], or NULL.  May be d_x itself
+ *                  (dense rows).
+ *   d_q            E4M3 [num_tokens, hidden], or NULL; rounded once, from the
+ *                  float y.
+ *   q_format       the layer's activation formats: 0 one scale per 128
+ *                  columns, MOE_FLAG_MXFP8 one per 32 (scale = least power of
+ *                  two 2^e with amax <= 448 * 2^e, e in [-127, 127], 0 for an
+ *                  all-zero block; E8M0 byte e + 127 into d_q_scale uint8
+ *                  [num_tokens, hidden/128 or hidden/32]), or
+ *                  MOE_FLAG_PER_TENSOR: code = E4M3_RNE_sat(y *
+ *                  float(1 / q_static_scale)), no d_q_scale.
+ * Any hidden from 1 to 2^20 (a multiple of the block for the block formats,
+ * else MOE_ERR_UNSUPPORTED); multiples of 8 up to 16384 with 16-byte aligned
+ * rows take the vector path.  Sums are float.  No other overlap of buffers.
+ * Asynchronous on `stream`.  MOE_ERR_INVALID_ARG: a NULL or misaligned
+ * pointer, a stride below hidden, eps negative or NaN, a static scale that is
+ * not positive and finite.  num_tokens 0 is a no-op.
+ */
+MOE_API moe_status moe_add_rms_norm(const uint16_t* d_x, int64_t x_stride, const uint16_t* d_residual,
+                                    int64_t residual_stride, const uint16_t* d_weight, float eps,
+                                    int64_t num_tokens, int32_t hidden, uint16_t* d_residual_out,
+                                    uint16_t* d_y, uint8_t* d_q, uint8_t* d_q_scale,
+                                    uint32_t q_format, float q_static_scale,
+                                    struct CUstream_st* stream);
+
+/*
+ * moe_topk_route -- gate logits to the expert ids and weights that
+ * moe_forward and moe_fp4_forward take.
+ *   d_logits   float (logits_bf16 = 0) or BF16 [num_tokens, num_experts], rows
+ *              logits_stride elements apart.
+ *   sigmoid 0: score = softmax over the row, the choice goes by the logit, a
+ *              group's score is its largest logit.
+ *   sigmoid 1: score = 1 / (1 + exp(-logit)), the choice goes by score + bias
+ *              (d_bias float [num_experts], or NULL), a group's score is the
+ *              sum of its two largest choice values.
+ *   The top_groups best of num_groups equal groups of consecutive experts are
+ *   kept, then the top_k experts among them in descending order; ties go to
+ *   the lowest index.  Weight = score (over the sum of the chosen scores when
+ *   renormalize != 0; 0 where that sum is 0) * scale.
+ *   d_topk_idx int32 [num_tokens, top_k], d_topk_w float [num_tokens, top_k].
+ * An expert whose logit or bias is -inf is masked; slots that no expert is
+ * left for get id -1 and weight 0 (masked slots of the forwards).  A row that
+ * holds a NaN gets NaN weights, which the forwards' route checks report.
+ * Asynchronous on `stream`; num_tokens 0 is a no-op.  MOE_ERR_UNSUPPORTED:
+ * num_experts not in 1..1024, top_k not in 1..min(32, num_experts),
+ * num_groups not in 1..32 or no divisor of num_experts, top_groups not in
+ * 1..num_groups, a bias without sigmoid.  MOE_ERR_INVALID_ARG: a NULL or
+ * misaligned pointer, a stride below num_experts.
+ */
+MOE_API moe_status moe_topk_route(const void* d_logits, int32_t logits_bf16, int64_t logits_stride,
+                                  const float* d_bias, int64_t num_tokens, int32_t num_experts,
+                                  int32_t top_k, int32_t sigmoid, int32_t num_groups,
+                                  int32_t top_groups, int32_t renormalize, float scale,
+                                  int32_t* d_topk_idx, float* d_topk_w, struct CUstream_st* stream);
+
+/*
+ * The few-token operators on NVFP4 weights, read as the checkpoint stores
+ * them (the parts moe_requantize_weights_nvfp4 takes): codes uint8
+ * [n, rows, cols/2], two E2M1 codes per byte, column 2b in the low nibble of
+ * byte b; scales uint8 [n, rows, cols/16], E4M3; global float [n];
+ *   v = e2m1(code) * e4m3(scale) * global.
+ * Weights stay in four bits, activations in BF16 or better, sums in float.  A
+ * handle binds one layer's or one matrix's device pointers and a workspace
+ * that no other handle uses at the same time.
+ */
+typedef struct moe_fp4_handle moe_fp4_handle;
+
+/*
+ * moe_fp4_workspace_query / moe_fp4_create -- the whole MoE layer for at most
+ * max_tokens (1..16) tokens.  dims as for moe_create; dims.flags 0 or
+ * MOE_FLAG_CHECK_ROUTES.
+ *   d_w1  [E, 2I, H]: rows [0, I) gate, rows [I, 2I) up;  d_w2  [E, H, I].
+ *   codes and scales 16-byte aligned.
+ * The query is host arithmetic.  The weights are read in place (kept by the
+ * caller, unchanged, while the handle lives), the workspace's counters are
+ * cleared on `stream`.  MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (dims or
+ * max_tokens out of range, another GPU), MOE_ERR_WORKSPACE, MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_fp4_workspace_query(const moe_dims* dims, int64_t max_tokens,
+                                           size_t* workspace_bytes);
+MOE_API moe_status moe_fp4_create(const moe_dims* dims, int64_t max_tokens, const uint8_t* d_w1,
+                                  const uint8_t* d_w1_scale, const float* d_w1_global,
+                                  const uint8_t* d_w2, const uint8_t* d_w2_scale,
+                                  const float* d_w2_global, void* d_workspace, size_t workspace_bytes,
+                                  struct CUstream_st* stream, moe_fp4_handle** out);
+
+/*
+ * moe_fp4_forward -- out[t] = sum_k w[t,k] * W2[e] (silu(g) * u), (g; u) =
+ * W1[e] x[t], e = topk_idx[t,k].  Inputs and -1 slots as for moe_forward; a
+ * token without an active slot gets zeros.  d_out BF16 [num_tokens, hidden].
+ * d_x and d_out 16-byte aligned.  An id outside [-1, E) sets
+ * MOE_DEV_ROUTE_RANGE and its slot is skipped; MOE_FLAG_CHECK_ROUTES adds the
+ * duplicate and finite-weight checks.  Asynchronous on `stream`, capturable in
+ * a CUDA graph.  num_tokens 0 is a no-op; MOE_ERR_CAPACITY above max_tokens.
+ */
+MOE_API moe_status moe_fp4_forward(moe_fp4_handle* h, const uint16_t* d_x, const int32_t* d_topk_idx,
+                                   const float* d_topk_w, int64_t num_tokens, uint16_t* d_out,
+                                   struct CUstream_st* stream);
+
+/*
+ * moe_fp4_linear -- y = x W^T for 1..16 tokens and one matrix [rows, cols]:
+ * d_x BF16 [num_tokens, cols], rows x_stride elements apart (a multiple of 8;
+ * 16-byte aligned), d_y [num_tokens, rows] float (y_float32 != 0) or BF16.
+ * Any rows up to 2^24; cols a multiple of 32 up to 32768.  Errors as above.
+ */
+MOE_API moe_status moe_fp4_linear_workspace_query(int32_t rows, int32_t cols, int64_t max_tokens,
+                                                  size_t* workspace_bytes);
+MOE_API moe_status moe_fp4_linear_create(int32_t rows, int32_t cols, int64_t max_tokens,
+                                         const uint8_t* d_codes, const uint8_t* d_scales,
+                                         const float* d_global, void* d_workspace,
+                                         size_t workspace_bytes, struct CUstream_st* stream,
+                                         moe_fp4_handle** out);
+MOE_API moe_status moe_fp4_linear(moe_fp4_handle* h, const uint16_t* d_x, int64_t x_stride,
+                                  int64_t num_tokens, void* d_y, int32_t y_float32,
+                                  struct CUstream_st* stream);
+
+/* moe_fp4_read_status -- the device status word of the handle's latest call
+ * (as moe_read_status: copies it on `stream` and synchronises that stream). */
+MOE_API moe_status moe_fp4_read_status(moe_fp4_handle* h, uint32_t* h_status,
+                                       struct CUstream_st* stream);
+/* moe_fp4_destroy -- frees the host handle; NULL is a no-op. */
+MOE_API void moe_fp4_destroy(moe_fp4_handle* h);
+
 /* moe_destroy -- frees the host handle (lifecycle only; the pages have no
  * passage on it).  Device memory stays the caller's.  NULL is a no-op. */
 MOE_API void moe_destroy(moe_handle* h);

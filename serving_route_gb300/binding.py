@@ -52,7 +52,10 @@ API_NAMES = ("moe_workspace_query", "moe_create", "moe_quantize_weights", "moe_q
              "moe_set_activation_scales",
              "moe_stage_inputs", "moe_forward", "moe_read_status", "moe_debug_views",
              "moe_set_profile_events", "moe_set_sm_budget", "moe_forward_plan", "moe_route_noalloc",
-             "moe_destroy", "moe_status_str")
+             "moe_destroy", "moe_status_str", "moe_add_rms_norm", "moe_topk_route",
+             "moe_fp4_workspace_query", "moe_fp4_create", "moe_fp4_forward",
+             "moe_fp4_linear_workspace_query", "moe_fp4_linear_create", "moe_fp4_linear",
+             "moe_fp4_read_status", "moe_fp4_destroy")
 
 
 class moe_dims(ctypes.Structure):
@@ -114,12 +117,28 @@ def lib() -> ctypes.CDLL:
         L.moe_set_sm_budget.argtypes = [vp, i32]
         L.moe_forward_plan.argtypes = [vp, i64, ctypes.POINTER(moe_plan)]
         L.moe_route_noalloc.argtypes = [vp, vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+        f32, u32, psz = ctypes.c_float, ctypes.c_uint32, ctypes.POINTER(ctypes.c_size_t)
+        L.moe_add_rms_norm.argtypes = [vp, i64, vp, i64, vp, f32, i64, i32, vp, vp, vp, vp, u32, f32,
+                                       vp]
+        L.moe_topk_route.argtypes = [vp, i32, i64, vp, i64, i32, i32, i32, i32, i32, i32, f32, vp, vp,
+                                     vp]
+        L.moe_fp4_workspace_query.argtypes = [ctypes.POINTER(moe_dims), i64, psz]
+        L.moe_fp4_create.argtypes = [ctypes.POINTER(moe_dims), i64, vp, vp, vp, vp, vp, vp, vp,
+                                     ctypes.c_size_t, vp, ctypes.POINTER(vp)]
+        L.moe_fp4_forward.argtypes = [vp, vp, vp, vp, i64, vp, vp]
+        L.moe_fp4_linear_workspace_query.argtypes = [i32, i32, i64, psz]
+        L.moe_fp4_linear_create.argtypes = [i32, i32, i64, vp, vp, vp, vp, ctypes.c_size_t, vp,
+                                            ctypes.POINTER(vp)]
+        L.moe_fp4_linear.argtypes = [vp, vp, i64, i64, vp, i32, vp]
+        L.moe_fp4_read_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
+        L.moe_fp4_destroy.argtypes = [vp]
+        L.moe_fp4_destroy.restype = None
         L.moe_destroy.argtypes = [vp]
         L.moe_destroy.restype = None
         L.moe_status_str.argtypes = [st]
         L.moe_status_str.restype = ctypes.c_char_p
         for n in API_NAMES:
-            if n not in ("moe_destroy", "moe_status_str"):
+            if n not in ("moe_destroy", "moe_status_str", "moe_fp4_destroy"):
                 getattr(L, n).restype = st
         _lib = L
     return _lib
@@ -238,3 +257,69 @@ def moe_route_noalloc(d_idx, d_w, num_tokens, top_k, num_experts, check_routes, 
 def moe_destroy(h) -> None:
     if h:
         lib().moe_destroy(h)
+
+
+def moe_add_rms_norm(d_x, x_stride, d_res, res_stride, d_w, eps, num_tokens, hidden, d_res_out, d_y,
+                     d_q, d_q_scale, q_format, q_static_scale, stream) -> None:
+    _check(lib().moe_add_rms_norm(d_x, x_stride, d_res, res_stride, d_w, eps, num_tokens, hidden,
+                                  d_res_out, d_y, d_q, d_q_scale, q_format, q_static_scale, stream),
+           "moe_add_rms_norm")
+
+
+def moe_topk_route(d_logits, bf16, stride, d_bias, num_tokens, E, K, sigmoid, groups, top_groups,
+                   renormalize, scale, d_idx, d_w, stream) -> None:
+    _check(lib().moe_topk_route(d_logits, bf16, stride, d_bias, num_tokens, E, K, sigmoid, groups,
+                                top_groups, renormalize, scale, d_idx, d_w, stream), "moe_topk_route")
+
+
+def moe_fp4_workspace_query(H, I, E, K, flags, max_tokens) -> int:
+    n = ctypes.c_size_t()
+    d = _dims(H, I, E, K, flags)
+    _check(lib().moe_fp4_workspace_query(ctypes.byref(d), max_tokens, ctypes.byref(n)),
+           "moe_fp4_workspace_query")
+    return n.value
+
+
+def moe_fp4_create(H, I, E, K, flags, max_tokens, d_w1, d_w1s, d_w1g, d_w2, d_w2s, d_w2g, d_ws,
+                   ws_bytes, stream) -> int:
+    h = ctypes.c_void_p()
+    d = _dims(H, I, E, K, flags)
+    _check(lib().moe_fp4_create(ctypes.byref(d), max_tokens, d_w1, d_w1s, d_w1g, d_w2, d_w2s, d_w2g,
+                                d_ws, ws_bytes, stream, ctypes.byref(h)), "moe_fp4_create")
+    return h.value
+
+
+def moe_fp4_forward(h, d_x, d_idx, d_w, num_tokens, d_out, stream) -> None:
+    _check(lib().moe_fp4_forward(h, d_x, d_idx, d_w, num_tokens, d_out, stream), "moe_fp4_forward")
+
+
+def moe_fp4_linear_workspace_query(rows, cols, max_tokens) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_fp4_linear_workspace_query(rows, cols, max_tokens, ctypes.byref(n)),
+           "moe_fp4_linear_workspace_query")
+    return n.value
+
+
+def moe_fp4_linear_create(rows, cols, max_tokens, d_codes, d_scales, d_global, d_ws, ws_bytes,
+                          stream) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().moe_fp4_linear_create(rows, cols, max_tokens, d_codes, d_scales, d_global, d_ws,
+                                       ws_bytes, stream, ctypes.byref(h)), "moe_fp4_linear_create")
+    return h.value
+
+
+def moe_fp4_linear(h, d_x, x_stride, num_tokens, d_y, y_float32, stream) -> None:
+    _check(lib().moe_fp4_linear(h, d_x, x_stride, num_tokens, d_y, y_float32, stream),
+           "moe_fp4_linear")
+
+
+def moe_fp4_read_status(h, stream):
+    """(status code, device status bits)"""
+    bits = ctypes.c_uint32()
+    s = lib().moe_fp4_read_status(h, ctypes.byref(bits), stream)
+    return s, bits.value
+
+
+def moe_fp4_destroy(h) -> None:
+    if h:
+        lib().moe_fp4_destroy(h)

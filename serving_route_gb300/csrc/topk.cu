@@ -1,0 +1,208 @@
+// topk.cu -- gate logits to expert ids and weights (moe_topk_route), one warp
+// per token.
+//
+//   softmax:  score p = softmax(l) over the row; the choice goes by l (same
+//             order); a group's score is its largest logit.
+//   sigmoid:  score p = 1 / (1 + exp(-l)); the choice goes by p + bias; a
+//             group's score is the sum of its two largest choice values.
+//   kept:     the top_groups groups of the highest score, then the top_k
+//             experts among them, ties to the lowest index;
+//   weight:   p of the chosen, divided by their sum (renormalize), times scale.
+//
+// An expert whose logit (or bias) is -inf is masked: it is never chosen, and
+// slots without an expert get id -1 and weight 0, which the layer skips.
+//
+// Every lane holds E / 32 choice values in registers as integers of the same
+// order (0: masked or taken), so a choice is two warp-wide integer reductions
+// (the largest value, then the lowest index that has it).  Bytes: the logits
+// once, 8 per chosen expert; for few tokens the chain of top_k choices bounds
+// it, for many the instructions issued.
+#include "common.cuh"
+#include "internal.h"
+
+namespace mm {
+
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+// Integers in the order of the floats, all above 0 (-inf gives 0x007FFFFF).
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // -0 and +0 are the same choice
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+__device__ __forceinline__ float sigmoid_score(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+struct TopkArgs {
+  const void* logits;
+  const float* bias;
+  int32_t* idx;
+  float* w;
+  int64_t ld, T;
+  int E, K, groups, top_groups;
+  float scale;
+  bool renorm;
+};
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
+  return BF16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p)[i])
+              : reinterpret_cast<const float*>(p)[i];
+}
+
+// V values per lane: expert 32 i + lane.
+template <int V, bool BF16, bool SIGMOID>
+__global__ void __launch_bounds__(128) topk_route_kernel(const TopkArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const int64_t row = t * a.ld;
+  float l[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = 32 * i + lane;
+    l[i] = e < a.E ? load_logit<BF16>(a.logits, row + e) : -INFINITY;
+  }
+  uint32_t key[V];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = 32 * i + lane;
+    float c = l[i];
+    if (SIGMOID) {
+      c = sigmoid_score(c);
+      if (a.bias && e < a.E) c += a.bias[e];
+    }
+    bad |= l[i] != l[i] || c != c;
+    key[i] = (l[i] != l[i] || c != c || l[i] == -INFINITY || c == -INFINITY) ? 0u : order_key(c);
+  }
+  const bool any_nan = __any_sync(kAll, bad);
+
+  if (a.groups > 1) {
+    const int gs = a.E / a.groups;
+    uint32_t mine = 0u;  // lane g: group g's score
+    for (int g = 0; g < a.groups; ++g) {
+      uint32_t m1 = 0u, m2 = 0u;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = 32 * i + lane;
+        const uint32_t k = (e >= g * gs && e < (g + 1) * gs) ? key[i] : 0u;
+        m2 = max(m2, min(m1, k));
+        m1 = max(m1, k);
+      }
+      const uint32_t b1 = __reduce_max_sync(kAll, m1);
+      uint32_t score = b1;
+      if (SIGMOID && b1) {
+        const int first = __ffs(__ballot_sync(kAll, m1 == b1)) - 1;
+        const uint32_t b2 = __reduce_max_sync(kAll, lane == first ? m2 : m1);
+        score = order_key(key_value(b1) + (b2 ? key_value(b2) : 0.f));
+      }
+      if (lane == g) mine = score;
+    }
+    uint32_t keep = 0u;
+    for (int n = 0; n < a.top_groups; ++n) {
+      const uint32_t b = __reduce_max_sync(kAll, mine);
+      if (b == 0u) break;
+      const int g = __ffs(__ballot_sync(kAll, mine == b)) - 1;
+      keep |= 1u << g;
+      if (lane == g) mine = 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (!((keep >> ((32 * i + lane) / gs & 31)) & 1u)) key[i] = 0u;
+  }
+
+  int my = -1;  // lane k: the k-th choice
+  for (int k = 0; k < a.K; ++k) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = max(m, key[i]);
+    const uint32_t b = __reduce_max_sync(kAll, m);
+    if (b == 0u) break;
+    uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i)
+      if (key[i] == b) at = 32 * i + lane;
+    at = __reduce_min_sync(kAll, at);
+    if (lane == k) my = (int)at;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (at == 32 * i + lane) key[i] = 0u;
+  }
+
+  float p = 0.f;
+  if (SIGMOID) {
+    if (my >= 0) p = sigmoid_score(load_logit<BF16>(a.logits, row + my));
+  } else {
+    float m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+    if (m > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s += expf(l[i] - m);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    if (my >= 0) p = expf(load_logit<BF16>(a.logits, row + my) - m) / s;
+  }
+  if (a.renorm) {
+    float s = p;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    p = s == 0.f ? 0.f : p / s;
+  }
+  if (lane < a.K) {
+    a.idx[t * a.K + lane] = my;
+    // a NaN logit or bias: NaN weights, which the layer's route check reports
+    a.w[t * a.K + lane] = any_nan ? NAN : p * a.scale;
+  }
+}
+
+template <int V>
+static cudaError_t launch_topk(const TopkArgs& a, bool bf16, bool sigmoid, cudaStream_t s) {
+  auto k = bf16 ? (sigmoid ? topk_route_kernel<V, true, true> : topk_route_kernel<V, true, false>)
+                : (sigmoid ? topk_route_kernel<V, false, true> : topk_route_kernel<V, false, false>);
+  k<<<(unsigned)((a.T + 3) / 4), 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace mm
+
+using namespace mm;
+
+extern "C" moe_status moe_topk_route(const void* d_logits, int32_t logits_bf16, int64_t logits_stride,
+                                     const float* d_bias, int64_t num_tokens, int32_t num_experts,
+                                     int32_t top_k, int32_t sigmoid, int32_t num_groups,
+                                     int32_t top_groups, int32_t renormalize, float scale,
+                                     int32_t* d_topk_idx, float* d_topk_w,
+                                     struct CUstream_st* stream) {
+  if (num_tokens < 0) return MOE_ERR_INVALID_ARG;
+  if (num_experts < 1 || num_experts > 1024 || top_k < 1 || top_k > 32 || top_k > num_experts)
+    return MOE_ERR_UNSUPPORTED;
+  if (num_groups < 1 || num_groups > 32 || num_experts % num_groups || top_groups < 1 ||
+      top_groups > num_groups || (d_bias && !sigmoid))
+    return MOE_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return MOE_OK;
+  if (num_tokens > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  if (!d_logits || !d_topk_idx || !d_topk_w || logits_stride < num_experts) return MOE_ERR_INVALID_ARG;
+  if (((uintptr_t)d_logits & (logits_bf16 ? 1 : 3)) || ((uintptr_t)d_bias & 3) ||
+      ((uintptr_t)d_topk_idx & 3) || ((uintptr_t)d_topk_w & 3))
+    return MOE_ERR_INVALID_ARG;
+  const TopkArgs a = {d_logits,     d_bias, d_topk_idx, d_topk_w,   logits_stride,
+                      num_tokens,   num_experts, top_k, num_groups, top_groups,
+                      scale,        renormalize != 0};
+  const int v = (num_experts + 31) / 32;
+  const bool b = logits_bf16 != 0, g = sigmoid != 0;
+  cudaError_t e = v <= 1   ? launch_topk<1>(a, b, g, stream)
+                  : v <= 2 ? launch_topk<2>(a, b, g, stream)
+                  : v <= 4 ? launch_topk<4>(a, b, g, stream)
+                  : v <= 8 ? launch_topk<8>(a, b, g, stream)
+                  : v <= 16 ? launch_topk<16>(a, b, g, stream)
+                            : launch_topk<32>(a, b, g, stream);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
