@@ -48,18 +48,25 @@ namespace mm {
 constexpr int kFp4MaxTokens = 16;
 constexpr int kFp4MaxRoutes = 128;
 constexpr int kFp4Grid = 152;        // one CTA per SM
-constexpr int kConsumers = 8;        // warps 0..7: dequantise and multiply
-constexpr int kWarpProducer = 8;     // one thread issues the TMA loads
-constexpr int kWarpEpilogue = 9;     // adds the warps' sums, finishes and joins tiles
-constexpr int kWarpLoader = 10;      // four warps: x and h rows to half in shared memory
+constexpr int kConsumers = 8;        // the first warps: dequantise and multiply
+constexpr int kProducers = 2;        // then two that issue the copies of the weights, in turn
+constexpr int kWarpProducer = kConsumers;
+constexpr int kWarpEpilogue = kWarpProducer + kProducers;  // adds the warps' sums, finishes and joins tiles
+constexpr int kWarpLoader = kWarpEpilogue + 1;             // x and h rows to half in shared memory
 constexpr int kLoaders = 4;
 constexpr int kFp4Threads = 32 * (kWarpLoader + kLoaders);
 constexpr int kUnitCols = 512;
-constexpr int kStageBytes = 32 * kUnitCols / 2;
+constexpr int kCodeBytes = 32 * kUnitCols / 2;
+constexpr int kScaleBytes = 32 * kUnitCols / 16;
+constexpr int kStageBytes = kCodeBytes + kScaleBytes;
 constexpr int kBoxBytes = 16 * 128;  // 16 rows x 256 columns
-constexpr int kMaxStages = 24;
-constexpr int kPartSlots = 3;
+// A multiple of kConsumers: then a slot's units are all one warp's, so no warp
+// waits for a phase while an earlier phase of the slot is open (it would take
+// the parity of the phase before that one for its own).
+constexpr int kMaxStages = 2 * kConsumers;
 constexpr int kItems = 8;            // operand items in flight (rows ring)
+constexpr int kCutUnits = 15;        // units of imbalance that a tile's join costs (about 3 us)
+constexpr int kTile2 = 128;          // output rows of an FC2 tile
 constexpr int kMaxSmem = 232448;
 
 struct Fp4Matrix {
@@ -74,34 +81,87 @@ struct Fp4Args {
   int64_t ldx;
   const int32_t* idx;
   const float* w;
-  float* h;             // [T*K, I]
+  uint8_t* h;           // [T*K] records of half values and their block exponents
   void* y;              // the layer's BF16 output, or the linear's
   uint32_t* status;
   uint32_t* ctl;        // [0] barrier, [1] finished CTAs, [2 + 152 p + c] joins of phase p
-  float* part;          // [2][152][2][512]: a CTA's cut tiles, first and last
+  float* part[2];       // by phase, [152][2][..]: a CTA's cut tiles, first and last
   int T, E, K, group;   // group: tokens of one operand item, at most 8 NT
   int stages, b_bytes;
   bool check, f32;
 };
 
 __host__ __device__ inline int padded_units(int cols) { return (cols + kUnitCols - 1) / kUnitCols; }
-// 64 bytes of padding: rows of different parity lie in different halves of the banks
-__host__ __device__ inline int row_bytes(int cols) { return padded_units(cols) * kUnitCols * 2 + 64; }
+// h of one route in global memory: halves, then one exponent byte per 16 of them
+__host__ __device__ inline int exponent_bytes(int cols) { return (cols / 16 + 15) & ~15; }
+__host__ __device__ inline int record_bytes(int cols) { return cols * 2 + exponent_bytes(cols); }
+// An operand row in shared memory: whole units, the exponents of an h row, and 64 bytes
+// past a multiple of 128, so that rows of different parity lie in different banks.
+__host__ __device__ inline int row_bytes(int cols, bool h) {
+  return ((padded_units(cols) * kUnitCols * 2 + (h ? exponent_bytes(cols) : 0) + 127) & ~127) + 64;
+}
 
 struct Fp4Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t pfull[kPartSlots], pempty[kPartSlots];
+  uint64_t pfull[kConsumers][2], pempty[kConsumers][2];
   uint64_t bfull[2][kItems], bempty[2][kItems];
-  float out[kFp4MaxTokens][33];
+  uint64_t raw[kLoaders];
+  alignas(16) float out[kFp4MaxTokens][kTile2];
+  alignas(16) int key[kFp4MaxRoutes];
   float rscale[2][kFp4MaxRoutes];       // per operand row: 2^-s
-  float red[kLoaders];
+  float vglobal[2][kFp4MaxRoutes];      // the items' matrix scales
   float route_w[kFp4MaxRoutes];         // by sorted position, as the next ones
-  int16_t route_e[kFp4MaxRoutes], route_id[kFp4MaxRoutes];
+  int16_t route_e[kFp4MaxRoutes], route_id[kFp4MaxRoutes], route_tok[kFp4MaxRoutes];
   int16_t vstart[kFp4MaxRoutes + 1];    // first sorted position of every item
   int16_t vexp[kFp4MaxRoutes];
+  uint8_t first[kFp4MaxRoutes];
+  float red[kLoaders];
   int warp_cnt[4];
   int nv, nroutes;
   int abort;
+};
+
+// Where a walk over a phase stands: segment seg = the U units of item v's
+// product with 32 matrix rows: block rb of tile j.
+struct SegPos {
+  int v, j, rb;
+};
+
+// One phase of one CTA: units [u0, u1), U to a segment.  Order of the segments:
+// first phase  item, tile (RT of 32 rows each);
+// second       tile (128 rows), item, block of 32 rows -- an item's rows serve four segments.
+struct Phase {
+  int p, U, RT, nv, u0, u1, cols;
+  __device__ int seg_begin() const { return u0 / U; }
+  __device__ SegPos at(int seg) const {
+    SegPos s;
+    if (p == 0) {
+      s.v = seg / RT;
+      s.j = seg - s.v * RT;
+      s.rb = 0;
+    } else {
+      s.j = seg / (nv * 4);
+      const int r = seg - s.j * nv * 4;
+      s.v = r >> 2;
+      s.rb = r & 3;
+    }
+    return s;
+  }
+  __device__ void step(SegPos& s) const {
+    if (p == 0) {
+      if (++s.j == RT) {
+        s.j = 0;
+        ++s.v;
+      }
+    } else if (++s.rb == 4) {
+      s.rb = 0;
+      if (++s.v == nv) {
+        s.v = 0;
+        ++s.j;
+      }
+    }
+  }
+  __device__ int tile_units() const { return p == 0 ? U : nv * 4 * U; }
 };
 
 template <bool MOE, int NT>
@@ -110,28 +170,11 @@ struct Fp4Ctx {
   Fp4Shared& sm;
   int nv;
 
-  // One phase: `total` units in segments of U; a segment is a row tile times an item.
-  struct Phase {
-    int p, U, RT, nv, u0, u1, cols;
-    __device__ int seg_begin() const { return u0 / U; }
-    __device__ void split(int seg, int& v, int& j) const {
-      if (p == 0) {
-        v = seg / RT;
-        j = seg - v * RT;
-      } else {
-        j = seg / nv;
-        v = seg - j * nv;
-      }
-    }
-    // units of the tile that holds seg
-    __device__ int tile_units() const { return p == 0 ? U : nv * U; }
-  };
-
   __device__ int64_t total_units(int p) const {
-    const int U = padded_units(a.m[p].cols);
-    const int RT = (a.m[p].rows + 31) / 32;
-    return (int64_t)nv * RT * U;
+    return (int64_t)nv * ((a.m[p].rows + 31) / 32) * padded_units(a.m[p].cols);
   }
+  // CTAs with work: none of them without a unit, so that a cut tile's CTAs are consecutive
+  __device__ static int64_t ctas(int64_t n) { return min(n, (int64_t)gridDim.x); }
 
   __device__ Phase phase(int p) const {
     Phase f;
@@ -140,53 +183,61 @@ struct Fp4Ctx {
     f.U = padded_units(f.cols);
     f.RT = (a.m[p].rows + 31) / 32;
     f.nv = nv;
-    const int64_t n = total_units(p), G = ctas(n);
-    f.u0 = (int)(n * min((int64_t)blockIdx.x, G) / G);
-    f.u1 = (int)(n * min((int64_t)blockIdx.x + 1, G) / G);
+    // whole tiles, unless the CTA with one more than the others would work
+    // longer than a join takes
+    const int64_t n = total_units(p), tu = f.tile_units(), tiles = n / tu;
+    const int64_t most = (tiles + gridDim.x - 1) / gridDim.x * tu;
+    const int64_t G = ctas(n), step = most - (n + G - 1) / G > kCutUnits ? 1 : tu;
+    const int64_t steps = n / step, H = min(steps, G);
+    f.u0 = (int)(steps * min((int64_t)blockIdx.x, H) / H * step);
+    f.u1 = (int)(steps * min((int64_t)blockIdx.x + 1, H) / H * step);
     return f;
   }
-  // CTAs with work: none of them without a unit, so that a cut tile's CTAs are consecutive
-  __device__ static int64_t ctas(int64_t n) { return min(n, (int64_t)gridDim.x); }
 
   __device__ int item_rows(int v) const { return sm.vstart[v + 1] - sm.vstart[v]; }
-  __device__ int resident_rows(int p) const { return p == 0 ? a.T : sm.nroutes; }
+  // x rows stay for the whole phase where all of them fit; h rows always pass
+  // through the ring, so that the first segment waits for its own rows only
   __device__ bool resident(int p) const {
-    return (int64_t)resident_rows(p) * row_bytes(a.m[p].cols) <= a.b_bytes;
+    return p == 0 && (int64_t)a.T * row_bytes(a.m[0].cols, false) <= a.b_bytes;
   }
   __device__ int ring_rows(int p) const {
-    const int r = a.b_bytes / row_bytes(a.m[p].cols);
-    return r < kFp4MaxRoutes ? r : kFp4MaxRoutes;
+    return min(a.b_bytes / row_bytes(a.m[p].cols, p == 1), kFp4MaxRoutes);
   }
-  // matrix row of row r (0..31) of tile j of item v
-  __device__ int64_t matrix_row(int p, int v, int j, int r) const {
-    if (MOE) {
-      const int64_t base = (int64_t)sm.vexp[v] * a.m[p].rows;
-      if (p == 0)  // 16 gate rows, then their 16 up rows
-        return base + (r < 16 ? 16 * j + r : a.m[0].rows / 2 + 16 * j + r - 16);
-      return base + 32 * j + r;
-    }
-    return 32 * (int64_t)j + r;
+  // place of an item's column among the operand rows
+  __device__ int row_slot(bool resident, int pos, int R, int s0, int col) const {
+    if (resident) return sm.route_tok[s0 + col];
+    return pos + col < R ? pos + col : pos + col - R;
+  }
+  // matrix row of row r (0..31) of a segment
+  __device__ int64_t matrix_row(int p, const SegPos& s, int r) const {
+    if (!MOE) return 32 * (int64_t)s.j + r;
+    const int64_t base = (int64_t)sm.vexp[s.v] * a.m[p].rows;
+    if (p == 0)  // 16 gate rows, then their 16 up rows
+      return base + (r < 16 ? 16 * s.j + r : a.m[0].rows / 2 + 16 * s.j + r - 16);
+    return base + kTile2 * s.j + 32 * s.rb + r;
   }
 };
 
 // Walks the operand items of a phase in segment order.  Resident: all rows stay
 // for the phase and there is one item.  Ring: an item is the rows of one token
-// group (first phase) or of one segment (second), at consecutive ring places.
+// group, for one run of segments, at consecutive ring places.
 struct ItemWalk {
-  int item = -1, v = -1, pos = 0, rows = 0;
-  template <class Ctx, class Ph>
-  __device__ bool next(const Ctx& c, const Ph& f, bool resident, int R, int nv_) {
+  int item = -1, v = -1, j = -1, pos = 0, rows = 0;
+  // whether a new item starts with segment s
+  template <class Ctx>
+  __device__ bool next(const Ctx& c, const Phase& f, bool resident, int R, const SegPos& s) {
     if (resident) {
       const bool fresh = item < 0;
       item = 0;
-      v = nv_;
       return fresh;
     }
-    if (f.p == 0 && v == nv_) return false;
-    if (item >= 0) pos = (pos + rows) % R;
+    if (s.v == v && (f.p == 0 || s.j == j)) return false;
+    pos += rows;
+    if (pos >= R) pos -= R;
     ++item;
-    v = nv_;
-    rows = c.item_rows(nv_);
+    v = s.v;
+    j = s.j;
+    rows = c.item_rows(s.v);
     return true;
   }
 };
@@ -214,8 +265,7 @@ __device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t codes) {
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -225,7 +275,8 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr));
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -235,94 +286,180 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
                : "memory");
 }
 
-// Eight scale codes of a row: groups first..first + 7 of ng (0 past the end).
-__device__ __forceinline__ uint2 load_scales(const uint8_t* row, int first, int ng, bool aligned8) {
-  uint2 r = make_uint2(0u, 0u);
-  if (aligned8) {
-    if (first < ng) r = __ldg(reinterpret_cast<const uint2*>(row + first));
-  } else {
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      h[i] = first + 2 * i < ng ? __ldg(reinterpret_cast<const uint16_t*>(row + first + 2 * i)) : 0u;
-    r = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-  }
-  return r;
+// Asynchronous copy of N bytes, of which the first `valid` are read and the rest zero.
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int valid) {
+  if (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(valid), "n"(N)
+                 : "memory");
 }
 
-// Eight consecutive values of an operand row.
-__device__ __forceinline__ void load8(const uint16_t* src, int k, float (&v)[8]) {
-  const uint4 p = __ldg(reinterpret_cast<const uint4*>(src + k));
-  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+// The 32 scale bytes of one row of a unit (n of them in the matrix, the rest
+// zero) to shared memory, in copies as wide as the rows' alignment allows.
+template <int N>
+__device__ __forceinline__ void copy_scale_row(uint32_t dst, const uint8_t* src, int n) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  for (int o = 0; o < 32; o += N) {
+    const int v = min(max(n - o, 0), N);
+    cp_async<N>(dst + o, v > 0 ? src + o : src, v);
   }
 }
 
-__device__ __forceinline__ void load8(const float* src, int k, float (&v)[8]) {
-  // h was written by other SMs in this launch: read it from L2
-  const float4 p = __ldcg(reinterpret_cast<const float4*>(src + k));
-  const float4 q = __ldcg(reinterpret_cast<const float4*>(src + k + 4));
-  v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w;
-  v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
+// Bounded wait of a whole warp: all of its lanes go on, or none.
+__device__ __forceinline__ bool warp_wait(uint64_t& bar, uint32_t parity, volatile int* abort,
+                                          uint32_t* status) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bar), parity, abort, status));
 }
 
-// One operand row: cols values (a multiple of 8) as half times 2^s, zeros up to
-// the unit's end, in the order of the MMAs' lanes: within a unit of 512 columns
-// lane t owns columns 128 t .. 128 t + 127 and takes its four 32-column chunks
-// in the order j -> chunk j ^ (t >= 2 ? 2 : 0); 16-byte piece i of step j of lane
-// t lies at ((j * 4 + i) * 4 + t) * 16.  team threads work on the row.
-template <typename SRC>
-__device__ __forceinline__ void fill_row(const SRC* src, int cols, uint32_t dst, int rank, int team,
-                                         float* red, float* rscale) {
-  const int n = cols >> 3, npad = padded_units(cols) * (kUnitCols / 8);
-  float m = 0.f;
+// Within a unit of 512 columns lane t of an MMA owns columns 128 t .. 128 t + 127
+// and takes its four 32-column chunks in the order j -> chunk j ^ (t >= 2 ? 2 : 0);
+// piece i (eight columns) of step j of lane t lies at ((j * 4 + i) * 4 + t) * 16.
+__device__ __forceinline__ int piece_offset(int q) {
+  const int t = q >> 4, ch = (q >> 2) & 3, i = q & 3;
+  return (((ch ^ ((t >> 1) << 1)) * 4 + i) * 4 + t) << 4;
+}
+
+// s with max * 2^s in [2^14, 2^15), kept so that 2^s and 2^-s are normal; 126 for 0.
+__device__ __forceinline__ int row_exponent(float max) {
+  const int ef = (int)(__float_as_uint(max) >> 23);
+  const int s = 141 - (ef < 1 ? 1 : ef);
+  return max == 0.f || s > 126 ? 126 : s;
+}
+
+__device__ __forceinline__ float pow2f(int s) { return __uint_as_float((uint32_t)(s + 127) << 23); }
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// Brings `bytes` (a multiple of 16) to shared memory and waits.  The places were
+// read and written through the generic proxy before: a fence orders them.
+__device__ __forceinline__ void raw_begin(uint64_t& bar, uint32_t bytes) {
+  fence_proxy_async_smem();
+  mbar_arrive_expect_tx(smem_u32(&bar), bytes);
+}
+
+// One x row (cols BF16 values, a multiple of 32) as half times 2^s, zeros up to
+// the unit's end.  The row is copied as it is and turned in place, unit by unit;
+// TEAM warps (one, or all loaders) work on it.
+template <int TEAM>
+__device__ __forceinline__ bool fill_x(const uint16_t* src, int cols, uint32_t dst, int rank,
+                                       uint64_t& bar, uint32_t& parity, float* red, float* rscale,
+                                       volatile int* abort, uint32_t* status) {
+  const int lane = threadIdx.x & 31, n = cols >> 3, U = padded_units(cols);
+  if (rank == 0 && lane == 0) {
+    raw_begin(bar, cols * 2);
+    bulk_load(dst, src, cols * 2, smem_u32(&bar));
+  }
+  const bool ok = warp_wait(bar, parity, abort, status);  // a team goes on to its barriers either way
+  parity ^= 1;
+  uint32_t m = 0u;  // the largest |value|, as BF16 bits
 #pragma unroll 4
-  for (int q = rank; q < n; q += team) {
-    float v[8];
-    load8(src, 8 * q, v);
+  for (int q = 32 * rank + lane; q < n; q += 32 * TEAM) {
+    const uint4 v = lds128(dst + 16 * q);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+      // NaN does not set the scale (it stays NaN in half); infinity does
+      m = max(m, max(lo > 0x7F80u ? 0u : lo, hi > 0x7F80u ? 0u : hi));
+    }
   }
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if (TEAM > 1) {
+    if (lane == 0) red[rank] = __uint_as_float(m);
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * TEAM) : "memory");
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  if (team > 32) {
-    if ((rank & 31) == 0) red[rank >> 5] = m;
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    asm volatile("bar.sync 1, 128;" ::: "memory");  // red is free for the next row
+    for (int i = 0; i < TEAM; ++i) m = max(m, __float_as_uint(red[i]));
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * TEAM) : "memory");  // red is free for the next row
   }
-  const int ef = (int)(__float_as_uint(m) >> 23);
-  int s = 141 - (ef < 1 ? 1 : ef);
-  s = m == 0.f ? 0 : (s > 126 ? 126 : s);
-  const float up = __uint_as_float((uint32_t)(s + 127) << 23);
-  if (rank == 0) *rscale = __uint_as_float((uint32_t)(127 - s) << 23);
-#pragma unroll 4
-  for (int q = rank; q < npad; q += team) {
-    uint4 o = make_uint4(0u, 0u, 0u, 0u);
-    if (q < n) {
-      float v[8];
-      load8(src, 8 * q, v);
+  const int s = row_exponent(__uint_as_float(m << 16));
+  const float up = pow2f(s);
+  if (rank == 0 && lane == 0) *rscale = pow2f(-s);
+  for (int u = rank; u < U; u += TEAM) {
+    const uint32_t base = dst + u * (kUnitCols * 2);
+    uint4 o[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int q = lane + 32 * k;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (64 * u + q < n) v = lds128(base + 16 * q);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       uint32_t h[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 p = __floats2half2_rn(v[2 * i] * up, v[2 * i + 1] * up);
-        h[i] = *reinterpret_cast<const uint32_t*>(&p);
-      }
-      o = make_uint4(h[0], h[1], h[2], h[3]);
+      for (int i = 0; i < 4; ++i)
+        h[i] = half2_bits(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
+      o[k] = make_uint4(h[0], h[1], h[2], h[3]);
     }
-    const int u = q >> 6, r = q & 63;  // 64 pieces per unit
-    const int t = r >> 4, c = (r >> 2) & 3, i = r & 3;
-    const int j = c ^ ((t >> 1) << 1);
-    sts128(dst + u * (kUnitCols * 2) + (((j * 4 + i) * 4 + t) << 4), o);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) sts128(base + piece_offset(lane + 32 * k), o[k]);
   }
+  return ok;
+}
+
+// 2^-d in half, 0 below the subnormals.
+__device__ __forceinline__ uint32_t half_pow2_neg(int d) {
+  const uint32_t b = d <= 14 ? (uint32_t)(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
+  return b | (b << 16);
+}
+
+// One h row: halves with one exponent per 16 (value = half * 2^-e) as halves of
+// the row's common exponent, turned in place like x.
+__device__ __forceinline__ bool fill_h(const uint8_t* src, int cols, uint32_t dst, uint64_t& bar,
+                                       uint32_t& parity, float* rscale, volatile int* abort,
+                                       uint32_t* status) {
+  const int lane = threadIdx.x & 31, n = cols >> 3, U = padded_units(cols);
+  const uint32_t ex = dst + U * (kUnitCols * 2);
+  if (lane == 0) {
+    raw_begin(bar, record_bytes(cols));
+    bulk_load(dst, src, cols * 2, smem_u32(&bar));
+    bulk_load(ex, src + cols * 2, exponent_bytes(cols), smem_u32(&bar));
+  }
+  if (!warp_wait(bar, parity, abort, status)) return false;
+  parity ^= 1;
+  auto exponent = [&](int block) {
+    int e;
+    asm volatile("ld.shared.s8 %0, [%1];" : "=r"(e) : "r"(ex + block) : "memory");
+    return e;
+  };
+  int s = 126;
+  for (int b = lane; b < (cols >> 4); b += 32) s = min(s, exponent(b));
+  s = __reduce_min_sync(0xFFFFFFFFu, s);
+  if (lane == 0) *rscale = pow2f(-s);
+  for (int u = 0; u < U; ++u) {
+    const uint32_t base = dst + u * (kUnitCols * 2);
+    uint4 o[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int q = lane + 32 * k;
+      o[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (64 * u + q < n) {
+        const uint4 v = lds128(base + 16 * q);
+        const int d = exponent((64 * u + q) >> 1) - s;
+        const uint32_t f1 = half_pow2_neg(min(d, 14)), f2 = half_pow2_neg(d - min(d, 14));
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(f1));
+          asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(f2));
+        }
+        o[k] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) sts128(base + piece_offset(lane + 32 * k), o[k]);
+  }
+  return true;
 }
 
 // Sorted routes, and the items: runs of at most `group` tokens of one expert.
 template <bool MOE>
-__device__ void build_items(const Fp4Args& a, Fp4Shared& sm) {
+__device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm) {
   const int tid = threadIdx.x;
   if (!MOE) {  // token groups of the linear
     if (tid == 0) {
@@ -336,84 +473,78 @@ __device__ void build_items(const Fp4Args& a, Fp4Shared& sm) {
       sm.nroutes = a.T;
       if (blockIdx.x == 0) atomicExch(a.status, 0u);
     }
-    if (tid < a.T) sm.route_id[tid] = tid;
-    __syncthreads();
+    if (tid < a.T) sm.route_id[tid] = sm.route_tok[tid] = tid;
     return;
   }
   const int R = a.T * a.K;
   int e = -1;
   float w = 0.f;
-  if (tid < kFp4MaxRoutes) {
-    if (tid < R) {
-      e = a.idx[tid];
-      w = a.w[tid];
-    }
-    sm.route_e[tid] = e >= 0 && e < a.E ? e : -1;
-  }
   uint32_t bits = 0u;
-  if (tid < R && (e < -1 || e >= a.E)) bits = MOE_DEV_ROUTE_RANGE;
-  if (e >= a.E) e = -1;
-  __syncthreads();
-  int pos = 0, within = 0, n = 0;
   if (tid < R) {
-    const int t0 = tid / a.K * a.K;
-    for (int r = 0; r < R; ++r) {
-      const int o = sm.route_e[r];
-      n += o >= 0;
-      pos += o >= 0 && (o < e || (o == e && r < tid));
-      within += o == e && r < tid;
-      if (a.check && e >= 0 && o == e && r >= t0 && r < tid) bits |= MOE_DEV_ROUTE_DUP;
-    }
-    if (a.check && e >= 0 && !(fabsf(w) < INFINITY)) bits |= MOE_DEV_ROUTE_NONFINITE;
+    e = a.idx[tid];
+    w = a.w[tid];
+    if (e < -1 || e >= a.E) bits = MOE_DEV_ROUTE_RANGE;
+    if (e >= a.E) e = -1;
   }
-  if (tid == 0) sm.nroutes = n;
-  __syncthreads();  // route_e is rewritten in sorted order
-  const bool live = tid < R && e >= 0;
-  int16_t* first = reinterpret_cast<int16_t*>(sm.out);  // scratch: item starts by position
-  if (tid < kFp4MaxRoutes) first[tid] = 0;
+  const bool live = e >= 0;  // (threads past the routes: not live)
+  const int mine = live ? e * kFp4MaxRoutes + tid : 0x7FFFFFFF;  // by expert, then by route
+  if (tid < kFp4MaxRoutes) {
+    sm.key[tid] = mine;
+    sm.first[tid] = 0;
+  }
   __syncthreads();
+  int pos = 0, within = 0;
   if (live) {
+    const int low = e * kFp4MaxRoutes;
+#pragma unroll 4
+    for (int r = 0; r < R; r += 4) {
+      const int4 k4 = *reinterpret_cast<const int4*>(&sm.key[r]);
+      const int k[4] = {k4.x, k4.y, k4.z, k4.w};  // past the routes: the largest key
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        pos += k[i] < mine;
+        within += k[i] < mine && k[i] >= low;
+      }
+    }
+    if (a.check) {
+      for (int r = tid / a.K * a.K; r < tid; ++r)
+        if (sm.key[r] >= low && sm.key[r] < mine) bits |= MOE_DEV_ROUTE_DUP;
+      if (!(fabsf(w) < INFINITY)) bits |= MOE_DEV_ROUTE_NONFINITE;
+    }
     sm.route_e[pos] = e;
     sm.route_id[pos] = tid;
+    sm.route_tok[pos] = tid / a.K;
     sm.route_w[pos] = w;
-    first[pos] = within % a.group == 0;
+    sm.first[pos] = within % a.group == 0;
   }
-  __syncthreads();
+  const int n = __syncthreads_count(live);
   if (tid < kFp4MaxRoutes) {
-    const bool f = first[tid] != 0;
-    const uint32_t b = __ballot_sync(0xFFFFFFFFu, f);
+    const uint32_t b = __ballot_sync(0xFFFFFFFFu, sm.first[tid] != 0);
     if ((tid & 31) == 0) sm.warp_cnt[tid >> 5] = __popc(b);
     within = __popc(b & ((1u << (tid & 31)) - 1u));
   }
-  __syncthreads();
+  // the status word is this call's: the first CTA sets it
+  if (__syncthreads_or(bits != 0u)) {
+    if (blockIdx.x == 0 && tid == 0) atomicExch(a.status, 0u);
+    __syncthreads();
+    if (blockIdx.x == 0 && bits) atomicOr(a.status, bits);
+  } else if (blockIdx.x == 0 && tid == 0) {
+    atomicExch(a.status, 0u);
+  }
   if (tid < kFp4MaxRoutes) {
     int v = within;
     for (int i = 0; i < (tid >> 5); ++i) v += sm.warp_cnt[i];
-    if (first[tid]) {
+    if (sm.first[tid]) {
       sm.vstart[v] = tid;
       sm.vexp[v] = sm.route_e[tid];
     }
     if (tid == 0) {
       const int nv = sm.warp_cnt[0] + sm.warp_cnt[1] + sm.warp_cnt[2] + sm.warp_cnt[3];
       sm.nv = nv;
-      sm.vstart[nv] = sm.nroutes;
+      sm.nroutes = n;
+      sm.vstart[nv] = n;
     }
   }
-  __syncthreads();
-  // the status word is this call's: the first CTA sets it
-  if (blockIdx.x == 0 && tid < kFp4MaxRoutes) {
-    const uint32_t all = __reduce_or_sync(0xFFFFFFFFu, bits);
-    if ((tid & 31) == 0) sm.warp_cnt[tid >> 5] = (int)all;
-  }
-  __syncthreads();
-  if (blockIdx.x == 0 && tid == 0)
-    atomicExch(a.status, (uint32_t)(sm.warp_cnt[0] | sm.warp_cnt[1] | sm.warp_cnt[2] | sm.warp_cnt[3]));
-}
-
-// Bounded wait of a whole warp: all of its lanes go on, or none.
-__device__ __forceinline__ bool warp_wait(uint64_t& bar, uint32_t parity, volatile int* abort,
-                                          uint32_t* status) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bar), parity, abort, status));
 }
 
 template <bool MOE, int NT>
@@ -423,28 +554,32 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ Fp4Shared sm;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t brow0 = ring + a.stages * kStageBytes;
-  const uint32_t pbuf = brow0 + a.b_bytes;
-  constexpr int kPartBytes = 2 * NT * 512;  // one warp's sums
+  const uint8_t* const smem = smem_raw + (ring - smem_u32(smem_raw));  // the same, for plain loads
+  const uint32_t srow0 = ring + a.stages * kCodeBytes;   // the stages' scales
+  const uint32_t brow0 = srow0 + a.stages * kScaleBytes; // operand rows
+  const uint32_t pbuf = brow0 + a.b_bytes;               // the consumers' sums
+  constexpr int kPartBytes = 2 * NT * 512;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) {
-    prefetch_tensormap(&tm0);
-    if (MOE) prefetch_tensormap(&tm1);
-    sm.abort = 0;
-    for (int i = 0; i < a.stages; ++i) {
-      mbar_init(smem_u32(&sm.full[i]), 1);
+  {
+    const int i = threadIdx.x;
+    if (i < kMaxStages) {
+      // copies: one arrival with the codes' bytes, one per lane with its scales
+      mbar_init(smem_u32(&sm.full[i]), 33);
       mbar_init(smem_u32(&sm.empty[i]), 1);
+    } else if (i >= 32 && i < 32 + 2 * kConsumers) {
+      mbar_init(smem_u32(&sm.pfull[0][0] + (i - 32)), 1);
+      mbar_init(smem_u32(&sm.pempty[0][0] + (i - 32)), 1);
+    } else if (i >= 64 && i < 64 + 2 * kItems) {
+      mbar_init(smem_u32(&sm.bfull[0][0] + (i - 64)), kLoaders);
+      mbar_init(smem_u32(&sm.bempty[0][0] + (i - 64)), kConsumers + 1);
+    } else if (i >= 96 && i < 96 + kLoaders) {
+      mbar_init(smem_u32(&sm.raw[i - 96]), 1);
+    } else if (i == 128) {
+      sm.abort = 0;
+      prefetch_tensormap(&tm0);
+      if (MOE) prefetch_tensormap(&tm1);
     }
-    for (int i = 0; i < kPartSlots; ++i) {
-      mbar_init(smem_u32(&sm.pfull[i]), kConsumers);
-      mbar_init(smem_u32(&sm.pempty[i]), 1);
-    }
-    for (int p = 0; p < 2; ++p)
-      for (int i = 0; i < kItems; ++i) {
-        mbar_init(smem_u32(&sm.bfull[p][i]), kLoaders);
-        mbar_init(smem_u32(&sm.bempty[p][i]), kConsumers + 1);
-      }
     fence_mbar_init();
   }
   build_items<MOE>(a, sm);
@@ -467,43 +602,26 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
   if (warp < kConsumers) {
     // ------------------------------------------------------------ consumers
     const int g = lane >> 2, t = lane & 3;
-    int nbase = 0;      // units of the CTA before this phase
-    int q = 0;          // segments of the CTA so far
+    int nbase = 0;  // units of the CTA before this phase
+    int pc = 0;     // sums this warp has handed over
     for (int p = 0; p < kPhases; ++p) {
-      const auto f = c.phase(p);
+      const Phase f = c.phase(p);
       if (f.u0 >= f.u1) continue;
-      const int ng = f.cols >> 4;
-      const bool al8 = (f.cols & 127) == 0;
-      const uint8_t* scales = a.m[p].scales;
-      const int64_t nrows = MOE ? (int64_t)a.E * a.m[p].rows : a.m[p].rows;
-      const int RB = row_bytes(f.cols);
+      const int RB = row_bytes(f.cols, p == 1);
       const bool res = c.resident(p);
       const int R = c.ring_rows(p);
-      uint2 sc[4];
-      auto fetch_scales = [&](int u) {
-        const int seg = u / f.U, k = u - seg * f.U;
-        int v, j;
-        f.split(seg, v, j);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const int64_t row = c.matrix_row(p, v, j, 16 * m + g);
-#pragma unroll
-          for (int hi = 0; hi < 2; ++hi)
-            sc[2 * m + hi] = row + 8 * hi < nrows
-                                 ? load_scales(scales + (row + 8 * hi) * ng, 32 * k + 8 * t, ng, al8)
-                                 : make_uint2(0u, 0u);
-        }
-      };
-      // this warp's units: n = warp mod 8, counted over both phases
-      int u = f.u0 + ((warp - nbase) & (kConsumers - 1));
-      if (u < f.u1) fetch_scales(u);
+      // this warp's units: every eighth, counted over both phases
+      const int n0 = (warp + kConsumers - nbase % kConsumers) % kConsumers;
+      int u = f.u0 + n0;
+      int slot = (nbase + n0) % a.stages;
+      uint32_t parity = ((nbase + n0) / a.stages) & 1;
       ItemWalk it;
-      for (int seg = f.seg_begin(); seg * f.U < f.u1; ++seg, ++q) {
+      int seg = f.seg_begin();
+      SegPos at = f.at(seg);
+      for (; seg * f.U < f.u1; ++seg, f.step(at)) {
         const int ub = min(f.u1, (seg + 1) * f.U);
-        int v, j;
-        f.split(seg, v, j);
         const int last_item = it.item;
-        if (it.next(c, f, res, R, v)) {
+        if (it.next(c, f, res, R, at)) {
           if (last_item >= 0) {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][last_item % kItems]));
@@ -511,148 +629,198 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
           if (!warp_wait(sm.bfull[p][it.item % kItems], (it.item / kItems) & 1, abort, a.status))
             goto done;
         }
-        float acc[2][NT][4] = {};
-        const bool any = u < ub;
-        if (any) {
-          const int n = c.item_rows(v), s0 = sm.vstart[v];
-          uint32_t brow[NT];
+        if (u >= ub) continue;
+        // two sums per tile, so that consecutive MMAs do not wait for each other
+        float acc[2][NT][2][4] = {};
+        const int n = c.item_rows(at.v), s0 = sm.vstart[at.v];
+        const uint8_t* brow[NT];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int col = min(8 * nt + g, n - 1);  // columns past n repeat a row; nothing reads them
-            const int slot = !res ? (it.pos + col) % R
-                             : p == 1 ? s0 + col
-                             : MOE ? sm.route_id[s0 + col] / a.K : s0 + col;
-            brow[nt] = brow0 + slot * RB + t * 16;
+        for (int nt = 0; nt < NT; ++nt) {
+          const int col = min(8 * nt + g, n - 1);  // columns past n repeat a row; nothing reads them
+          brow[nt] = smem + (brow0 - ring) + c.row_slot(res, it.pos, R, s0, col) * RB + t * 16;
+        }
+        for (; u < ub; u += kConsumers) {
+          const int boff = (u - seg * f.U) * (kUnitCols * 2);
+          if (!warp_wait(sm.full[slot], parity, abort, a.status)) goto done;
+          const uint8_t* base = smem + slot * kCodeBytes + (t >> 1) * kBoxBytes + g * 128;
+          const uint8_t* sbase = smem + (srow0 - ring) + slot * kScaleBytes + g * 32 + 8 * t;
+          uint2 s[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // rows g, g + 8, g + 16, g + 24
+            const uint2 v = *reinterpret_cast<const uint2*>(sbase + i * 256);
+            s[i] = t < 2 ? v : make_uint2(v.y, v.x);  // chunk order of lanes t >= 2
           }
-          for (; u < ub; u += kConsumers) {
-            const int nu = nbase + u - f.u0;
-            const int slot = nu % a.stages;
-            const int k = u - seg * f.U;
-            uint2 s[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              s[i] = t < 2 ? sc[i] : make_uint2(sc[i].y, sc[i].x);  // chunk order of lanes t >= 2
-            if (u + kConsumers < f.u1) fetch_scales(u + kConsumers);
-            if (!warp_wait(sm.full[slot], (nu / a.stages) & 1, abort, a.status)) goto done;
-            const uint32_t base = ring + slot * kStageBytes + (t >> 1) * kBoxBytes + g * 128;
-            const uint32_t boff = (uint32_t)k * (kUnitCols * 2);
+          for (int jj = 0; jj < 4; ++jj) {
+            const int chunk = (((t & 1) * 4 + (jj ^ ((t >> 1) << 1))) ^ g) << 4;
+            uint32_t cw[2][2][4], sw[2][2];
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-              const uint32_t chunk = (uint32_t)(((t & 1) * 4 + (jj ^ ((t >> 1) << 1))) ^ g) << 4;
-              uint32_t cw[2][2][4], sw[2][2];
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-              for (int m = 0; m < 2; ++m)
+              for (int hi = 0; hi < 2; ++hi) {
+                const uint4 x = *reinterpret_cast<const uint4*>(base + m * (2 * kBoxBytes) + hi * 1024 + chunk);
+                cw[m][hi][0] = x.x, cw[m][hi][1] = x.y, cw[m][hi][2] = x.z, cw[m][hi][3] = x.w;
+                const uint32_t word = jj < 2 ? s[2 * m + hi].x : s[2 * m + hi].y;
+                sw[m][hi] = e4m3x2_half2((jj & 1) ? word >> 16 : word & 0xFFFFu);
+              }
 #pragma unroll
-                for (int hi = 0; hi < 2; ++hi) {
-                  const uint4 x = lds128(base + m * (2 * kBoxBytes) + hi * 1024 + chunk);
-                  cw[m][hi][0] = x.x, cw[m][hi][1] = x.y, cw[m][hi][2] = x.z, cw[m][hi][3] = x.w;
-                  const uint32_t word = jj < 2 ? s[2 * m + hi].x : s[2 * m + hi].y;
-                  sw[m][hi] = e4m3x2_half2((jj & 1) ? word >> 16 : word & 0xFFFFu);
-                }
+            for (int i = 0; i < 4; ++i) {
+              uint4 b[NT];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint4 b[NT];
+              for (int nt = 0; nt < NT; ++nt)
+                b[nt] = *reinterpret_cast<const uint4*>(brow[nt] + boff + ((jj * 4 + i) << 6));
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) b[nt] = lds128(brow[nt] + boff + ((jj * 4 + i) << 6));
+              for (int m = 0; m < 2; ++m) {
+                uint32_t lo[4], hi[4];
+                const uint32_t sel = i < 2 ? 0x1010u : 0x3232u;
+                e2m1x8_scaled(cw[m][0][i], __byte_perm(sw[m][0], 0u, sel), lo);
+                e2m1x8_scaled(cw[m][1][i], __byte_perm(sw[m][1], 0u, sel), hi);
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                  uint32_t lo[4], hi[4];
-                  const uint32_t sel = i < 2 ? 0x1010u : 0x3232u;
-                  e2m1x8_scaled(cw[m][0][i], __byte_perm(sw[m][0], 0u, sel), lo);
-                  e2m1x8_scaled(cw[m][1][i], __byte_perm(sw[m][1], 0u, sel), hi);
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) {
-                    mma_16816(acc[m][nt], lo[0], hi[0], lo[1], hi[1], b[nt].x, b[nt].y);
-                    mma_16816(acc[m][nt], lo[2], hi[2], lo[3], hi[3], b[nt].z, b[nt].w);
-                  }
+                for (int nt = 0; nt < NT; ++nt) {
+                  mma_16816(acc[m][nt][0], lo[0], hi[0], lo[1], hi[1], b[nt].x, b[nt].y);
+                  mma_16816(acc[m][nt][1], lo[2], hi[2], lo[3], hi[3], b[nt].z, b[nt].w);
                 }
               }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.empty[slot]));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.empty[slot]));
+          slot += kConsumers;
+          if (slot >= a.stages) {
+            slot -= a.stages;
+            parity ^= 1;
           }
         }
-        const int ps = q % kPartSlots;
-        if (!warp_wait(sm.pempty[ps], ((q / kPartSlots) & 1) ^ 1, abort, a.status)) goto done;
-        if (any) {
-          const uint32_t dst = pbuf + (ps * kConsumers + warp) * kPartBytes + lane * 16;
+        if (!warp_wait(sm.pempty[warp][pc & 1], ((pc >> 1) & 1) ^ 1, abort, a.status)) goto done;
+        const uint32_t dst = pbuf + (2 * warp + (pc & 1)) * kPartBytes + lane * 16;
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              sts128(dst + (m * NT + nt) * 512,
-                     make_uint4(__float_as_uint(acc[m][nt][0]), __float_as_uint(acc[m][nt][1]),
-                                __float_as_uint(acc[m][nt][2]), __float_as_uint(acc[m][nt][3])));
-        }
+          for (int nt = 0; nt < NT; ++nt)
+            sts128(dst + (m * NT + nt) * 512,
+                   make_uint4(__float_as_uint(acc[m][nt][0][0] + acc[m][nt][1][0]),
+                              __float_as_uint(acc[m][nt][0][1] + acc[m][nt][1][1]),
+                              __float_as_uint(acc[m][nt][0][2] + acc[m][nt][1][2]),
+                              __float_as_uint(acc[m][nt][0][3] + acc[m][nt][1][3])));
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[ps]));
+        if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[warp][pc & 1]));
+        ++pc;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][it.item % kItems]));
       nbase += f.u1 - f.u0;
     }
-  } else if (warp == kWarpProducer) {
-    // ------------------------------------------------------------- producer
-    if (lane == 0) {
-      int nu = 0;
-      bool ok = true;
-      for (int p = 0; p < kPhases && ok; ++p) {
-        const auto f = c.phase(p);
-        const void* map = p == 0 ? &tm0 : &tm1;
-        int seg = f.seg_begin(), k = f.u0 - seg * f.U;
-        for (int u = f.u0; u < f.u1; ++u, ++nu) {
-          int v, j;
-          f.split(seg, v, j);
-          const int slot = nu % a.stages;
-          if (!mbar_wait(smem_u32(&sm.empty[slot]), ((nu / a.stages) & 1) ^ 1, abort, a.status)) {
-            ok = false;
-            break;
-          }
-          const int nbox = k * kUnitCols + kUnitCols / 2 < f.cols ? 2 : 1;  // 256-column boxes with columns
-          const uint32_t bar = smem_u32(&sm.full[slot]), dst = ring + slot * kStageBytes;
-          mbar_arrive_expect_tx(bar, 2 * nbox * kBoxBytes);
-          for (int m = 0; m < 2; ++m)
-            for (int b = 0; b < nbox; ++b)
-              tma_load_2d(dst + (2 * m + b) * kBoxBytes, map, bar, k * (kUnitCols / 2) + 128 * b,
-                          (int)c.matrix_row(p, v, j, 16 * m));
-          if (++k == f.U) {
-            k = 0;
-            ++seg;
+  } else if (warp < kWarpEpilogue) {
+    // ------------------------------------------------------------ producers
+    const int pw = warp - kWarpProducer;  // this one's units: n = pw mod 2, counted over both phases
+    int nbase = 0;
+    bool ok = true;
+    for (int p = 0; p < kPhases && ok; ++p) {
+      const Phase f = c.phase(p);
+      if (f.u0 >= f.u1) continue;
+      const void* map = p == 0 ? &tm0 : &tm1;
+      const Fp4Matrix& m = a.m[p];
+      const int ng = f.cols >> 4;
+      const int first = (pw + kProducers - nbase % kProducers) % kProducers;
+      int slot = (nbase + first) % a.stages;
+      uint32_t parity = (((nbase + first) / a.stages) & 1) ^ 1;
+      int k = (f.u0 + first) % f.U;
+      SegPos at = f.at((f.u0 + first) / f.U);
+      for (int u = f.u0 + first; u < f.u1; u += kProducers) {
+        if (!warp_wait(sm.empty[slot], parity, abort, a.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = smem_u32(&sm.full[slot]);
+        if (lane == 0) {
+          const uint32_t dst = ring + slot * kCodeBytes;
+          const int x = k * (kUnitCols / 2), r0 = (int)c.matrix_row(p, at, 0), r1 = (int)c.matrix_row(p, at, 16);
+          if (k * kUnitCols + kUnitCols / 2 < f.cols) {  // both 256-column boxes hold columns
+            mbar_arrive_expect_tx(bar, 4 * kBoxBytes);
+            tma_load_2d(dst, map, bar, x, r0);
+            tma_load_2d(dst + kBoxBytes, map, bar, x + 128, r0);
+            tma_load_2d(dst + 2 * kBoxBytes, map, bar, x, r1);
+            tma_load_2d(dst + 3 * kBoxBytes, map, bar, x + 128, r1);
+          } else {
+            mbar_arrive_expect_tx(bar, 2 * kBoxBytes);
+            tma_load_2d(dst, map, bar, x, r0);
+            tma_load_2d(dst + 2 * kBoxBytes, map, bar, x, r1);
           }
         }
+        __syncwarp();
+        {
+          const int64_t row = c.matrix_row(p, at, lane);
+          const bool in = MOE || row < m.rows;
+          const uint8_t* src = m.scales + (in ? row * ng + 32 * k : 0);
+          const int n = in ? min(32, ng - 32 * k) : 0;
+          const uint32_t dst = srow0 + slot * kScaleBytes + lane * 32;
+          if ((ng & 15) == 0)
+            copy_scale_row<16>(dst, src, n);
+          else if ((ng & 7) == 0)
+            copy_scale_row<8>(dst, src, n);
+          else if ((ng & 3) == 0)
+            copy_scale_row<4>(dst, src, n);
+          else {  // rows on odd multiples of two bytes: through registers
+            for (int o = 0; o < 32; o += 4) {
+              uint32_t w = 0u;
+              if (o < n) w = __ldg(reinterpret_cast<const uint16_t*>(src + o));
+              if (o + 2 < n) w |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src + o + 2)) << 16;
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + o), "r"(w) : "memory");
+            }
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+        }
+        slot += kProducers;
+        if (slot >= a.stages) {
+          slot -= a.stages;
+          parity ^= 1;
+        }
+        k += kProducers;
+        while (k >= f.U) {
+          k -= f.U;
+          f.step(at);
+        }
       }
-      // no copy outlives the CTA, also when the other warps have given up
-      int none = 0;
-      for (int i = nu > a.stages ? nu - a.stages : 0; i < nu; ++i)
-        mbar_wait_bounded(smem_u32(&sm.full[i % a.stages]), (i / a.stages) & 1, &none, nullptr, 100000000ull);
+      if (ok) nbase += f.u1 - f.u0;
     }
+    // no copy outlives the CTA, also when the other warps have given up: every
+    // slot's last fill has arrived, or is waited for
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    int none = 0;
+    if (*abort && lane < a.stages)
+      for (int parity = 0; parity < 2; ++parity)
+        mbar_wait_bounded(smem_u32(&sm.full[lane]), parity, &none, nullptr, 100000000ull);
   } else if (warp == kWarpEpilogue) {
     // ------------------------------------------------------------- epilogue
     const int g = lane >> 2, t = lane & 3;
-    int nbase = 0, q = 0;
+    int nbase = 0;
+    int taken = 0;  // lane w: sums taken from warp w
+    for (int v = lane; v < c.nv; v += 32)
+      for (int p = 0; p < kPhases; ++p) sm.vglobal[p][v] = __ldg(&a.m[p].global[sm.vexp[v]]);
+    __syncwarp();
     for (int p = 0; p < kPhases; ++p) {
-      const auto f = c.phase(p);
+      const Phase f = c.phase(p);
       const int64_t total = c.total_units(p);
       const bool res = c.resident(p);
       const int R = c.ring_rows(p);
+      const int tu = f.tile_units();
       ItemWalk it;
-      for (int seg = f.seg_begin(); seg * f.U < f.u1; ++seg, ++q) {
+      int seg = f.seg_begin();
+      SegPos at = f.at(seg);
+      bool fresh = true;  // first segment of a tile in this CTA
+      for (; seg * f.U < f.u1; ++seg, f.step(at)) {
         const int ua = max(f.u0, seg * f.U), ub = min(f.u1, (seg + 1) * f.U);
-        int v, j;
-        f.split(seg, v, j);
         const int last_item = it.item;
-        if (it.next(c, f, res, R, v) && last_item >= 0) {
+        if (it.next(c, f, res, R, at) && last_item >= 0) {
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][last_item % kItems]));
         }
-        const int ps = q % kPartSlots;
-        if (!warp_wait(sm.pfull[ps], (q / kPartSlots) & 1, abort, a.status)) goto done;
         float acc[2][NT][4] = {};
-        const int cnt = min(ub - ua, kConsumers);
+        const int cnt = min(ub - ua, kConsumers), w0 = (nbase + ua - f.u0) % kConsumers;
         for (int i = 0; i < cnt; ++i) {
-          const uint32_t src = pbuf +
-                               (ps * kConsumers + ((nbase + ua - f.u0 + i) & (kConsumers - 1))) * kPartBytes +
-                               lane * 16;
+          const int w = (w0 + i) % kConsumers, tk = __shfl_sync(0xFFFFFFFFu, taken, w);
+          if (!warp_wait(sm.pfull[w][tk & 1], (tk >> 1) & 1, abort, a.status)) goto done;
+          const uint32_t src = pbuf + (2 * w + (tk & 1)) * kPartBytes + lane * 16;
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -663,11 +831,12 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
               acc[m][nt][2] += __uint_as_float(x.z);
               acc[m][nt][3] += __uint_as_float(x.w);
             }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.pempty[w][tk & 1]));
+          if (lane == w) ++taken;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.pempty[ps]));
-        const int n = c.item_rows(v), s0 = sm.vstart[v];
-        const float gl = __ldg(&a.m[p].global[sm.vexp[v]]);
+        const int n = c.item_rows(at.v), s0 = sm.vstart[at.v];
+        const float gl = sm.vglobal[p][at.v];
         // lane (g, t) holds rows g and g + 8 of tokens 8 nt + 2 t and + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -675,10 +844,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
           for (int o = 0; o < 2; ++o) {
             const int col = 8 * nt + 2 * t + o;
             if (col < n) {
-              const int slot = !res ? (it.pos + col) % R
-                               : p == 1 ? s0 + col
-                               : MOE ? sm.route_id[s0 + col] / a.K : s0 + col;
-              const float rs = sm.rscale[p][slot] * gl;
+              const float rs = sm.rscale[p][c.row_slot(res, it.pos, R, s0, col)] * gl;
 #pragma unroll
               for (int m = 0; m < 2; ++m) {
                 acc[m][nt][o] *= rs;
@@ -686,40 +852,46 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
               }
             }
           }
-        const int tu = f.tile_units();
-        const int tile = p == 0 ? seg : j;
+        const int tile = p == 0 ? seg : at.j;
         const int64_t tb = (int64_t)tile * tu, te = tb + tu;  // the tile's units
         if (p == 1) {
           // out[token][row] over the tile's experts
-          if (ua == max((int64_t)f.u0, tb)) {
-            for (int i = lane; i < kFp4MaxTokens * 33; i += 32) (&sm.out[0][0])[i] = 0.f;
+          if (fresh) {
+            for (int i = lane; i < a.T * kTile2; i += 32) (&sm.out[0][0])[i] = 0.f;
+            __syncwarp();
           }
-          __syncwarp();
 #pragma unroll
           for (int o = 0; o < 2; ++o) {
             const int col = 2 * t + o;
             if (col < n) {
-              const int tok = sm.route_id[s0 + col] / a.K;
               const float w = sm.route_w[s0 + col];
+              float* row = &sm.out[sm.route_tok[s0 + col]][32 * at.rb + g];
 #pragma unroll
               for (int m = 0; m < 2; ++m) {
-                sm.out[tok][16 * m + g] = fmaf(w, acc[m][0][o], sm.out[tok][16 * m + g]);
-                sm.out[tok][16 * m + g + 8] = fmaf(w, acc[m][0][2 + o], sm.out[tok][16 * m + g + 8]);
+                row[16 * m] = fmaf(w, acc[m][0][o], row[16 * m]);
+                row[16 * m + 8] = fmaf(w, acc[m][0][2 + o], row[16 * m + 8]);
               }
             }
           }
           __syncwarp();
-          if (ub < min((int64_t)f.u1, te)) continue;  // more experts of this tile to come
+          fresh = false;
+          if (ub < min((int64_t)f.u1, te)) continue;  // more of this tile to come
+          fresh = true;
         }
         const bool whole = tb >= f.u0 && te <= f.u1;
         if (!whole) {
           // join: this CTA's share goes to its slot; whoever arrives last adds the shares in CTA order
           const int64_t G = Ctx::ctas(total);
           const int c0 = (int)(((tb + 1) * G - 1) / total), c1 = (int)((te * G - 1) / total);
-          auto slot = [&](int cta) { return a.part + ((size_t)(p * kFp4Grid + cta) * 2 + (cta == c0)) * 512; };
-          float* mine = slot(blockIdx.x);
+          constexpr int kSlot0 = 512, kSlot1 = kFp4MaxTokens * kTile2;
+          auto share = [&](int cta) {
+            return a.part[p] + (size_t)(2 * cta + (cta == c0)) * (p == 0 ? kSlot0 : kSlot1);
+          };
+          float* mine = share(blockIdx.x);
           if (p == 1) {
-            for (int tok = 0; tok < a.T; ++tok) __stcg(&mine[tok * 32 + lane], sm.out[tok][lane]);
+            for (int tok = 0; tok < a.T; ++tok)
+              __stcg(reinterpret_cast<float4*>(mine + tok * kTile2) + lane,
+                     *reinterpret_cast<const float4*>(&sm.out[tok][4 * lane]));
           } else {
 #pragma unroll
             for (int m = 0; m < 2; ++m)
@@ -739,9 +911,13 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
           if (lane == 0) *cnt_p = 0u;
           if (p == 1) {
             for (int tok = 0; tok < a.T; ++tok) {
-              float s = 0.f;
-              for (int i = c0; i <= c1; ++i) s += __ldcg(&slot(i)[tok * 32 + lane]);
-              sm.out[tok][lane] = s;
+              float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+              for (int i = c0; i <= c1; ++i) {
+                const float4 z = __ldcg(reinterpret_cast<const float4*>(share(i) + tok * kTile2) + lane);
+                s.x += z.x, s.y += z.y, s.z += z.z, s.w += z.w;
+              }
+              *reinterpret_cast<float4*>(&sm.out[tok][4 * lane]) = s;
             }
           } else {
 #pragma unroll
@@ -750,7 +926,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
               for (int nt = 0; nt < NT; ++nt) {
                 float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
                 for (int i = c0; i <= c1; ++i) {
-                  const float4 z = __ldcg(reinterpret_cast<const float4*>(slot(i)) + (m * NT + nt) * 32 + lane);
+                  const float4 z = __ldcg(reinterpret_cast<const float4*>(share(i)) + (m * NT + nt) * 32 + lane);
                   s.x += z.x, s.y += z.y, s.z += z.z, s.w += z.w;
                 }
                 acc[m][nt][0] = s.x, acc[m][nt][1] = s.y, acc[m][nt][2] = s.z, acc[m][nt][3] = s.w;
@@ -759,9 +935,12 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         }
         if (p == 1) {
           __syncwarp();
-          uint16_t* y = reinterpret_cast<uint16_t*>(a.y);
-          for (int tok = 0; tok < a.T; ++tok)
-            y[(int64_t)tok * a.m[1].rows + 32 * j + lane] = pack_bf16x2(sm.out[tok][lane], 0.f) & 0xFFFFu;
+          uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + kTile2 * at.j + 4 * lane;
+          for (int tok = 0; tok < a.T; ++tok) {
+            const float4 v = *reinterpret_cast<const float4*>(&sm.out[tok][4 * lane]);
+            *reinterpret_cast<uint2*>(y + (int64_t)tok * a.m[1].rows) =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+          }
           __syncwarp();
           continue;
         }
@@ -770,24 +949,36 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
 #pragma unroll
           for (int o = 0; o < 2; ++o) {
             const int col = 8 * nt + 2 * t + o;
-            if (col >= n) continue;
             if (MOE) {
-              float* h = a.h + (int64_t)sm.route_id[s0 + col] * (a.m[0].rows / 2) + 16 * j + g;
-              __stcg(&h[0], swiglu(acc[0][nt][o], acc[1][nt][o]));
-              __stcg(&h[8], swiglu(acc[0][nt][2 + o], acc[1][nt][2 + o]));
-            } else {
-              const int64_t at = (int64_t)(s0 + col) * a.m[0].rows;
+              // 16 values of h: half times 2^s of their largest, and s
+              const float h0 = swiglu(acc[0][nt][o], acc[1][nt][o]);
+              const float h1 = swiglu(acc[0][nt][2 + o], acc[1][nt][2 + o]);
+              float m = fmaxf(fabsf(h0), fabsf(h1));
+#pragma unroll
+              for (int x = 4; x <= 16; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+              const int s = row_exponent(m);
+              if (col < n) {
+                const int I = a.m[1].cols;
+                uint8_t* rec = a.h + (int64_t)sm.route_id[s0 + col] * record_bytes(I);
+                const uint32_t b = half2_bits(h0 * pow2f(s), h1 * pow2f(s));
+                uint16_t* hv = reinterpret_cast<uint16_t*>(rec) + 16 * at.j + g;
+                hv[0] = (uint16_t)b;
+                hv[8] = (uint16_t)(b >> 16);
+                if (g == 0) reinterpret_cast<int8_t*>(rec)[2 * I + at.j] = (int8_t)s;
+              }
+            } else if (col < n) {
+              const int64_t to = (int64_t)(s0 + col) * a.m[0].rows;
 #pragma unroll
               for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int hi = 0; hi < 2; ++hi) {
-                  const int row = 32 * j + 16 * m + 8 * hi + g;
+                  const int row = 32 * at.j + 16 * m + 8 * hi + g;
                   if (row >= a.m[0].rows) continue;
                   const float val = acc[m][nt][2 * hi + o];
                   if (a.f32)
-                    reinterpret_cast<float*>(a.y)[at + row] = val;
+                    reinterpret_cast<float*>(a.y)[to + row] = val;
                   else
-                    reinterpret_cast<uint16_t*>(a.y)[at + row] = pack_bf16x2(val, 0.f) & 0xFFFFu;
+                    reinterpret_cast<uint16_t*>(a.y)[to + row] = pack_bf16x2(val, 0.f) & 0xFFFFu;
                 }
             }
           }
@@ -796,7 +987,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][it.item % kItems]));
       }
-      if (MOE && p == 0) {  // every h value of this CTA is stored
+      if (MOE && p == 0) {  // every h value of this CTA is stored, also for bulk copies
+        fence_proxy_async_global();
         __threadfence();
         __syncwarp();
         if (lane == 0) atomicAdd(&a.ctl[0], 1u);
@@ -805,9 +997,10 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     }
   } else {
     // -------------------------------------------------------------- loaders
-    const int lw = warp - kWarpLoader, lt = threadIdx.x - 32 * kWarpLoader;
+    const int lw = warp - kWarpLoader;
+    uint32_t raw_parity = 0;
     for (int p = 0; p < kPhases; ++p) {
-      const auto f = c.phase(p);
+      const Phase f = c.phase(p);
       if (MOE && p == 1) {
         bool ok = true;
         if (lane == 0) {
@@ -824,29 +1017,28 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
               break;
             }
           }
+          fence_proxy_async_global();
         }
         if (!__shfl_sync(0xFFFFFFFFu, (int)ok, 0)) goto done;
       }
       if (f.u0 >= f.u1) continue;
-      const int RB = row_bytes(f.cols);
-      auto fill = [&](int src_row, int slot, int rank, int team) {
-        // src_row: token (first phase) or sorted route position (second)
-        if (p == 0)
-          fill_row(a.x + (int64_t)src_row * a.ldx, f.cols, brow0 + slot * RB, rank, team, sm.red,
-                   &sm.rscale[0][slot]);
-        else
-          fill_row(a.h + (int64_t)sm.route_id[src_row] * f.cols, f.cols, brow0 + slot * RB, rank, team,
-                   sm.red, &sm.rscale[1][slot]);
-      };
+      const int RB = row_bytes(f.cols, p == 1);
       if (c.resident(p)) {
-        const int n = c.resident_rows(p);
-        // (a named barrier of the four warps only where no wait that one of them
-        // could give up on comes before it)
-        if (p == 0 && n < kLoaders) {
-          for (int r = 0; r < n; ++r) fill(r, r, lt, 32 * kLoaders);
+        // all loader warps work on each row where there are few; a warp that gives
+        // up on its copy still meets the others at their barrier
+        bool ok = true;
+        if (a.T < kLoaders) {
+          for (int r = 0; r < a.T; ++r)
+            ok &= fill_x<kLoaders>(a.x + r * a.ldx, f.cols, brow0 + r * RB, lw, sm.raw[0], raw_parity,
+                                   sm.red, &sm.rscale[0][r], abort, a.status);
+          // from here every warp has a barrier of its own
+          if (lw > 0) raw_parity = 0;
         } else {
-          for (int r = lw; r < n; r += kLoaders) fill(r, r, lane, 32);
+          for (int r = lw; r < a.T && ok; r += kLoaders)
+            ok = fill_x<1>(a.x + r * a.ldx, f.cols, brow0 + r * RB, 0, sm.raw[lw], raw_parity, sm.red,
+                           &sm.rscale[0][r], abort, a.status);
         }
+        if (!ok) goto done;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.bfull[p][0]));
         // the rows' memory is the next phase's when everyone is done with them
@@ -865,10 +1057,10 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
           ++oldest;
           return true;
         };
-        for (int seg = f.seg_begin(); seg * f.U < f.u1; ++seg) {
-          int v, j;
-          f.split(seg, v, j);
-          if (!it.next(c, f, false, R, v)) continue;
+        int seg = f.seg_begin();
+        SegPos at = f.at(seg);
+        for (; seg * f.U < f.u1; ++seg, f.step(at)) {
+          if (!it.next(c, f, false, R, at)) continue;
           while (used + it.rows > R || it.item - oldest >= kItems)
             if (!retire()) goto done;
           used += it.rows;
@@ -877,8 +1069,14 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             if (i == it.item % kItems) rows_of[i] = it.rows;
           for (int r = 0; r < it.rows; ++r, ++counter)
             if (counter % kLoaders == lw) {
-              const int s = sm.vstart[v] + r;
-              fill(p == 1 ? s : MOE ? sm.route_id[s] / a.K : s, (it.pos + r) % R, lane, 32);
+              const int s = sm.vstart[at.v] + r, place = c.row_slot(false, it.pos, R, 0, r);
+              const bool ok =
+                  p == 0 ? fill_x<1>(a.x + sm.route_tok[s] * a.ldx, f.cols, brow0 + place * RB, 0,
+                                     sm.raw[lw], raw_parity, sm.red, &sm.rscale[0][place], abort, a.status)
+                         : fill_h(a.h + (int64_t)sm.route_id[s] * record_bytes(f.cols), f.cols,
+                                  brow0 + place * RB, sm.raw[lw], raw_parity, &sm.rscale[1][place], abort,
+                                  a.status);
+              if (!ok) goto done;
             }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sm.bfull[p][it.item % kItems]));
@@ -909,27 +1107,28 @@ struct Fp4Plan {
 };
 
 static int fp4_row_budget(int nt) {
-  return kMaxSmem - (int)sizeof(Fp4Shared) - 2048 - kPartSlots * kConsumers * 2 * nt * 512 -
-         8 * kStageBytes;  // at least eight stages
+  return kMaxSmem - (int)sizeof(Fp4Shared) - 2048 - 2 * kConsumers * 2 * nt * 512 -
+         kConsumers * kStageBytes;  // the least number of stages
 }
 
 static void fp4_finish_plan(Fp4Plan* p) {
   p->b_bytes = (p->b_bytes + 127) / 128 * 128;
   const int left = fp4_row_budget(p->nt) - p->b_bytes;
-  p->stages = 8 + left / kStageBytes;
-  if (p->stages > kMaxStages) p->stages = kMaxStages;
-  p->smem = 1024 + p->stages * kStageBytes + p->b_bytes + kPartSlots * kConsumers * 2 * p->nt * 512;
+  p->stages = left >= kConsumers * kStageBytes ? kMaxStages : kConsumers;
+  p->smem = 1024 + p->stages * kStageBytes + p->b_bytes + 2 * kConsumers * 2 * p->nt * 512;
 }
 
-// The layer: tokens in groups of at most 8.  Rows stay for a phase where all of
-// them fit (x: T rows, h: T * K), else they pass through a ring of the full budget.
+// The layer: tokens in groups of at most 8.
 static Fp4Plan fp4_plan_layer(int H, int I, int T, int K) {
   Fp4Plan p = {8, 1, 0, 0, 0};
-  const int budget = fp4_row_budget(1) / 128 * 128, r1 = row_bytes(H), r2 = row_bytes(I);
+  const int budget = fp4_row_budget(1) / 128 * 128, r1 = row_bytes(H, false), r2 = row_bytes(I, true);
   if (budget / r1 < p.group) p.group = budget / r1;
   if (budget / r2 < p.group) p.group = budget / r2;
-  const int64_t n1 = (int64_t)T * r1, n2 = (int64_t)T * K * r2;
-  p.b_bytes = n1 > budget || n2 > budget ? budget : (int)(n1 > n2 ? n1 : n2);
+  // x: T rows, or one group's; h: two groups' or all, as far as they fit
+  const int n1 = (int64_t)T * r1 <= budget ? T * r1 : p.group * r1;
+  int rows2 = T * K < 2 * p.group ? T * K : 2 * p.group;
+  if (rows2 > budget / r2) rows2 = budget / r2;
+  p.b_bytes = n1 > rows2 * r2 ? n1 : rows2 * r2;
   fp4_finish_plan(&p);
   return p;
 }
@@ -939,14 +1138,14 @@ static Fp4Plan fp4_plan_layer(int H, int I, int T, int K) {
 // the matrix fits there).
 static Fp4Plan fp4_plan_linear(int cols, int T) {
   Fp4Plan p = {0, 1, 0, 0, 0};
-  const int rb = row_bytes(cols);
+  const int rb = row_bytes(cols, false);
   const int fit1 = fp4_row_budget(1) / 128 * 128 / rb, fit2 = fp4_row_budget(2) / 128 * 128 / rb;
   const int most = fit2 > 8 ? (fit2 < 16 ? fit2 : 16) : (fit1 < 8 ? fit1 : 8);
   const int groups = (T + most - 1) / most;
   p.group = (T + groups - 1) / groups;
   p.nt = p.group > 8 ? 2 : 1;
   const int budget = fp4_row_budget(p.nt) / 128 * 128;
-  p.b_bytes = (int64_t)T * rb <= budget ? T * rb : budget;
+  p.b_bytes = (int64_t)T * rb <= budget ? T * rb : p.group * rb;
   fp4_finish_plan(&p);
   return p;
 }
@@ -974,8 +1173,8 @@ struct moe_fp4_handle {
   int max_tokens, grid;
   uint32_t* status;
   uint32_t* ctl;
-  float* part;
-  float* h;
+  float* part[2];
+  uint8_t* h;
 };
 
 namespace {
@@ -983,7 +1182,8 @@ namespace {
 // Workspace: a line for the status word, counters, the cut tiles' shares, h.
 constexpr size_t kFp4Align = 256;
 constexpr size_t kFp4Ctl = 2048;
-constexpr size_t kFp4Part = (size_t)kFp4Grid * 2 * 512 * 4;  // one phase
+constexpr size_t kFp4Part0 = (size_t)kFp4Grid * 2 * 512 * 4;
+constexpr size_t kFp4Part1 = (size_t)kFp4Grid * 2 * kFp4MaxTokens * kTile2 * 4;
 static_assert((2 + 2 * kFp4Grid) * 4 <= kFp4Ctl, "counters");
 
 bool fp4_dims_ok(const moe_dims* d) {
@@ -1037,8 +1237,9 @@ moe_status fp4_set_up(moe_fp4_handle* h, void* d_workspace, cudaStream_t stream)
   uint8_t* b = reinterpret_cast<uint8_t*>(((uintptr_t)d_workspace + kFp4Align - 1) & ~(kFp4Align - 1));
   h->status = reinterpret_cast<uint32_t*>(b);
   h->ctl = reinterpret_cast<uint32_t*>(b + kFp4Align);
-  h->part = reinterpret_cast<float*>(b + kFp4Align + kFp4Ctl);
-  h->h = reinterpret_cast<float*>(b + kFp4Align + kFp4Ctl + 2 * kFp4Part);
+  h->part[0] = reinterpret_cast<float*>(b + kFp4Align + kFp4Ctl);
+  h->part[1] = reinterpret_cast<float*>(b + kFp4Align + kFp4Ctl + kFp4Part0);  // the layer
+  h->h = b + kFp4Align + kFp4Ctl + kFp4Part0 + kFp4Part1;
   return cudaMemsetAsync(b, 0, kFp4Align + kFp4Ctl, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -1049,8 +1250,8 @@ extern "C" {
 moe_status moe_fp4_workspace_query(const moe_dims* dims, int64_t max_tokens, size_t* workspace_bytes) {
   if (!dims || !workspace_bytes || max_tokens < 1) return MOE_ERR_INVALID_ARG;
   if (!fp4_dims_ok(dims) || max_tokens > kFp4MaxTokens) return MOE_ERR_UNSUPPORTED;
-  *workspace_bytes = 2 * kFp4Align + kFp4Ctl + 2 * kFp4Part +
-                     (size_t)max_tokens * dims->top_k * dims->inter * 4;
+  *workspace_bytes = 2 * kFp4Align + kFp4Ctl + kFp4Part0 + kFp4Part1 +
+                     (size_t)max_tokens * dims->top_k * record_bytes(dims->inter);
   return MOE_OK;
 }
 
@@ -1113,7 +1314,8 @@ moe_status moe_fp4_forward(moe_fp4_handle* h, const uint16_t* d_x, const int32_t
   a.y = d_out;
   a.status = h->status;
   a.ctl = h->ctl;
-  a.part = h->part;
+  a.part[0] = h->part[0];
+  a.part[1] = h->part[1];
   a.T = (int)num_tokens;
   a.E = d.num_experts;
   a.K = d.top_k;
@@ -1131,7 +1333,7 @@ moe_status moe_fp4_linear_workspace_query(int32_t rows, int32_t cols, int64_t ma
   if (!workspace_bytes || max_tokens < 1 || rows < 1 || cols < 1) return MOE_ERR_INVALID_ARG;
   if (cols % 32 || cols > 32768 || rows > (1 << 24) || max_tokens > kFp4MaxTokens)
     return MOE_ERR_UNSUPPORTED;
-  *workspace_bytes = 2 * kFp4Align + kFp4Ctl + 2 * kFp4Part;
+  *workspace_bytes = 2 * kFp4Align + kFp4Ctl + kFp4Part0;
   return MOE_OK;
 }
 
@@ -1180,7 +1382,8 @@ moe_status moe_fp4_linear(moe_fp4_handle* h, const uint16_t* d_x, int64_t x_stri
   a.y = d_y;
   a.status = h->status;
   a.ctl = h->ctl;
-  a.part = h->part;
+  a.part[0] = h->part[0];
+  a.part[1] = h->part[1];
   a.T = (int)num_tokens;
   a.E = 1;
   a.K = 1;
