@@ -37,6 +37,7 @@
 
 #include <cstring>
 #include <new>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -48,22 +49,26 @@ namespace mm {
 constexpr int kFp4MaxTokens = 16;
 constexpr int kFp4MaxRoutes = 128;
 constexpr int kFp4Grid = 152;        // one CTA per SM
-constexpr int kConsumers = 8;        // the first warps: dequantise and multiply
-constexpr int kProducers = 2;        // then two that issue the copies of the weights, in turn
-constexpr int kWarpProducer = kConsumers;
-constexpr int kWarpEpilogue = kWarpProducer + kProducers;  // adds the warps' sums, finishes and joins tiles
-constexpr int kWarpLoader = kWarpEpilogue + 1;             // x and h rows to half in shared memory
-constexpr int kLoaders = 4;
-constexpr int kFp4Threads = 32 * (kWarpLoader + kLoaders);
+// The warps' roles.  The service warps come first: where several warps of a
+// scheduler are ready it serves the older ones, and the consumers, with
+// instructions ready nearly always, would starve what they wait for.
+constexpr int kProducers = 3;        // issue the copies of the weights, in turn
+constexpr int kLoaders = 4;          // x and h rows to half in shared memory
+constexpr int kConsumers = 8;        // dequantise and multiply
+constexpr int kWarpEpilogue = 0;     // adds the consumers' sums, finishes and joins tiles
+constexpr int kWarpProducer = 1;
+constexpr int kWarpLoader = kWarpProducer + kProducers;
+constexpr int kWarpConsumer = kWarpLoader + kLoaders;
+constexpr int kFp4Threads = 32 * (kWarpConsumer + kConsumers);
+// Units in flight: at least what covers the latency of HBM at the copy rate; a
+// multiple of kProducers, so that each place is one producer's (another one could
+// wait for a phase two laps ahead, whose parity is that of the lap before)
+constexpr int kMinStages = 12, kMaxStages = 18;
 constexpr int kUnitCols = 512;
 constexpr int kCodeBytes = 32 * kUnitCols / 2;
 constexpr int kScaleBytes = 32 * kUnitCols / 16;
-constexpr int kStageBytes = kCodeBytes + kScaleBytes;
+constexpr int kUnitBytes = kCodeBytes + kScaleBytes;
 constexpr int kBoxBytes = 16 * 128;  // 16 rows x 256 columns
-// A multiple of kConsumers: then a slot's units are all one warp's, so no warp
-// waits for a phase while an earlier phase of the slot is open (it would take
-// the parity of the phase before that one for its own).
-constexpr int kMaxStages = 2 * kConsumers;
 constexpr int kItems = 8;            // operand items in flight (rows ring)
 constexpr int kCutUnits = 15;        // units of imbalance that a tile's join costs (about 3 us)
 constexpr int kTile2 = 128;          // output rows of an FC2 tile
@@ -87,7 +92,8 @@ struct Fp4Args {
   uint32_t* ctl;        // [0] barrier, [1] finished CTAs, [2 + 152 p + c] joins of phase p
   float* part[2];       // by phase, [152][2][..]: a CTA's cut tiles, first and last
   int T, E, K, group;   // group: tokens of one operand item, at most 8 NT
-  int stages, b_bytes;
+  int b_bytes, stages;
+  uint32_t stage_rcp;   // floor(2^32 / stages) + 1
   bool check, f32;
 };
 
@@ -101,11 +107,18 @@ __host__ __device__ inline int row_bytes(int cols, bool h) {
   return ((padded_units(cols) * kUnitCols * 2 + (h ? exponent_bytes(cols) : 0) + 127) & ~127) + 64;
 }
 
+// Codes as TMA tensors.  unit: 128-byte (256-column) blocks of the rows, a box is
+// a unit's 32 rows x 2 blocks, block-major ({128 B, row, block}; FC1: {128 B, row
+// of the half, gate or up, block, expert}).  box: the rows as they are, a box is
+// 16 rows x 128 B.  128-byte swizzle; what lies past an extent reads as zero.
+struct Fp4Maps {
+  CUtensorMap unit[2], box[2];
+};
+
 struct Fp4Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t pfull[kConsumers][2], pempty[kConsumers][2];
   uint64_t bfull[2][kItems], bempty[2][kItems];
-  uint64_t raw[kLoaders];
+  uint64_t raw[kLoaders], go;
   alignas(16) float out[kFp4MaxTokens][kTile2];
   alignas(16) int key[kFp4MaxRoutes];
   float rscale[2][kFp4MaxRoutes];       // per operand row: 2^-s
@@ -117,6 +130,8 @@ struct Fp4Shared {
   uint8_t first[kFp4MaxRoutes];
   float red[kLoaders];
   int warp_cnt[4];
+  int issued[kProducers];               // units each producer has begun
+  int done[kConsumers], taken[kConsumers];  // sums each consumer has left, and that were taken
   int nv, nroutes;
   int abort;
 };
@@ -286,25 +301,105 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
                : "memory");
 }
 
+// TMA loads and copies with an L2 policy: the weights pass once, and what else the
+// kernel reads (instructions, x, h, tables) should stay.
+__device__ __forceinline__ uint64_t policy_evict_first() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+__device__ __forceinline__ void load_box_2d(uint32_t dst, const void* map, uint32_t bar, int c0, int c1,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"((uint64_t)map), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void load_box_3d(uint32_t dst, const void* map, uint32_t bar, int c0, int c1,
+                                            int c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"((uint64_t)map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void load_box_5d(uint32_t dst, const void* map, uint32_t bar, int c0, int c1,
+                                            int c2, int c3, int c4, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(dst),
+      "l"((uint64_t)map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "l"(policy)
+      : "memory");
+}
+
 // Asynchronous copy of N bytes, of which the first `valid` are read and the rest zero.
 template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int valid) {
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int valid, uint64_t policy) {
   if (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+                 "r"(valid), "l"(policy)
+                 : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(valid), "n"(N)
+    asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %4, %2, %3;" ::"r"(dst), "l"(src),
+                 "r"(valid), "l"(policy), "n"(N)
                  : "memory");
 }
 
 // The 32 scale bytes of one row of a unit (n of them in the matrix, the rest
 // zero) to shared memory, in copies as wide as the rows' alignment allows.
 template <int N>
-__device__ __forceinline__ void copy_scale_row(uint32_t dst, const uint8_t* src, int n) {
+__device__ __forceinline__ void copy_scale_row(uint32_t dst, const uint8_t* src, int n, uint64_t policy) {
 #pragma unroll
   for (int o = 0; o < 32; o += N) {
     const int v = min(max(n - o, 0), N);
-    cp_async<N>(dst + o, v > 0 ? src + o : src, v);
+    cp_async<N>(dst + o, v > 0 ? src + o : src, v, policy);
   }
+}
+
+// Counts in shared memory that one warp raises and others wait for: cheaper than
+// an mbarrier where lanes wait on different ones.
+__device__ __forceinline__ int load_count(const int* count) {
+  int v;
+  asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(count)) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void store_count(int* count, int v) {
+  asm volatile("st.release.cta.shared.s32 [%0], %1;" ::"r"(smem_u32(count)), "r"(v) : "memory");
+}
+
+__device__ __noinline__ bool wait_count_slow(const int* count, int n, volatile int* abort, uint32_t* status) {
+  const uint64_t t0 = globaltimer_ns();
+  bool ok;
+  while (!(ok = __all_sync(0xFFFFFFFFu, load_count(count) >= n))) {
+    if (__any_sync(0xFFFFFFFFu, *abort != 0)) break;
+    if (__any_sync(0xFFFFFFFFu, globaltimer_ns() - t0 > kWaitLimitNs)) {
+      *abort = 1;
+      record_status(status, MOE_DEV_TIMEOUT);
+      break;
+    }
+  }
+  __syncwarp();
+  return ok;
+}
+
+// Bounded wait of a whole warp until every lane's count has reached its n.
+__device__ __forceinline__ bool wait_count(const int* count, int n, volatile int* abort, uint32_t* status) {
+  if (__all_sync(0xFFFFFFFFu, load_count(count) >= n)) {
+    __syncwarp();
+    return true;
+  }
+  return wait_count_slow(count, n, abort, status);
 }
 
 // Bounded wait of a whole warp: all of its lanes go on, or none.
@@ -348,12 +443,14 @@ __device__ __forceinline__ void raw_begin(uint64_t& bar, uint32_t bytes) {
 template <int TEAM>
 __device__ __forceinline__ bool fill_x(const uint16_t* src, int cols, uint32_t dst, int rank,
                                        uint64_t& bar, uint32_t& parity, float* red, float* rscale,
-                                       volatile int* abort, uint32_t* status) {
+                                       volatile int* abort, uint32_t* status, bool asked,
+                                       uint64_t* go = nullptr) {
   const int lane = threadIdx.x & 31, n = cols >> 3, U = padded_units(cols);
-  if (rank == 0 && lane == 0) {
+  if (rank == 0 && lane == 0 && !asked) {
     raw_begin(bar, cols * 2);
     bulk_load(dst, src, cols * 2, smem_u32(&bar));
   }
+  if (go && lane == 0) mbar_arrive(smem_u32(go));
   const bool ok = warp_wait(bar, parity, abort, status);  // a team goes on to its barriers either way
   parity ^= 1;
   uint32_t m = 0u;  // the largest |value|, as BF16 bits
@@ -379,6 +476,7 @@ __device__ __forceinline__ bool fill_x(const uint16_t* src, int cols, uint32_t d
   const int s = row_exponent(__uint_as_float(m << 16));
   const float up = pow2f(s);
   if (rank == 0 && lane == 0) *rscale = pow2f(-s);
+#pragma unroll 2
   for (int u = rank; u < U; u += TEAM) {
     const uint32_t base = dst + u * (kUnitCols * 2);
     uint4 o[2];
@@ -549,17 +647,16 @@ __device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm) {
 
 template <bool MOE, int NT>
 __global__ void __launch_bounds__(kFp4Threads, 1)
-    fp4_stream_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
-                      const Fp4Args a) {
+    fp4_stream_kernel(const __grid_constant__ Fp4Maps maps, const Fp4Args a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Fp4Shared sm;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint8_t* const smem = smem_raw + (ring - smem_u32(smem_raw));  // the same, for plain loads
-  const uint32_t srow0 = ring + a.stages * kCodeBytes;   // the stages' scales
-  const uint32_t brow0 = srow0 + a.stages * kScaleBytes; // operand rows
-  const uint32_t pbuf = brow0 + a.b_bytes;               // the consumers' sums
+  const uint32_t srow0 = ring + a.stages * kCodeBytes;    // the units' scales
+  const uint32_t brow0 = srow0 + a.stages * kScaleBytes;  // operand rows
+  const uint32_t pbuf = brow0 + a.b_bytes;                  // the consumers' sums
   constexpr int kPartBytes = 2 * NT * 512;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp_id = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   {
     const int i = threadIdx.x;
@@ -567,20 +664,35 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       // copies: one arrival with the codes' bytes, one per lane with its scales
       mbar_init(smem_u32(&sm.full[i]), 33);
       mbar_init(smem_u32(&sm.empty[i]), 1);
-    } else if (i >= 32 && i < 32 + 2 * kConsumers) {
-      mbar_init(smem_u32(&sm.pfull[0][0] + (i - 32)), 1);
-      mbar_init(smem_u32(&sm.pempty[0][0] + (i - 32)), 1);
+    } else if (i >= 32 && i < 32 + kConsumers) {
+      sm.done[i - 32] = sm.taken[i - 32] = 0;
     } else if (i >= 64 && i < 64 + 2 * kItems) {
       mbar_init(smem_u32(&sm.bfull[0][0] + (i - 64)), kLoaders);
       mbar_init(smem_u32(&sm.bempty[0][0] + (i - 64)), kConsumers + 1);
-    } else if (i >= 96 && i < 96 + kLoaders) {
-      mbar_init(smem_u32(&sm.raw[i - 96]), 1);
     } else if (i == 128) {
+      mbar_init(smem_u32(&sm.go), kLoaders);
       sm.abort = 0;
-      prefetch_tensormap(&tm0);
-      if (MOE) prefetch_tensormap(&tm1);
+      for (int k = 0; k < kProducers; ++k) sm.issued[k] = 0;
+      for (int p = 0; p < (MOE ? 2 : 1); ++p) {
+        prefetch_tensormap(&maps.unit[p]);
+        prefetch_tensormap(&maps.box[p]);
+      }
     }
     fence_mbar_init();
+  }
+  // x rows that stay are asked for before anything else: behind the first weights
+  // they would wait for a full ring's copies
+  const bool early = (int64_t)a.T * row_bytes(a.m[0].cols, false) <= a.b_bytes;
+  const bool loader = warp_id >= kWarpLoader && warp_id < kWarpConsumer;
+  if (loader && lane == 0) {
+    const int r = warp_id - kWarpLoader;
+    uint64_t& bar = sm.raw[r];
+    mbar_init(smem_u32(&bar), 1);
+    fence_mbar_init();
+    if (early && r < (a.T < kLoaders ? 1 : a.T)) {
+      raw_begin(bar, a.m[0].cols * 2);
+      bulk_load(brow0 + r * row_bytes(a.m[0].cols, false), a.x + r * a.ldx, a.m[0].cols * 2, smem_u32(&bar));
+    }
   }
   build_items<MOE>(a, sm);
   __syncthreads();
@@ -596,204 +708,242 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
          i += (int64_t)gridDim.x * blockDim.x)
       o[i] = make_uint4(0u, 0u, 0u, 0u);
+    // no copy outlives the CTA
+    if (early && loader && warp_id - kWarpLoader < (a.T < kLoaders ? 1 : a.T))
+      mbar_wait(smem_u32(&sm.raw[warp_id - kWarpLoader]), 0, abort, a.status);
     return;
   }
 
-  if (warp < kConsumers) {
+  if (warp_id >= kWarpConsumer) {
     // ------------------------------------------------------------ consumers
-    const int g = lane >> 2, t = lane & 3;
-    int nbase = 0;  // units of the CTA before this phase
+    const int warp = warp_id - kWarpConsumer, g = lane >> 2, t = lane & 3;
     int pc = 0;     // sums this warp has handed over
-    for (int p = 0; p < kPhases; ++p) {
+    int n0 = 0;     // the CTA's units before this segment: its n-th unit is warp n mod 8's
+    auto consume = [&](auto phase_constant) {
+      constexpr int p = decltype(phase_constant)::value;
       const Phase f = c.phase(p);
-      if (f.u0 >= f.u1) continue;
+      if (f.u0 >= f.u1) return true;
       const int RB = row_bytes(f.cols, p == 1);
-      const bool res = c.resident(p);
+      const bool res = p == 0 && c.resident(0);
       const int R = c.ring_rows(p);
-      // this warp's units: every eighth, counted over both phases
-      const int n0 = (warp + kConsumers - nbase % kConsumers) % kConsumers;
-      int u = f.u0 + n0;
-      int slot = (nbase + n0) % a.stages;
-      uint32_t parity = ((nbase + n0) / a.stages) & 1;
       ItemWalk it;
-      int seg = f.seg_begin();
+      int seg = f.seg_begin(), ka = f.u0 - seg * f.U;
+      const int segs = (f.u1 - 1) / f.U + 1, k_last = f.u1 - (segs - 1) * f.U;
       SegPos at = f.at(seg);
-      for (; seg * f.U < f.u1; ++seg, f.step(at)) {
-        const int ub = min(f.u1, (seg + 1) * f.U);
+      for (; seg < segs; ++seg, f.step(at)) {
+        const int kb = seg == segs - 1 ? k_last : f.U;
         const int last_item = it.item;
         if (it.next(c, f, res, R, at)) {
           if (last_item >= 0) {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][last_item % kItems]));
           }
-          if (!warp_wait(sm.bfull[p][it.item % kItems], (it.item / kItems) & 1, abort, a.status))
-            goto done;
+          if (!warp_wait(sm.bfull[p][it.item % kItems], (it.item / kItems) & 1, abort, a.status)) return false;
         }
-        if (u >= ub) continue;
-        // two sums per tile, so that consecutive MMAs do not wait for each other
-        float acc[2][NT][2][4] = {};
-        const int n = c.item_rows(at.v), s0 = sm.vstart[at.v];
-        const uint8_t* brow[NT];
+        const int first = ka + ((warp - n0) & (kConsumers - 1));  // this warp's first unit of the segment
+        if (first < kb) {
+          // two sums per tile, so that consecutive MMAs do not wait for each other
+          float acc[2][NT][2][4] = {};
+          const int n = c.item_rows(at.v), s0 = sm.vstart[at.v];
+          const uint8_t* brow[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int col = min(8 * nt + g, n - 1);  // columns past n repeat a row; nothing reads them
-          brow[nt] = smem + (brow0 - ring) + c.row_slot(res, it.pos, R, s0, col) * RB + t * 16;
-        }
-        for (; u < ub; u += kConsumers) {
-          const int boff = (u - seg * f.U) * (kUnitCols * 2);
-          if (!warp_wait(sm.full[slot], parity, abort, a.status)) goto done;
-          const uint8_t* base = smem + slot * kCodeBytes + (t >> 1) * kBoxBytes + g * 128;
-          const uint8_t* sbase = smem + (srow0 - ring) + slot * kScaleBytes + g * 32 + 8 * t;
-          uint2 s[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {  // rows g, g + 8, g + 16, g + 24
-            const uint2 v = *reinterpret_cast<const uint2*>(sbase + i * 256);
-            s[i] = t < 2 ? v : make_uint2(v.y, v.x);  // chunk order of lanes t >= 2
+          for (int nt = 0; nt < NT; ++nt) {
+            const int col = min(8 * nt + g, n - 1);  // columns past n repeat a row; nothing reads them
+            brow[nt] = smem + (brow0 - ring) + c.row_slot(res, it.pos, R, s0, col) * RB + t * 16;
           }
+#pragma unroll 1
+          for (int k = first; k < kb; k += kConsumers) {
+            const int nu = n0 + k - ka;  // the unit's count, which gives its place in the ring
+            const int lap = (int)__umulhi((uint32_t)nu, a.stage_rcp), slot = nu - lap * a.stages;
+            // Only once the unit's copies have begun is the place in this lap's
+            // phase, and the parity that of this lap
+            if (!wait_count(&sm.issued[nu % kProducers], nu / kProducers + 1, abort, a.status)) return false;
+            if (!warp_wait(sm.full[slot], lap & 1, abort, a.status)) return false;
+            const uint8_t* base = smem + slot * kCodeBytes + (t >> 1) * (2 * kBoxBytes) + g * 128;
+            const uint8_t* sbase = smem + (srow0 - ring) + slot * kScaleBytes + g * 32 + 8 * t;
+            uint2 s[4];
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj) {
-            const int chunk = (((t & 1) * 4 + (jj ^ ((t >> 1) << 1))) ^ g) << 4;
-            uint32_t cw[2][2][4], sw[2][2];
+            for (int i = 0; i < 4; ++i) {  // rows g, g + 8, g + 16, g + 24
+              const uint2 v = *reinterpret_cast<const uint2*>(sbase + i * 256);
+              s[i] = t < 2 ? v : make_uint2(v.y, v.x);  // chunk order of lanes t >= 2
+            }
+            // two of the four steps at a time: their codes to registers, and with the
+            // second two the unit's place is free for the next copies
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int half = 0; half < 2; ++half) {
+              uint4 cw[2][2][2];  // [step][16-row half of the tile][rows g, g + 8]
 #pragma unroll
-              for (int hi = 0; hi < 2; ++hi) {
-                const uint4 x = *reinterpret_cast<const uint4*>(base + m * (2 * kBoxBytes) + hi * 1024 + chunk);
-                cw[m][hi][0] = x.x, cw[m][hi][1] = x.y, cw[m][hi][2] = x.z, cw[m][hi][3] = x.w;
-                const uint32_t word = jj < 2 ? s[2 * m + hi].x : s[2 * m + hi].y;
-                sw[m][hi] = e4m3x2_half2((jj & 1) ? word >> 16 : word & 0xFFFFu);
+              for (int jj = 0; jj < 2; ++jj) {
+                const int chunk = (((t & 1) * 4 + ((2 * half + jj) ^ ((t >> 1) << 1))) ^ g) << 4;
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                  for (int hi = 0; hi < 2; ++hi)
+                    cw[jj][m][hi] = *reinterpret_cast<const uint4*>(base + m * kBoxBytes + hi * 1024 + chunk);
+              }
+              if (half == 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.empty[slot]));
               }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 b[NT];
+              for (int jj = 0; jj < 2; ++jj) {
+                uint32_t sw[2][2];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                b[nt] = *reinterpret_cast<const uint4*>(brow[nt] + boff + ((jj * 4 + i) << 6));
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                uint32_t lo[4], hi[4];
-                const uint32_t sel = i < 2 ? 0x1010u : 0x3232u;
-                e2m1x8_scaled(cw[m][0][i], __byte_perm(sw[m][0], 0u, sel), lo);
-                e2m1x8_scaled(cw[m][1][i], __byte_perm(sw[m][1], 0u, sel), hi);
+                  for (int hi = 0; hi < 2; ++hi) {
+                    const uint32_t word = half == 0 ? s[2 * m + hi].x : s[2 * m + hi].y;
+                    sw[m][hi] = e4m3x2_half2(jj ? word >> 16 : word & 0xFFFFu);
+                  }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  mma_16816(acc[m][nt][0], lo[0], hi[0], lo[1], hi[1], b[nt].x, b[nt].y);
-                  mma_16816(acc[m][nt][1], lo[2], hi[2], lo[3], hi[3], b[nt].z, b[nt].w);
+                for (int i = 0; i < 4; ++i) {
+                  uint4 b[NT];
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+                    b[nt] = *reinterpret_cast<const uint4*>(brow[nt] + k * (kUnitCols * 2) +
+                                                            (((2 * half + jj) * 4 + i) << 6));
+#pragma unroll
+                  for (int m = 0; m < 2; ++m) {
+                    uint32_t lo[4], hi[4];
+                    const uint32_t sel = i < 2 ? 0x1010u : 0x3232u;
+                    const uint4 wl = cw[jj][m][0], wh = cw[jj][m][1];
+                    e2m1x8_scaled(i == 0 ? wl.x : i == 1 ? wl.y : i == 2 ? wl.z : wl.w,
+                                  __byte_perm(sw[m][0], 0u, sel), lo);
+                    e2m1x8_scaled(i == 0 ? wh.x : i == 1 ? wh.y : i == 2 ? wh.z : wh.w,
+                                  __byte_perm(sw[m][1], 0u, sel), hi);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                      mma_16816(acc[m][nt][0], lo[0], hi[0], lo[1], hi[1], b[nt].x, b[nt].y);
+                      mma_16816(acc[m][nt][1], lo[2], hi[2], lo[3], hi[3], b[nt].z, b[nt].w);
+                    }
+                  }
                 }
               }
             }
           }
+          if (!wait_count(&sm.taken[warp], pc - 1, abort, a.status)) return false;
+          const uint32_t dst = pbuf + (2 * warp + (pc & 1)) * kPartBytes + lane * 16;
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              sts128(dst + (m * NT + nt) * 512,
+                     make_uint4(__float_as_uint(acc[m][nt][0][0] + acc[m][nt][1][0]),
+                                __float_as_uint(acc[m][nt][0][1] + acc[m][nt][1][1]),
+                                __float_as_uint(acc[m][nt][0][2] + acc[m][nt][1][2]),
+                                __float_as_uint(acc[m][nt][0][3] + acc[m][nt][1][3])));
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.empty[slot]));
-          slot += kConsumers;
+          ++pc;
+          if (lane == 0) store_count(&sm.done[warp], pc);
+        }
+        n0 += kb - ka;
+        ka = 0;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][it.item % kItems]));
+      return true;
+    };
+    if (consume(std::integral_constant<int, 0>{})) {
+      if constexpr (MOE) consume(std::integral_constant<int, 1>{});
+    }
+  } else if (warp_id >= kWarpProducer && warp_id < kWarpLoader) {
+    // ------------------------------------------------------------ producers
+    const uint64_t pass = policy_evict_first(), keep = policy_evict_normal();
+    const int pw = warp_id - kWarpProducer;  // this one's units: every third, counted over both phases
+    int n0 = 0;                           // the CTA's count of the segment's first unit
+    int slot = pw, mine = 0;
+    uint32_t parity = 1;
+    // the first operand rows go ahead of the weights
+    bool ok = warp_wait(sm.go, 0, abort, a.status);
+    for (int p = 0; p < kPhases && ok; ++p) {
+      const Phase f = c.phase(p);
+      if (f.u0 >= f.u1) continue;
+      const Fp4Matrix& m = a.m[p];
+      const int cols = f.cols, ng = cols >> 4, blocks = (cols + 255) >> 8;
+      // units that are one copy: all but one that ends within a 256-column block,
+      // past which lies the next row
+      const int one_copy = (cols & 255) == 0 ? f.U : (blocks - 1) >> 1;
+      const int full_scales = (ng & 15) == 0 ? ng >> 5 : 0;  // units with 32 scales in 16-byte copies
+      int seg = f.seg_begin(), ka = f.u0 - seg * f.U;
+      SegPos at = f.at(seg);
+      for (; seg * f.U < f.u1 && ok; ++seg, f.step(at)) {
+        const int kb = min(f.U, f.u1 - seg * f.U);
+        int k = ka + (pw + kProducers - n0 % kProducers) % kProducers;
+        n0 += kb - ka;
+        ka = 0;
+        if (k >= kb) continue;
+        const int64_t row = c.matrix_row(p, at, lane);
+        const bool in = MOE || row < m.rows;
+        const uint8_t* srow = m.scales + (in ? row * ng : 0);
+        const int r0 = __shfl_sync(0xFFFFFFFFu, (int)row, 0), r1 = __shfl_sync(0xFFFFFFFFu, (int)row, 16);
+        const int expert = sm.vexp[at.v];
+        // read again by the next item: the same matrix, more tokens
+        const uint64_t policy = at.v + 1 < c.nv && sm.vexp[at.v + 1] == expert ? keep : pass;
+        for (; k < kb; k += kProducers) {
+          if (!warp_wait(sm.empty[slot], parity, abort, a.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = smem_u32(&sm.full[slot]), dst = ring + slot * kCodeBytes;
+          if (lane == 0) {
+            store_count(&sm.issued[pw], ++mine);
+            if (k < one_copy) {
+              mbar_arrive_expect_tx(bar, kCodeBytes);
+              if (MOE && p == 0)
+                load_box_5d(dst, &maps.unit[0], bar, 0, 16 * at.j, 0, 2 * k, expert, policy);
+              else
+                load_box_3d(dst, &maps.unit[p], bar, 0, r0, 2 * k, policy);
+            } else {  // a copy per 16 rows x 256 columns, cut off at the row's end
+              mbar_arrive_expect_tx(bar, (blocks - 2 * k) * 2 * kBoxBytes);
+              for (int b = 0; b < blocks - 2 * k; ++b) {
+                load_box_2d(dst + 2 * b * kBoxBytes, &maps.box[p], bar, 128 * (2 * k + b), r0, policy);
+                load_box_2d(dst + (2 * b + 1) * kBoxBytes, &maps.box[p], bar, 128 * (2 * k + b), r1, policy);
+              }
+            }
+          }
+          __syncwarp();
+          {  // lane: the scales of its row
+            const uint8_t* src = srow + (in ? 32 * k : 0);
+            const int n = in ? min(32, ng - 32 * k) : 0;
+            const uint32_t to = srow0 + slot * kScaleBytes + lane * 32;
+            if (k < full_scales) {
+              cp_async<16>(to, src, in ? 16 : 0, policy);
+              cp_async<16>(to + 16, in ? src + 16 : src, in ? 16 : 0, policy);
+            } else if ((ng & 15) == 0)
+              copy_scale_row<16>(to, src, n, policy);
+            else if ((ng & 7) == 0)
+              copy_scale_row<8>(to, src, n, policy);
+            else if ((ng & 3) == 0)
+              copy_scale_row<4>(to, src, n, policy);
+            else {  // rows on odd multiples of two bytes: through registers
+              for (int o = 0; o < 32; o += 4) {
+                uint32_t x = 0u;
+                if (o < n) x = __ldg(reinterpret_cast<const uint16_t*>(src + o));
+                if (o + 2 < n) x |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src + o + 2)) << 16;
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + o), "r"(x) : "memory");
+              }
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+          }
+          slot += kProducers;
           if (slot >= a.stages) {
             slot -= a.stages;
             parity ^= 1;
           }
         }
-        if (!warp_wait(sm.pempty[warp][pc & 1], ((pc >> 1) & 1) ^ 1, abort, a.status)) goto done;
-        const uint32_t dst = pbuf + (2 * warp + (pc & 1)) * kPartBytes + lane * 16;
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            sts128(dst + (m * NT + nt) * 512,
-                   make_uint4(__float_as_uint(acc[m][nt][0][0] + acc[m][nt][1][0]),
-                              __float_as_uint(acc[m][nt][0][1] + acc[m][nt][1][1]),
-                              __float_as_uint(acc[m][nt][0][2] + acc[m][nt][1][2]),
-                              __float_as_uint(acc[m][nt][0][3] + acc[m][nt][1][3])));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.pfull[warp][pc & 1]));
-        ++pc;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][it.item % kItems]));
-      nbase += f.u1 - f.u0;
     }
-  } else if (warp < kWarpEpilogue) {
-    // ------------------------------------------------------------ producers
-    const int pw = warp - kWarpProducer;  // this one's units: n = pw mod 2, counted over both phases
-    int nbase = 0;
-    bool ok = true;
-    for (int p = 0; p < kPhases && ok; ++p) {
-      const Phase f = c.phase(p);
-      if (f.u0 >= f.u1) continue;
-      const void* map = p == 0 ? &tm0 : &tm1;
-      const Fp4Matrix& m = a.m[p];
-      const int ng = f.cols >> 4;
-      const int first = (pw + kProducers - nbase % kProducers) % kProducers;
-      int slot = (nbase + first) % a.stages;
-      uint32_t parity = (((nbase + first) / a.stages) & 1) ^ 1;
-      int k = (f.u0 + first) % f.U;
-      SegPos at = f.at((f.u0 + first) / f.U);
-      for (int u = f.u0 + first; u < f.u1; u += kProducers) {
-        if (!warp_wait(sm.empty[slot], parity, abort, a.status)) {
-          ok = false;
-          break;
-        }
-        const uint32_t bar = smem_u32(&sm.full[slot]);
-        if (lane == 0) {
-          const uint32_t dst = ring + slot * kCodeBytes;
-          const int x = k * (kUnitCols / 2), r0 = (int)c.matrix_row(p, at, 0), r1 = (int)c.matrix_row(p, at, 16);
-          if (k * kUnitCols + kUnitCols / 2 < f.cols) {  // both 256-column boxes hold columns
-            mbar_arrive_expect_tx(bar, 4 * kBoxBytes);
-            tma_load_2d(dst, map, bar, x, r0);
-            tma_load_2d(dst + kBoxBytes, map, bar, x + 128, r0);
-            tma_load_2d(dst + 2 * kBoxBytes, map, bar, x, r1);
-            tma_load_2d(dst + 3 * kBoxBytes, map, bar, x + 128, r1);
-          } else {
-            mbar_arrive_expect_tx(bar, 2 * kBoxBytes);
-            tma_load_2d(dst, map, bar, x, r0);
-            tma_load_2d(dst + 2 * kBoxBytes, map, bar, x, r1);
-          }
-        }
-        __syncwarp();
-        {
-          const int64_t row = c.matrix_row(p, at, lane);
-          const bool in = MOE || row < m.rows;
-          const uint8_t* src = m.scales + (in ? row * ng + 32 * k : 0);
-          const int n = in ? min(32, ng - 32 * k) : 0;
-          const uint32_t dst = srow0 + slot * kScaleBytes + lane * 32;
-          if ((ng & 15) == 0)
-            copy_scale_row<16>(dst, src, n);
-          else if ((ng & 7) == 0)
-            copy_scale_row<8>(dst, src, n);
-          else if ((ng & 3) == 0)
-            copy_scale_row<4>(dst, src, n);
-          else {  // rows on odd multiples of two bytes: through registers
-            for (int o = 0; o < 32; o += 4) {
-              uint32_t w = 0u;
-              if (o < n) w = __ldg(reinterpret_cast<const uint16_t*>(src + o));
-              if (o + 2 < n) w |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src + o + 2)) << 16;
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + o), "r"(w) : "memory");
-            }
-          }
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-        }
-        slot += kProducers;
-        if (slot >= a.stages) {
-          slot -= a.stages;
-          parity ^= 1;
-        }
-        k += kProducers;
-        while (k >= f.U) {
-          k -= f.U;
-          f.step(at);
-        }
-      }
-      if (ok) nbase += f.u1 - f.u0;
-    }
-    // no copy outlives the CTA, also when the other warps have given up: every
-    // slot's last fill has arrived, or is waited for
+    // no copy outlives the CTA, also when the other warps have given up
     asm volatile("cp.async.wait_all;" ::: "memory");
-    int none = 0;
-    if (*abort && lane < a.stages)
-      for (int parity = 0; parity < 2; ++parity)
-        mbar_wait_bounded(smem_u32(&sm.full[lane]), parity, &none, nullptr, 100000000ull);
-  } else if (warp == kWarpEpilogue) {
+    if (*abort && lane < a.stages) {
+      int none = 0;
+      for (int i = 0; i < 2; ++i)
+        mbar_wait_bounded(smem_u32(&sm.full[lane]), i, &none, nullptr, 100000000ull);
+    }
+  } else if (warp_id == kWarpEpilogue) {
     // ------------------------------------------------------------- epilogue
     const int g = lane >> 2, t = lane & 3;
-    int nbase = 0;
+    int n0 = 0;     // the CTA's units before this segment
     int taken = 0;  // lane w: sums taken from warp w
     for (int v = lane; v < c.nv; v += 32)
       for (int p = 0; p < kPhases; ++p) sm.vglobal[p][v] = __ldg(&a.m[p].global[sm.vexp[v]]);
@@ -808,6 +958,9 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       int seg = f.seg_begin();
       SegPos at = f.at(seg);
       bool fresh = true;  // first segment of a tile in this CTA
+      int n = 0, s0 = 0;
+      float factor[NT][2];
+      float* out_row[2] = {&sm.out[0][0], &sm.out[0][0]};
       for (; seg * f.U < f.u1; ++seg, f.step(at)) {
         const int ua = max(f.u0, seg * f.U), ub = min(f.u1, (seg + 1) * f.U);
         const int last_item = it.item;
@@ -815,43 +968,68 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][last_item % kItems]));
         }
-        float acc[2][NT][4] = {};
-        const int cnt = min(ub - ua, kConsumers), w0 = (nbase + ua - f.u0) % kConsumers;
-        for (int i = 0; i < cnt; ++i) {
-          const int w = (w0 + i) % kConsumers, tk = __shfl_sync(0xFFFFFFFFu, taken, w);
-          if (!warp_wait(sm.pfull[w][tk & 1], (tk >> 1) & 1, abort, a.status)) goto done;
-          const uint32_t src = pbuf + (2 * w + (tk & 1)) * kPartBytes + lane * 16;
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint4 x = lds128(src + (m * NT + nt) * 512);
-              acc[m][nt][0] += __uint_as_float(x.x);
-              acc[m][nt][1] += __uint_as_float(x.y);
-              acc[m][nt][2] += __uint_as_float(x.z);
-              acc[m][nt][3] += __uint_as_float(x.w);
-            }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.pempty[w][tk & 1]));
-          if (lane == w) ++taken;
+        const bool fresh_item = it.item != last_item || seg == f.seg_begin();
+        if (fresh_item || p == 0) {
+          n = c.item_rows(at.v);
+          s0 = sm.vstart[at.v];
         }
-        const int n = c.item_rows(at.v), s0 = sm.vstart[at.v];
-        const float gl = sm.vglobal[p][at.v];
-        // lane (g, t) holds rows g and g + 8 of tokens 8 nt + 2 t and + 1
+        // the sums of the warps that had units of the segment, in their order:
+        // lane i waits for the i-th of them, all lanes add
+        float acc[2][NT][4] = {};
+        const int cnt = min(ub - ua, kConsumers), w0 = n0 % kConsumers;
+        n0 += ub - ua;
+        const int mine = (w0 + lane) % kConsumers, mine_tk = __shfl_sync(0xFFFFFFFFu, taken, mine);
+        if (!wait_count(&sm.done[mine], lane < cnt ? mine_tk + 1 : 0, abort, a.status)) goto done;
+        const uint32_t mine_src = pbuf + (2 * mine + (mine_tk & 1)) * kPartBytes;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int i0 = 0; i0 < kConsumers; i0 += 4) {
+          if (i0 >= cnt) break;
+          uint4 x[4][2][NT];
 #pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const int col = 8 * nt + 2 * t + o;
-            if (col < n) {
-              const float rs = sm.rscale[p][c.row_slot(res, it.pos, R, s0, col)] * gl;
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t src = __shfl_sync(0xFFFFFFFFu, mine_src, i0 + i) + lane * 16;
+            if (i0 + i < cnt) {
 #pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                acc[m][nt][o] *= rs;
-                acc[m][nt][2 + o] *= rs;
-              }
+              for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) x[i][m][nt] = lds128(src + (m * NT + nt) * 512);
             }
           }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i0 + i < cnt) {
+#pragma unroll
+              for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  acc[m][nt][0] += __uint_as_float(x[i][m][nt].x);
+                  acc[m][nt][1] += __uint_as_float(x[i][m][nt].y);
+                  acc[m][nt][2] += __uint_as_float(x[i][m][nt].z);
+                  acc[m][nt][3] += __uint_as_float(x[i][m][nt].w);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane < cnt) store_count(&sm.taken[mine], mine_tk + 1);
+        if (lane < kConsumers && (lane - w0 + kConsumers) % kConsumers < cnt) ++taken;
+        // lane (g, t) holds rows g and g + 8 of tokens 8 nt + 2 t and + 1; their factors:
+        if (fresh_item || p == 0) {
+          const float gl = sm.vglobal[p][at.v];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const int col = 8 * nt + 2 * t + o;
+              factor[nt][o] = 0.f;
+              if (col < n) {
+                factor[nt][o] = sm.rscale[p][c.row_slot(res, it.pos, R, s0, col)] * gl;
+                if (p == 1) {
+                  factor[nt][o] *= sm.route_w[s0 + col];
+                  out_row[o] = &sm.out[sm.route_tok[s0 + col]][g];
+                }
+              }
+            }
+        }
         const int tile = p == 0 ? seg : at.j;
         const int64_t tb = (int64_t)tile * tu, te = tb + tu;  // the tile's units
         if (p == 1) {
@@ -861,22 +1039,29 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             __syncwarp();
           }
 #pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const int col = 2 * t + o;
-            if (col < n) {
-              const float w = sm.route_w[s0 + col];
-              float* row = &sm.out[sm.route_tok[s0 + col]][32 * at.rb + g];
-#pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                row[16 * m] = fmaf(w, acc[m][0][o], row[16 * m]);
-                row[16 * m + 8] = fmaf(w, acc[m][0][2 + o], row[16 * m + 8]);
-              }
+          for (int o = 0; o < 2; ++o)
+            if (2 * t + o < n) {
+              float* row = out_row[o] + 32 * at.rb;
+              const float r[4] = {row[0], row[8], row[16], row[24]};
+              row[0] = fmaf(factor[0][o], acc[0][0][o], r[0]);
+              row[8] = fmaf(factor[0][o], acc[0][0][2 + o], r[1]);
+              row[16] = fmaf(factor[0][o], acc[1][0][o], r[2]);
+              row[24] = fmaf(factor[0][o], acc[1][0][2 + o], r[3]);
             }
-          }
           __syncwarp();
           fresh = false;
           if (ub < min((int64_t)f.u1, te)) continue;  // more of this tile to come
           fresh = true;
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                acc[m][nt][o] *= factor[nt][o];
+                acc[m][nt][2 + o] *= factor[nt][o];
+              }
         }
         const bool whole = tb >= f.u0 && te <= f.u1;
         if (!whole) {
@@ -949,6 +1134,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
 #pragma unroll
           for (int o = 0; o < 2; ++o) {
             const int col = 8 * nt + 2 * t + o;
+            if (8 * nt + o >= n) continue;  // no lane has a column
             if (MOE) {
               // 16 values of h: half times 2^s of their largest, and s
               const float h0 = swiglu(acc[0][nt][o], acc[1][nt][o]);
@@ -993,12 +1179,13 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         __syncwarp();
         if (lane == 0) atomicAdd(&a.ctl[0], 1u);
       }
-      nbase += f.u1 - f.u0;
     }
   } else {
     // -------------------------------------------------------------- loaders
-    const int lw = warp - kWarpLoader;
+    const int lw = warp_id - kWarpLoader;
     uint32_t raw_parity = 0;
+    bool went = early;  // whether the producers need not wait for this warp's first copy
+    if (went && lane == 0) mbar_arrive(smem_u32(&sm.go));
     for (int p = 0; p < kPhases; ++p) {
       const Phase f = c.phase(p);
       if (MOE && p == 1) {
@@ -1021,7 +1208,15 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         }
         if (!__shfl_sync(0xFFFFFFFFu, (int)ok, 0)) goto done;
       }
-      if (f.u0 >= f.u1) continue;
+      if (f.u0 >= f.u1) {
+        if (p == 0 && early && lw < (a.T < kLoaders ? 1 : a.T)) {  // the copy asked for has to end
+          if (!warp_wait(sm.raw[lw], 0, abort, a.status)) goto done;
+          raw_parity = 1;
+        }
+        if (!went && lane == 0) mbar_arrive(smem_u32(&sm.go));
+        went = true;
+        continue;
+      }
       const int RB = row_bytes(f.cols, p == 1);
       if (c.resident(p)) {
         // all loader warps work on each row where there are few; a warp that gives
@@ -1030,13 +1225,13 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         if (a.T < kLoaders) {
           for (int r = 0; r < a.T; ++r)
             ok &= fill_x<kLoaders>(a.x + r * a.ldx, f.cols, brow0 + r * RB, lw, sm.raw[0], raw_parity,
-                                   sm.red, &sm.rscale[0][r], abort, a.status);
+                                   sm.red, &sm.rscale[0][r], abort, a.status, r == 0);
           // from here every warp has a barrier of its own
           if (lw > 0) raw_parity = 0;
         } else {
           for (int r = lw; r < a.T && ok; r += kLoaders)
             ok = fill_x<1>(a.x + r * a.ldx, f.cols, brow0 + r * RB, 0, sm.raw[lw], raw_parity, sm.red,
-                           &sm.rscale[0][r], abort, a.status);
+                           &sm.rscale[0][r], abort, a.status, r < kLoaders);
         }
         if (!ok) goto done;
         __syncwarp();
@@ -1072,14 +1267,20 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
               const int s = sm.vstart[at.v] + r, place = c.row_slot(false, it.pos, R, 0, r);
               const bool ok =
                   p == 0 ? fill_x<1>(a.x + sm.route_tok[s] * a.ldx, f.cols, brow0 + place * RB, 0,
-                                     sm.raw[lw], raw_parity, sm.red, &sm.rscale[0][place], abort, a.status)
+                                     sm.raw[lw], raw_parity, sm.red, &sm.rscale[0][place], abort, a.status,
+                                     false, went ? nullptr : &sm.go)
                          : fill_h(a.h + (int64_t)sm.route_id[s] * record_bytes(f.cols), f.cols,
                                   brow0 + place * RB, sm.raw[lw], raw_parity, &sm.rscale[1][place], abort,
                                   a.status);
+              went = true;
               if (!ok) goto done;
             }
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.bfull[p][it.item % kItems]));
+          if (lane == 0) {
+            if (!went) mbar_arrive(smem_u32(&sm.go));
+            mbar_arrive(smem_u32(&sm.bfull[p][it.item % kItems]));
+          }
+          went = true;
         }
         if (p + 1 < kPhases)
           while (oldest <= it.item)
@@ -1103,25 +1304,26 @@ done:
 
 // Shared memory of a launch: the operand rows' share, and what is left for the ring.
 struct Fp4Plan {
-  int group, nt, stages, b_bytes, smem;
+  int group, nt, b_bytes, stages, smem;
 };
 
+static int fp4_part_bytes(int nt) { return kConsumers * 2 * 2 * nt * 512; }
+
 static int fp4_row_budget(int nt) {
-  return kMaxSmem - (int)sizeof(Fp4Shared) - 2048 - 2 * kConsumers * 2 * nt * 512 -
-         kConsumers * kStageBytes;  // the least number of stages
+  return (kMaxSmem - (int)sizeof(Fp4Shared) - 2048 - fp4_part_bytes(nt) - kMinStages * kUnitBytes) / 128 * 128;
 }
 
 static void fp4_finish_plan(Fp4Plan* p) {
   p->b_bytes = (p->b_bytes + 127) / 128 * 128;
-  const int left = fp4_row_budget(p->nt) - p->b_bytes;
-  p->stages = left >= kConsumers * kStageBytes ? kMaxStages : kConsumers;
-  p->smem = 1024 + p->stages * kStageBytes + p->b_bytes + 2 * kConsumers * 2 * p->nt * 512;
+  p->stages = kMinStages + (fp4_row_budget(p->nt) - p->b_bytes) / (kProducers * kUnitBytes) * kProducers;
+  if (p->stages > kMaxStages) p->stages = kMaxStages;
+  p->smem = 1024 + p->stages * kUnitBytes + p->b_bytes + fp4_part_bytes(p->nt);
 }
 
 // The layer: tokens in groups of at most 8.
 static Fp4Plan fp4_plan_layer(int H, int I, int T, int K) {
   Fp4Plan p = {8, 1, 0, 0, 0};
-  const int budget = fp4_row_budget(1) / 128 * 128, r1 = row_bytes(H, false), r2 = row_bytes(I, true);
+  const int budget = fp4_row_budget(1), r1 = row_bytes(H, false), r2 = row_bytes(I, true);
   if (budget / r1 < p.group) p.group = budget / r1;
   if (budget / r2 < p.group) p.group = budget / r2;
   // x: T rows, or one group's; h: two groups' or all, as far as they fit
@@ -1139,26 +1341,25 @@ static Fp4Plan fp4_plan_layer(int H, int I, int T, int K) {
 static Fp4Plan fp4_plan_linear(int cols, int T) {
   Fp4Plan p = {0, 1, 0, 0, 0};
   const int rb = row_bytes(cols, false);
-  const int fit1 = fp4_row_budget(1) / 128 * 128 / rb, fit2 = fp4_row_budget(2) / 128 * 128 / rb;
+  const int fit1 = fp4_row_budget(1) / rb, fit2 = fp4_row_budget(2) / rb;
   const int most = fit2 > 8 ? (fit2 < 16 ? fit2 : 16) : (fit1 < 8 ? fit1 : 8);
   const int groups = (T + most - 1) / most;
   p.group = (T + groups - 1) / groups;
   p.nt = p.group > 8 ? 2 : 1;
-  const int budget = fp4_row_budget(p.nt) / 128 * 128;
+  const int budget = fp4_row_budget(p.nt);
   p.b_bytes = (int64_t)T * rb <= budget ? T * rb : p.group * rb;
   fp4_finish_plan(&p);
   return p;
 }
 
 template <bool MOE, int NT>
-static cudaError_t fp4_launch(const CUtensorMap& t0, const CUtensorMap& t1, const Fp4Args& a, int grid,
-                              int smem, cudaStream_t s) {
+static cudaError_t fp4_launch(const Fp4Maps& maps, const Fp4Args& a, int grid, int smem, cudaStream_t s) {
   cudaLaunchAttribute coop;
   coop.id = cudaLaunchAttributeCooperative;
   coop.val.cooperative = 1;
   // the layer's CTAs wait for one another (all resident, or the launch fails); the linear's do not
   return launch_k(fp4_stream_kernel<MOE, NT>, dim3(grid), dim3(kFp4Threads), smem, s, false,
-                  MOE ? &coop : nullptr, t0, t1, a);
+                  MOE ? &coop : nullptr, maps, a);
 }
 
 }  // namespace mm
@@ -1169,7 +1370,7 @@ struct moe_fp4_handle {
   bool layer;
   moe_dims dims;         // the layer
   Fp4Matrix m[2];        // the linear: the first
-  CUtensorMap map[2];
+  Fp4Maps maps;
   int max_tokens, grid;
   uint32_t* status;
   uint32_t* ctl;
@@ -1196,9 +1397,10 @@ bool fp4_dims_ok(const moe_dims* d) {
 
 bool misaligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
-// Codes [rows, cols/2] as a byte matrix; boxes of 16 rows x 128 bytes with the
-// 128-byte swizzle; bytes past a row's or the matrix's end read as zero.
-bool fp4_encode_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols) {
+// The two maps of a matrix (Fp4Maps).  halves: FC1's, [E][gate, up][rows][cols],
+// else [rows][cols].
+bool fp4_encode_maps(CUtensorMap* unit, CUtensorMap* box, const void* base, uint64_t rows, uint64_t cols,
+                     uint64_t experts) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
     void* p = nullptr;
@@ -1209,13 +1411,33 @@ bool fp4_encode_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t co
       return false;
     fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   }
-  cuuint64_t dims[2] = {cols / 2, rows};
-  cuuint64_t strides[1] = {cols / 2};
-  cuuint32_t box[2] = {128, 16};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto encode = [&](CUtensorMap* m, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                    const cuuint32_t* b) {
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, b, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const uint64_t pitch = cols / 2, all = rows * (experts ? 2 * experts : 1);
+  // whole 256-column blocks (one, never used past its end, where there is none)
+  const uint64_t blocks = cols / 256 ? cols / 256 : 1;
+  const uint64_t inner = cols / 256 ? 128 : pitch < 128 ? pitch : 128;
+  bool ok;
+  if (experts) {
+    const cuuint64_t dims[5] = {inner, rows, 2, blocks, experts};
+    const cuuint64_t strides[4] = {pitch, rows * pitch, 128, 2 * rows * pitch};
+    const cuuint32_t b[5] = {128, 16, 2, 2, 1};
+    ok = encode(unit, 5, dims, strides, b);
+  } else {
+    const cuuint64_t dims[3] = {inner, all, blocks};
+    const cuuint64_t strides[2] = {pitch, 128};
+    const cuuint32_t b[3] = {128, 32, 2};
+    ok = encode(unit, 3, dims, strides, b);
+  }
+  const cuuint64_t dims[2] = {pitch, all};
+  const cuuint64_t strides[1] = {pitch};
+  const cuuint32_t b[2] = {128, 16};
+  return ok && encode(box, 2, dims, strides, b);
 }
 
 // The device checks, kernel attributes and workspace of a new handle.
@@ -1281,8 +1503,9 @@ moe_status moe_fp4_create(const moe_dims* dims, int64_t max_tokens, const uint8_
   h->max_tokens = (int)max_tokens;
   st = fp4_set_up(h, d_workspace, stream);
   const uint64_t E = dims->num_experts;
-  if (st == MOE_OK && (!fp4_encode_map(&h->map[0], d_w1, E * 2 * dims->inter, dims->hidden) ||
-                       !fp4_encode_map(&h->map[1], d_w2, E * dims->hidden, dims->inter)))
+  if (st == MOE_OK &&
+      (!fp4_encode_maps(&h->maps.unit[0], &h->maps.box[0], d_w1, dims->inter, dims->hidden, E) ||
+       !fp4_encode_maps(&h->maps.unit[1], &h->maps.box[1], d_w2, E * dims->hidden, dims->inter, 0)))
     st = MOE_ERR_CUDA;
   if (st != MOE_OK) {
     delete h;
@@ -1320,10 +1543,11 @@ moe_status moe_fp4_forward(moe_fp4_handle* h, const uint16_t* d_x, const int32_t
   a.E = d.num_experts;
   a.K = d.top_k;
   a.group = p.group;
-  a.stages = p.stages;
   a.b_bytes = p.b_bytes;
+  a.stages = p.stages;
+  a.stage_rcp = (uint32_t)(0x100000000ull / p.stages) + 1;
   a.check = (d.flags & MOE_FLAG_CHECK_ROUTES) != 0;
-  return fp4_launch<true, 1>(h->map[0], h->map[1], a, h->grid, p.smem, stream) == cudaSuccess
+  return fp4_launch<true, 1>(h->maps, a, h->grid, p.smem, stream) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -1356,7 +1580,8 @@ moe_status moe_fp4_linear_create(int32_t rows, int32_t cols, int64_t max_tokens,
   h->m[0] = {d_scales, d_global, rows, cols};
   h->max_tokens = (int)max_tokens;
   st = fp4_set_up(h, d_workspace, stream);
-  if (st == MOE_OK && !fp4_encode_map(&h->map[0], d_codes, rows, cols)) st = MOE_ERR_CUDA;
+  if (st == MOE_OK && !fp4_encode_maps(&h->maps.unit[0], &h->maps.box[0], d_codes, rows, cols, 0))
+    st = MOE_ERR_CUDA;
   if (st != MOE_OK) {
     delete h;
     return st;
@@ -1388,12 +1613,13 @@ moe_status moe_fp4_linear(moe_fp4_handle* h, const uint16_t* d_x, int64_t x_stri
   a.E = 1;
   a.K = 1;
   a.group = p.group;
-  a.stages = p.stages;
   a.b_bytes = p.b_bytes;
+  a.stages = p.stages;
+  a.stage_rcp = (uint32_t)(0x100000000ull / p.stages) + 1;
   a.f32 = y_float32 != 0;
   const cudaError_t e = p.nt == 2
-                            ? fp4_launch<false, 2>(h->map[0], h->map[0], a, h->grid, p.smem, stream)
-                            : fp4_launch<false, 1>(h->map[0], h->map[0], a, h->grid, p.smem, stream);
+                            ? fp4_launch<false, 2>(h->maps, a, h->grid, p.smem, stream)
+                            : fp4_launch<false, 1>(h->maps, a, h->grid, p.smem, stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
