@@ -259,17 +259,20 @@ def moe_destroy(h) -> None:
         lib().moe_destroy(h)
 
 
-def moe_add_rms_norm(d_x, x_stride, d_res, res_stride, d_w, eps, num_tokens, hidden, d_res_out, d_y,
-                     d_q, d_q_scale, q_format, q_static_scale, stream) -> None:
-    _check(lib().moe_add_rms_norm(d_x, x_stride, d_res, res_stride, d_w, eps, num_tokens, hidden,
-                                  d_res_out, d_y, d_q, d_q_scale, q_format, q_static_scale, stream),
-           "moe_add_rms_norm")
+def moe_add_rms_norm(*args) -> None:
+    """d_x, x_stride, d_residual, residual_stride, d_weight, eps, num_tokens, hidden,
+    d_residual_out, d_y, d_q, d_q_scale, q_format, q_static_scale, stream"""
+    s = (_lib or lib()).moe_add_rms_norm(*args)
+    if s:
+        raise MoEError(s, "moe_add_rms_norm")
 
 
-def moe_topk_route(d_logits, bf16, stride, d_bias, num_tokens, E, K, sigmoid, groups, top_groups,
-                   renormalize, scale, d_idx, d_w, stream) -> None:
-    _check(lib().moe_topk_route(d_logits, bf16, stride, d_bias, num_tokens, E, K, sigmoid, groups,
-                                top_groups, renormalize, scale, d_idx, d_w, stream), "moe_topk_route")
+def moe_topk_route(*args) -> None:
+    """d_logits, logits_bf16, stride, d_bias, num_tokens, E, K, sigmoid, num_groups, top_groups,
+    renormalize, scale, d_topk_idx, d_topk_w, stream"""
+    s = (_lib or lib()).moe_topk_route(*args)
+    if s:
+        raise MoEError(s, "moe_topk_route")
 
 
 def moe_fp4_workspace_query(H, I, E, K, flags, max_tokens) -> int:
@@ -290,7 +293,9 @@ def moe_fp4_create(H, I, E, K, flags, max_tokens, d_w1, d_w1s, d_w1g, d_w2, d_w2
 
 
 def moe_fp4_forward(h, d_x, d_idx, d_w, num_tokens, d_out, stream) -> None:
-    _check(lib().moe_fp4_forward(h, d_x, d_idx, d_w, num_tokens, d_out, stream), "moe_fp4_forward")
+    s = (_lib or lib()).moe_fp4_forward(h, d_x, d_idx, d_w, num_tokens, d_out, stream)
+    if s:
+        raise MoEError(s, "moe_fp4_forward")
 
 
 def moe_fp4_linear_workspace_query(rows, cols, max_tokens) -> int:
@@ -309,8 +314,9 @@ def moe_fp4_linear_create(rows, cols, max_tokens, d_codes, d_scales, d_global, d
 
 
 def moe_fp4_linear(h, d_x, x_stride, num_tokens, d_y, y_float32, stream) -> None:
-    _check(lib().moe_fp4_linear(h, d_x, x_stride, num_tokens, d_y, y_float32, stream),
-           "moe_fp4_linear")
+    s = (_lib or lib()).moe_fp4_linear(h, d_x, x_stride, num_tokens, d_y, y_float32, stream)
+    if s:
+        raise MoEError(s, "moe_fp4_linear")
 
 
 def moe_fp4_read_status(h, stream):

@@ -128,7 +128,7 @@ struct Fp4Shared {
   int16_t vstart[kFp4MaxRoutes + 1];    // first sorted position of every item
   int16_t vexp[kFp4MaxRoutes];
   uint8_t first[kFp4MaxRoutes];
-  float red[kLoaders];
+  uint32_t row_max[kFp4MaxTokens];
   int warp_cnt[4];
   int issued[kProducers];               // units each producer has begun
   int done[kConsumers], taken[kConsumers];  // sums each consumer has left, and that were taken
@@ -437,65 +437,102 @@ __device__ __forceinline__ void raw_begin(uint64_t& bar, uint32_t bytes) {
   mbar_arrive_expect_tx(smem_u32(&bar), bytes);
 }
 
-// One x row (cols BF16 values, a multiple of 32) as half times 2^s, zeros up to
-// the unit's end.  The row is copied as it is and turned in place, unit by unit;
-// TEAM warps (one, or all loaders) work on it.
-template <int TEAM>
-__device__ __forceinline__ bool fill_x(const uint16_t* src, int cols, uint32_t dst, int rank,
-                                       uint64_t& bar, uint32_t& parity, float* red, float* rscale,
-                                       volatile int* abort, uint32_t* status, bool asked,
-                                       uint64_t* go = nullptr) {
+// x as half: 16 BF16 values (a lane's two pieces of a unit), their largest
+// magnitude as BF16 bits.  NaN does not set the scale (it stays NaN in half);
+// infinity does.
+__device__ __forceinline__ uint32_t max_bf16x8(const uint4 v, uint32_t m) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+    m = max(m, max(lo > 0x7F80u ? 0u : lo, hi > 0x7F80u ? 0u : hi));
+  }
+  return m;
+}
+
+__device__ __forceinline__ uint4 bf16x8_to_half(const uint4 v, float up) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = half2_bits(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
+  return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+// The two pieces of unit u that are this lane's, of a row of n pieces (zeros past them).
+__device__ __forceinline__ void load_pieces(uint32_t row, int u, int n, uint4 (&v)[2]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int q = 64 * u + 32 * k + lane;
+    v[k] = q < n ? lds128(row + 16 * q) : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+__device__ __forceinline__ void turn_unit(uint32_t row, int u, uint4 (&v)[2], float up) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();  // all of the unit is in registers
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    sts128(row + u * (kUnitCols * 2) + piece_offset(32 * k + lane), bf16x8_to_half(v[k], up));
+}
+
+// One x row (cols BF16 values, a multiple of 32) by one warp: copied as it is,
+// then turned in place, unit by unit, to half times 2^s with zeros up to the
+// unit's end.
+__device__ __forceinline__ bool fill_x(const uint16_t* src, int cols, uint32_t dst, uint64_t& bar,
+                                       uint32_t& parity, float* rscale, volatile int* abort,
+                                       uint32_t* status, uint64_t* go) {
   const int lane = threadIdx.x & 31, n = cols >> 3, U = padded_units(cols);
-  if (rank == 0 && lane == 0 && !asked) {
+  if (lane == 0) {
     raw_begin(bar, cols * 2);
     bulk_load(dst, src, cols * 2, smem_u32(&bar));
+    if (go) mbar_arrive(smem_u32(go));
   }
-  if (go && lane == 0) mbar_arrive(smem_u32(go));
-  const bool ok = warp_wait(bar, parity, abort, status);  // a team goes on to its barriers either way
+  if (!warp_wait(bar, parity, abort, status)) return false;
   parity ^= 1;
-  uint32_t m = 0u;  // the largest |value|, as BF16 bits
-#pragma unroll 4
-  for (int q = 32 * rank + lane; q < n; q += 32 * TEAM) {
-    const uint4 v = lds128(dst + 16 * q);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-      // NaN does not set the scale (it stays NaN in half); infinity does
-      m = max(m, max(lo > 0x7F80u ? 0u : lo, hi > 0x7F80u ? 0u : hi));
-    }
-  }
-  m = __reduce_max_sync(0xFFFFFFFFu, m);
-  if (TEAM > 1) {
-    if (lane == 0) red[rank] = __uint_as_float(m);
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * TEAM) : "memory");
-#pragma unroll
-    for (int i = 0; i < TEAM; ++i) m = max(m, __float_as_uint(red[i]));
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * TEAM) : "memory");  // red is free for the next row
-  }
-  const int s = row_exponent(__uint_as_float(m << 16));
-  const float up = pow2f(s);
-  if (rank == 0 && lane == 0) *rscale = pow2f(-s);
+  uint32_t m = 0u;
 #pragma unroll 2
-  for (int u = rank; u < U; u += TEAM) {
-    const uint32_t base = dst + u * (kUnitCols * 2);
-    uint4 o[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int q = lane + 32 * k;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (64 * u + q < n) v = lds128(base + 16 * q);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t h[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        h[i] = half2_bits(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
-      o[k] = make_uint4(h[0], h[1], h[2], h[3]);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) sts128(base + piece_offset(lane + 32 * k), o[k]);
+  for (int u = 0; u < U; ++u) {
+    uint4 v[2];
+    load_pieces(dst, u, n, v);
+    m = max_bf16x8(v[1], max_bf16x8(v[0], m));
   }
+  const int s = row_exponent(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m) << 16));
+  if (lane == 0) *rscale = pow2f(-s);
+  for (int u = 0; u < U; ++u) {
+    uint4 v[2];
+    load_pieces(dst, u, n, v);
+    turn_unit(dst, u, v, pow2f(s));
+  }
+  return true;
+}
+
+// All T rows of a resident phase by `warps` warps, this one the rank-th: their
+// copies have been asked for on `bar`.  Every warp meets the others at both
+// barriers, also one that gave up on the copies.
+__device__ __forceinline__ bool fill_x_rows(int T, int cols, uint32_t rows, int pitch, int rank, int warps,
+                                            uint64_t& bar, uint32_t* row_max, float* rscale,
+                                            volatile int* abort, uint32_t* status) {
+  const int lane = threadIdx.x & 31, n = cols >> 3, U = padded_units(cols);
+  const bool ok = warp_wait(bar, 0, abort, status);
+  for (int i = rank; i < T * U; i += warps) {
+    const int t = i / U, u = i - t * U;
+    uint4 v[2];
+    load_pieces(rows + t * pitch, u, n, v);
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max_bf16x8(v[1], max_bf16x8(v[0], 0u)));
+    if (lane == 0) atomicMax(&row_max[t], m);
+  }
+  asm volatile("bar.sync 1, %0;" ::"r"(32 * warps) : "memory");
+  for (int i = rank; i < T * U; i += warps) {
+    const int t = i / U, u = i - t * U;
+    uint4 v[2];
+    load_pieces(rows + t * pitch, u, n, v);
+    const int s = row_exponent(__uint_as_float(row_max[t] << 16));
+    if (u == 0 && lane == 0) rscale[t] = pow2f(-s);
+    turn_unit(rows + t * pitch, u, v, pow2f(s));
+  }
+  asm volatile("bar.sync 1, %0;" ::"r"(32 * warps) : "memory");
   return ok;
 }
 
@@ -528,29 +565,36 @@ __device__ __forceinline__ bool fill_h(const uint8_t* src, int cols, uint32_t ds
   for (int b = lane; b < (cols >> 4); b += 32) s = min(s, exponent(b));
   s = __reduce_min_sync(0xFFFFFFFFu, s);
   if (lane == 0) *rscale = pow2f(-s);
-  for (int u = 0; u < U; ++u) {
-    const uint32_t base = dst + u * (kUnitCols * 2);
-    uint4 o[2];
+  for (int u0 = 0; u0 < U; u0 += 2) {
+    uint4 v[2][2];
+    int d[2][2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int q = lane + 32 * k;
-      o[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (64 * u + q < n) {
-        const uint4 v = lds128(base + 16 * q);
-        const int d = exponent((64 * u + q) >> 1) - s;
-        const uint32_t f1 = half_pow2_neg(min(d, 14)), f2 = half_pow2_neg(d - min(d, 14));
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int o = 0; o < 2; ++o)
+      if (u0 + o < U) {
+        load_pieces(dst, u0 + o, n, v[o]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(f1));
-          asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(f2));
+        for (int k = 0; k < 2; ++k) {
+          const int q = 64 * (u0 + o) + 32 * k + lane;
+          d[o][k] = q < n ? exponent(q >> 1) - s : 0;
         }
-        o[k] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-    }
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 2; ++k) sts128(base + piece_offset(lane + 32 * k), o[k]);
+    for (int o = 0; o < 2; ++o)
+      if (u0 + o < U) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t f1 = half_pow2_neg(min(d[o][k], 14)), f2 = half_pow2_neg(d[o][k] - min(d[o][k], 14));
+          uint32_t w[4] = {v[o][k].x, v[o][k].y, v[o][k].z, v[o][k].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(f1));
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(f2));
+          }
+          sts128(dst + (u0 + o) * (kUnitCols * 2) + piece_offset(32 * k + lane),
+                 make_uint4(w[0], w[1], w[2], w[3]));
+        }
+      }
   }
   return true;
 }
@@ -664,6 +708,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       // copies: one arrival with the codes' bytes, one per lane with its scales
       mbar_init(smem_u32(&sm.full[i]), 33);
       mbar_init(smem_u32(&sm.empty[i]), 1);
+    } else if (i >= 96 && i < 96 + kFp4MaxTokens) {
+      sm.row_max[i - 96] = 0u;
     } else if (i >= 32 && i < 32 + kConsumers) {
       sm.done[i - 32] = sm.taken[i - 32] = 0;
     } else if (i >= 64 && i < 64 + 2 * kItems) {
@@ -685,13 +731,13 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
   const bool early = (int64_t)a.T * row_bytes(a.m[0].cols, false) <= a.b_bytes;
   const bool loader = warp_id >= kWarpLoader && warp_id < kWarpConsumer;
   if (loader && lane == 0) {
-    const int r = warp_id - kWarpLoader;
-    uint64_t& bar = sm.raw[r];
+    uint64_t& bar = sm.raw[warp_id - kWarpLoader];
     mbar_init(smem_u32(&bar), 1);
     fence_mbar_init();
-    if (early && r < (a.T < kLoaders ? 1 : a.T)) {
-      raw_begin(bar, a.m[0].cols * 2);
-      bulk_load(brow0 + r * row_bytes(a.m[0].cols, false), a.x + r * a.ldx, a.m[0].cols * 2, smem_u32(&bar));
+    if (early && warp_id == kWarpLoader) {
+      raw_begin(bar, a.T * a.m[0].cols * 2);
+      for (int r = 0; r < a.T; ++r)
+        bulk_load(brow0 + r * row_bytes(a.m[0].cols, false), a.x + r * a.ldx, a.m[0].cols * 2, smem_u32(&bar));
     }
   }
   build_items<MOE>(a, sm);
@@ -709,9 +755,17 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
          i += (int64_t)gridDim.x * blockDim.x)
       o[i] = make_uint4(0u, 0u, 0u, 0u);
     // no copy outlives the CTA
-    if (early && loader && warp_id - kWarpLoader < (a.T < kLoaders ? 1 : a.T))
-      mbar_wait(smem_u32(&sm.raw[warp_id - kWarpLoader]), 0, abort, a.status);
+    if (early && warp_id == kWarpLoader) mbar_wait(smem_u32(&sm.raw[0]), 0, abort, a.status);
     return;
+  }
+
+  // rows that stay: the loaders and the consumers, who have nothing to do yet,
+  // turn them together
+  if (early && warp_id >= kWarpLoader) {
+    if (loader && lane == 0) mbar_arrive(smem_u32(&sm.go));
+    if (!fill_x_rows(a.T, a.m[0].cols, brow0, row_bytes(a.m[0].cols, false), warp_id - kWarpLoader,
+                     kLoaders + kConsumers, sm.raw[0], sm.row_max, sm.rscale[0], abort, a.status))
+      goto done;
   }
 
   if (warp_id >= kWarpConsumer) {
@@ -738,7 +792,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][last_item % kItems]));
           }
-          if (!warp_wait(sm.bfull[p][it.item % kItems], (it.item / kItems) & 1, abort, a.status)) return false;
+          if (!res && !warp_wait(sm.bfull[p][it.item % kItems], (it.item / kItems) & 1, abort, a.status))
+            return false;
         }
         const int first = ka + ((warp - n0) & (kConsumers - 1));  // this warp's first unit of the segment
         if (first < kb) {
@@ -1183,9 +1238,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
   } else {
     // -------------------------------------------------------------- loaders
     const int lw = warp_id - kWarpLoader;
-    uint32_t raw_parity = 0;
+    uint32_t raw_parity = early && lw == 0;
     bool went = early;  // whether the producers need not wait for this warp's first copy
-    if (went && lane == 0) mbar_arrive(smem_u32(&sm.go));
     for (int p = 0; p < kPhases; ++p) {
       const Phase f = c.phase(p);
       if (MOE && p == 1) {
@@ -1209,33 +1263,12 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         if (!__shfl_sync(0xFFFFFFFFu, (int)ok, 0)) goto done;
       }
       if (f.u0 >= f.u1) {
-        if (p == 0 && early && lw < (a.T < kLoaders ? 1 : a.T)) {  // the copy asked for has to end
-          if (!warp_wait(sm.raw[lw], 0, abort, a.status)) goto done;
-          raw_parity = 1;
-        }
         if (!went && lane == 0) mbar_arrive(smem_u32(&sm.go));
         went = true;
         continue;
       }
       const int RB = row_bytes(f.cols, p == 1);
       if (c.resident(p)) {
-        // all loader warps work on each row where there are few; a warp that gives
-        // up on its copy still meets the others at their barrier
-        bool ok = true;
-        if (a.T < kLoaders) {
-          for (int r = 0; r < a.T; ++r)
-            ok &= fill_x<kLoaders>(a.x + r * a.ldx, f.cols, brow0 + r * RB, lw, sm.raw[0], raw_parity,
-                                   sm.red, &sm.rscale[0][r], abort, a.status, r == 0);
-          // from here every warp has a barrier of its own
-          if (lw > 0) raw_parity = 0;
-        } else {
-          for (int r = lw; r < a.T && ok; r += kLoaders)
-            ok = fill_x<1>(a.x + r * a.ldx, f.cols, brow0 + r * RB, 0, sm.raw[lw], raw_parity, sm.red,
-                           &sm.rscale[0][r], abort, a.status, r < kLoaders);
-        }
-        if (!ok) goto done;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.bfull[p][0]));
         // the rows' memory is the next phase's when everyone is done with them
         if (p + 1 < kPhases && !warp_wait(sm.bempty[p][0], 0, abort, a.status)) goto done;
       } else {
@@ -1266,9 +1299,9 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             if (counter % kLoaders == lw) {
               const int s = sm.vstart[at.v] + r, place = c.row_slot(false, it.pos, R, 0, r);
               const bool ok =
-                  p == 0 ? fill_x<1>(a.x + sm.route_tok[s] * a.ldx, f.cols, brow0 + place * RB, 0,
-                                     sm.raw[lw], raw_parity, sm.red, &sm.rscale[0][place], abort, a.status,
-                                     false, went ? nullptr : &sm.go)
+                  p == 0 ? fill_x(a.x + sm.route_tok[s] * a.ldx, f.cols, brow0 + place * RB, sm.raw[lw],
+                                  raw_parity, &sm.rscale[0][place], abort, a.status,
+                                  went ? nullptr : &sm.go)
                          : fill_h(a.h + (int64_t)sm.route_id[s] * record_bytes(f.cols), f.cols,
                                   brow0 + place * RB, sm.raw[lw], raw_parity, &sm.rscale[1][place], abort,
                                   a.status);

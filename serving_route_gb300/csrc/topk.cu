@@ -13,8 +13,8 @@
 // slots without an expert get id -1 and weight 0, which the layer skips.
 //
 // Every lane holds E / 32 choice values in registers as integers of the same
-// order (0: masked or taken), so a choice is two warp-wide integer reductions
-// (the largest value, then the lowest index that has it).  Bytes: the logits
+// order (0: masked or taken), so a choice is a warp-wide integer maximum and
+// ballots, row by row, for the lowest index that has it.  Bytes: the logits
 // once, 8 per chosen expert; for few tokens the chain of top_k choices bounds
 // it, for many the instructions issued.
 #include "common.cuh"
@@ -83,16 +83,11 @@ __global__ void __launch_bounds__(128) topk_route_kernel(const TopkArgs a) {
 
   if (a.groups > 1) {
     const int gs = a.E / a.groups;
+    // whole rows of 32 to a group: a value's group is that of its row
+    const bool by_row = (gs & 31) == 0;
     uint32_t mine = 0u;  // lane g: group g's score
-    for (int g = 0; g < a.groups; ++g) {
-      uint32_t m1 = 0u, m2 = 0u;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = 32 * i + lane;
-        const uint32_t k = (e >= g * gs && e < (g + 1) * gs) ? key[i] : 0u;
-        m2 = max(m2, min(m1, k));
-        m1 = max(m1, k);
-      }
+    uint32_t m1 = 0u, m2 = 0u;
+    auto group_done = [&](int g) {
       const uint32_t b1 = __reduce_max_sync(kAll, m1);
       uint32_t score = b1;
       if (SIGMOID && b1) {
@@ -101,6 +96,33 @@ __global__ void __launch_bounds__(128) topk_route_kernel(const TopkArgs a) {
         score = order_key(key_value(b1) + (b2 ? key_value(b2) : 0.f));
       }
       if (lane == g) mine = score;
+      m1 = m2 = 0u;
+    };
+    if (by_row) {
+      int g = 0, left = gs;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (32 * i < a.E) {
+          m2 = max(m2, min(m1, key[i]));
+          m1 = max(m1, key[i]);
+          left -= 32;
+          if (left == 0) {
+            group_done(g++);
+            left = gs;
+          }
+        }
+      }
+    } else {
+      for (int g = 0; g < a.groups; ++g) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = 32 * i + lane;
+          const uint32_t k = (e >= g * gs && e < (g + 1) * gs) ? key[i] : 0u;
+          m2 = max(m2, min(m1, k));
+          m1 = max(m1, k);
+        }
+        group_done(g);
+      }
     }
     uint32_t keep = 0u;
     for (int n = 0; n < a.top_groups; ++n) {
@@ -110,9 +132,21 @@ __global__ void __launch_bounds__(128) topk_route_kernel(const TopkArgs a) {
       keep |= 1u << g;
       if (lane == g) mine = 0u;
     }
+    if (by_row) {
+      int g = 0, left = gs;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (!((keep >> ((32 * i + lane) / gs & 31)) & 1u)) key[i] = 0u;
+      for (int i = 0; i < V; ++i) {
+        if (!((keep >> g) & 1u)) key[i] = 0u;
+        if ((left -= 32) == 0) {
+          ++g;
+          left = gs;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (!((keep >> ((32 * i + lane) / gs & 31)) & 1u)) key[i] = 0u;
+    }
   }
 
   int my = -1;  // lane k: the k-th choice
@@ -122,15 +156,20 @@ __global__ void __launch_bounds__(128) topk_route_kernel(const TopkArgs a) {
     for (int i = 0; i < V; ++i) m = max(m, key[i]);
     const uint32_t b = __reduce_max_sync(kAll, m);
     if (b == 0u) break;
-    uint32_t at = 0xFFFFFFFFu;
+    // the first row that holds it, and there the first lane
+    int at = -1;
 #pragma unroll
-    for (int i = V - 1; i >= 0; --i)
-      if (key[i] == b) at = 32 * i + lane;
-    at = __reduce_min_sync(kAll, at);
-    if (lane == k) my = (int)at;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (at == 32 * i + lane) key[i] = 0u;
+    for (int i = 0; i < V; ++i) {
+      if (at < 0) {
+        const uint32_t who = __ballot_sync(kAll, key[i] == b);
+        if (who) {
+          const int first = __ffs(who) - 1;
+          at = 32 * i + first;
+          if (lane == first) key[i] = 0u;
+        }
+      }
+    }
+    if (lane == k) my = at;
   }
 
   float p = 0.f;

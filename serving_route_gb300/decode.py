@@ -18,17 +18,17 @@ _Q_FORMATS = {"deepseek": 0, "mxfp8": B.MOE_FLAG_MXFP8, "per_tensor": B.MOE_FLAG
 _Q_BLOCK = {"deepseek": 128, "mxfp8": 32}
 
 
-def _dense(t: torch.Tensor, dtype, shape) -> bool:
-    return t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()
+_BF16, _F32, _U8, _I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
 
 
-def _rows_ok(t: torch.Tensor, cols: int) -> bool:
-    return t.is_cuda and t.dim() == 2 and t.shape[1] == cols and (cols == 1 or t.stride(1) == 1)
+def _stream(stream, like: torch.Tensor) -> int:
+    # the raw handle of the current stream, without making a Stream object of it
+    return torch._C._cuda_getCurrentRawStream(like.get_device()) if stream is None else stream.cuda_stream
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    # the stride of a single row says nothing
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+# The checks below are written out, not shared: at a few microseconds a call
+# the calls of helper functions are a good part of these operators' time for
+# one token.
 
 
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
@@ -43,31 +43,52 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
     or None, q uint8 E4M3 codes [T, H] or None, q_scale uint8 E8M0 bytes
     [T, H/128 or H/32] or None.  out: such a tuple of buffers to write
     (y may be x, r may be residual; y may be None where q is wanted)."""
-    assert x.dim() == 2 and x.dtype is torch.bfloat16
-    T, H = x.shape
-    assert _rows_ok(x, H) and _dense(weight, torch.bfloat16, (H,))
-    assert residual is None or (residual.dtype is torch.bfloat16 and residual.shape[0] == T
-                                and _rows_ok(residual, H))
-    assert fmt is None or fmt in _Q_FORMATS
-    block = _Q_BLOCK.get(fmt)
-    if block and H % block:  # the library's refusal, before a scale buffer of a wrong shape is made
-        raise B.MoEError(B.MOE_ERR_UNSUPPORTED, "moe_add_rms_norm")
+    shape = x.shape
+    T, H = shape
+    ldx, one = x.stride()
+    assert x.dtype is _BF16 and x.is_cuda and (one == 1 or H == 1)
+    assert weight.dtype is _BF16 and weight.is_cuda and weight.shape == (H,) and weight.is_contiguous()
+    if T <= 1:  # the stride of a single row says nothing
+        ldx = H
+    res = ldr = 0
+    if residual is not None:
+        ldr, one = residual.stride()
+        assert residual.dtype is _BF16 and residual.is_cuda and residual.shape == shape
+        assert one == 1 or H == 1
+        res = residual.data_ptr()
+        if T <= 1:
+            ldr = H
+    block = 0
+    if fmt is not None:
+        assert fmt in _Q_FORMATS
+        block = _Q_BLOCK.get(fmt, 0)
+        if block and H % block:  # the library's refusal, before a scale buffer of a wrong shape is made
+            raise B.MoEError(B.MOE_ERR_UNSUPPORTED, "moe_add_rms_norm")
     if out is None:
-        y = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+        y = torch.empty(T, H, dtype=_BF16, device=x.device)
         r = torch.empty_like(y) if residual is not None else None
-        q = torch.empty(T, H, dtype=torch.uint8, device=x.device) if fmt else None
-        s = torch.empty(T, H // block, dtype=torch.uint8, device=x.device) if block else None
+        q = torch.empty(T, H, dtype=_U8, device=x.device) if fmt else None
+        s = torch.empty(T, H // block, dtype=_U8, device=x.device) if block else None
+        out = y, r, q, s
     else:
         y, r, q, s = out
-        assert y is None or _dense(y, torch.bfloat16, (T, H))
-        assert (r is None) == (residual is None) and (r is None or _dense(r, torch.bfloat16, (T, H)))
-        assert (q is None) == (fmt is None) and (q is None or _dense(q, torch.uint8, (T, H)))
-        assert (s is None) == (block is None) and (s is None or _dense(s, torch.uint8, (T, H // block)))
-    B.moe_add_rms_norm(x.data_ptr(), _row_stride(x), residual.data_ptr() if residual is not None else None,
-                       _row_stride(residual) if residual is not None else 0, weight.data_ptr(), eps, T, H,
-                       r.data_ptr() if r is not None else None, y.data_ptr() if y is not None else None,
-                       q.data_ptr() if q is not None else None, s.data_ptr() if s is not None else None,
-                       _Q_FORMATS[fmt] if fmt else 0, scale, _stream_ptr(stream))
+        assert y is None or (y.dtype is _BF16 and y.is_cuda and y.shape == shape and y.is_contiguous())
+        if residual is None:
+            assert r is None
+        else:
+            assert r.dtype is _BF16 and r.is_cuda and r.shape == shape and r.is_contiguous()
+        if fmt is None:
+            assert q is None and s is None
+        else:
+            assert q.dtype is _U8 and q.is_cuda and q.shape == shape and q.is_contiguous()
+            if block:
+                assert s.dtype is _U8 and s.is_cuda and s.shape == (T, H // block) and s.is_contiguous()
+            else:
+                assert s is None
+    B.moe_add_rms_norm(x.data_ptr(), ldx, res, ldr, weight.data_ptr(), eps, T, H,
+                       0 if r is None else r.data_ptr(), 0 if y is None else y.data_ptr(),
+                       0 if q is None else q.data_ptr(), 0 if s is None else s.data_ptr(),
+                       _Q_FORMATS[fmt] if fmt is not None else 0, scale, _stream(stream, x))
     return y, r, q, s
 
 
@@ -81,21 +102,28 @@ def topk_route(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
     The choice is limited to the top_groups best of num_groups equal groups (a
     group's score: its largest logit, or the sum of its two largest biased
     scores).  Logits of -inf mask an expert; slots left over get id -1."""
-    assert logits.dim() == 2 and logits.dtype in (torch.float32, torch.bfloat16)
-    assert scoring in ("softmax", "sigmoid")
     T, E = logits.shape
-    assert _rows_ok(logits, E) and (bias is None or _dense(bias, torch.float32, (E,)))
+    ld, one = logits.stride()
+    bf16 = logits.dtype is _BF16
+    assert (bf16 or logits.dtype is _F32) and logits.is_cuda and (one == 1 or E == 1)
+    assert scoring == "softmax" or scoring == "sigmoid"
+    assert bias is None or (bias.dtype is _F32 and bias.is_cuda and bias.shape == (E,) and bias.is_contiguous())
     if out is None:
-        idx = torch.empty(T, top_k, dtype=torch.int32, device=logits.device)
-        w = torch.empty(T, top_k, dtype=torch.float32, device=logits.device)
+        idx = torch.empty(T, top_k, dtype=_I32, device=logits.device)
+        w = torch.empty(T, top_k, dtype=_F32, device=logits.device)
     else:
         idx, w = out
-        assert _dense(idx, torch.int32, (T, top_k)) and _dense(w, torch.float32, (T, top_k))
-    B.moe_topk_route(logits.data_ptr(), logits.dtype is torch.bfloat16, _row_stride(logits),
-                     bias.data_ptr() if bias is not None else None, T, E, top_k, scoring == "sigmoid",
-                     num_groups, top_groups, renormalize, scale, idx.data_ptr(), w.data_ptr(),
-                     _stream_ptr(stream))
+        shape = (T, top_k)
+        assert idx.dtype is _I32 and idx.is_cuda and idx.shape == shape and idx.is_contiguous()
+        assert w.dtype is _F32 and w.is_cuda and w.shape == shape and w.is_contiguous()
+    B.moe_topk_route(logits.data_ptr(), bf16, E if T <= 1 else ld, 0 if bias is None else bias.data_ptr(), T, E,
+                     top_k, scoring == "sigmoid", num_groups, top_groups, renormalize, scale, idx.data_ptr(),
+                     w.data_ptr(), _stream(stream, logits))
     return idx, w
+
+
+def _dense(t: torch.Tensor, dtype, shape) -> bool:
+    return t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()
 
 
 class _Fp4Handle:
@@ -143,15 +171,16 @@ class Fp4Linear(_Fp4Handle):
                 out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
         """x BF16 [T, cols] (rows may be strided by a multiple of 8) -> [T, rows] in
         out_dtype (bfloat16 or float32) or in `out`'s type."""
-        assert x.dtype is torch.bfloat16 and _rows_ok(x, self.cols)
-        T = x.shape[0]
+        T, cols = x.shape
+        ldx, one = x.stride()
+        assert x.dtype is _BF16 and x.is_cuda and cols == self.cols and one == 1
         if out is None:
-            assert out_dtype in (torch.bfloat16, torch.float32)
+            assert out_dtype is _BF16 or out_dtype is _F32
             out = torch.empty(T, self.rows, dtype=out_dtype, device=x.device)
-        else:
-            assert out.dtype in (torch.bfloat16, torch.float32) and _dense(out, out.dtype, (T, self.rows))
-        B.moe_fp4_linear(self.handle, x.data_ptr(), _row_stride(x), T, out.data_ptr(),
-                         out.dtype is torch.float32, _stream_ptr(stream))
+        f32 = out.dtype is _F32
+        assert (f32 or out.dtype is _BF16) and out.is_cuda and out.shape == (T, self.rows) and out.is_contiguous()
+        B.moe_fp4_linear(self.handle, x.data_ptr(), cols if T <= 1 else ldx, T, out.data_ptr(), f32,
+                         _stream(stream, x))
         return out
 
 
@@ -188,13 +217,15 @@ class Fp4MoELayer(_Fp4Handle):
         """x BF16 [T, H], topk_idx int32 [T, K] (-1: masked slot), topk_w float32 [T, K] -> BF16 [T, H]."""
         if self.handle is None:
             raise B.MoEError(B.MOE_ERR_NOT_BOUND, "moe_fp4_forward")
-        T = x.shape[0]
-        assert _dense(x, torch.bfloat16, (T, self.H))
-        assert _dense(topk_idx, torch.int32, (T, self.K)) and _dense(topk_w, torch.float32, (T, self.K))
+        shape, routes = x.shape, topk_idx.shape
+        T, H = shape
+        assert x.dtype is _BF16 and x.is_cuda and H == self.H and x.is_contiguous()
+        assert topk_idx.dtype is _I32 and topk_idx.is_cuda and routes == (T, self.K) and topk_idx.is_contiguous()
+        assert topk_w.dtype is _F32 and topk_w.is_cuda and topk_w.shape == routes and topk_w.is_contiguous()
         if out is None:
-            out = torch.empty(T, self.H, dtype=torch.bfloat16, device=x.device)
+            out = torch.empty(T, H, dtype=_BF16, device=x.device)
         else:
-            assert _dense(out, torch.bfloat16, (T, self.H))
+            assert out.dtype is _BF16 and out.is_cuda and out.shape == shape and out.is_contiguous()
         B.moe_fp4_forward(self.handle, x.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), T,
-                          out.data_ptr(), _stream_ptr(stream))
+                          out.data_ptr(), _stream(stream, x))
         return out
