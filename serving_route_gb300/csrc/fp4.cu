@@ -107,35 +107,6 @@ __host__ __device__ inline int row_bytes(int cols, bool h) {
   return ((padded_units(cols) * kUnitCols * 2 + (h ? exponent_bytes(cols) : 0) + 127) & ~127) + 64;
 }
 
-// Codes as TMA tensors.  unit: 128-byte (256-column) blocks of the rows, a box is
-// a unit's 32 rows x 2 blocks, block-major ({128 B, row, block}; FC1: {128 B, row
-// of the half, gate or up, block, expert}).  box: the rows as they are, a box is
-// 16 rows x 128 B.  128-byte swizzle; what lies past an extent reads as zero.
-struct Fp4Maps {
-  CUtensorMap unit[2], box[2];
-};
-
-struct Fp4Shared {
-  uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t bfull[2][kItems], bempty[2][kItems];
-  uint64_t raw[kLoaders], go;
-  alignas(16) float out[kFp4MaxTokens][kTile2];
-  alignas(16) int key[kFp4MaxRoutes];
-  float rscale[2][kFp4MaxRoutes];       // per operand row: 2^-s
-  float vglobal[2][kFp4MaxRoutes];      // the items' matrix scales
-  float route_w[kFp4MaxRoutes];         // by sorted position, as the next ones
-  int16_t route_e[kFp4MaxRoutes], route_id[kFp4MaxRoutes], route_tok[kFp4MaxRoutes];
-  int16_t vstart[kFp4MaxRoutes + 1];    // first sorted position of every item
-  int16_t vexp[kFp4MaxRoutes];
-  uint8_t first[kFp4MaxRoutes];
-  uint32_t row_max[kFp4MaxTokens];
-  int warp_cnt[4];
-  int issued[kProducers];               // units each producer has begun
-  int done[kConsumers], taken[kConsumers];  // sums each consumer has left, and that were taken
-  int nv, nroutes;
-  int abort;
-};
-
 // Where a walk over a phase stands: segment seg = the U units of item v's
 // product with 32 matrix rows: block rb of tile j.
 struct SegPos {
@@ -147,6 +118,14 @@ struct SegPos {
 // second       tile (128 rows), item, block of 32 rows -- an item's rows serve four segments.
 struct Phase {
   int p, U, RT, nv, u0, u1, cols;
+  // the CTAs' shares: steps of `stride` units, `base` or (the first `extra` CTAs)
+  // one more of them
+  int stride, base, extra;
+  // the CTA that holds unit u
+  __device__ int cta_of(int u) const {
+    const int s = u / stride, big = extra * (base + 1);
+    return s < big ? s / (base + 1) : extra + (s - big) / base;
+  }
   __device__ int seg_begin() const { return u0 / U; }
   __device__ SegPos at(int seg) const {
     SegPos s;
@@ -179,19 +158,44 @@ struct Phase {
   __device__ int tile_units() const { return p == 0 ? U : nv * 4 * U; }
 };
 
+// Codes as TMA tensors.  unit: 128-byte (256-column) blocks of the rows, a box is
+// a unit's 32 rows x 2 blocks, block-major ({128 B, row, block}; FC1: {128 B, row
+// of the half, gate or up, block, expert}).  box: the rows as they are, a box is
+// 16 rows x 128 B.  128-byte swizzle; what lies past an extent reads as zero.
+struct Fp4Maps {
+  CUtensorMap unit[2], box[2];
+};
+
+struct Fp4Shared {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t bfull[2][kItems], bempty[2][kItems];
+  uint64_t raw[kLoaders], go;
+  alignas(16) float out[kFp4MaxTokens][kTile2];
+  alignas(16) int key[kFp4MaxRoutes];
+  float rscale[2][kFp4MaxRoutes];       // per operand row: 2^-s
+  float vglobal[2][kFp4MaxRoutes];      // the items' matrix scales
+  float route_w[kFp4MaxRoutes];         // by sorted position, as the next ones
+  int16_t route_e[kFp4MaxRoutes], route_id[kFp4MaxRoutes], route_tok[kFp4MaxRoutes];
+  int16_t vstart[kFp4MaxRoutes + 1];    // first sorted position of every item
+  int16_t vexp[kFp4MaxRoutes];
+  uint8_t first[kFp4MaxRoutes];
+  uint32_t row_max[kFp4MaxTokens];
+  int warp_cnt[4];
+  Phase phase[2];
+  int issued[kProducers];               // units each producer has begun
+  int done[kConsumers], taken[kConsumers];  // sums each consumer has left, and that were taken
+  int nv, nroutes;
+  int abort;
+};
+
 template <bool MOE, int NT>
 struct Fp4Ctx {
   const Fp4Args& a;
   Fp4Shared& sm;
   int nv;
 
-  __device__ int64_t total_units(int p) const {
-    return (int64_t)nv * ((a.m[p].rows + 31) / 32) * padded_units(a.m[p].cols);
-  }
-  // CTAs with work: none of them without a unit, so that a cut tile's CTAs are consecutive
-  __device__ static int64_t ctas(int64_t n) { return min(n, (int64_t)gridDim.x); }
-
-  __device__ Phase phase(int p) const {
+  // (units: at most 2^28, the linear's)
+  __device__ Phase make_phase(int p) const {
     Phase f;
     f.p = p;
     f.cols = a.m[p].cols;
@@ -200,14 +204,17 @@ struct Fp4Ctx {
     f.nv = nv;
     // whole tiles, unless the CTA with one more than the others would work
     // longer than a join takes
-    const int64_t n = total_units(p), tu = f.tile_units(), tiles = n / tu;
-    const int64_t most = (tiles + gridDim.x - 1) / gridDim.x * tu;
-    const int64_t G = ctas(n), step = most - (n + G - 1) / G > kCutUnits ? 1 : tu;
-    const int64_t steps = n / step, H = min(steps, G);
-    f.u0 = (int)(steps * min((int64_t)blockIdx.x, H) / H * step);
-    f.u1 = (int)(steps * min((int64_t)blockIdx.x + 1, H) / H * step);
+    const int G = gridDim.x, n = nv * f.RT * f.U, tu = f.tile_units(), most = (n / tu + G - 1) / G * tu;
+    f.stride = most - (n + G - 1) / G > kCutUnits ? 1 : tu;
+    const int steps = n / f.stride;
+    f.base = steps / G;
+    f.extra = steps - f.base * G;
+    const int b = blockIdx.x;
+    f.u0 = (b * f.base + min(b, f.extra)) * f.stride;
+    f.u1 = f.u0 + (f.base + (b < f.extra)) * f.stride;
     return f;
   }
+  __device__ const Phase& phase(int p) const { return sm.phase[p]; }
 
   __device__ int item_rows(int v) const { return sm.vstart[v + 1] - sm.vstart[v]; }
   // x rows stay for the whole phase where all of them fit; h rows always pass
@@ -257,6 +264,8 @@ struct ItemWalk {
   }
 };
 
+// Four E2M1 pairs (one 32-bit word, low nibble first) times one half of the scale pair s.
+template <int HI>
 __device__ __forceinline__ void e2m1x8_scaled(uint32_t w, uint32_t s, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "mov.b32 {a, b, c, d}, %4;\n\t"
@@ -266,9 +275,12 @@ __device__ __forceinline__ void e2m1x8_scaled(uint32_t w, uint32_t s, uint32_t (
       "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
+  const __half2 sp = *reinterpret_cast<const __half2*>(&s), sd = HI ? __high2half2(sp) : __low2half2(sp);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(h[i]), "r"(s));
+  for (int i = 0; i < 4; ++i) {
+    const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), sd);
+    h[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
 }
 
 // Two E4M3 codes to half2.
@@ -516,21 +528,33 @@ __device__ __forceinline__ bool fill_x_rows(int T, int cols, uint32_t rows, int 
                                             volatile int* abort, uint32_t* status) {
   const int lane = threadIdx.x & 31, n = cols >> 3, U = padded_units(cols);
   const bool ok = warp_wait(bar, 0, abort, status);
-  for (int i = rank; i < T * U; i += warps) {
-    const int t = i / U, u = i - t * U;
-    uint4 v[2];
-    load_pieces(rows + t * pitch, u, n, v);
+  // (two units at a time)
+  for (int i = rank; i < T * U; i += 2 * warps) {
+    const int t0 = i / U, j = i + warps, t1 = j / U;
+    uint4 v[2], w[2];
+    load_pieces(rows + t0 * pitch, i - t0 * U, n, v);
+    if (j < T * U) load_pieces(rows + t1 * pitch, j - t1 * U, n, w);
     const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max_bf16x8(v[1], max_bf16x8(v[0], 0u)));
-    if (lane == 0) atomicMax(&row_max[t], m);
+    if (lane == 0) atomicMax(&row_max[t0], m);
+    if (j < T * U) {
+      const uint32_t m1 = __reduce_max_sync(0xFFFFFFFFu, max_bf16x8(w[1], max_bf16x8(w[0], 0u)));
+      if (lane == 0) atomicMax(&row_max[t1], m1);
+    }
   }
   asm volatile("bar.sync 1, %0;" ::"r"(32 * warps) : "memory");
-  for (int i = rank; i < T * U; i += warps) {
-    const int t = i / U, u = i - t * U;
-    uint4 v[2];
-    load_pieces(rows + t * pitch, u, n, v);
-    const int s = row_exponent(__uint_as_float(row_max[t] << 16));
-    if (u == 0 && lane == 0) rscale[t] = pow2f(-s);
-    turn_unit(rows + t * pitch, u, v, pow2f(s));
+  for (int i = rank; i < T * U; i += 2 * warps) {
+    const int t0 = i / U, u0 = i - t0 * U, j = i + warps, t1 = j / U, u1 = j - t1 * U;
+    uint4 v[2], w[2];
+    load_pieces(rows + t0 * pitch, u0, n, v);
+    if (j < T * U) load_pieces(rows + t1 * pitch, u1, n, w);
+    const int s0 = row_exponent(__uint_as_float(row_max[t0] << 16));
+    if (u0 == 0 && lane == 0) rscale[t0] = pow2f(-s0);
+    turn_unit(rows + t0 * pitch, u0, v, pow2f(s0));
+    if (j < T * U) {
+      const int s1 = row_exponent(__uint_as_float(row_max[t1] << 16));
+      if (u1 == 0 && lane == 0) rscale[t1] = pow2f(-s1);
+      turn_unit(rows + t1 * pitch, u1, w, pow2f(s1));
+    }
   }
   asm volatile("bar.sync 1, %0;" ::"r"(32 * warps) : "memory");
   return ok;
@@ -745,6 +769,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
 
   using Ctx = Fp4Ctx<MOE, NT>;
   const Ctx c{a, sm, sm.nv};
+  if (c.nv > 0 && lane == 0 && warp_id < (MOE ? 2 : 1)) sm.phase[warp_id] = c.make_phase(warp_id);
   constexpr int kPhases = MOE ? 2 : 1;
   volatile int* abort = &sm.abort;
 
@@ -758,6 +783,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     if (early && warp_id == kWarpLoader) mbar_wait(smem_u32(&sm.raw[0]), 0, abort, a.status);
     return;
   }
+
+  __syncthreads();  // the phases
 
   // rows that stay: the loaders and the consumers, who have nothing to do yet,
   // turn them together
@@ -775,7 +802,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     int n0 = 0;     // the CTA's units before this segment: its n-th unit is warp n mod 8's
     auto consume = [&](auto phase_constant) {
       constexpr int p = decltype(phase_constant)::value;
-      const Phase f = c.phase(p);
+      const Phase& f = c.phase(p);
       if (f.u0 >= f.u1) return true;
       const int RB = row_bytes(f.cols, p == 1);
       const bool res = p == 0 && c.resident(0);
@@ -860,12 +887,14 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
 #pragma unroll
                   for (int m = 0; m < 2; ++m) {
                     uint32_t lo[4], hi[4];
-                    const uint32_t sel = i < 2 ? 0x1010u : 0x3232u;
                     const uint4 wl = cw[jj][m][0], wh = cw[jj][m][1];
-                    e2m1x8_scaled(i == 0 ? wl.x : i == 1 ? wl.y : i == 2 ? wl.z : wl.w,
-                                  __byte_perm(sw[m][0], 0u, sel), lo);
-                    e2m1x8_scaled(i == 0 ? wh.x : i == 1 ? wh.y : i == 2 ? wh.z : wh.w,
-                                  __byte_perm(sw[m][1], 0u, sel), hi);
+                    if (i < 2) {
+                      e2m1x8_scaled<0>(i == 0 ? wl.x : wl.y, sw[m][0], lo);
+                      e2m1x8_scaled<0>(i == 0 ? wh.x : wh.y, sw[m][1], hi);
+                    } else {
+                      e2m1x8_scaled<1>(i == 2 ? wl.z : wl.w, sw[m][0], lo);
+                      e2m1x8_scaled<1>(i == 2 ? wh.z : wh.w, sw[m][1], hi);
+                    }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                       mma_16816(acc[m][nt][0], lo[0], hi[0], lo[1], hi[1], b[nt].x, b[nt].y);
@@ -911,7 +940,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     // the first operand rows go ahead of the weights
     bool ok = warp_wait(sm.go, 0, abort, a.status);
     for (int p = 0; p < kPhases && ok; ++p) {
-      const Phase f = c.phase(p);
+      const Phase& f = c.phase(p);
       if (f.u0 >= f.u1) continue;
       const Fp4Matrix& m = a.m[p];
       const int cols = f.cols, ng = cols >> 4, blocks = (cols + 255) >> 8;
@@ -1004,8 +1033,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       for (int p = 0; p < kPhases; ++p) sm.vglobal[p][v] = __ldg(&a.m[p].global[sm.vexp[v]]);
     __syncwarp();
     for (int p = 0; p < kPhases; ++p) {
-      const Phase f = c.phase(p);
-      const int64_t total = c.total_units(p);
+      const Phase& f = c.phase(p);
       const bool res = c.resident(p);
       const int R = c.ring_rows(p);
       const int tu = f.tile_units();
@@ -1086,7 +1114,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             }
         }
         const int tile = p == 0 ? seg : at.j;
-        const int64_t tb = (int64_t)tile * tu, te = tb + tu;  // the tile's units
+        const int tb = tile * tu, te = tb + tu;  // the tile's units
         if (p == 1) {
           // out[token][row] over the tile's experts
           if (fresh) {
@@ -1105,7 +1133,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             }
           __syncwarp();
           fresh = false;
-          if (ub < min((int64_t)f.u1, te)) continue;  // more of this tile to come
+          if (ub < min(f.u1, te)) continue;  // more of this tile to come
           fresh = true;
         } else {
 #pragma unroll
@@ -1121,8 +1149,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         const bool whole = tb >= f.u0 && te <= f.u1;
         if (!whole) {
           // join: this CTA's share goes to its slot; whoever arrives last adds the shares in CTA order
-          const int64_t G = Ctx::ctas(total);
-          const int c0 = (int)(((tb + 1) * G - 1) / total), c1 = (int)((te * G - 1) / total);
+          const int c0 = f.cta_of(tb), c1 = f.cta_of(te - 1);
           constexpr int kSlot0 = 512, kSlot1 = kFp4MaxTokens * kTile2;
           auto share = [&](int cta) {
             return a.part[p] + (size_t)(2 * cta + (cta == c0)) * (p == 0 ? kSlot0 : kSlot1);
@@ -1241,7 +1268,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     uint32_t raw_parity = early && lw == 0;
     bool went = early;  // whether the producers need not wait for this warp's first copy
     for (int p = 0; p < kPhases; ++p) {
-      const Phase f = c.phase(p);
+      const Phase& f = c.phase(p);
       if (MOE && p == 1) {
         bool ok = true;
         if (lane == 0) {
