@@ -107,15 +107,19 @@ __host__ __device__ inline int row_bytes(int cols, bool h) {
   return ((padded_units(cols) * kUnitCols * 2 + (h ? exponent_bytes(cols) : 0) + 127) & ~127) + 64;
 }
 
-// Where a walk over a phase stands: segment seg = the U units of item v's
-// product with 32 matrix rows: block rb of tile j.
-struct SegPos {
-  int v, j, rb;
+// Where a walk over a phase stands: item v's product with the rows of tile j.
+struct TilePos {
+  int v, j;
 };
 
-// One phase of one CTA: units [u0, u1), U to a segment.  Order of the segments:
-// first phase  item, tile (RT of 32 rows each);
-// second       tile (128 rows), item, block of 32 rows -- an item's rows serve four segments.
+// One phase of one CTA: units [u0, u1) in the order
+//   first phase   item, tile: a tile is 32 matrix rows, U units of 512 columns;
+//                 the CTA's n-th unit is warp n mod 8's.
+//   second phase  tile, item: a tile is 128 rows, an item's share of it four
+//                 blocks of 32 rows of U units.  Warp w has one half of block
+//                 w / 2's units, so that few sums are to be added (I / 512 units
+//                 are few), and the i-th units of the eight warps follow each
+//                 other, so that none holds a place of the ring for long.
 struct Phase {
   int p, U, RT, nv, u0, u1, cols;
   // the CTAs' shares: steps of `stride` units, `base` or (the first `extra` CTAs)
@@ -126,34 +130,27 @@ struct Phase {
     const int s = u / stride, big = extra * (base + 1);
     return s < big ? s / (base + 1) : extra + (s - big) / base;
   }
-  __device__ int seg_begin() const { return u0 / U; }
-  __device__ SegPos at(int seg) const {
-    SegPos s;
-    if (p == 0) {
-      s.v = seg / RT;
-      s.j = seg - s.v * RT;
-      s.rb = 0;
-    } else {
-      s.j = seg / (nv * 4);
-      const int r = seg - s.j * nv * 4;
-      s.v = r >> 2;
-      s.rb = r & 3;
-    }
-    return s;
+  __device__ int visit() const { return p == 0 ? U : 4 * U; }  // units of an item at a tile
+  __device__ TilePos at(int u) const {
+    const int i = u / visit(), inner = p == 0 ? RT : nv, o = i / inner;
+    return p == 0 ? TilePos{o, i - o * inner} : TilePos{i - o * inner, o};
   }
-  __device__ void step(SegPos& s) const {
+  __device__ void step(TilePos& s) const {
     if (p == 0) {
       if (++s.j == RT) {
         s.j = 0;
         ++s.v;
       }
-    } else if (++s.rb == 4) {
-      s.rb = 0;
-      if (++s.v == nv) {
-        s.v = 0;
-        ++s.j;
-      }
+    } else if (++s.v == nv) {
+      s.v = 0;
+      ++s.j;
     }
+  }
+  // second phase: the i-th unit in order is warp w's with columns from 512 k
+  __device__ void unit_of(int i, int& w, int& k) const {
+    const int full = U >> 1, r = i >> 3;  // rounds in which all eight warps have a unit
+    w = r < full ? i & 7 : 2 * (i - 8 * full);
+    k = (w & 1) * (U - full) + (r < full ? r : full);
   }
   __device__ int tile_units() const { return p == 0 ? U : nv * 4 * U; }
 };
@@ -205,7 +202,7 @@ struct Fp4Ctx {
     // whole tiles, unless the CTA with one more than the others would work
     // longer than a join takes
     const int G = gridDim.x, n = nv * f.RT * f.U, tu = f.tile_units(), most = (n / tu + G - 1) / G * tu;
-    f.stride = most - (n + G - 1) / G > kCutUnits ? 1 : tu;
+    f.stride = most - (n + G - 1) / G <= kCutUnits ? tu : p == 0 ? 1 : f.visit();
     const int steps = n / f.stride;
     f.base = steps / G;
     f.extra = steps - f.base * G;
@@ -230,24 +227,24 @@ struct Fp4Ctx {
     if (resident) return sm.route_tok[s0 + col];
     return pos + col < R ? pos + col : pos + col - R;
   }
-  // matrix row of row r (0..31) of a segment
-  __device__ int64_t matrix_row(int p, const SegPos& s, int r) const {
+  // matrix row of row r of a tile (0..31, second phase 0..127)
+  __device__ int64_t matrix_row(int p, const TilePos& s, int r) const {
     if (!MOE) return 32 * (int64_t)s.j + r;
     const int64_t base = (int64_t)sm.vexp[s.v] * a.m[p].rows;
     if (p == 0)  // 16 gate rows, then their 16 up rows
       return base + (r < 16 ? 16 * s.j + r : a.m[0].rows / 2 + 16 * s.j + r - 16);
-    return base + kTile2 * s.j + 32 * s.rb + r;
+    return base + kTile2 * s.j + r;
   }
 };
 
 // Walks the operand items of a phase in segment order.  Resident: all rows stay
 // for the phase and there is one item.  Ring: an item is the rows of one token
-// group, for one run of segments, at consecutive ring places.
+// group, for its tiles in a row (first phase) or for one tile, at consecutive ring places.
 struct ItemWalk {
   int item = -1, v = -1, j = -1, pos = 0, rows = 0;
-  // whether a new item starts with segment s
+  // whether a new item starts at s
   template <class Ctx>
-  __device__ bool next(const Ctx& c, const Phase& f, bool resident, int R, const SegPos& s) {
+  __device__ bool next(const Ctx& c, const Phase& f, bool resident, int R, const TilePos& s) {
     if (resident) {
       const bool fresh = item < 0;
       item = 0;
@@ -808,11 +805,11 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       const bool res = p == 0 && c.resident(0);
       const int R = c.ring_rows(p);
       ItemWalk it;
-      int seg = f.seg_begin(), ka = f.u0 - seg * f.U;
-      const int segs = (f.u1 - 1) / f.U + 1, k_last = f.u1 - (segs - 1) * f.U;
-      SegPos at = f.at(seg);
-      for (; seg < segs; ++seg, f.step(at)) {
-        const int kb = seg == segs - 1 ? k_last : f.U;
+      const int visit = f.visit();
+      TilePos at = f.at(f.u0);
+      int ka = f.u0 % visit;  // first unit of the visit (second phase: 0)
+      for (int u = f.u0 - ka; u < f.u1; u += visit, f.step(at)) {
+        const int kb = min(visit, f.u1 - u);
         const int last_item = it.item;
         if (it.next(c, f, res, R, at)) {
           if (last_item >= 0) {
@@ -822,8 +819,12 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
           if (!res && !warp_wait(sm.bfull[p][it.item % kItems], (it.item / kItems) & 1, abort, a.status))
             return false;
         }
-        const int first = ka + ((warp - n0) & (kConsumers - 1));  // this warp's first unit of the segment
-        if (first < kb) {
+        // this warp's units of the visit: columns from 512 k, k = first, first + dk, .. < last
+        const int full = f.U >> 1, half = warp & 1;
+        const int first = p == 0 ? ka + ((warp - n0) & (kConsumers - 1)) : half * (f.U - full);
+        const int last = p == 0 ? kb : half ? f.U : f.U - full;
+        constexpr int dk = p == 0 ? kConsumers : 1;
+        if (first < last) {
           // two sums per tile, so that consecutive MMAs do not wait for each other
           float acc[2][NT][2][4] = {};
           const int n = c.item_rows(at.v), s0 = sm.vstart[at.v];
@@ -834,8 +835,10 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             brow[nt] = smem + (brow0 - ring) + c.row_slot(res, it.pos, R, s0, col) * RB + t * 16;
           }
 #pragma unroll 1
-          for (int k = first; k < kb; k += kConsumers) {
-            const int nu = n0 + k - ka;  // the unit's count, which gives its place in the ring
+          for (int k = first; k < last; k += dk) {
+            // the unit's count, which gives its place in the ring
+            const int i = k - first;
+            const int nu = n0 + (p == 0 ? k - ka : i < full ? 8 * i + warp : 8 * full + (warp >> 1));
             const int lap = (int)__umulhi((uint32_t)nu, a.stage_rcp), slot = nu - lap * a.stages;
             // Only once the unit's copies have begun is the place in this lap's
             // phase, and the parity that of this lap
@@ -934,87 +937,105 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     // ------------------------------------------------------------ producers
     const uint64_t pass = policy_evict_first(), keep = policy_evict_normal();
     const int pw = warp_id - kWarpProducer;  // this one's units: every third, counted over both phases
-    int n0 = 0;                           // the CTA's count of the segment's first unit
     int slot = pw, mine = 0;
     uint32_t parity = 1;
-    // the first operand rows go ahead of the weights
-    bool ok = warp_wait(sm.go, 0, abort, a.status);
-    for (int p = 0; p < kPhases && ok; ++p) {
-      const Phase& f = c.phase(p);
-      if (f.u0 >= f.u1) continue;
+    // the copies of a unit: columns from 512 k of the 32 rows from `row` on (FC1: 16
+    // gate rows of `tile` and their up rows); lane_row: the lane's row.  False: gave up.
+    auto issue = [&](auto phase_constant, const Phase& f, int k, int row, int row16, int64_t lane_row,
+                     int tile, int expert, uint64_t policy) {
+      constexpr int p = decltype(phase_constant)::value;
+      if (!warp_wait(sm.empty[slot], parity, abort, a.status)) return false;
       const Fp4Matrix& m = a.m[p];
-      const int cols = f.cols, ng = cols >> 4, blocks = (cols + 255) >> 8;
-      // units that are one copy: all but one that ends within a 256-column block,
-      // past which lies the next row
-      const int one_copy = (cols & 255) == 0 ? f.U : (blocks - 1) >> 1;
-      const int full_scales = (ng & 15) == 0 ? ng >> 5 : 0;  // units with 32 scales in 16-byte copies
-      int seg = f.seg_begin(), ka = f.u0 - seg * f.U;
-      SegPos at = f.at(seg);
-      for (; seg * f.U < f.u1 && ok; ++seg, f.step(at)) {
-        const int kb = min(f.U, f.u1 - seg * f.U);
-        int k = ka + (pw + kProducers - n0 % kProducers) % kProducers;
-        n0 += kb - ka;
-        ka = 0;
-        if (k >= kb) continue;
-        const int64_t row = c.matrix_row(p, at, lane);
-        const bool in = MOE || row < m.rows;
-        const uint8_t* srow = m.scales + (in ? row * ng : 0);
-        const int r0 = __shfl_sync(0xFFFFFFFFu, (int)row, 0), r1 = __shfl_sync(0xFFFFFFFFu, (int)row, 16);
-        const int expert = sm.vexp[at.v];
-        // read again by the next item: the same matrix, more tokens
-        const uint64_t policy = at.v + 1 < c.nv && sm.vexp[at.v + 1] == expert ? keep : pass;
-        for (; k < kb; k += kProducers) {
-          if (!warp_wait(sm.empty[slot], parity, abort, a.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = smem_u32(&sm.full[slot]), dst = ring + slot * kCodeBytes;
-          if (lane == 0) {
-            store_count(&sm.issued[pw], ++mine);
-            if (k < one_copy) {
-              mbar_arrive_expect_tx(bar, kCodeBytes);
-              if (MOE && p == 0)
-                load_box_5d(dst, &maps.unit[0], bar, 0, 16 * at.j, 0, 2 * k, expert, policy);
-              else
-                load_box_3d(dst, &maps.unit[p], bar, 0, r0, 2 * k, policy);
-            } else {  // a copy per 16 rows x 256 columns, cut off at the row's end
-              mbar_arrive_expect_tx(bar, (blocks - 2 * k) * 2 * kBoxBytes);
-              for (int b = 0; b < blocks - 2 * k; ++b) {
-                load_box_2d(dst + 2 * b * kBoxBytes, &maps.box[p], bar, 128 * (2 * k + b), r0, policy);
-                load_box_2d(dst + (2 * b + 1) * kBoxBytes, &maps.box[p], bar, 128 * (2 * k + b), r1, policy);
-              }
-            }
-          }
-          __syncwarp();
-          {  // lane: the scales of its row
-            const uint8_t* src = srow + (in ? 32 * k : 0);
-            const int n = in ? min(32, ng - 32 * k) : 0;
-            const uint32_t to = srow0 + slot * kScaleBytes + lane * 32;
-            if (k < full_scales) {
-              cp_async<16>(to, src, in ? 16 : 0, policy);
-              cp_async<16>(to + 16, in ? src + 16 : src, in ? 16 : 0, policy);
-            } else if ((ng & 15) == 0)
-              copy_scale_row<16>(to, src, n, policy);
-            else if ((ng & 7) == 0)
-              copy_scale_row<8>(to, src, n, policy);
-            else if ((ng & 3) == 0)
-              copy_scale_row<4>(to, src, n, policy);
-            else {  // rows on odd multiples of two bytes: through registers
-              for (int o = 0; o < 32; o += 4) {
-                uint32_t x = 0u;
-                if (o < n) x = __ldg(reinterpret_cast<const uint16_t*>(src + o));
-                if (o + 2 < n) x |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src + o + 2)) << 16;
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + o), "r"(x) : "memory");
-              }
-            }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-          }
-          slot += kProducers;
-          if (slot >= a.stages) {
-            slot -= a.stages;
-            parity ^= 1;
+      const int ng = f.cols >> 4;
+      const uint32_t bar = smem_u32(&sm.full[slot]), dst = ring + slot * kCodeBytes;
+      if (lane == 0) {
+        store_count(&sm.issued[pw], ++mine);
+        // one copy, but for a unit that ends within a 256-column block, past which
+        // lies the next row: a copy per 16 rows x 256 columns, cut off at the row's end
+        const int blocks = (f.cols + 255) >> 8;
+        if ((f.cols & 255) == 0 || 2 * k + 2 < blocks) {
+          mbar_arrive_expect_tx(bar, kCodeBytes);
+          if (MOE && p == 0)
+            load_box_5d(dst, &maps.unit[0], bar, 0, 16 * tile, 0, 2 * k, expert, policy);
+          else
+            load_box_3d(dst, &maps.unit[p], bar, 0, row, 2 * k, policy);
+        } else {
+          mbar_arrive_expect_tx(bar, (blocks - 2 * k) * 2 * kBoxBytes);
+          for (int b = 0; b < blocks - 2 * k; ++b) {
+            load_box_2d(dst + 2 * b * kBoxBytes, &maps.box[p], bar, 128 * (2 * k + b), row, policy);
+            load_box_2d(dst + (2 * b + 1) * kBoxBytes, &maps.box[p], bar, 128 * (2 * k + b), row16, policy);
           }
         }
+      }
+      __syncwarp();
+      // lane: the scales of its row
+      const bool in = MOE || lane_row < m.rows;
+      const uint8_t* src = m.scales + (in ? lane_row * ng + 32 * k : 0);
+      const int n = in ? min(32, ng - 32 * k) : 0;
+      const uint32_t to = srow0 + slot * kScaleBytes + lane * 32;
+      if ((ng & 15) == 0) {
+        cp_async<16>(to, src, n > 0 ? 16 : 0, policy);
+        cp_async<16>(to + 16, n > 16 ? src + 16 : src, n > 16 ? 16 : 0, policy);
+      } else if ((ng & 7) == 0)
+        copy_scale_row<8>(to, src, n, policy);
+      else if ((ng & 3) == 0)
+        copy_scale_row<4>(to, src, n, policy);
+      else {  // rows on odd multiples of two bytes: through registers
+        for (int o = 0; o < 32; o += 4) {
+          uint32_t x = 0u;
+          if (o < n) x = __ldg(reinterpret_cast<const uint16_t*>(src + o));
+          if (o + 2 < n) x |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src + o + 2)) << 16;
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + o), "r"(x) : "memory");
+        }
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+      slot += kProducers;
+      if (slot >= a.stages) {
+        slot -= a.stages;
+        parity ^= 1;
+      }
+      return true;
+    };
+    // read again by the next item: the same matrix, more tokens
+    auto item_policy = [&](int v) {
+      return v + 1 < c.nv && sm.vexp[v + 1] == sm.vexp[v] ? keep : pass;
+    };
+    // the first operand rows go ahead of the weights
+    bool ok = warp_wait(sm.go, 0, abort, a.status);
+    int to_mine = pw;  // units until this warp's next one
+    {
+      const Phase& f = c.phase(0);
+      TilePos at = f.at(f.u0);
+      int ka = f.u0 % f.U;
+      for (int u = f.u0 - ka; u < f.u1 && ok; u += f.U, f.step(at)) {
+        const int kb = min(f.U, f.u1 - u);
+        int k = ka + to_mine;
+        if (k < kb) {
+          const int64_t row = c.matrix_row(0, at, lane);
+          const int r0 = __shfl_sync(0xFFFFFFFFu, (int)row, 0), r16 = __shfl_sync(0xFFFFFFFFu, (int)row, 16);
+          const uint64_t policy = item_policy(at.v);
+          for (; k < kb && ok; k += kProducers)
+            ok = issue(std::integral_constant<int, 0>{}, f, k, r0, r16, row, at.j, sm.vexp[at.v], policy);
+        }
+        to_mine = k - kb;
+        ka = 0;
+      }
+    }
+    if constexpr (MOE) {
+      const Phase& f = c.phase(1);
+      TilePos at = f.at(f.u0);
+      const int visit = f.visit();
+      for (int u = f.u0; u < f.u1 && ok; u += visit, f.step(at)) {
+        const int r0 = (int)c.matrix_row(1, at, 0);
+        const uint64_t policy = item_policy(at.v);
+        int i = to_mine;
+        for (; i < visit && ok; i += kProducers) {
+          int w, k;
+          f.unit_of(i, w, k);
+          const int r = r0 + 32 * (w >> 1);
+          ok = issue(std::integral_constant<int, 1>{}, f, k, r, r + 16, (int64_t)r + lane, 0, 0, policy);
+        }
+        to_mine = i - visit;
       }
     }
     // no copy outlives the CTA, also when the other warps have given up
@@ -1027,50 +1048,69 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
   } else if (warp_id == kWarpEpilogue) {
     // ------------------------------------------------------------- epilogue
     const int g = lane >> 2, t = lane & 3;
-    int n0 = 0;     // the CTA's units before this segment
+    int n0 = 0;     // the CTA's units before this tile
     int taken = 0;  // lane w: sums taken from warp w
     for (int v = lane; v < c.nv; v += 32)
       for (int p = 0; p < kPhases; ++p) sm.vglobal[p][v] = __ldg(&a.m[p].global[sm.vexp[v]]);
     __syncwarp();
-    for (int p = 0; p < kPhases; ++p) {
-      const Phase& f = c.phase(p);
-      const bool res = c.resident(p);
-      const int R = c.ring_rows(p);
-      const int tu = f.tile_units();
+    // Where the sums of the warps first, first + step, .. (cnt of them) lie: lane i
+    // gets the i-th one's address, once all of them are there
+    auto await_sums = [&](int first, int step, int cnt, int& from, uint32_t& src) {
+      from = (first + step * lane) & (kConsumers - 1);
+      const int tk = __shfl_sync(0xFFFFFFFFu, taken, from);
+      src = pbuf + (2 * from + (tk & 1)) * kPartBytes;
+      return wait_count(&sm.done[from], lane < cnt ? tk + 1 : 0, abort, a.status);
+    };
+    auto give_back = [&](int from, int cnt) {
+      __syncwarp();
+      const int tk = __shfl_sync(0xFFFFFFFFu, taken, from);
+      if (lane < cnt) store_count(&sm.taken[from], tk + 1);
+      uint32_t mask = lane < cnt ? 1u << from : 0u;
+      mask = __reduce_or_sync(0xFFFFFFFFu, mask);
+      taken += lane < kConsumers && (mask >> lane & 1u);
+    };
+    // A cut tile: this CTA's share goes to its slot, and the CTA that comes last
+    // adds the shares in the order of the CTAs.  False: not the last one.
+    auto last_to_join = [&](const Phase& f, int c0, int c1) {
+      __threadfence();
+      __syncwarp();
+      uint32_t old = 0;
+      uint32_t* count = &a.ctl[2 + f.p * kFp4Grid + c0];
+      if (lane == 0) old = atomicAdd(count, 1u);
+      old = __shfl_sync(0xFFFFFFFFu, old, 0);
+      if (old != (uint32_t)(c1 - c0)) return false;
+      __threadfence();
+      if (lane == 0) *count = 0u;
+      return true;
+    };
+    {
+      const Phase& f = c.phase(0);
+      const bool res = c.resident(0);
+      const int R = c.ring_rows(0);
       ItemWalk it;
-      int seg = f.seg_begin();
-      SegPos at = f.at(seg);
-      bool fresh = true;  // first segment of a tile in this CTA
-      int n = 0, s0 = 0;
+      TilePos at = f.at(f.u0);
+      int ka = f.u0 % f.U, n = 0, s0 = 0;
       float factor[NT][2];
-      float* out_row[2] = {&sm.out[0][0], &sm.out[0][0]};
-      for (; seg * f.U < f.u1; ++seg, f.step(at)) {
-        const int ua = max(f.u0, seg * f.U), ub = min(f.u1, (seg + 1) * f.U);
-        const int last_item = it.item;
+      bool fresh = true;
+      for (int u = f.u0 - ka; u < f.u1; u += f.U, f.step(at)) {
+        const int units = min(f.U, f.u1 - u) - ka, last_item = it.item;
         if (it.next(c, f, res, R, at) && last_item >= 0) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][last_item % kItems]));
+          if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[0][last_item % kItems]));
         }
-        const bool fresh_item = it.item != last_item || seg == f.seg_begin();
-        if (fresh_item || p == 0) {
-          n = c.item_rows(at.v);
-          s0 = sm.vstart[at.v];
-        }
-        // the sums of the warps that had units of the segment, in their order:
-        // lane i waits for the i-th of them, all lanes add
+        // the sums of the warps that had units of the tile, in their order
         float acc[2][NT][4] = {};
-        const int cnt = min(ub - ua, kConsumers), w0 = n0 % kConsumers;
-        n0 += ub - ua;
-        const int mine = (w0 + lane) % kConsumers, mine_tk = __shfl_sync(0xFFFFFFFFu, taken, mine);
-        if (!wait_count(&sm.done[mine], lane < cnt ? mine_tk + 1 : 0, abort, a.status)) goto done;
-        const uint32_t mine_src = pbuf + (2 * mine + (mine_tk & 1)) * kPartBytes;
+        const int cnt = min(units, kConsumers);
+        int from;
+        uint32_t my_src;
+        if (!await_sums(n0, 1, cnt, from, my_src)) goto done;
 #pragma unroll
         for (int i0 = 0; i0 < kConsumers; i0 += 4) {
           if (i0 >= cnt) break;
           uint4 x[4][2][NT];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t src = __shfl_sync(0xFFFFFFFFu, mine_src, i0 + i) + lane * 16;
+            const uint32_t src = __shfl_sync(0xFFFFFFFFu, my_src, i0 + i) + lane * 16;
             if (i0 + i < cnt) {
 #pragma unroll
               for (int m = 0; m < 2; ++m)
@@ -1092,124 +1132,56 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 }
             }
         }
-        __syncwarp();
-        if (lane < cnt) store_count(&sm.taken[mine], mine_tk + 1);
-        if (lane < kConsumers && (lane - w0 + kConsumers) % kConsumers < cnt) ++taken;
+        give_back(from, cnt);
+        n0 += units;
+        ka = 0;
         // lane (g, t) holds rows g and g + 8 of tokens 8 nt + 2 t and + 1; their factors:
-        if (fresh_item || p == 0) {
-          const float gl = sm.vglobal[p][at.v];
+        if (fresh || at.j == 0) {
+          fresh = false;
+          n = c.item_rows(at.v);
+          s0 = sm.vstart[at.v];
+          const float gl = sm.vglobal[0][at.v];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
               const int col = 8 * nt + 2 * t + o;
-              factor[nt][o] = 0.f;
-              if (col < n) {
-                factor[nt][o] = sm.rscale[p][c.row_slot(res, it.pos, R, s0, col)] * gl;
-                if (p == 1) {
-                  factor[nt][o] *= sm.route_w[s0 + col];
-                  out_row[o] = &sm.out[sm.route_tok[s0 + col]][g];
-                }
-              }
+              factor[nt][o] = col < n ? sm.rscale[0][c.row_slot(res, it.pos, R, s0, col)] * gl : 0.f;
             }
         }
-        const int tile = p == 0 ? seg : at.j;
-        const int tb = tile * tu, te = tb + tu;  // the tile's units
-        if (p == 1) {
-          // out[token][row] over the tile's experts
-          if (fresh) {
-            for (int i = lane; i < a.T * kTile2; i += 32) (&sm.out[0][0])[i] = 0.f;
-            __syncwarp();
-          }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int o = 0; o < 2; ++o)
-            if (2 * t + o < n) {
-              float* row = out_row[o] + 32 * at.rb;
-              const float r[4] = {row[0], row[8], row[16], row[24]};
-              row[0] = fmaf(factor[0][o], acc[0][0][o], r[0]);
-              row[8] = fmaf(factor[0][o], acc[0][0][2 + o], r[1]);
-              row[16] = fmaf(factor[0][o], acc[1][0][o], r[2]);
-              row[24] = fmaf(factor[0][o], acc[1][0][2 + o], r[3]);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              acc[m][nt][o] *= factor[nt][o];
+              acc[m][nt][2 + o] *= factor[nt][o];
             }
-          __syncwarp();
-          fresh = false;
-          if (ub < min(f.u1, te)) continue;  // more of this tile to come
-          fresh = true;
-        } else {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int o = 0; o < 2; ++o)
-#pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                acc[m][nt][o] *= factor[nt][o];
-                acc[m][nt][2 + o] *= factor[nt][o];
-              }
-        }
-        const bool whole = tb >= f.u0 && te <= f.u1;
-        if (!whole) {
-          // join: this CTA's share goes to its slot; whoever arrives last adds the shares in CTA order
-          const int c0 = f.cta_of(tb), c1 = f.cta_of(te - 1);
-          constexpr int kSlot0 = 512, kSlot1 = kFp4MaxTokens * kTile2;
+        if (units != f.U) {
+          const int c0 = f.cta_of(u), c1 = f.cta_of(u + f.U - 1);
           auto share = [&](int cta) {
-            return a.part[p] + (size_t)(2 * cta + (cta == c0)) * (p == 0 ? kSlot0 : kSlot1);
+            return reinterpret_cast<float4*>(a.part[0] + (size_t)(2 * cta + (cta == c0)) * 512) + lane;
           };
-          float* mine = share(blockIdx.x);
-          if (p == 1) {
-            for (int tok = 0; tok < a.T; ++tok)
-              __stcg(reinterpret_cast<float4*>(mine + tok * kTile2) + lane,
-                     *reinterpret_cast<const float4*>(&sm.out[tok][4 * lane]));
-          } else {
+          float4* mine = share(blockIdx.x);
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                __stcg(reinterpret_cast<float4*>(mine) + (m * NT + nt) * 32 + lane,
-                       make_float4(acc[m][nt][0], acc[m][nt][1], acc[m][nt][2], acc[m][nt][3]));
-          }
-          __threadfence();
-          __syncwarp();
-          uint32_t old = 0;
-          uint32_t* cnt_p = &a.ctl[2 + p * kFp4Grid + c0];
-          if (lane == 0) old = atomicAdd(cnt_p, 1u);
-          old = __shfl_sync(0xFFFFFFFFu, old, 0);
-          if (old != (uint32_t)(c1 - c0)) continue;
-          __threadfence();
-          if (lane == 0) *cnt_p = 0u;
-          if (p == 1) {
-            for (int tok = 0; tok < a.T; ++tok) {
+            for (int nt = 0; nt < NT; ++nt)
+              __stcg(mine + (m * NT + nt) * 32,
+                     make_float4(acc[m][nt][0], acc[m][nt][1], acc[m][nt][2], acc[m][nt][3]));
+          if (!last_to_join(f, c0, c1)) continue;
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
               float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
               for (int i = c0; i <= c1; ++i) {
-                const float4 z = __ldcg(reinterpret_cast<const float4*>(share(i) + tok * kTile2) + lane);
+                const float4 z = __ldcg(share(i) + (m * NT + nt) * 32);
                 s.x += z.x, s.y += z.y, s.z += z.z, s.w += z.w;
               }
-              *reinterpret_cast<float4*>(&sm.out[tok][4 * lane]) = s;
+              acc[m][nt][0] = s.x, acc[m][nt][1] = s.y, acc[m][nt][2] = s.z, acc[m][nt][3] = s.w;
             }
-          } else {
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int i = c0; i <= c1; ++i) {
-                  const float4 z = __ldcg(reinterpret_cast<const float4*>(share(i)) + (m * NT + nt) * 32 + lane);
-                  s.x += z.x, s.y += z.y, s.z += z.z, s.w += z.w;
-                }
-                acc[m][nt][0] = s.x, acc[m][nt][1] = s.y, acc[m][nt][2] = s.z, acc[m][nt][3] = s.w;
-              }
-          }
-        }
-        if (p == 1) {
-          __syncwarp();
-          uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + kTile2 * at.j + 4 * lane;
-          for (int tok = 0; tok < a.T; ++tok) {
-            const float4 v = *reinterpret_cast<const float4*>(&sm.out[tok][4 * lane]);
-            *reinterpret_cast<uint2*>(y + (int64_t)tok * a.m[1].rows) =
-                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-          }
-          __syncwarp();
-          continue;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -1253,13 +1225,114 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       }
       if (f.u0 < f.u1) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][it.item % kItems]));
+        if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[0][it.item % kItems]));
       }
-      if (MOE && p == 0) {  // every h value of this CTA is stored, also for bulk copies
+      if (MOE) {  // every h value of this CTA is stored, also for bulk copies
         fence_proxy_async_global();
         __threadfence();
         __syncwarp();
         if (lane == 0) atomicAdd(&a.ctl[0], 1u);
+      }
+    }
+    if constexpr (MOE) {
+      const Phase& f = c.phase(1);
+      const int R = c.ring_rows(1), visit = f.visit(), tu = f.tile_units();
+      const int cnt = f.U > 1 ? kConsumers : kConsumers / 2;  // the warps with units
+      ItemWalk it;
+      TilePos at = f.at(f.u0);
+      bool fresh = true;  // first visit of a tile by this CTA
+      for (int u = f.u0; u < f.u1; u += visit, f.step(at)) {
+        const int last_item = it.item;
+        it.next(c, f, false, R, at);
+        if (last_item >= 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[1][last_item % kItems]));
+        }
+        if (fresh) {
+          for (int i = lane; i < a.T * kTile2 / 4; i += 32)
+            reinterpret_cast<float4*>(&sm.out[0][0])[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          fresh = false;
+        }
+        const int n = c.item_rows(at.v), s0 = sm.vstart[at.v];
+        int from;
+        uint32_t my_src;
+        if (!await_sums(0, f.U > 1 ? 1 : 2, cnt, from, my_src)) goto done;
+        // lane (g, t) holds rows g and g + 8 of tokens 2 t and 2 t + 1: their factors
+        // and places in out[token][row], which sums over the tile's items
+        const float gl = sm.vglobal[1][at.v];
+        float factor[2] = {0.f, 0.f};
+        float* row[2];
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          const int col = min(2 * t + o, n - 1), s = s0 + col;
+          factor[o] = sm.rscale[1][c.row_slot(false, it.pos, R, s0, col)] * gl * sm.route_w[s];
+          row[o] = &sm.out[sm.route_tok[s]][g];
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {  // blocks of 32 rows
+          uint4 x[2][2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t src = __shfl_sync(0xFFFFFFFFu, my_src, f.U > 1 ? 2 * b + h : b) + lane * 16;
+            if (h == 0 || f.U > 1) {
+              x[h][0] = lds128(src);
+              x[h][1] = lds128(src + 512);
+            } else {
+              x[h][0] = x[h][1] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+#pragma unroll
+          for (int o = 0; o < 2; ++o)
+            if (2 * t + o < n) {
+              float* to = row[o] + 32 * b;
+              auto add = [&](const uint4& p, const uint4& q, int hi) {
+                const uint32_t y = hi ? (o ? p.w : p.z) : (o ? p.y : p.x);
+                const uint32_t z = hi ? (o ? q.w : q.z) : (o ? q.y : q.x);
+                return __uint_as_float(y) + __uint_as_float(z);
+              };
+              const float r[4] = {to[0], to[8], to[16], to[24]};
+              to[0] = fmaf(factor[o], add(x[0][0], x[1][0], 0), r[0]);
+              to[8] = fmaf(factor[o], add(x[0][0], x[1][0], 1), r[1]);
+              to[16] = fmaf(factor[o], add(x[0][1], x[1][1], 0), r[2]);
+              to[24] = fmaf(factor[o], add(x[0][1], x[1][1], 1), r[3]);
+            }
+        }
+        give_back(from, cnt);
+        const int tb = at.j * tu, te = tb + tu;  // the tile's units
+        if (u + visit < min(f.u1, te)) continue;  // more of this tile to come
+        fresh = true;
+        if (tb < f.u0 || te > f.u1) {
+          const int c0 = f.cta_of(tb), c1 = f.cta_of(te - 1);
+          auto share = [&](int cta) {
+            return reinterpret_cast<float4*>(a.part[1] + (size_t)(2 * cta + (cta == c0)) *
+                                                             (kFp4MaxTokens * kTile2)) + lane;
+          };
+          float4* mine = share(blockIdx.x);
+          for (int tok = 0; tok < a.T; ++tok)
+            __stcg(mine + tok * (kTile2 / 4), *reinterpret_cast<const float4*>(&sm.out[tok][4 * lane]));
+          if (!last_to_join(f, c0, c1)) continue;
+          for (int tok = 0; tok < a.T; ++tok) {
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int i = c0; i <= c1; ++i) {
+              const float4 z = __ldcg(share(i) + tok * (kTile2 / 4));
+              s.x += z.x, s.y += z.y, s.z += z.z, s.w += z.w;
+            }
+            *reinterpret_cast<float4*>(&sm.out[tok][4 * lane]) = s;
+          }
+        }
+        __syncwarp();
+        uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + kTile2 * at.j + 4 * lane;
+        for (int tok = 0; tok < a.T; ++tok) {
+          const float4 v = *reinterpret_cast<const float4*>(&sm.out[tok][4 * lane]);
+          *reinterpret_cast<uint2*>(y + (int64_t)tok * a.m[1].rows) =
+              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        }
+        __syncwarp();
+      }
+      if (f.u0 < f.u1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[1][it.item % kItems]));
       }
     }
   } else {
@@ -1312,9 +1385,9 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
           ++oldest;
           return true;
         };
-        int seg = f.seg_begin();
-        SegPos at = f.at(seg);
-        for (; seg * f.U < f.u1; ++seg, f.step(at)) {
+        TilePos at = f.at(f.u0);
+        const int visit = f.visit();
+        for (int u = f.u0 - f.u0 % visit; u < f.u1; u += visit, f.step(at)) {
           if (!it.next(c, f, false, R, at)) continue;
           while (used + it.rows > R || it.item - oldest >= kItems)
             if (!retire()) goto done;
