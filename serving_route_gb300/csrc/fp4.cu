@@ -52,8 +52,8 @@ constexpr int kFp4Grid = 152;        // one CTA per SM
 // The warps' roles.  The service warps come first: where several warps of a
 // scheduler are ready it serves the older ones, and the consumers, with
 // instructions ready nearly always, would starve what they wait for.
-constexpr int kProducers = 3;        // issue the copies of the weights, in turn
-constexpr int kLoaders = 4;          // x and h rows to half in shared memory
+constexpr int kProducers = 4;        // issue the copies of the weights, in turn
+constexpr int kLoaders = 3;          // x and h rows to half in shared memory
 constexpr int kConsumers = 8;        // dequantise and multiply
 constexpr int kWarpEpilogue = 0;     // adds the consumers' sums, finishes and joins tiles
 constexpr int kWarpProducer = 1;
@@ -63,7 +63,7 @@ constexpr int kFp4Threads = 32 * (kWarpConsumer + kConsumers);
 // Units in flight: at least what covers the latency of HBM at the copy rate; a
 // multiple of kProducers, so that each place is one producer's (another one could
 // wait for a phase two laps ahead, whose parity is that of the lap before)
-constexpr int kMinStages = 12, kMaxStages = 18;
+constexpr int kMinStages = 12, kMaxStages = 16;
 constexpr int kUnitCols = 512;
 constexpr int kCodeBytes = 32 * kUnitCols / 2;
 constexpr int kScaleBytes = 32 * kUnitCols / 16;
@@ -936,7 +936,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
   } else if (warp_id >= kWarpProducer && warp_id < kWarpLoader) {
     // ------------------------------------------------------------ producers
     const uint64_t pass = policy_evict_first(), keep = policy_evict_normal();
-    const int pw = warp_id - kWarpProducer;  // this one's units: every third, counted over both phases
+    const int pw = warp_id - kWarpProducer;  // this one's units: every fourth, counted over both phases
     int slot = pw, mine = 0;
     uint32_t parity = 1;
     // the copies of a unit: columns from 512 k of the 32 rows from `row` on (FC1: 16
