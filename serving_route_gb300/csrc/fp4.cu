@@ -52,11 +52,13 @@ constexpr int kFp4Grid = 152;        // one CTA per SM
 // The warps' roles.  The service warps come first: where several warps of a
 // scheduler are ready it serves the older ones, and the consumers, with
 // instructions ready nearly always, would starve what they wait for.
+constexpr int kEpilogues = 2;        // add the consumers' sums, finish and join tiles: in turn, the
+                                     // second phase's tiles by the first of them
 constexpr int kProducers = 4;        // issue the copies of the weights, in turn
-constexpr int kLoaders = 3;          // x and h rows to half in shared memory
+constexpr int kLoaders = 2;          // x and h rows to half in shared memory
 constexpr int kConsumers = 8;        // dequantise and multiply
-constexpr int kWarpEpilogue = 0;     // adds the consumers' sums, finishes and joins tiles
-constexpr int kWarpProducer = 1;
+constexpr int kWarpEpilogue = 0;
+constexpr int kWarpProducer = kWarpEpilogue + kEpilogues;
 constexpr int kWarpLoader = kWarpProducer + kProducers;
 constexpr int kWarpConsumer = kWarpLoader + kLoaders;
 constexpr int kFp4Threads = 32 * (kWarpConsumer + kConsumers);
@@ -177,11 +179,13 @@ struct Fp4Shared {
   int16_t vexp[kFp4MaxRoutes];
   uint8_t first[kFp4MaxRoutes];
   uint32_t row_max[kFp4MaxTokens];
-  int warp_cnt[4];
+  int warp_cnt[4], warp_live[4];
+  uint32_t warp_bits[4];
   Phase phase[2];
   int issued[kProducers];               // units each producer has begun
-  int done[kConsumers], taken[kConsumers];  // sums each consumer has left, and that were taken
-  int nv, nroutes;
+  int done[kConsumers];                 // sums each consumer has left
+  int taken[kConsumers][2];             // by place of a sum: how many were taken from it
+  int nv;
   int abort;
 };
 
@@ -620,11 +624,12 @@ __device__ __forceinline__ bool fill_h(const uint8_t* src, int cols, uint32_t ds
   return true;
 }
 
-// Sorted routes, and the items: runs of at most `group` tokens of one expert.
+// Sorted routes, and the items: runs of at most `group` tokens of one expert (the
+// linear: groups of tokens).  By the first 128 threads; e, w: the thread's route.
 template <bool MOE>
-__device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm) {
-  const int tid = threadIdx.x;
-  if (!MOE) {  // token groups of the linear
+__device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm, int e, float w) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (!MOE) {
     if (tid == 0) {
       int v = 0;
       for (int t = 0; t < a.T; t += a.group) {
@@ -633,33 +638,23 @@ __device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm) {
       }
       sm.vstart[v] = a.T;
       sm.nv = v;
-      sm.nroutes = a.T;
       if (blockIdx.x == 0) atomicExch(a.status, 0u);
     }
     if (tid < a.T) sm.route_id[tid] = sm.route_tok[tid] = tid;
     return;
   }
+  auto sync = [] { asm volatile("bar.sync 2, 128;" ::: "memory"); };
   const int R = a.T * a.K;
-  int e = -1;
-  float w = 0.f;
-  uint32_t bits = 0u;
-  if (tid < R) {
-    e = a.idx[tid];
-    w = a.w[tid];
-    if (e < -1 || e >= a.E) bits = MOE_DEV_ROUTE_RANGE;
-    if (e >= a.E) e = -1;
-  }
-  const bool live = e >= 0;  // (threads past the routes: not live)
-  const int mine = live ? e * kFp4MaxRoutes + tid : 0x7FFFFFFF;  // by expert, then by route
-  if (tid < kFp4MaxRoutes) {
-    sm.key[tid] = mine;
-    sm.first[tid] = 0;
-  }
-  __syncthreads();
+  uint32_t bits = tid < R && (e < -1 || e >= a.E) ? MOE_DEV_ROUTE_RANGE : 0u;
+  const bool live = tid < R && e >= 0 && e < a.E;
+  const int low = e * kFp4MaxRoutes;
+  const int mine = live ? low + tid : 0x7FFFFFFF;  // by expert, then by route
+  sm.key[tid] = mine;
+  sm.first[tid] = 0;
+  sync();
   int pos = 0, within = 0;
   if (live) {
-    const int low = e * kFp4MaxRoutes;
-#pragma unroll 4
+#pragma unroll 2
     for (int r = 0; r < R; r += 4) {
       const int4 k4 = *reinterpret_cast<const int4*>(&sm.key[r]);
       const int k[4] = {k4.x, k4.y, k4.z, k4.w};  // past the routes: the largest key
@@ -680,33 +675,30 @@ __device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm) {
     sm.route_w[pos] = w;
     sm.first[pos] = within % a.group == 0;
   }
-  const int n = __syncthreads_count(live);
-  if (tid < kFp4MaxRoutes) {
-    const uint32_t b = __ballot_sync(0xFFFFFFFFu, sm.first[tid] != 0);
-    if ((tid & 31) == 0) sm.warp_cnt[tid >> 5] = __popc(b);
-    within = __popc(b & ((1u << (tid & 31)) - 1u));
+  bits = __reduce_or_sync(0xFFFFFFFFu, bits);
+  const int live_here = __popc(__ballot_sync(0xFFFFFFFFu, live));
+  if (lane == 0) {
+    sm.warp_bits[warp] = bits;
+    sm.warp_live[warp] = live_here;
   }
-  // the status word is this call's: the first CTA sets it
-  if (__syncthreads_or(bits != 0u)) {
-    if (blockIdx.x == 0 && tid == 0) atomicExch(a.status, 0u);
-    __syncthreads();
-    if (blockIdx.x == 0 && bits) atomicOr(a.status, bits);
-  } else if (blockIdx.x == 0 && tid == 0) {
-    atomicExch(a.status, 0u);
+  sync();
+  const bool first = sm.first[tid] != 0;
+  const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, first);
+  if (lane == 0) sm.warp_cnt[warp] = __popc(firsts);
+  sync();
+  int v = __popc(firsts & ((1u << lane) - 1u));
+  for (int i = 0; i < warp; ++i) v += sm.warp_cnt[i];
+  if (first) {
+    sm.vstart[v] = tid;
+    sm.vexp[v] = sm.route_e[tid];
   }
-  if (tid < kFp4MaxRoutes) {
-    int v = within;
-    for (int i = 0; i < (tid >> 5); ++i) v += sm.warp_cnt[i];
-    if (sm.first[tid]) {
-      sm.vstart[v] = tid;
-      sm.vexp[v] = sm.route_e[tid];
-    }
-    if (tid == 0) {
-      const int nv = sm.warp_cnt[0] + sm.warp_cnt[1] + sm.warp_cnt[2] + sm.warp_cnt[3];
-      sm.nv = nv;
-      sm.nroutes = n;
-      sm.vstart[nv] = n;
-    }
+  if (tid == 0) {
+    const int nv = sm.warp_cnt[0] + sm.warp_cnt[1] + sm.warp_cnt[2] + sm.warp_cnt[3];
+    sm.nv = nv;
+    sm.vstart[nv] = sm.warp_live[0] + sm.warp_live[1] + sm.warp_live[2] + sm.warp_live[3];
+    // the status word is this call's: the first CTA sets it
+    if (blockIdx.x == 0)
+      atomicExch(a.status, sm.warp_bits[0] | sm.warp_bits[1] | sm.warp_bits[2] | sm.warp_bits[3]);
   }
 }
 
@@ -732,10 +724,10 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     } else if (i >= 96 && i < 96 + kFp4MaxTokens) {
       sm.row_max[i - 96] = 0u;
     } else if (i >= 32 && i < 32 + kConsumers) {
-      sm.done[i - 32] = sm.taken[i - 32] = 0;
+      sm.done[i - 32] = sm.taken[i - 32][0] = sm.taken[i - 32][1] = 0;
     } else if (i >= 64 && i < 64 + 2 * kItems) {
       mbar_init(smem_u32(&sm.bfull[0][0] + (i - 64)), kLoaders);
-      mbar_init(smem_u32(&sm.bempty[0][0] + (i - 64)), kConsumers + 1);
+      mbar_init(smem_u32(&sm.bempty[0][0] + (i - 64)), kConsumers + (i - 64 < kItems ? kEpilogues : 1));
     } else if (i == 128) {
       mbar_init(smem_u32(&sm.go), kLoaders);
       sm.abort = 0;
@@ -761,12 +753,38 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         bulk_load(brow0 + r * row_bytes(a.m[0].cols, false), a.x + r * a.ldx, a.m[0].cols * 2, smem_u32(&bar));
     }
   }
-  build_items<MOE>(a, sm);
+  int route = -1;
+  float route_w = 0.f;
+  if (MOE && threadIdx.x < a.T * a.K) {
+    route = a.idx[threadIdx.x];
+    route_w = a.w[threadIdx.x];
+  }
   __syncthreads();
 
+  // Two groups of warps: the tables, after which the copies of the weights start at
+  // once; and meanwhile, where the x rows stay, the loaders and consumers turn them.
   using Ctx = Fp4Ctx<MOE, NT>;
+  constexpr int kTableThreads = 32 * kWarpLoader;
+  static_assert(kTableThreads >= kFp4MaxRoutes, "one thread per route");
+  bool rows_ok = true;
+  if (warp_id < kWarpLoader) {
+    if (threadIdx.x < kFp4MaxRoutes) {
+      build_items<MOE>(a, sm, route, route_w);
+      asm volatile("bar.sync 2, 128;" ::: "memory");
+      if (sm.nv > 0 && lane == 0 && warp_id < (MOE ? 2 : 1))
+        sm.phase[warp_id] = Ctx{a, sm, sm.nv}.make_phase(warp_id);
+    }
+    asm volatile("bar.sync 3, %0;" ::"n"(kTableThreads) : "memory");
+    asm volatile("bar.arrive 4, %0;" ::"n"(kFp4Threads) : "memory");
+  } else {
+    if (early) {
+      if (loader && lane == 0) mbar_arrive(smem_u32(&sm.go));
+      rows_ok = fill_x_rows(a.T, a.m[0].cols, brow0, row_bytes(a.m[0].cols, false), warp_id - kWarpLoader,
+                            kLoaders + kConsumers, sm.raw[0], sm.row_max, sm.rscale[0], &sm.abort, a.status);
+    }
+    asm volatile("bar.sync 4, %0;" ::"n"(kFp4Threads) : "memory");
+  }
   const Ctx c{a, sm, sm.nv};
-  if (c.nv > 0 && lane == 0 && warp_id < (MOE ? 2 : 1)) sm.phase[warp_id] = c.make_phase(warp_id);
   constexpr int kPhases = MOE ? 2 : 1;
   volatile int* abort = &sm.abort;
 
@@ -776,21 +794,10 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
          i += (int64_t)gridDim.x * blockDim.x)
       o[i] = make_uint4(0u, 0u, 0u, 0u);
-    // no copy outlives the CTA
-    if (early && warp_id == kWarpLoader) mbar_wait(smem_u32(&sm.raw[0]), 0, abort, a.status);
     return;
   }
 
-  __syncthreads();  // the phases
-
-  // rows that stay: the loaders and the consumers, who have nothing to do yet,
-  // turn them together
-  if (early && warp_id >= kWarpLoader) {
-    if (loader && lane == 0) mbar_arrive(smem_u32(&sm.go));
-    if (!fill_x_rows(a.T, a.m[0].cols, brow0, row_bytes(a.m[0].cols, false), warp_id - kWarpLoader,
-                     kLoaders + kConsumers, sm.raw[0], sm.row_max, sm.rscale[0], abort, a.status))
-      goto done;
-  }
+  if (!rows_ok) goto done;
 
   if (warp_id >= kWarpConsumer) {
     // ------------------------------------------------------------ consumers
@@ -908,7 +915,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
               }
             }
           }
-          if (!wait_count(&sm.taken[warp], pc - 1, abort, a.status)) return false;
+          if (!wait_count(&sm.taken[warp][pc & 1], pc >> 1, abort, a.status)) return false;
           const uint32_t dst = pbuf + (2 * warp + (pc & 1)) * kPartBytes + lane * 16;
 #pragma unroll
           for (int m = 0; m < 2; ++m)
@@ -1045,29 +1052,31 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       for (int i = 0; i < 2; ++i)
         mbar_wait_bounded(smem_u32(&sm.full[lane]), i, &none, nullptr, 100000000ull);
     }
-  } else if (warp_id == kWarpEpilogue) {
+  } else if (warp_id < kWarpProducer) {
     // ------------------------------------------------------------- epilogue
     const int g = lane >> 2, t = lane & 3;
     int n0 = 0;     // the CTA's units before this tile
-    int taken = 0;  // lane w: sums taken from warp w
+    int left = 0;   // lane w: sums that warp w has left before this tile
     for (int v = lane; v < c.nv; v += 32)
       for (int p = 0; p < kPhases; ++p) sm.vglobal[p][v] = __ldg(&a.m[p].global[sm.vexp[v]]);
     __syncwarp();
     // Where the sums of the warps first, first + step, .. (cnt of them) lie: lane i
-    // gets the i-th one's address, once all of them are there
+    // gets the i-th one's warp and address, once all of them are there
     auto await_sums = [&](int first, int step, int cnt, int& from, uint32_t& src) {
       from = (first + step * lane) & (kConsumers - 1);
-      const int tk = __shfl_sync(0xFFFFFFFFu, taken, from);
-      src = pbuf + (2 * from + (tk & 1)) * kPartBytes;
-      return wait_count(&sm.done[from], lane < cnt ? tk + 1 : 0, abort, a.status);
+      const int n = __shfl_sync(0xFFFFFFFFu, left, from);
+      src = pbuf + (2 * from + (n & 1)) * kPartBytes;
+      return wait_count(&sm.done[from], lane < cnt ? n + 1 : 0, abort, a.status);
     };
     auto give_back = [&](int from, int cnt) {
       __syncwarp();
-      const int tk = __shfl_sync(0xFFFFFFFFu, taken, from);
-      if (lane < cnt) store_count(&sm.taken[from], tk + 1);
-      uint32_t mask = lane < cnt ? 1u << from : 0u;
-      mask = __reduce_or_sync(0xFFFFFFFFu, mask);
-      taken += lane < kConsumers && (mask >> lane & 1u);
+      const int n = __shfl_sync(0xFFFFFFFFu, left, from);
+      if (lane < cnt) store_count(&sm.taken[from][n & 1], (n >> 1) + 1);
+    };
+    // on to the next tile
+    auto count_sums = [&](int first, int step, int cnt) {
+      const int i = ((lane - first) & (kConsumers - 1)) / step;
+      left += ((lane - first) & (step - 1)) == 0 && i < cnt;
     };
     // A cut tile: this CTA's share goes to its slot, and the CTA that comes last
     // adds the shares in the order of the CTAs.  False: not the last one.
@@ -1091,19 +1100,33 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       TilePos at = f.at(f.u0);
       int ka = f.u0 % f.U, n = 0, s0 = 0;
       float factor[NT][2];
-      bool fresh = true;
+      bool fresh = true;  // a new item since this warp's last tile
+      int turn = 0;
       for (int u = f.u0 - ka; u < f.u1; u += f.U, f.step(at)) {
         const int units = min(f.U, f.u1 - u) - ka, last_item = it.item;
-        if (it.next(c, f, res, R, at) && last_item >= 0) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[0][last_item % kItems]));
+        if (it.next(c, f, res, R, at)) {
+          fresh = true;
+          if (last_item >= 0) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[0][last_item % kItems]));
+          }
+        } else if (at.j == 0) {
+          fresh = true;
+        }
+        const bool cut = units != f.U;
+        const int cnt = min(units, kConsumers), first = n0;
+        n0 += units;
+        ka = 0;
+        turn ^= 1;
+        if (turn == warp_id) {  // the other warp's
+          count_sums(first, 1, cnt);
+          continue;
         }
         // the sums of the warps that had units of the tile, in their order
         float acc[2][NT][4] = {};
-        const int cnt = min(units, kConsumers);
         int from;
         uint32_t my_src;
-        if (!await_sums(n0, 1, cnt, from, my_src)) goto done;
+        if (!await_sums(first, 1, cnt, from, my_src)) goto done;
 #pragma unroll
         for (int i0 = 0; i0 < kConsumers; i0 += 4) {
           if (i0 >= cnt) break;
@@ -1133,10 +1156,9 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             }
         }
         give_back(from, cnt);
-        n0 += units;
-        ka = 0;
+        count_sums(first, 1, cnt);
         // lane (g, t) holds rows g and g + 8 of tokens 8 nt + 2 t and + 1; their factors:
-        if (fresh || at.j == 0) {
+        if (fresh) {
           fresh = false;
           n = c.item_rows(at.v);
           s0 = sm.vstart[at.v];
@@ -1158,7 +1180,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
               acc[m][nt][o] *= factor[nt][o];
               acc[m][nt][2 + o] *= factor[nt][o];
             }
-        if (units != f.U) {
+        if (cut) {
           const int c0 = f.cta_of(u), c1 = f.cta_of(u + f.U - 1);
           auto share = [&](int cta) {
             return reinterpret_cast<float4*>(a.part[0] + (size_t)(2 * cta + (cta == c0)) * 512) + lane;
@@ -1229,15 +1251,14 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       }
       if (MOE) {  // every h value of this CTA is stored, also for bulk copies
         fence_proxy_async_global();
-        __threadfence();
         __syncwarp();
-        if (lane == 0) atomicAdd(&a.ctl[0], 1u);
+        if (lane == 0) red_release_gpu_add(reinterpret_cast<int32_t*>(&a.ctl[0]), 1);
       }
     }
-    if constexpr (MOE) {
+    if (MOE && warp_id == kWarpEpilogue) {
       const Phase& f = c.phase(1);
       const int R = c.ring_rows(1), visit = f.visit(), tu = f.tile_units();
-      const int cnt = f.U > 1 ? kConsumers : kConsumers / 2;  // the warps with units
+      const int step = f.U > 1 ? 1 : 2, cnt = kConsumers / step;  // the warps with units
       ItemWalk it;
       TilePos at = f.at(f.u0);
       bool fresh = true;  // first visit of a tile by this CTA
@@ -1256,7 +1277,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         const int n = c.item_rows(at.v), s0 = sm.vstart[at.v];
         int from;
         uint32_t my_src;
-        if (!await_sums(0, f.U > 1 ? 1 : 2, cnt, from, my_src)) goto done;
+        if (!await_sums(0, step, cnt, from, my_src)) goto done;
         // lane (g, t) holds rows g and g + 8 of tokens 2 t and 2 t + 1: their factors
         // and places in out[token][row], which sums over the tile's items
         const float gl = sm.vglobal[1][at.v];
@@ -1298,6 +1319,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             }
         }
         give_back(from, cnt);
+        count_sums(0, step, cnt);
         const int tb = at.j * tu, te = tb + tu;  // the tile's units
         if (u + visit < min(f.u1, te)) continue;  // more of this tile to come
         fresh = true;
@@ -1346,7 +1368,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         bool ok = true;
         if (lane == 0) {
           const uint64_t t0 = globaltimer_ns();
-          while (ld_acquire_gpu_u32(&a.ctl[0]) < gridDim.x) {
+          while (ld_acquire_gpu_u32(&a.ctl[0]) < kEpilogues * gridDim.x) {
             if (*abort) {
               ok = false;
               break;
