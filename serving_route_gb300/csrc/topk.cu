@@ -83,37 +83,38 @@ __global__ void __launch_bounds__(128) topk_route_kernel(const TopkArgs a) {
 
   if (a.groups > 1) {
     const int gs = a.E / a.groups;
-    // whole rows of 32 to a group: a value's group is that of its row
-    const bool by_row = (gs & 31) == 0;
-    uint32_t mine = 0u;  // lane g: group g's score
-    uint32_t m1 = 0u, m2 = 0u;
-    auto group_done = [&](int g) {
-      const uint32_t b1 = __reduce_max_sync(kAll, m1);
-      uint32_t score = b1;
-      if (SIGMOID && b1) {
-        const int first = __ffs(__ballot_sync(kAll, m1 == b1)) - 1;
-        const uint32_t b2 = __reduce_max_sync(kAll, lane == first ? m2 : m1);
-        score = order_key(key_value(b1) + (b2 ? key_value(b2) : 0.f));
-      }
-      if (lane == g) mine = score;
-      m1 = m2 = 0u;
+    uint32_t mine = 0u;  // this lane's group's score (0: no expert left)
+    int shift = 0;       // that group: lane >> shift
+    auto group_score = [&](uint32_t m1, uint32_t m2) {
+      return SIGMOID && m1 ? order_key(key_value(m1) + (m2 ? key_value(m2) : 0.f)) : m1;
     };
-    if (by_row) {
-      int g = 0, left = gs;
+    if (V > 1 && gs == 32) {
+      // Row i is group i: the lanes exchange halves of their rows until each has
+      // one, with its two largest values so far, then those.
+      uint32_t m1[V], m2[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if (32 * i < a.E) {
-          m2 = max(m2, min(m1, key[i]));
-          m1 = max(m1, key[i]);
-          left -= 32;
-          if (left == 0) {
-            group_done(g++);
-            left = gs;
-          }
+        m1[i] = key[i];
+        m2[i] = 0u;
+      }
+#pragma unroll
+      for (int n = V, o = 16; o >= 1; n >>= 1, o >>= 1) {
+        const bool up = n > 1 && (lane & o) != 0;
+        const int h = n > 1 ? n / 2 : 0;
+#pragma unroll
+        for (int i = 0; i < (n > 1 ? n / 2 : 1); ++i) {
+          const uint32_t r1 = __shfl_xor_sync(kAll, n > 1 && !up ? m1[i + h] : m1[i], o);
+          const uint32_t r2 = n == V ? 0u : __shfl_xor_sync(kAll, n > 1 && !up ? m2[i + h] : m2[i], o);
+          const uint32_t k1 = up ? m1[i + h] : m1[i], k2 = up ? m2[i + h] : m2[i];
+          m2[i] = max(min(k1, r1), max(k2, r2));
+          m1[i] = max(k1, r1);
         }
       }
+      shift = V == 2 ? 4 : V == 4 ? 3 : V == 8 ? 2 : V == 16 ? 1 : 0;
+      mine = group_score(m1[0], m2[0]);
     } else {
       for (int g = 0; g < a.groups; ++g) {
+        uint32_t m1 = 0u, m2 = 0u;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int e = 32 * i + lane;
@@ -121,31 +122,24 @@ __global__ void __launch_bounds__(128) topk_route_kernel(const TopkArgs a) {
           m2 = max(m2, min(m1, k));
           m1 = max(m1, k);
         }
-        group_done(g);
+        const uint32_t b1 = __reduce_max_sync(kAll, m1);
+        const int first = __ffs(__ballot_sync(kAll, m1 == b1)) - 1;
+        const uint32_t b2 = __reduce_max_sync(kAll, lane == first ? m2 : m1);
+        if (lane == g) mine = group_score(b1, b2);
       }
     }
     uint32_t keep = 0u;
     for (int n = 0; n < a.top_groups; ++n) {
       const uint32_t b = __reduce_max_sync(kAll, mine);
       if (b == 0u) break;
-      const int g = __ffs(__ballot_sync(kAll, mine == b)) - 1;
+      const int g = (__ffs(__ballot_sync(kAll, mine == b)) - 1) >> shift;
       keep |= 1u << g;
-      if (lane == g) mine = 0u;
+      if (lane >> shift == g) mine = 0u;
     }
-    if (by_row) {
-      int g = 0, left = gs;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (!((keep >> g) & 1u)) key[i] = 0u;
-        if ((left -= 32) == 0) {
-          ++g;
-          left = gs;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (!((keep >> ((32 * i + lane) / gs & 31)) & 1u)) key[i] = 0u;
+    for (int i = 0; i < V; ++i) {
+      const int g = gs == 32 ? i : (32 * i + lane) / gs;
+      if (!((keep >> (g & 31)) & 1u)) key[i] = 0u;
     }
   }
 

@@ -211,7 +211,9 @@ def test_route_softmax(S, T, E, K, dtype):
 
 
 @pytest.mark.parametrize("T,E,K,G,TG", [(1, 256, 8, 8, 4), (77, 256, 8, 8, 4), (5, 160, 6, 8, 3), (4, 96, 4, 32, 5),
-                                        (6, 60, 2, 20, 1), (3, 24, 4, 3, 3), (2, 1024, 8, 16, 2), (9, 40, 6, 1, 1)])
+                                        (6, 60, 2, 20, 1), (3, 24, 4, 3, 3), (2, 1024, 8, 16, 2), (9, 40, 6, 1, 1),
+                                        (5, 64, 4, 2, 1), (7, 128, 8, 4, 2), (6, 160, 4, 5, 2), (3, 512, 8, 16, 4),
+                                        (2, 1024, 8, 32, 9)])
 def test_route_sigmoid_groups(S, T, E, K, G, TG):
     gen = torch.Generator("cuda").manual_seed(T + E + G)
     l = torch.randn(T, E, device="cuda", generator=gen)
