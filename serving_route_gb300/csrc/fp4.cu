@@ -450,17 +450,19 @@ __device__ __forceinline__ void raw_begin(uint64_t& bar, uint32_t bytes) {
   mbar_arrive_expect_tx(smem_u32(&bar), bytes);
 }
 
-// x as half: 16 BF16 values (a lane's two pieces of a unit), their largest
-// magnitude as BF16 bits.  NaN does not set the scale (it stays NaN in half);
-// infinity does.
+// The largest magnitudes of BF16 values, in pairs.  NaN does not set the scale (it
+// stays NaN in half); infinity does.
 __device__ __forceinline__ uint32_t max_bf16x8(const uint4 v, uint32_t m) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-    m = max(m, max(lo > 0x7F80u ? 0u : lo, hi > 0x7F80u ? 0u : hi));
-  }
+  for (int i = 0; i < 4; ++i)
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7FFF7FFFu));
   return m;
+}
+
+// The larger of a pair, over the warp, as BF16 bits.
+__device__ __forceinline__ uint32_t warp_max_pair(uint32_t m) {
+  return __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
 }
 
 __device__ __forceinline__ uint4 bf16x8_to_half(const uint4 v, float up) {
@@ -511,7 +513,7 @@ __device__ __forceinline__ bool fill_x(const uint16_t* src, int cols, uint32_t d
     load_pieces(dst, u, n, v);
     m = max_bf16x8(v[1], max_bf16x8(v[0], m));
   }
-  const int s = row_exponent(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m) << 16));
+  const int s = row_exponent(__uint_as_float(warp_max_pair(m) << 16));
   if (lane == 0) *rscale = pow2f(-s);
   for (int u = 0; u < U; ++u) {
     uint4 v[2];
@@ -535,10 +537,10 @@ __device__ __forceinline__ bool fill_x_rows(int T, int cols, uint32_t rows, int 
     uint4 v[2], w[2];
     load_pieces(rows + t0 * pitch, i - t0 * U, n, v);
     if (j < T * U) load_pieces(rows + t1 * pitch, j - t1 * U, n, w);
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max_bf16x8(v[1], max_bf16x8(v[0], 0u)));
+    const uint32_t m = warp_max_pair(max_bf16x8(v[1], max_bf16x8(v[0], 0u)));
     if (lane == 0) atomicMax(&row_max[t0], m);
     if (j < T * U) {
-      const uint32_t m1 = __reduce_max_sync(0xFFFFFFFFu, max_bf16x8(w[1], max_bf16x8(w[0], 0u)));
+      const uint32_t m1 = warp_max_pair(max_bf16x8(w[1], max_bf16x8(w[0], 0u)));
       if (lane == 0) atomicMax(&row_max[t1], m1);
     }
   }
