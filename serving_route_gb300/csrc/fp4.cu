@@ -741,6 +741,11 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     }
     fence_mbar_init();
   }
+  // The kernel before this one in the stream may still be at work; nothing above
+  // reads global memory.  (Of the linear: the layer's cooperative launch does not
+  // overlap.)
+  pdl_wait();
+  pdl_trigger();
   // x rows that stay are asked for before anything else: behind the first weights
   // they would wait for a full ring's copies
   const bool early = (int64_t)a.T * row_bytes(a.m[0].cols, false) <= a.b_bytes;
@@ -1514,8 +1519,10 @@ static cudaError_t fp4_launch(const Fp4Maps& maps, const Fp4Args& a, int grid, i
   cudaLaunchAttribute coop;
   coop.id = cudaLaunchAttributeCooperative;
   coop.val.cooperative = 1;
-  // the layer's CTAs wait for one another (all resident, or the launch fails); the linear's do not
-  return launch_k(fp4_stream_kernel<MOE, NT>, dim3(grid), dim3(kFp4Threads), smem, s, false,
+  // the layer's CTAs wait for one another (all resident, or the launch fails); the
+  // linear's do not, and its launch and prologue overlap the kernel before (10.2 -> 8.7 us
+  // for 4096 x 7168, T = 1, one after the other)
+  return launch_k(fp4_stream_kernel<MOE, NT>, dim3(grid), dim3(kFp4Threads), smem, s, !MOE,
                   MOE ? &coop : nullptr, maps, a);
 }
 

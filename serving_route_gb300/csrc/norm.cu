@@ -67,6 +67,8 @@ __device__ __forceinline__ uint4 float_to_bf16x8(const float (&v)[8]) {
 template <int NV, int FMT>
 __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormArgs a) {
   __shared__ float red[32];
+  pdl_wait();  // its launch overlaps the kernel before
+  pdl_trigger();
   const int64_t row = blockIdx.x;
   const int nvec = a.H >> 3;
   const uint4* x = reinterpret_cast<const uint4*>(a.x + row * a.ldx);
@@ -165,6 +167,8 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormArgs a) {
 template <int FMT>
 __global__ void __launch_bounds__(256) add_rms_norm_any_kernel(const NormArgs a) {
   __shared__ float red[32];
+  pdl_wait();
+  pdl_trigger();
   const int64_t row = blockIdx.x;
   const uint16_t* x = a.x + row * a.ldx;
   float ss = 0.f;
@@ -214,8 +218,7 @@ __global__ void __launch_bounds__(256) add_rms_norm_any_kernel(const NormArgs a)
 template <int FMT>
 static cudaError_t launch_norm(const NormArgs& a, int64_t T, bool vec, cudaStream_t s) {
   if (!vec) {
-    add_rms_norm_any_kernel<FMT><<<(unsigned)T, 256, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_k(add_rms_norm_any_kernel<FMT>, dim3((unsigned)T), dim3(256), 0, s, true, nullptr, a);
   }
   const int nvec = a.H >> 3;
   auto threads = [&](int nv) { return ((nvec + nv - 1) / nv + 31) / 32 * 32; };
@@ -223,12 +226,10 @@ static cudaError_t launch_norm(const NormArgs& a, int64_t T, bool vec, cudaStrea
   // short; many rows: four vectors a thread, so that several rows are in
   // flight on an SM
   if (T <= 152 && nvec <= 1024)
-    add_rms_norm_kernel<1, FMT><<<(unsigned)T, threads(1), 0, s>>>(a);
-  else if (T <= 152)
-    add_rms_norm_kernel<2, FMT><<<(unsigned)T, threads(2), 0, s>>>(a);
-  else
-    add_rms_norm_kernel<4, FMT><<<(unsigned)T, threads(4), 0, s>>>(a);
-  return cudaGetLastError();
+    return launch_k(add_rms_norm_kernel<1, FMT>, dim3((unsigned)T), dim3(threads(1)), 0, s, true, nullptr, a);
+  if (T <= 152)
+    return launch_k(add_rms_norm_kernel<2, FMT>, dim3((unsigned)T), dim3(threads(2)), 0, s, true, nullptr, a);
+  return launch_k(add_rms_norm_kernel<4, FMT>, dim3((unsigned)T), dim3(threads(4)), 0, s, true, nullptr, a);
 }
 
 }  // namespace mm

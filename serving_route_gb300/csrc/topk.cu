@@ -57,6 +57,8 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 template <int V, bool BF16, bool SIGMOID>
 __global__ void __launch_bounds__(128) topk_route_kernel(const TopkArgs a) {
   const int lane = threadIdx.x & 31;
+  pdl_wait();  // its launch overlaps the kernel before
+  pdl_trigger();
   const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= a.T) return;
   const int64_t row = t * a.ld;
@@ -200,8 +202,7 @@ template <int V>
 static cudaError_t launch_topk(const TopkArgs& a, bool bf16, bool sigmoid, cudaStream_t s) {
   auto k = bf16 ? (sigmoid ? topk_route_kernel<V, true, true> : topk_route_kernel<V, true, false>)
                 : (sigmoid ? topk_route_kernel<V, false, true> : topk_route_kernel<V, false, false>);
-  k<<<(unsigned)((a.T + 3) / 4), 128, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_k(k, dim3((unsigned)((a.T + 3) / 4)), dim3(128), 0, s, true, nullptr, a);
 }
 
 }  // namespace mm
