@@ -343,6 +343,22 @@ MOE_API moe_status moe_forward(moe_handle* h, const uint16_t* d_x, const int32_t
                        const float* d_topk_w, int64_t num_tokens, struct CUstream_st* stream);
 
 /*
+ * moe_forward_quantized -- moe_forward for activations that come in the layer's
+ * own 8-bit format, as moe_add_rms_norm writes them: the dispatch copies them
+ * and quantises nothing.
+ *   d_xq        E4M3 codes [num_tokens, H], 16-byte aligned.
+ *   d_xq_scale  E8M0 bytes [num_tokens, H/128] (MOE_FLAG_MXFP8: H/32); NULL
+ *               allowed under MOE_FLAG_PER_TENSOR, whose codes are of the
+ *               x_scale given with moe_set_activation_scales.
+ * Codes and bytes that quantising x would give yield moe_forward's output bit
+ * for bit.  Everything else as moe_forward.
+ */
+MOE_API moe_status moe_forward_quantized(moe_handle* h, const uint8_t* d_xq,
+                                         const uint8_t* d_xq_scale, const int32_t* d_topk_idx,
+                                         const float* d_topk_w, int64_t num_tokens,
+                                         struct CUstream_st* stream);
+
+/*
  * moe_read_status -- the read-back of the device-side route checker of
  * flashinfer PR #6398 ("perf(moe_ep): fuse Rubin MegaMoE forward
  * preparation", Description and the follow-up on the fused routing checker:
@@ -570,8 +586,10 @@ typedef struct moe_fp4_handle moe_fp4_handle;
 
 /*
  * moe_fp4_workspace_query / moe_fp4_create -- the whole MoE layer for at most
- * max_tokens (1..16) tokens.  dims as for moe_create; dims.flags 0 or
- * MOE_FLAG_CHECK_ROUTES.
+ * max_tokens (1..16) tokens.  dims as for moe_create; dims.flags may hold
+ * MOE_FLAG_CHECK_ROUTES and MOE_FLAG_WATCHDOG_TEST (every wait of the kernel
+ * is bounded by 1 s; here by 20 ms, and the first CTA withholds some of its
+ * copies, so that the call records MOE_DEV_TIMEOUT).
  *   d_w1  [E, 2I, H]: rows [0, I) gate, rows [I, 2I) up;  d_w2  [E, H, I].
  *   codes and scales 16-byte aligned.
  * The query is host arithmetic.  The weights are read in place (kept by the
@@ -593,7 +611,8 @@ MOE_API moe_status moe_fp4_create(const moe_dims* dims, int64_t max_tokens, cons
  * token without an active slot gets zeros.  d_out BF16 [num_tokens, hidden].
  * d_x and d_out 16-byte aligned.  An id outside [-1, E) sets
  * MOE_DEV_ROUTE_RANGE and its slot is skipped; MOE_FLAG_CHECK_ROUTES adds the
- * duplicate and finite-weight checks.  Asynchronous on `stream`, capturable in
+ * duplicate and finite-weight checks.  A token's active ids are distinct: where
+ * an expert is named twice its output is undefined.  Asynchronous on `stream`, capturable in
  * a CUDA graph.  num_tokens 0 is a no-op; MOE_ERR_CAPACITY above max_tokens.
  */
 MOE_API moe_status moe_fp4_forward(moe_fp4_handle* h, const uint16_t* d_x, const int32_t* d_topk_idx,

@@ -53,6 +53,7 @@ API_NAMES = ("moe_workspace_query", "moe_create", "moe_quantize_weights", "moe_q
              "moe_stage_inputs", "moe_forward", "moe_read_status", "moe_debug_views",
              "moe_set_profile_events", "moe_set_sm_budget", "moe_forward_plan", "moe_route_noalloc",
              "moe_destroy", "moe_status_str", "moe_add_rms_norm", "moe_topk_route",
+             "moe_forward_quantized",
              "moe_fp4_workspace_query", "moe_fp4_create", "moe_fp4_forward",
              "moe_fp4_linear_workspace_query", "moe_fp4_linear_create", "moe_fp4_linear",
              "moe_fp4_read_status", "moe_fp4_destroy")
@@ -111,6 +112,7 @@ def lib() -> ctypes.CDLL:
         L.moe_bind_weights.argtypes = [vp, vp, vp, vp, vp, vp]
         L.moe_stage_inputs.argtypes = [vp, vp]
         L.moe_forward.argtypes = [vp, vp, vp, vp, i64, vp]
+        L.moe_forward_quantized.argtypes = [vp, vp, vp, vp, vp, i64, vp]
         L.moe_read_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
         L.moe_debug_views.argtypes = [vp, ctypes.POINTER(moe_debug_view)]
         L.moe_set_profile_events.argtypes = [vp, ctypes.POINTER(vp), i32]
@@ -211,6 +213,11 @@ def moe_stage_inputs(h, d_out) -> None:
 
 def moe_forward(h, d_x, d_idx, d_w, num_tokens, stream) -> None:
     _check(lib().moe_forward(h, d_x, d_idx, d_w, num_tokens, stream), "moe_forward")
+
+
+def moe_forward_quantized(h, d_xq, d_xq_scale, d_idx, d_w, num_tokens, stream) -> None:
+    _check(lib().moe_forward_quantized(h, d_xq, d_xq_scale, d_idx, d_w, num_tokens, stream),
+           "moe_forward_quantized")
 
 
 def moe_forward_status(h, d_x, d_idx, d_w, num_tokens, stream) -> int:

@@ -493,16 +493,19 @@ moe_status moe_stage_inputs(moe_handle* h, uint16_t* d_out) {
   return MOE_OK;
 }
 
-moe_status moe_forward(moe_handle* h, const uint16_t* d_x, const int32_t* d_topk_idx,
-                       const float* d_topk_w, int64_t num_tokens, struct CUstream_st* stream) {
+// moe_forward (d_x) and moe_forward_quantized (d_xq, d_xs).
+static moe_status forward_any(moe_handle* h, const uint16_t* d_x, const uint8_t* d_xq,
+                              const uint8_t* d_xs, const int32_t* d_topk_idx, const float* d_topk_w,
+                              int64_t num_tokens, struct CUstream_st* stream) {
   if (!h) return MOE_ERR_INVALID_ARG;
   if (!h->bound || !h->out || (h->L.pt && !h->pt_scales)) return MOE_ERR_NOT_BOUND;
   if (num_tokens < 0) return MOE_ERR_INVALID_ARG;
   if (num_tokens > h->L.max_rows) return MOE_ERR_CAPACITY;
   if (num_tokens == 0) return MOE_OK;
-  if (!d_x || !d_topk_idx || !d_topk_w) return MOE_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(d_x) % 16) return MOE_ERR_INVALID_ARG;
   const Layout& L = h->L;
+  if (!d_topk_idx || !d_topk_w || (!d_x && !d_xq) || (d_xq && !L.pt && !d_xs)) return MOE_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(d_x) % 16 || reinterpret_cast<uintptr_t>(d_xq) % 16)
+    return MOE_ERR_INVALID_ARG;
   const Workspace& ws = h->ws;
   cudaStream_t s = stream;
   const cudaEvent_t* ev = h->n_ev ? h->ev : nullptr;
@@ -545,8 +548,9 @@ moe_status moe_forward(moe_handle* h, const uint16_t* d_x, const int32_t* d_topk
   // per-tensor: the reciprocals and per-expert factors in the weight store
   const float* pt_rx = L.pt ? h->wst.pt + 4 * L.E : nullptr;
   const float* pt_rh = L.pt ? h->wst.pt + 4 * L.E + 1 : nullptr;
-  if (launch_quant_dispatch(ws, L, d_x, num_tokens, s, pdl, stream_ctas, h->quant_resident[0],
-                            h->quant_resident[1], pt_rx) != cudaSuccess)
+  if ((d_xq ? launch_dispatch_quantized(ws, L, d_xq, d_xs, num_tokens, s, pdl, stream_ctas)
+            : launch_quant_dispatch(ws, L, d_x, num_tokens, s, pdl, stream_ctas, h->quant_resident[0],
+                                    h->quant_resident[1], pt_rx)) != cudaSuccess)
     return MOE_ERR_CUDA;
 
   GemmArgs g1;
@@ -662,6 +666,17 @@ moe_status moe_forward(moe_handle* h, const uint16_t* d_x, const int32_t* d_topk
     return MOE_ERR_CUDA;
   if (ev) record_event(ev[9], s);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status moe_forward(moe_handle* h, const uint16_t* d_x, const int32_t* d_topk_idx,
+                       const float* d_topk_w, int64_t num_tokens, struct CUstream_st* stream) {
+  return forward_any(h, d_x, nullptr, nullptr, d_topk_idx, d_topk_w, num_tokens, stream);
+}
+
+moe_status moe_forward_quantized(moe_handle* h, const uint8_t* d_xq, const uint8_t* d_xq_scale,
+                                 const int32_t* d_topk_idx, const float* d_topk_w, int64_t num_tokens,
+                                 struct CUstream_st* stream) {
+  return forward_any(h, nullptr, d_xq, d_xq_scale, d_topk_idx, d_topk_w, num_tokens, stream);
 }
 
 moe_status moe_read_status(moe_handle* h, uint32_t* h_status, struct CUstream_st* stream) {

@@ -96,7 +96,8 @@ struct Fp4Args {
   int T, E, K, group;   // group: tokens of one operand item, at most 8 NT
   int b_bytes, stages;
   uint32_t stage_rcp;   // floor(2^32 / stages) + 1
-  bool check, f32;
+  uint64_t wait_ns;     // limit of every wait
+  bool check, f32, watchdog_test;
 };
 
 __host__ __device__ inline int padded_units(int cols) { return (cols + kUnitCols - 1) / kUnitCols; }
@@ -165,6 +166,15 @@ struct Fp4Maps {
   CUtensorMap unit[2], box[2];
 };
 
+// What bounds every wait: the CTA's abort flag (when one warp gives up the others
+// do), the status word that it marks, and the time.  In shared memory, so that it
+// costs registers only where a warp does wait.
+struct WaitLimit {
+  int abort;
+  uint32_t* status;
+  uint64_t ns;
+};
+
 struct Fp4Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t bfull[2][kItems], bempty[2][kItems];
@@ -186,7 +196,7 @@ struct Fp4Shared {
   int done[kConsumers];                 // sums each consumer has left
   int taken[kConsumers][2];             // by place of a sum: how many were taken from it
   int nv;
-  int abort;
+  WaitLimit lim;
 };
 
 template <bool MOE, int NT>
@@ -379,6 +389,10 @@ __device__ __forceinline__ void copy_scale_row(uint32_t dst, const uint8_t* src,
   }
 }
 
+__device__ __forceinline__ bool gave_up(const WaitLimit& lim) {
+  return *const_cast<const volatile int*>(&lim.abort) != 0;
+}
+
 // Counts in shared memory that one warp raises and others wait for: cheaper than
 // an mbarrier where lanes wait on different ones.
 __device__ __forceinline__ int load_count(const int* count) {
@@ -391,14 +405,14 @@ __device__ __forceinline__ void store_count(int* count, int v) {
   asm volatile("st.release.cta.shared.s32 [%0], %1;" ::"r"(smem_u32(count)), "r"(v) : "memory");
 }
 
-__device__ __noinline__ bool wait_count_slow(const int* count, int n, volatile int* abort, uint32_t* status) {
+__device__ __noinline__ bool wait_count_slow(const int* count, int n, WaitLimit& lim) {
   const uint64_t t0 = globaltimer_ns();
   bool ok;
   while (!(ok = __all_sync(0xFFFFFFFFu, load_count(count) >= n))) {
-    if (__any_sync(0xFFFFFFFFu, *abort != 0)) break;
-    if (__any_sync(0xFFFFFFFFu, globaltimer_ns() - t0 > kWaitLimitNs)) {
-      *abort = 1;
-      record_status(status, MOE_DEV_TIMEOUT);
+    if (__any_sync(0xFFFFFFFFu, gave_up(lim))) break;
+    if (__any_sync(0xFFFFFFFFu, globaltimer_ns() - t0 > lim.ns)) {
+      lim.abort = 1;
+      record_status(lim.status, MOE_DEV_TIMEOUT);
       break;
     }
   }
@@ -407,18 +421,31 @@ __device__ __noinline__ bool wait_count_slow(const int* count, int n, volatile i
 }
 
 // Bounded wait of a whole warp until every lane's count has reached its n.
-__device__ __forceinline__ bool wait_count(const int* count, int n, volatile int* abort, uint32_t* status) {
+__device__ __forceinline__ bool wait_count(const int* count, int n, WaitLimit& lim) {
   if (__all_sync(0xFFFFFFFFu, load_count(count) >= n)) {
     __syncwarp();
     return true;
   }
-  return wait_count_slow(count, n, abort, status);
+  return wait_count_slow(count, n, lim);
+}
+
+__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, WaitLimit& lim) {
+  return mbar_wait_bounded(bar, parity, &lim.abort, lim.status, lim.ns);
 }
 
 // Bounded wait of a whole warp: all of its lanes go on, or none.
-__device__ __forceinline__ bool warp_wait(uint64_t& bar, uint32_t parity, volatile int* abort,
-                                          uint32_t* status) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bar), parity, abort, status));
+__device__ __forceinline__ bool warp_wait(uint64_t& bar, uint32_t parity, WaitLimit& lim) {
+  const uint32_t b = smem_u32(&bar);
+  return __all_sync(0xFFFFFFFFu, mbar_test_wait(b, parity) || bar_wait_slow(b, parity, lim));
+}
+
+// The same for copies in flight to this CTA's memory, which must not outlive it: whoever
+// gives up for another reason still gives them a while.
+__device__ __forceinline__ bool copy_wait(uint64_t& bar, uint32_t parity, WaitLimit& lim) {
+  if (warp_wait(bar, parity, lim)) return true;
+  int none = 0;
+  mbar_wait_bounded(smem_u32(&bar), parity, &none, nullptr, 100000000ull);
+  return false;
 }
 
 // Within a unit of 512 columns lane t of an MMA owns columns 128 t .. 128 t + 127
@@ -443,8 +470,8 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// Brings `bytes` (a multiple of 16) to shared memory and waits.  The places were
-// read and written through the generic proxy before: a fence orders them.
+// Before bulk copies of `bytes` to places that were read and written through the
+// generic proxy before: a fence orders them.
 __device__ __forceinline__ void raw_begin(uint64_t& bar, uint32_t bytes) {
   fence_proxy_async_smem();
   mbar_arrive_expect_tx(smem_u32(&bar), bytes);
@@ -496,15 +523,15 @@ __device__ __forceinline__ void turn_unit(uint32_t row, int u, uint4 (&v)[2], fl
 // then turned in place, unit by unit, to half times 2^s with zeros up to the
 // unit's end.
 __device__ __forceinline__ bool fill_x(const uint16_t* src, int cols, uint32_t dst, uint64_t& bar,
-                                       uint32_t& parity, float* rscale, volatile int* abort,
-                                       uint32_t* status, uint64_t* go) {
+                                       uint32_t& parity, float* rscale, WaitLimit& lim,
+                                       uint64_t* go) {
   const int lane = threadIdx.x & 31, n = cols >> 3, U = padded_units(cols);
   if (lane == 0) {
     raw_begin(bar, cols * 2);
     bulk_load(dst, src, cols * 2, smem_u32(&bar));
     if (go) mbar_arrive(smem_u32(go));
   }
-  if (!warp_wait(bar, parity, abort, status)) return false;
+  if (!copy_wait(bar, parity, lim)) return false;
   parity ^= 1;
   uint32_t m = 0u;
 #pragma unroll 2
@@ -528,9 +555,9 @@ __device__ __forceinline__ bool fill_x(const uint16_t* src, int cols, uint32_t d
 // barriers, also one that gave up on the copies.
 __device__ __forceinline__ bool fill_x_rows(int T, int cols, uint32_t rows, int pitch, int rank, int warps,
                                             uint64_t& bar, uint32_t* row_max, float* rscale,
-                                            volatile int* abort, uint32_t* status) {
+                                            WaitLimit& lim) {
   const int lane = threadIdx.x & 31, n = cols >> 3, U = padded_units(cols);
-  const bool ok = warp_wait(bar, 0, abort, status);
+  const bool ok = copy_wait(bar, 0, lim);
   // (two units at a time)
   for (int i = rank; i < T * U; i += 2 * warps) {
     const int t0 = i / U, j = i + warps, t1 = j / U;
@@ -572,8 +599,7 @@ __device__ __forceinline__ uint32_t half_pow2_neg(int d) {
 // One h row: halves with one exponent per 16 (value = half * 2^-e) as halves of
 // the row's common exponent, turned in place like x.
 __device__ __forceinline__ bool fill_h(const uint8_t* src, int cols, uint32_t dst, uint64_t& bar,
-                                       uint32_t& parity, float* rscale, volatile int* abort,
-                                       uint32_t* status) {
+                                       uint32_t& parity, float* rscale, WaitLimit& lim) {
   const int lane = threadIdx.x & 31, n = cols >> 3, U = padded_units(cols);
   const uint32_t ex = dst + U * (kUnitCols * 2);
   if (lane == 0) {
@@ -581,7 +607,7 @@ __device__ __forceinline__ bool fill_h(const uint8_t* src, int cols, uint32_t ds
     bulk_load(dst, src, cols * 2, smem_u32(&bar));
     bulk_load(ex, src + cols * 2, exponent_bytes(cols), smem_u32(&bar));
   }
-  if (!warp_wait(bar, parity, abort, status)) return false;
+  if (!copy_wait(bar, parity, lim)) return false;
   parity ^= 1;
   auto exponent = [&](int block) {
     int e;
@@ -732,7 +758,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       mbar_init(smem_u32(&sm.bempty[0][0] + (i - 64)), kConsumers + (i - 64 < kItems ? kEpilogues : 1));
     } else if (i == 128) {
       mbar_init(smem_u32(&sm.go), kLoaders);
-      sm.abort = 0;
+      sm.lim = {0, a.status, a.wait_ns};
       for (int k = 0; k < kProducers; ++k) sm.issued[k] = 0;
       for (int p = 0; p < (MOE ? 2 : 1); ++p) {
         prefetch_tensormap(&maps.unit[p]);
@@ -774,6 +800,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
   constexpr int kTableThreads = 32 * kWarpLoader;
   static_assert(kTableThreads >= kFp4MaxRoutes, "one thread per route");
   bool rows_ok = true;
+  WaitLimit& lim = sm.lim;
   if (warp_id < kWarpLoader) {
     if (threadIdx.x < kFp4MaxRoutes) {
       build_items<MOE>(a, sm, route, route_w);
@@ -787,13 +814,12 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     if (early) {
       if (loader && lane == 0) mbar_arrive(smem_u32(&sm.go));
       rows_ok = fill_x_rows(a.T, a.m[0].cols, brow0, row_bytes(a.m[0].cols, false), warp_id - kWarpLoader,
-                            kLoaders + kConsumers, sm.raw[0], sm.row_max, sm.rscale[0], &sm.abort, a.status);
+                            kLoaders + kConsumers, sm.raw[0], sm.row_max, sm.rscale[0], lim);
     }
     asm volatile("bar.sync 4, %0;" ::"n"(kFp4Threads) : "memory");
   }
   const Ctx c{a, sm, sm.nv};
   constexpr int kPhases = MOE ? 2 : 1;
-  volatile int* abort = &sm.abort;
 
   if (MOE && c.nv == 0) {  // no active route: zeros
     uint4* o = reinterpret_cast<uint4*>(a.y);
@@ -830,7 +856,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][last_item % kItems]));
           }
-          if (!res && !warp_wait(sm.bfull[p][it.item % kItems], (it.item / kItems) & 1, abort, a.status))
+          if (!res && !warp_wait(sm.bfull[p][it.item % kItems], (it.item / kItems) & 1, lim))
             return false;
         }
         // this warp's units of the visit: columns from 512 k, k = first, first + dk, .. < last
@@ -856,8 +882,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             const int lap = (int)__umulhi((uint32_t)nu, a.stage_rcp), slot = nu - lap * a.stages;
             // Only once the unit's copies have begun is the place in this lap's
             // phase, and the parity that of this lap
-            if (!wait_count(&sm.issued[nu % kProducers], nu / kProducers + 1, abort, a.status)) return false;
-            if (!warp_wait(sm.full[slot], lap & 1, abort, a.status)) return false;
+            if (!wait_count(&sm.issued[nu % kProducers], nu / kProducers + 1, lim)) return false;
+            if (!warp_wait(sm.full[slot], lap & 1, lim)) return false;
             const uint8_t* base = smem + slot * kCodeBytes + (t >> 1) * (2 * kBoxBytes) + g * 128;
             const uint8_t* sbase = smem + (srow0 - ring) + slot * kScaleBytes + g * 32 + 8 * t;
             uint2 s[4];
@@ -922,7 +948,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
               }
             }
           }
-          if (!wait_count(&sm.taken[warp][pc & 1], pc >> 1, abort, a.status)) return false;
+          if (!wait_count(&sm.taken[warp][pc & 1], pc >> 1, lim)) return false;
           const uint32_t dst = pbuf + (2 * warp + (pc & 1)) * kPartBytes + lane * 16;
 #pragma unroll
           for (int m = 0; m < 2; ++m)
@@ -958,7 +984,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     auto issue = [&](auto phase_constant, const Phase& f, int k, int row, int row16, int64_t lane_row,
                      int tile, int expert, uint64_t policy) {
       constexpr int p = decltype(phase_constant)::value;
-      if (!warp_wait(sm.empty[slot], parity, abort, a.status)) return false;
+      if (!warp_wait(sm.empty[slot], parity, lim)) return false;
       const Fp4Matrix& m = a.m[p];
       const int ng = f.cols >> 4;
       const uint32_t bar = smem_u32(&sm.full[slot]), dst = ring + slot * kCodeBytes;
@@ -1015,7 +1041,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       return v + 1 < c.nv && sm.vexp[v + 1] == sm.vexp[v] ? keep : pass;
     };
     // the first operand rows go ahead of the weights
-    bool ok = warp_wait(sm.go, 0, abort, a.status);
+    bool ok = warp_wait(sm.go, 0, lim);
+    if (MOE && a.watchdog_test && blockIdx.x == 0 && pw == 0) ok = false;  // its copies are missing
     int to_mine = pw;  // units until this warp's next one
     {
       const Phase& f = c.phase(0);
@@ -1054,7 +1081,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     }
     // no copy outlives the CTA, also when the other warps have given up
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (*abort && lane < a.stages) {
+    if (gave_up(lim) && lane < a.stages) {
       int none = 0;
       for (int i = 0; i < 2; ++i)
         mbar_wait_bounded(smem_u32(&sm.full[lane]), i, &none, nullptr, 100000000ull);
@@ -1073,7 +1100,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       from = (first + step * lane) & (kConsumers - 1);
       const int n = __shfl_sync(0xFFFFFFFFu, left, from);
       src = pbuf + (2 * from + (n & 1)) * kPartBytes;
-      return wait_count(&sm.done[from], lane < cnt ? n + 1 : 0, abort, a.status);
+      return wait_count(&sm.done[from], lane < cnt ? n + 1 : 0, lim);
     };
     auto give_back = [&](int from, int cnt) {
       __syncwarp();
@@ -1376,12 +1403,12 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         if (lane == 0) {
           const uint64_t t0 = globaltimer_ns();
           while (ld_acquire_gpu_u32(&a.ctl[0]) < kEpilogues * gridDim.x) {
-            if (*abort) {
+            if (gave_up(lim)) {
               ok = false;
               break;
             }
-            if (globaltimer_ns() - t0 > kWaitLimitNs) {
-              *abort = 1;
+            if (globaltimer_ns() - t0 > lim.ns) {
+              lim.abort = 1;
               record_status(a.status, MOE_DEV_TIMEOUT);
               ok = false;
               break;
@@ -1399,14 +1426,14 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       const int RB = row_bytes(f.cols, p == 1);
       if (c.resident(p)) {
         // the rows' memory is the next phase's when everyone is done with them
-        if (p + 1 < kPhases && !warp_wait(sm.bempty[p][0], 0, abort, a.status)) goto done;
+        if (p + 1 < kPhases && !warp_wait(sm.bempty[p][0], 0, lim)) goto done;
       } else {
         const int R = c.ring_rows(p);
         ItemWalk it;
         int oldest = 0, used = 0, counter = 0;
         int rows_of[kItems];  // rows of the items in flight
         auto retire = [&]() {
-          if (!warp_wait(sm.bempty[p][oldest % kItems], (oldest / kItems) & 1, abort, a.status))
+          if (!warp_wait(sm.bempty[p][oldest % kItems], (oldest / kItems) & 1, lim))
             return false;
 #pragma unroll
           for (int i = 0; i < kItems; ++i)
@@ -1429,11 +1456,9 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
               const int s = sm.vstart[at.v] + r, place = c.row_slot(false, it.pos, R, 0, r);
               const bool ok =
                   p == 0 ? fill_x(a.x + sm.route_tok[s] * a.ldx, f.cols, brow0 + place * RB, sm.raw[lw],
-                                  raw_parity, &sm.rscale[0][place], abort, a.status,
-                                  went ? nullptr : &sm.go)
+                                  raw_parity, &sm.rscale[0][place], lim, went ? nullptr : &sm.go)
                          : fill_h(a.h + (int64_t)sm.route_id[s] * record_bytes(f.cols), f.cols,
-                                  brow0 + place * RB, sm.raw[lw], raw_parity, &sm.rscale[1][place], abort,
-                                  a.status);
+                                  brow0 + place * RB, sm.raw[lw], raw_parity, &sm.rscale[1][place], lim);
               went = true;
               if (!ok) goto done;
             }
@@ -1556,7 +1581,7 @@ bool fp4_dims_ok(const moe_dims* d) {
   const bool ik = d->inter >= 128 && d->inter <= 16384 && d->inter % 128 == 0;
   const bool kk = d->top_k == 1 || d->top_k == 2 || d->top_k == 4 || d->top_k == 6 || d->top_k == 8;
   return hk && ik && kk && d->num_experts >= 1 && d->num_experts <= 1024 &&
-         (d->flags & ~MOE_FLAG_CHECK_ROUTES) == 0;
+         (d->flags & ~(MOE_FLAG_CHECK_ROUTES | MOE_FLAG_WATCHDOG_TEST)) == 0;
 }
 
 bool misaligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
@@ -1711,6 +1736,8 @@ moe_status moe_fp4_forward(moe_fp4_handle* h, const uint16_t* d_x, const int32_t
   a.stages = p.stages;
   a.stage_rcp = (uint32_t)(0x100000000ull / p.stages) + 1;
   a.check = (d.flags & MOE_FLAG_CHECK_ROUTES) != 0;
+  a.watchdog_test = (d.flags & MOE_FLAG_WATCHDOG_TEST) != 0;
+  a.wait_ns = a.watchdog_test ? 20000000ull : kWaitLimitNs;
   return fp4_launch<true, 1>(h->maps, a, h->grid, p.smem, stream) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
@@ -1781,6 +1808,7 @@ moe_status moe_fp4_linear(moe_fp4_handle* h, const uint16_t* d_x, int64_t x_stri
   a.stages = p.stages;
   a.stage_rcp = (uint32_t)(0x100000000ull / p.stages) + 1;
   a.f32 = y_float32 != 0;
+  a.wait_ns = kWaitLimitNs;
   const cudaError_t e = p.nt == 2
                             ? fp4_launch<false, 2>(h->maps, a, h->grid, p.smem, stream)
                             : fp4_launch<false, 1>(h->maps, a, h->grid, p.smem, stream);

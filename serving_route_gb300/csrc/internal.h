@@ -109,6 +109,10 @@ int quant_dispatch_resident(int fmt, int batch);
 cudaError_t launch_quant_dispatch(const Workspace& ws, const Layout& L, const uint16_t* x,
                                   int64_t T, cudaStream_t s, bool pdl, int max_ctas,
                                   int resident2, int resident4, const float* pt_rx);
+// the same rows from activations that come quantised (xs: E8M0 bytes, unused per-tensor)
+cudaError_t launch_dispatch_quantized(const Workspace& ws, const Layout& L, const uint8_t* xq,
+                                      const uint8_t* xs, int64_t T, cudaStream_t s, bool pdl,
+                                      int max_ctas);
 cudaError_t launch_swiglu_quant(const Workspace& ws, const Layout& L, int max_ctas, cudaStream_t s,
                                 bool pdl, const float* pt_rh);
 cudaError_t launch_quantize_weights_pt(const float* w, int64_t nmat, int rows, int cols, uint8_t* q,

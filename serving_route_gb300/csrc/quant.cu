@@ -63,6 +63,27 @@ __device__ __forceinline__ float group8_max(float v) {
   return v;
 }
 
+// A lane's 16 codes of block b, and its scale byte, to the GEMM rows of the
+// token's routes (lane k of p_lane: the k-th route's row, or -1).
+template <bool MX>
+__device__ __forceinline__ void dispatch_store(const uint4 q, uint8_t scale, bool valid, int p_lane,
+                                               int b, int H, int K, int l8, uint8_t* __restrict__ a,
+                                               uint8_t* __restrict__ a_sf) {
+  const int KB = H >> 7;
+  for (int k = 0; k < K; ++k) {
+    const int p = __shfl_sync(0xFFFFFFFFu, p_lane, k);
+    if (p >= 0 && valid) {
+      *reinterpret_cast<uint4*>(a + blocked_offset(p, b * 128 + l8 * 16, H)) = q;
+      if (MX) {
+        // scale unit = 32-wide chunk 4b + l8/2 of the row
+        if ((l8 & 1) == 0) a_sf[sf_atom_offset(p, 4 * b + (l8 >> 1), 4 * KB)] = scale;
+      } else if (l8 == 0) {
+        a_sf[sf_atom_offset(p, b, KB)] = scale;
+      }
+    }
+  }
+}
+
 // FMT 0: one power-of-two scale per 128 columns; 1 (MXFP8): one per 32
 // columns (a lane pair); 2 (per-tensor): the static scale's float reciprocal
 // rx for every value, block scales 1.
@@ -101,19 +122,7 @@ __device__ __forceinline__ void quant_dispatch_unit(const uint4 (&raw)[2], bool 
   q.y = e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
   q.z = e4m3x4(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv);
   q.w = e4m3x4(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv);
-  const int KB = H >> 7;
-  for (int k = 0; k < K; ++k) {
-    const int p = __shfl_sync(0xFFFFFFFFu, p_lane, k);
-    if (p >= 0 && valid) {
-      *reinterpret_cast<uint4*>(a + blocked_offset(p, b * 128 + l8 * 16, H)) = q;
-      if (MX) {
-        // scale unit = 32-wide chunk 4b + l8/2 of the row
-        if ((l8 & 1) == 0) a_sf[sf_atom_offset(p, 4 * b + (l8 >> 1), 4 * KB)] = (uint8_t)(e + 127);
-      } else if (l8 == 0) {
-        a_sf[sf_atom_offset(p, b, KB)] = (uint8_t)(e + 127);
-      }
-    }
-  }
+  dispatch_store<MX>(q, (uint8_t)(e + 127), valid, p_lane, b, H, K, l8, a, a_sf);
 }
 
 // B = 2: two units per pass, one unit per warp while the grid is not capped.
@@ -168,6 +177,36 @@ __global__ void __launch_bounds__(256, B == 4 ? 4 : 1) quant_dispatch_kernel(
 #pragma unroll
     for (int i = 0; i < B; ++i)
       quant_dispatch_unit<FMT>(r[i], v[i], p[i], b[i], H, K, l8, rx, a, a_sf);
+  }
+  pdl_trigger();
+}
+
+// The dispatch of activations that come quantised (E4M3 codes [T, H], E8M0 bytes
+// [T, H/128], or [T, H/32] under MXFP8, none per-tensor): quant_dispatch's walk and
+// stores without its arithmetic, at half the bytes read.  Unlike there the codes
+// are read after the programmatic wait: the routing kernel's launch may overlap
+// whatever wrote them.
+template <int FMT>
+__global__ void __launch_bounds__(256) dispatch_quantized_kernel(
+    const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs,
+    const int32_t* __restrict__ inv_pad, int64_t T, int H, int K, uint8_t* __restrict__ a,
+    uint8_t* __restrict__ a_sf) {
+  const int lane = threadIdx.x & 31, grp = lane >> 3, l8 = lane & 7;
+  const int KB = H >> 7, units = (KB + 3) >> 2;
+  const int64_t total = T * units, nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  pdl_wait();
+  for (int64_t u = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; u < total; u += nwarps) {
+    const int t = (int)(u / units), b = (int)(u - (int64_t)t * units) * 4 + grp;
+    const bool valid = b < KB;
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    uint8_t s = 127;
+    if (valid) {
+      q = *reinterpret_cast<const uint4*>(xq + (int64_t)t * H + b * 128 + l8 * 16);
+      if (FMT == 0) s = xs[(int64_t)t * KB + b];
+      if (FMT == 1) s = xs[((int64_t)t * KB + b) * 4 + (l8 >> 1)];
+    }
+    const int p = lane < K ? inv_pad[(int64_t)t * K + lane] : -1;
+    dispatch_store<FMT == 1>(q, s, valid, p, b, H, K, l8, a, a_sf);
   }
   pdl_trigger();
 }
@@ -492,6 +531,16 @@ cudaError_t launch_quant_dispatch(const Workspace& ws, const Layout& L, const ui
                     : (fmt == 1 ? quant_dispatch_kernel<1, 2> : quant_dispatch_kernel<0, 2>);
   return launch_k(k, dim3(g2), dim3(256), 0, s, pdl, nullptr, x, (const int32_t*)ws.inv_pad, T,
                   L.H, L.K, pt_rx, ws.a, ws.a_sf);
+}
+
+cudaError_t launch_dispatch_quantized(const Workspace& ws, const Layout& L, const uint8_t* xq,
+                                      const uint8_t* xs, int64_t T, cudaStream_t s, bool pdl,
+                                      int max_ctas) {
+  const int64_t units = T * ((L.H / 128 + 3) / 4);
+  auto k = L.pt ? dispatch_quantized_kernel<2>
+                : (L.mx ? dispatch_quantized_kernel<1> : dispatch_quantized_kernel<0>);
+  return launch_k(k, dim3(stream_grid(units, 8, max_ctas)), dim3(256), 0, s, pdl, nullptr, xq, xs,
+                  (const int32_t*)ws.inv_pad, T, L.H, L.K, ws.a, ws.a_sf);
 }
 
 cudaError_t launch_swiglu_quant(const Workspace& ws, const Layout& L, int max_ctas,

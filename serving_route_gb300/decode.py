@@ -191,10 +191,11 @@ class Fp4MoELayer(_Fp4Handle):
     object must not overlap on the GPU."""
 
     def __init__(self, hidden: int, inter: int, num_experts: int, top_k: int, *, max_tokens: int = 16,
-                 check_routes: bool = True):
+                 check_routes: bool = True, watchdog_test: bool = False):
         self.H, self.I, self.E, self.K = hidden, inter, num_experts, top_k
         self.max_tokens = max_tokens
-        self.flags = B.MOE_FLAG_CHECK_ROUTES if check_routes else 0
+        self.flags = ((B.MOE_FLAG_CHECK_ROUTES if check_routes else 0)
+                      | (B.MOE_FLAG_WATCHDOG_TEST if watchdog_test else 0))
         self._ws_bytes = B.moe_fp4_workspace_query(hidden, inter, num_experts, top_k, self.flags, max_tokens)
 
     def bind_weights(self, w1, w1_scales, w1_global, w2, w2_scales, w2_global, stream=None) -> None:

@@ -170,6 +170,25 @@ class MegaMoELayer:
                       _stream_ptr(stream))
         return self.out[:T]
 
+    def forward_quantized(self, xq: torch.Tensor, xq_scale: torch.Tensor | None,
+                          topk_idx: torch.Tensor, topk_w: torch.Tensor, stream=None) -> torch.Tensor:
+        """forward() of activations in this layer's format, as add_rms_norm(fmt=...) gives
+        them: xq uint8 E4M3 codes [T, H], xq_scale uint8 E8M0 bytes [T, H/128] ("mxfp8":
+        [T, H/32]; "per_tensor": None)."""
+        T = xq.shape[0]
+        cols = {"deepseek": self.H // 128, "mxfp8": self.H // 32}.get(self.fmt)
+        assert xq.dtype == torch.uint8 and xq.is_cuda and xq.is_contiguous() and tuple(xq.shape) == (T, self.H)
+        if cols is None:
+            assert xq_scale is None
+        else:
+            assert xq_scale.dtype == torch.uint8 and xq_scale.is_cuda and xq_scale.is_contiguous()
+            assert tuple(xq_scale.shape) == (T, cols)
+        assert topk_idx.dtype == torch.int32 and topk_w.dtype == torch.float32
+        B.moe_forward_quantized(self.handle, xq.data_ptr(),
+                                xq_scale.data_ptr() if xq_scale is not None else None,
+                                topk_idx.data_ptr(), topk_w.data_ptr(), T, _stream_ptr(stream))
+        return self.out[:T]
+
     def set_sm_budget(self, max_sms: int) -> None:
         """Cap the SMs the following forwards occupy (0: every SM)."""
         B.moe_set_sm_budget(self.handle, max_sms)
