@@ -95,7 +95,6 @@ struct Fp4Args {
   float* part[2];       // by phase, [152][2][..]: a CTA's cut tiles, first and last
   int T, E, K, group;   // group: tokens of one operand item, at most 8 NT
   int b_bytes, stages;
-  uint32_t stage_rcp;   // floor(2^32 / stages) + 1
   uint64_t wait_ns;     // limit of every wait
   bool check, f32, watchdog_test;
 };
@@ -839,51 +838,76 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     int n0 = 0;     // the CTA's units before this segment: its n-th unit is warp n mod 8's
     auto consume = [&](auto phase_constant) {
       constexpr int p = decltype(phase_constant)::value;
+      // what the walk needs of the phase, in registers: reading it where it is used costs a
+      // round trip to shared memory each time (a tile's set-up took 1200 clocks)
       const Phase& f = c.phase(p);
-      if (f.u0 >= f.u1) return true;
+      const int u0 = f.u0, u1 = f.u1, U = f.U, visit = f.visit(), inner = p == 0 ? f.RT : f.nv;
+      if (u0 >= u1) return true;
       const int RB = row_bytes(f.cols, p == 1);
       const bool res = p == 0 && c.resident(0);
       const int R = c.ring_rows(p);
-      ItemWalk it;
-      const int visit = f.visit();
-      TilePos at = f.at(f.u0);
-      int ka = f.u0 % visit;  // first unit of the visit (second phase: 0)
-      for (int u = f.u0 - ka; u < f.u1; u += visit, f.step(at)) {
-        const int kb = min(visit, f.u1 - u);
-        const int last_item = it.item;
-        if (it.next(c, f, res, R, at)) {
-          if (last_item >= 0) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][last_item % kItems]));
+      int item = -1, pos = 0, rows = 0;
+      const TilePos start = f.at(u0);
+      int v = start.v, left = inner - (p == 0 ? start.j : start.v);  // steps to the next item / tile
+      bool fresh = true;        // a new item
+      const uint8_t* brow[NT];  // this lane's operand rows
+      int ka = u0 % visit;      // first unit of the visit (second phase: 0)
+      // second phase: where the i-th of this warp's units of a visit comes in the order
+      const int full = U >> 1, half = warp & 1;
+      auto place = [&](int i) { return i < full ? 8 * i + warp : 8 * full + (warp >> 1); };
+      // The warp's next unit: its count, place in the ring and lap's parity, and whether its
+      // copies were seen to be there.  Only once the copies have begun is the place in this
+      // lap's phase, and the parity that of this lap.
+      int nu = p == 0 ? warp : n0 + place(0);
+      int slot = (int)((uint32_t)nu % (uint32_t)a.stages), parity = (nu / a.stages) & 1;
+      bool ready = false;
+      for (int u = u0 - ka; u < u1; u += visit) {
+        const int kb = min(visit, u1 - u);
+        if (fresh) {
+          if (!res) {
+            if (item >= 0) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][item % kItems]));
+            }
+            pos += rows;
+            if (pos >= R) pos -= R;
+            ++item;
+            if (!warp_wait(sm.bfull[p][item % kItems], (item / kItems) & 1, lim)) return false;
           }
-          if (!res && !warp_wait(sm.bfull[p][it.item % kItems], (it.item / kItems) & 1, lim))
-            return false;
+          const int s0 = sm.vstart[v];
+          rows = sm.vstart[v + 1] - s0;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int col = min(8 * nt + g, rows - 1);  // columns past the item repeat a row; nothing reads them
+            brow[nt] = smem + (brow0 - ring) + c.row_slot(res, pos, R, s0, col) * RB + t * 16;
+          }
+        }
+        // the next visit's item
+        if (p == 0) {
+          fresh = --left == 0;
+          if (fresh) {
+            ++v;
+            left = inner;
+          }
+        } else if (--left == 0) {
+          v = 0;
+          left = inner;
+        } else {
+          ++v;
         }
         // this warp's units of the visit: columns from 512 k, k = first, first + dk, .. < last
-        const int full = f.U >> 1, half = warp & 1;
-        const int first = p == 0 ? ka + ((warp - n0) & (kConsumers - 1)) : half * (f.U - full);
-        const int last = p == 0 ? kb : half ? f.U : f.U - full;
+        const int first = p == 0 ? ka + ((warp - n0) & (kConsumers - 1)) : half * (U - full);
+        const int last = p == 0 ? kb : half ? U : U - full;
         constexpr int dk = p == 0 ? kConsumers : 1;
         if (first < last) {
           // two sums per tile, so that consecutive MMAs do not wait for each other
           float acc[2][NT][2][4] = {};
-          const int n = c.item_rows(at.v), s0 = sm.vstart[at.v];
-          const uint8_t* brow[NT];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int col = min(8 * nt + g, n - 1);  // columns past n repeat a row; nothing reads them
-            brow[nt] = smem + (brow0 - ring) + c.row_slot(res, it.pos, R, s0, col) * RB + t * 16;
-          }
 #pragma unroll 1
           for (int k = first; k < last; k += dk) {
-            // the unit's count, which gives its place in the ring
-            const int i = k - first;
-            const int nu = n0 + (p == 0 ? k - ka : i < full ? 8 * i + warp : 8 * full + (warp >> 1));
-            const int lap = (int)__umulhi((uint32_t)nu, a.stage_rcp), slot = nu - lap * a.stages;
-            // Only once the unit's copies have begun is the place in this lap's
-            // phase, and the parity that of this lap
-            if (!wait_count(&sm.issued[nu % kProducers], nu / kProducers + 1, lim)) return false;
-            if (!warp_wait(sm.full[slot], lap & 1, lim)) return false;
+            if (!ready) {
+              if (!wait_count(&sm.issued[nu % kProducers], nu / kProducers + 1, lim)) return false;
+              if (!warp_wait(sm.full[slot], parity, lim)) return false;
+            }
             const uint8_t* base = smem + slot * kCodeBytes + (t >> 1) * (2 * kBoxBytes) + g * 128;
             const uint8_t* sbase = smem + (srow0 - ring) + slot * kScaleBytes + g * 32 + 8 * t;
             uint2 s[4];
@@ -909,6 +933,20 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
               if (half == 1) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm.empty[slot]));
+                // on to the next one (at most a lap further), looked at while this one's
+                // products are under way
+                const int i = k - first, step = p == 0 ? kConsumers
+                                                : i + 1 < last - first ? place(i + 1) - place(i)
+                                                                       : visit + place(0) - place(i);
+                nu += step;
+                slot += step;
+                if (slot >= a.stages) {
+                  slot -= a.stages;
+                  parity ^= 1;
+                }
+                const bool begun = load_count(&sm.issued[nu % kProducers]) > nu / kProducers;
+                ready = mbar_test_wait(smem_u32(&sm.full[slot]), parity) && begun;
+                ready = __all_sync(0xFFFFFFFFu, ready);
               }
 #pragma unroll
               for (int jj = 0; jj < 2; ++jj) {
@@ -967,7 +1005,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         ka = 0;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][it.item % kItems]));
+      if (lane == 0) mbar_arrive(smem_u32(&sm.bempty[p][max(item, 0) % kItems]));
       return true;
     };
     if (consume(std::integral_constant<int, 0>{})) {
@@ -1734,7 +1772,6 @@ moe_status moe_fp4_forward(moe_fp4_handle* h, const uint16_t* d_x, const int32_t
   a.group = p.group;
   a.b_bytes = p.b_bytes;
   a.stages = p.stages;
-  a.stage_rcp = (uint32_t)(0x100000000ull / p.stages) + 1;
   a.check = (d.flags & MOE_FLAG_CHECK_ROUTES) != 0;
   a.watchdog_test = (d.flags & MOE_FLAG_WATCHDOG_TEST) != 0;
   a.wait_ns = a.watchdog_test ? 20000000ull : kWaitLimitNs;
@@ -1806,7 +1843,6 @@ moe_status moe_fp4_linear(moe_fp4_handle* h, const uint16_t* d_x, int64_t x_stri
   a.group = p.group;
   a.b_bytes = p.b_bytes;
   a.stages = p.stages;
-  a.stage_rcp = (uint32_t)(0x100000000ull / p.stages) + 1;
   a.f32 = y_float32 != 0;
   a.wait_ns = kWaitLimitNs;
   const cudaError_t e = p.nt == 2
