@@ -7,32 +7,41 @@
 //   linear: y = x W^T;   layer: out_t = sum_k w_tk * W2[e] (silu(g) * u),
 //   (g; u) = W1[e] x_t, e = topk_idx[t, k].
 //
-// What bounds it: the weights, 9/16 byte each, are read once and used for a
-// few tokens, so the time is theirs through HBM.  At the copy rate an SM gets
-// about 42 weights per clock, which leaves three issue slots per weight and
-// lane; the loop below takes about 1.3:
-//   * four codes pairs of a 32-bit word become half2 with one hardware convert
+// What bounds it: the weights, 9/16 byte each, are read once and used for a few
+// tokens, so the floor is their time through HBM.  At the copy rate an SM gets
+// about 42 weights a clock; dequantising them costs one convert and one product
+// per two weights, which is as much again, so the two have to overlap.  Measured
+// for the layer of 256 experts, H 7168, I 2048, 16 tokens (2.52 GB): copies alone
+// 374 us, products alone 374 us, the kernel 414 us, 6.1 TB/s.
+//   * four code pairs of a 32-bit word become half2 with one hardware convert
 //     each, one half2 product applies the E4M3 scale (6 significant bits: both
 //     exact in half), and m16n8k16 half MMAs with float accumulators take 8
-//     tokens as their N side.  The checkpoint's order is kept: lane (g, t) owns
-//     128 consecutive columns of rows g and g + 8, so a 16-byte load of codes
-//     feeds eight MMAs of its own, and x is stored in shared memory in the order
-//     in which the same lanes need it.
+//     tokens as their N side.  Up to 16 tokens leave a 128-row tensor-memory MMA
+//     nothing to do that would pay for bringing the dequantised weights back to
+//     shared memory; here they go from registers to the tensor cores.  The
+//     checkpoint's order is kept: lane (g, t) owns 128 consecutive columns of
+//     rows g and g + 8, so a 16-byte load of codes feeds eight MMAs of its own,
+//     and x is stored in shared memory in the order in which the lanes need it.
 //   * x (BF16) and h (float) enter as half, each row multiplied by the power of
 //     two that brings its largest value to [2^14, 2^15): for BF16 values exact
 //     down to 2^-32 of the row's largest, below that rounded at 2^-40 of it; h
 //     is rounded to 11 bits.  The inverse is applied to the float sums.
-//   * a stage of the shared-memory ring is one warp's unit of work, 32 rows x
-//     512 columns (8 KB of codes), copied by TMA as stored; eight warps take the
-//     units in turn, so no barrier but the unit's own stands between the copies
-//     and the MMAs.  The scales (one ninth of the bytes) go to registers, one
-//     unit ahead.
-//   * every CTA owns one contiguous range of the units (of the 152 per phase);
-//     a tile of 32 rows that a range's end cuts is joined from float partial
-//     sums by whichever CTA finishes it last, in the order of the CTAs.
+//   * a place of the shared-memory ring is one consumer warp's unit of work, 32
+//     rows x 512 columns: 8 KB of codes, copied by TMA as stored, and 1 KB of
+//     scales by asynchronous copies (their rows need not be multiples of 16
+//     bytes).  Eight warps take the units in turn, so no barrier but the unit's
+//     own stands between the copies and the MMAs; 12 to 16 places are in flight.
+//   * every CTA owns one contiguous range of a phase's units; a tile that a
+//     range's end cuts is joined from float partial sums by whichever CTA
+//     finishes it last, in the order of the CTAs, so that results never change.
 //   * the layer is one cooperative launch: FC1 units, a grid barrier on h, FC2
 //     units.  The weights' copies do not wait at the barrier: the ring fills
 //     with FC2 weights while the last FC1 sums and h are on their way.
+// Where one token's 47.7 us go (H 7168, I 2048, 8 of 256 experts; 29.2 us at the copy
+// rate): tables and the first copies 5.5 us, FC1 to 25, its last sums and the barrier
+// to 28.7, h rows to 30.8, FC2 to 40.5, joining and leaving to 44, the launch.  FC2
+// there is bound by its products (its first third is in the ring before the barrier
+// opens; sending the rest to L2 ahead made it slower).
 #include <cudaTypedefs.h>
 
 #include <cstring>
@@ -49,9 +58,10 @@ namespace mm {
 constexpr int kFp4MaxTokens = 16;
 constexpr int kFp4MaxRoutes = 128;
 constexpr int kFp4Grid = 152;        // one CTA per SM
-// The warps' roles.  The service warps come first: where several warps of a
-// scheduler are ready it serves the older ones, and the consumers, with
-// instructions ready nearly always, would starve what they wait for.
+// The warps' roles.  More service warps than copies need by their number: each
+// wait and each copy is a chain of round trips, and several chains overlap (two
+// copying warps 449 us, four 409, at 16 tokens; one finishing FC1's tiles 36.9, two
+// 35.6, at 3 tokens of H 2048, I 1408, 64 experts).
 constexpr int kEpilogues = 2;        // add the consumers' sums, finish and join tiles: in turn, the
                                      // second phase's tiles by the first of them
 constexpr int kProducers = 4;        // issue the copies of the weights, in turn
@@ -72,7 +82,9 @@ constexpr int kScaleBytes = 32 * kUnitCols / 16;
 constexpr int kUnitBytes = kCodeBytes + kScaleBytes;
 constexpr int kBoxBytes = 16 * 128;  // 16 rows x 256 columns
 constexpr int kItems = 8;            // operand items in flight (rows ring)
-constexpr int kCutUnits = 15;        // units of imbalance that a tile's join costs (about 3 us)
+// Ranges are cut within tiles where whole tiles would leave the fullest CTA with more
+// than this many units above the mean: a join takes about 3 us, 15 units of copies
+constexpr int kCutUnits = 15;
 constexpr int kTile2 = 128;          // output rows of an FC2 tile
 constexpr int kMaxSmem = 232448;
 
@@ -204,7 +216,7 @@ struct Fp4Ctx {
   Fp4Shared& sm;
   int nv;
 
-  // (units: at most 2^28, the linear's)
+  // (units: below 2^30, also the linear's in 16 groups)
   __device__ Phase make_phase(int p) const {
     Phase f;
     f.p = p;
@@ -228,7 +240,7 @@ struct Fp4Ctx {
 
   __device__ int item_rows(int v) const { return sm.vstart[v + 1] - sm.vstart[v]; }
   // x rows stay for the whole phase where all of them fit; h rows always pass
-  // through the ring, so that the first segment waits for its own rows only
+  // through the ring, so that the first item waits for its own rows only
   __device__ bool resident(int p) const {
     return p == 0 && (int64_t)a.T * row_bytes(a.m[0].cols, false) <= a.b_bytes;
   }
@@ -250,7 +262,7 @@ struct Fp4Ctx {
   }
 };
 
-// Walks the operand items of a phase in segment order.  Resident: all rows stay
+// Walks the operand items of a phase in the order of its visits.  Resident: all rows stay
 // for the phase and there is one item.  Ring: an item is the rows of one token
 // group, for its tiles in a row (first phase) or for one tile, at consecutive ring places.
 struct ItemWalk {
@@ -767,8 +779,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     fence_mbar_init();
   }
   // The kernel before this one in the stream may still be at work; nothing above
-  // reads global memory.  (Of the linear: the layer's cooperative launch does not
-  // overlap.)
+  // reads global memory.  (So the linear is launched; the layer's cooperative launch
+  // does not overlap, and returns from here at once.)
   pdl_wait();
   pdl_trigger();
   // x rows that stay are asked for before anything else: behind the first weights
@@ -835,7 +847,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     // ------------------------------------------------------------ consumers
     const int warp = warp_id - kWarpConsumer, g = lane >> 2, t = lane & 3;
     int pc = 0;     // sums this warp has handed over
-    int n0 = 0;     // the CTA's units before this segment: its n-th unit is warp n mod 8's
+    int n0 = 0;     // the CTA's units before this visit; FC1: its n-th unit is warp n mod 8's
     auto consume = [&](auto phase_constant) {
       constexpr int p = decltype(phase_constant)::value;
       // what the walk needs of the phase, in registers: reading it where it is used costs a
