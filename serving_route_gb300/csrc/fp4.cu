@@ -12,7 +12,7 @@
 // about 42 weights a clock; dequantising them costs one convert and one product
 // per two weights, which is as much again, so the two have to overlap.  Measured
 // for the layer of 256 experts, H 7168, I 2048, 16 tokens (2.52 GB): copies alone
-// 374 us, products alone 374 us, the kernel 414 us, 6.1 TB/s.
+// 374 us, products alone 374 us, the kernel 385 to 413 us, 6.1 to 6.5 TB/s.
 //   * four code pairs of a 32-bit word become half2 with one hardware convert
 //     each, one half2 product applies the E4M3 scale (6 significant bits: both
 //     exact in half), and m16n8k16 half MMAs with float accumulators take 8
@@ -105,8 +105,11 @@ struct Fp4Args {
   uint32_t* status;
   uint32_t* ctl;        // [0] barrier, [1] finished CTAs, [2 + 152 p + c] joins of phase p
   float* part[2];       // by phase, [152][2][..]: a CTA's cut tiles, first and last
-  int T, E, K, group;   // group: tokens of one operand item, at most 8 NT
-  int b_bytes, stages;
+  int T, E, K;
+  // how shared memory is divided: tokens of one operand item (at most 8 NT), bytes of
+  // operand rows, places of the ring.  The layer may have a second division (group 0:
+  // it has not), of which the routes choose.
+  int group[2], b_bytes[2], stages[2];
   uint64_t wait_ns;     // limit of every wait
   bool check, f32, watchdog_test;
 };
@@ -200,13 +203,13 @@ struct Fp4Shared {
   int16_t vexp[kFp4MaxRoutes];
   uint8_t first[kFp4MaxRoutes];
   uint32_t row_max[kFp4MaxTokens];
-  int warp_cnt[4], warp_live[4];
+  int warp_cnt[2][4], warp_live[4];
   uint32_t warp_bits[4];
   Phase phase[2];
   int issued[kProducers];               // units each producer has begun
   int done[kConsumers];                 // sums each consumer has left
   int taken[kConsumers][2];             // by place of a sum: how many were taken from it
-  int nv;
+  int nv, plan;
   WaitLimit lim;
 };
 
@@ -237,15 +240,16 @@ struct Fp4Ctx {
     return f;
   }
   __device__ const Phase& phase(int p) const { return sm.phase[p]; }
+  __device__ int b_bytes() const { return MOE && sm.plan ? a.b_bytes[1] : a.b_bytes[0]; }
 
   __device__ int item_rows(int v) const { return sm.vstart[v + 1] - sm.vstart[v]; }
   // x rows stay for the whole phase where all of them fit; h rows always pass
   // through the ring, so that the first item waits for its own rows only
   __device__ bool resident(int p) const {
-    return p == 0 && (int64_t)a.T * row_bytes(a.m[0].cols, false) <= a.b_bytes;
+    return p == 0 && (int64_t)a.T * row_bytes(a.m[0].cols, false) <= b_bytes();
   }
   __device__ int ring_rows(int p) const {
-    return min(a.b_bytes / row_bytes(a.m[p].cols, p == 1), kFp4MaxRoutes);
+    return min(b_bytes() / row_bytes(a.m[p].cols, p == 1), kFp4MaxRoutes);
   }
   // place of an item's column among the operand rows
   __device__ int row_slot(bool resident, int pos, int R, int s0, int col) const {
@@ -671,12 +675,13 @@ __device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm, int
   if (!MOE) {
     if (tid == 0) {
       int v = 0;
-      for (int t = 0; t < a.T; t += a.group) {
+      for (int t = 0; t < a.T; t += a.group[0]) {
         sm.vexp[v] = 0;
         sm.vstart[v++] = t;
       }
       sm.vstart[v] = a.T;
       sm.nv = v;
+      sm.plan = 0;
       if (blockIdx.x == 0) atomicExch(a.status, 0u);
     }
     if (tid < a.T) sm.route_id[tid] = sm.route_tok[tid] = tid;
@@ -712,7 +717,7 @@ __device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm, int
     sm.route_id[pos] = tid;
     sm.route_tok[pos] = tid / a.K;
     sm.route_w[pos] = w;
-    sm.first[pos] = within % a.group == 0;
+    sm.first[pos] = (within % a.group[0] == 0) | (a.group[1] && within % a.group[1] == 0 ? 2 : 0);
   }
   bits = __reduce_or_sync(0xFFFFFFFFu, bits);
   const int live_here = __popc(__ballot_sync(0xFFFFFFFFu, live));
@@ -721,18 +726,26 @@ __device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm, int
     sm.warp_live[warp] = live_here;
   }
   sync();
-  const bool first = sm.first[tid] != 0;
-  const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, first);
-  if (lane == 0) sm.warp_cnt[warp] = __popc(firsts);
+  const int first = sm.first[tid];
+  const uint32_t firsts[2] = {__ballot_sync(0xFFFFFFFFu, first & 1), __ballot_sync(0xFFFFFFFFu, first & 2)};
+  if (lane == 0) {
+    sm.warp_cnt[0][warp] = __popc(firsts[0]);
+    sm.warp_cnt[1][warp] = __popc(firsts[1]);
+  }
   sync();
-  int v = __popc(firsts & ((1u << lane) - 1u));
-  for (int i = 0; i < warp; ++i) v += sm.warp_cnt[i];
-  if (first) {
+  // The second division has more places in the ring and takes fewer tokens at a time: an
+  // expert with more of them is swept again.  For 16 tokens of 256 experts, H 7168, 16
+  // places are 5% faster than 12 (402 and 424 us) and a sweep more is 1% of the products.
+  auto items = [&](int i) { return sm.warp_cnt[i][0] + sm.warp_cnt[i][1] + sm.warp_cnt[i][2] + sm.warp_cnt[i][3]; };
+  const int plan = a.group[1] && 17 * items(0) >= 16 * items(1), nv = items(plan);
+  int v = __popc((plan ? firsts[1] : firsts[0]) & ((1u << lane) - 1u));
+  for (int i = 0; i < warp; ++i) v += sm.warp_cnt[plan][i];
+  if (first >> plan & 1) {
     sm.vstart[v] = tid;
     sm.vexp[v] = sm.route_e[tid];
   }
   if (tid == 0) {
-    const int nv = sm.warp_cnt[0] + sm.warp_cnt[1] + sm.warp_cnt[2] + sm.warp_cnt[3];
+    sm.plan = plan;
     sm.nv = nv;
     sm.vstart[nv] = sm.warp_live[0] + sm.warp_live[1] + sm.warp_live[2] + sm.warp_live[3];
     // the status word is this call's: the first CTA sets it
@@ -746,12 +759,10 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     fp4_stream_kernel(const __grid_constant__ Fp4Maps maps, const Fp4Args a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Fp4Shared sm;
-  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint8_t* const smem = smem_raw + (ring - smem_u32(smem_raw));  // the same, for plain loads
-  const uint32_t srow0 = ring + a.stages * kCodeBytes;    // the units' scales
-  const uint32_t brow0 = srow0 + a.stages * kScaleBytes;  // operand rows
-  const uint32_t pbuf = brow0 + a.b_bytes;                  // the consumers' sums
   constexpr int kPartBytes = 2 * NT * 512;
+  const uint32_t pbuf = (smem_u32(smem_raw) + 1023u) & ~1023u;  // the consumers' sums
+  const uint32_t ring = pbuf + 2 * kConsumers * kPartBytes;     // the units: codes, then scales
+  const uint8_t* const smem = smem_raw + (ring - smem_u32(smem_raw));  // the same, for plain loads
   const int warp_id = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   {
@@ -785,7 +796,9 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
   pdl_trigger();
   // x rows that stay are asked for before anything else: behind the first weights
   // they would wait for a full ring's copies
-  const bool early = (int64_t)a.T * row_bytes(a.m[0].cols, false) <= a.b_bytes;
+  // (the first division: with the second one they do not stay)
+  const bool early = (int64_t)a.T * row_bytes(a.m[0].cols, false) <= a.b_bytes[0];
+  const uint32_t early_rows = ring + a.stages[0] * kUnitBytes;
   const bool loader = warp_id >= kWarpLoader && warp_id < kWarpConsumer;
   if (loader && lane == 0) {
     uint64_t& bar = sm.raw[warp_id - kWarpLoader];
@@ -794,7 +807,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     if (early && warp_id == kWarpLoader) {
       raw_begin(bar, a.T * a.m[0].cols * 2);
       for (int r = 0; r < a.T; ++r)
-        bulk_load(brow0 + r * row_bytes(a.m[0].cols, false), a.x + r * a.ldx, a.m[0].cols * 2, smem_u32(&bar));
+        bulk_load(early_rows + r * row_bytes(a.m[0].cols, false), a.x + r * a.ldx, a.m[0].cols * 2, smem_u32(&bar));
     }
   }
   int route = -1;
@@ -824,13 +837,15 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
   } else {
     if (early) {
       if (loader && lane == 0) mbar_arrive(smem_u32(&sm.go));
-      rows_ok = fill_x_rows(a.T, a.m[0].cols, brow0, row_bytes(a.m[0].cols, false), warp_id - kWarpLoader,
+      rows_ok = fill_x_rows(a.T, a.m[0].cols, early_rows, row_bytes(a.m[0].cols, false), warp_id - kWarpLoader,
                             kLoaders + kConsumers, sm.raw[0], sm.row_max, sm.rscale[0], lim);
     }
     asm volatile("bar.sync 4, %0;" ::"n"(kFp4Threads) : "memory");
   }
   const Ctx c{a, sm, sm.nv};
   constexpr int kPhases = MOE ? 2 : 1;
+  const int stages = MOE && sm.plan ? a.stages[1] : a.stages[0];
+  const uint32_t brow0 = ring + stages * kUnitBytes;  // operand rows
 
   if (MOE && c.nv == 0) {  // no active route: zeros
     uint4* o = reinterpret_cast<uint4*>(a.y);
@@ -871,7 +886,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       // copies were seen to be there.  Only once the copies have begun is the place in this
       // lap's phase, and the parity that of this lap.
       int nu = p == 0 ? warp : n0 + place(0);
-      int slot = (int)((uint32_t)nu % (uint32_t)a.stages), parity = (nu / a.stages) & 1;
+      int slot = (int)((uint32_t)nu % (uint32_t)stages), parity = (nu / stages) & 1;
       bool ready = false;
       for (int u = u0 - ka; u < u1; u += visit) {
         const int kb = min(visit, u1 - u);
@@ -920,8 +935,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
               if (!wait_count(&sm.issued[nu % kProducers], nu / kProducers + 1, lim)) return false;
               if (!warp_wait(sm.full[slot], parity, lim)) return false;
             }
-            const uint8_t* base = smem + slot * kCodeBytes + (t >> 1) * (2 * kBoxBytes) + g * 128;
-            const uint8_t* sbase = smem + (srow0 - ring) + slot * kScaleBytes + g * 32 + 8 * t;
+            const uint8_t* base = smem + slot * kUnitBytes + (t >> 1) * (2 * kBoxBytes) + g * 128;
+            const uint8_t* sbase = smem + slot * kUnitBytes + kCodeBytes + g * 32 + 8 * t;
             uint2 s[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // rows g, g + 8, g + 16, g + 24
@@ -952,8 +967,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                                                                        : visit + place(0) - place(i);
                 nu += step;
                 slot += step;
-                if (slot >= a.stages) {
-                  slot -= a.stages;
+                if (slot >= stages) {
+                  slot -= stages;
                   parity ^= 1;
                 }
                 const bool begun = load_count(&sm.issued[nu % kProducers]) > nu / kProducers;
@@ -1037,7 +1052,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       if (!warp_wait(sm.empty[slot], parity, lim)) return false;
       const Fp4Matrix& m = a.m[p];
       const int ng = f.cols >> 4;
-      const uint32_t bar = smem_u32(&sm.full[slot]), dst = ring + slot * kCodeBytes;
+      const uint32_t bar = smem_u32(&sm.full[slot]), dst = ring + slot * kUnitBytes;
       if (lane == 0) {
         store_count(&sm.issued[pw], ++mine);
         // one copy, but for a unit that ends within a 256-column block, past which
@@ -1062,7 +1077,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       const bool in = MOE || lane_row < m.rows;
       const uint8_t* src = m.scales + (in ? lane_row * ng + 32 * k : 0);
       const int n = in ? min(32, ng - 32 * k) : 0;
-      const uint32_t to = srow0 + slot * kScaleBytes + lane * 32;
+      const uint32_t to = dst + kCodeBytes + lane * 32;
       if ((ng & 15) == 0) {
         cp_async<16>(to, src, n > 0 ? 16 : 0, policy);
         cp_async<16>(to + 16, n > 16 ? src + 16 : src, n > 16 ? 16 : 0, policy);
@@ -1080,8 +1095,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
       slot += kProducers;
-      if (slot >= a.stages) {
-        slot -= a.stages;
+      if (slot >= stages) {
+        slot -= stages;
         parity ^= 1;
       }
       return true;
@@ -1131,7 +1146,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     }
     // no copy outlives the CTA, also when the other warps have given up
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (gave_up(lim) && lane < a.stages) {
+    if (gave_up(lim) && lane < stages) {
       int none = 0;
       for (int i = 0; i < 2; ++i)
         mbar_wait_bounded(smem_u32(&sm.full[lane]), i, &none, nullptr, 100000000ull);
@@ -1557,12 +1572,13 @@ static void fp4_finish_plan(Fp4Plan* p) {
   p->smem = 1024 + p->stages * kUnitBytes + p->b_bytes + fp4_part_bytes(p->nt);
 }
 
-// The layer: tokens in groups of at most 8.
-static Fp4Plan fp4_plan_layer(int H, int I, int T, int K) {
+// The layer: tokens in groups of at most 8, with at most `budget` bytes of operand rows.
+static Fp4Plan fp4_plan_layer(int H, int I, int T, int K, int budget) {
   Fp4Plan p = {8, 1, 0, 0, 0};
-  const int budget = fp4_row_budget(1), r1 = row_bytes(H, false), r2 = row_bytes(I, true);
+  const int r1 = row_bytes(H, false), r2 = row_bytes(I, true);
   if (budget / r1 < p.group) p.group = budget / r1;
   if (budget / r2 < p.group) p.group = budget / r2;
+  if (p.group < 1) return p;
   // x: T rows, or one group's; h: two groups' or all, as far as they fit
   const int n1 = (int64_t)T * r1 <= budget ? T * r1 : p.group * r1;
   int rows2 = T * K < 2 * p.group ? T * K : 2 * p.group;
@@ -1764,7 +1780,14 @@ moe_status moe_fp4_forward(moe_fp4_handle* h, const uint16_t* d_x, const int32_t
       misaligned(d_topk_idx, 4) || misaligned(d_topk_w, 4) || misaligned(d_out, 16))
     return MOE_ERR_INVALID_ARG;
   const moe_dims& d = h->dims;
-  const Fp4Plan p = fp4_plan_layer(d.hidden, d.inter, (int)num_tokens, d.top_k);
+  const int budget = fp4_row_budget(1);
+  const Fp4Plan p = fp4_plan_layer(d.hidden, d.inter, (int)num_tokens, d.top_k, budget);
+  // where the x rows do not stay and the ring is short of its most places, the division
+  // that is not
+  const Fp4Plan p2 = p.stages == kMaxStages || num_tokens * row_bytes(d.hidden, false) <= budget
+                         ? Fp4Plan{}
+                         : fp4_plan_layer(d.hidden, d.inter, (int)num_tokens, d.top_k,
+                                          budget - (kMaxStages - kMinStages) * kUnitBytes);
   Fp4Args a = {};
   a.m[0] = h->m[0];
   a.m[1] = h->m[1];
@@ -1781,13 +1804,16 @@ moe_status moe_fp4_forward(moe_fp4_handle* h, const uint16_t* d_x, const int32_t
   a.T = (int)num_tokens;
   a.E = d.num_experts;
   a.K = d.top_k;
-  a.group = p.group;
-  a.b_bytes = p.b_bytes;
-  a.stages = p.stages;
+  a.group[0] = p.group;
+  a.b_bytes[0] = p.b_bytes;
+  a.stages[0] = p.stages;
+  a.group[1] = p2.group;
+  a.b_bytes[1] = p2.b_bytes;
+  a.stages[1] = p2.stages;
   a.check = (d.flags & MOE_FLAG_CHECK_ROUTES) != 0;
   a.watchdog_test = (d.flags & MOE_FLAG_WATCHDOG_TEST) != 0;
   a.wait_ns = a.watchdog_test ? 20000000ull : kWaitLimitNs;
-  return fp4_launch<true, 1>(h->maps, a, h->grid, p.smem, stream) == cudaSuccess
+  return fp4_launch<true, 1>(h->maps, a, h->grid, p.smem > p2.smem ? p.smem : p2.smem, stream) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -1852,9 +1878,9 @@ moe_status moe_fp4_linear(moe_fp4_handle* h, const uint16_t* d_x, int64_t x_stri
   a.T = (int)num_tokens;
   a.E = 1;
   a.K = 1;
-  a.group = p.group;
-  a.b_bytes = p.b_bytes;
-  a.stages = p.stages;
+  a.group[0] = p.group;
+  a.b_bytes[0] = p.b_bytes;
+  a.stages[0] = p.stages;
   a.f32 = y_float32 != 0;
   a.wait_ns = kWaitLimitNs;
   const cudaError_t e = p.nt == 2
