@@ -110,6 +110,7 @@ struct Fp4Args {
   // operand rows, places of the ring.  The layer may have a second division (group 0:
   // it has not), of which the routes choose.
   int group[2], b_bytes[2], stages[2];
+  uint32_t grid_rcp;    // floor(2^32 / CTAs) + 1
   uint64_t wait_ns;     // limit of every wait
   bool check, f32, watchdog_test;
 };
@@ -142,16 +143,14 @@ struct Phase {
   // the CTAs' shares: steps of `stride` units, `base` or (the first `extra` CTAs)
   // one more of them
   int stride, base, extra;
+  TilePos start;  // the visit that u0 lies in, and its units before u0
+  int ka;
   // the CTA that holds unit u
   __device__ int cta_of(int u) const {
     const int s = u / stride, big = extra * (base + 1);
     return s < big ? s / (base + 1) : extra + (s - big) / base;
   }
   __device__ int visit() const { return p == 0 ? U : 4 * U; }  // units of an item at a tile
-  __device__ TilePos at(int u) const {
-    const int i = u / visit(), inner = p == 0 ? RT : nv, o = i / inner;
-    return p == 0 ? TilePos{o, i - o * inner} : TilePos{i - o * inner, o};
-  }
   __device__ void step(TilePos& s) const {
     if (p == 0) {
       if (++s.j == RT) {
@@ -219,7 +218,13 @@ struct Fp4Ctx {
   Fp4Shared& sm;
   int nv;
 
-  // (units: below 2^30, also the linear's in 16 groups)
+  // n over the grid's CTAs, n below 2^32: the reciprocal's quotient is right or one too many
+  __device__ uint32_t per_cta(uint32_t n) const {
+    const uint32_t q = __umulhi(n, a.grid_rcp);
+    return q * gridDim.x > n ? q - 1 : q;
+  }
+  // (units: below 2^30, also the linear's in 16 groups.  Divisions cost about 0.1 us each
+  // here, where everyone waits: few, and once for all roles)
   __device__ Phase make_phase(int p) const {
     Phase f;
     f.p = p;
@@ -229,14 +234,23 @@ struct Fp4Ctx {
     f.nv = nv;
     // whole tiles, unless the CTA with one more than the others would work
     // longer than a join takes
-    const int G = gridDim.x, n = nv * f.RT * f.U, tu = f.tile_units(), most = (n / tu + G - 1) / G * tu;
-    f.stride = most - (n + G - 1) / G <= kCutUnits ? tu : p == 0 ? 1 : f.visit();
-    const int steps = n / f.stride;
-    f.base = steps / G;
+    const int G = gridDim.x, tiles = p == 0 ? nv * f.RT : f.RT >> 2, tu = f.tile_units(), n = tiles * tu;
+    const bool whole = (int)(per_cta(tiles + G - 1) * tu - per_cta(n + G - 1)) <= kCutUnits;
+    f.stride = whole ? tu : p == 0 ? 1 : f.visit();
+    const int steps = whole ? tiles : p == 0 ? n : nv * tiles;
+    f.base = per_cta(steps);
     f.extra = steps - f.base * G;
-    const int b = blockIdx.x;
-    f.u0 = (b * f.base + min(b, f.extra)) * f.stride;
+    const int b = blockIdx.x, step0 = b * f.base + min(b, f.extra);
+    f.u0 = step0 * f.stride;
     f.u1 = f.u0 + (f.base + (b < f.extra)) * f.stride;
+    if (whole && p == 1) {
+      f.ka = 0;
+      f.start = {0, step0};
+    } else {  // a step is a tile, a unit or an item's visit
+      const int i = whole || p == 1 ? step0 : step0 / f.U, inner = p == 0 ? f.RT : nv, o = i / inner;
+      f.ka = f.u0 - i * f.visit();
+      f.start = p == 0 ? TilePos{o, i - o * inner} : TilePos{i - o * inner, o};
+    }
     return f;
   }
   __device__ const Phase& phase(int p) const { return sm.phase[p]; }
@@ -874,11 +888,11 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       const bool res = p == 0 && c.resident(0);
       const int R = c.ring_rows(p);
       int item = -1, pos = 0, rows = 0;
-      const TilePos start = f.at(u0);
+      const TilePos start = f.start;
       int v = start.v, left = inner - (p == 0 ? start.j : start.v);  // steps to the next item / tile
       bool fresh = true;        // a new item
       const uint8_t* brow[NT];  // this lane's operand rows
-      int ka = u0 % visit;      // first unit of the visit (second phase: 0)
+      int ka = f.ka;            // first unit of the visit (second phase: 0)
       // second phase: where the i-th of this warp's units of a visit comes in the order
       const int full = U >> 1, half = warp & 1;
       auto place = [&](int i) { return i < full ? 8 * i + warp : 8 * full + (warp >> 1); };
@@ -1111,8 +1125,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     int to_mine = pw;  // units until this warp's next one
     {
       const Phase& f = c.phase(0);
-      TilePos at = f.at(f.u0);
-      int ka = f.u0 % f.U;
+      TilePos at = f.start;
+      int ka = f.ka;
       for (int u = f.u0 - ka; u < f.u1 && ok; u += f.U, f.step(at)) {
         const int kb = min(f.U, f.u1 - u);
         int k = ka + to_mine;
@@ -1129,7 +1143,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     }
     if constexpr (MOE) {
       const Phase& f = c.phase(1);
-      TilePos at = f.at(f.u0);
+      TilePos at = f.start;
       const int visit = f.visit();
       for (int u = f.u0; u < f.u1 && ok; u += visit, f.step(at)) {
         const int r0 = (int)c.matrix_row(1, at, 0);
@@ -1196,8 +1210,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       const bool res = c.resident(0);
       const int R = c.ring_rows(0);
       ItemWalk it;
-      TilePos at = f.at(f.u0);
-      int ka = f.u0 % f.U, n = 0, s0 = 0;
+      TilePos at = f.start;
+      int ka = f.ka, n = 0, s0 = 0;
       float factor[NT][2];
       bool fresh = true;  // a new item since this warp's last tile
       int turn = 0;
@@ -1214,6 +1228,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         }
         const bool cut = units != f.U;
         const int cnt = min(units, kConsumers), first = n0;
+        // a cut tile's CTAs, while its sums are on their way
+        const int c0 = cut ? f.cta_of(u) : 0, c1 = cut ? f.cta_of(u + f.U - 1) : 0;
         n0 += units;
         ka = 0;
         turn ^= 1;
@@ -1280,7 +1296,6 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
               acc[m][nt][2 + o] *= factor[nt][o];
             }
         if (cut) {
-          const int c0 = f.cta_of(u), c1 = f.cta_of(u + f.U - 1);
           auto share = [&](int cta) {
             return reinterpret_cast<float4*>(a.part[0] + (size_t)(2 * cta + (cta == c0)) * 512) + lane;
           };
@@ -1359,8 +1374,9 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       const int R = c.ring_rows(1), visit = f.visit(), tu = f.tile_units();
       const int step = f.U > 1 ? 1 : 2, cnt = kConsumers / step;  // the warps with units
       ItemWalk it;
-      TilePos at = f.at(f.u0);
+      TilePos at = f.start;
       bool fresh = true;  // first visit of a tile by this CTA
+      int c0 = 0, c1 = 0;  // the tile's CTAs
       for (int u = f.u0; u < f.u1; u += visit, f.step(at)) {
         const int last_item = it.item;
         it.next(c, f, false, R, at);
@@ -1372,6 +1388,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
           for (int i = lane; i < a.T * kTile2 / 4; i += 32)
             reinterpret_cast<float4*>(&sm.out[0][0])[i] = make_float4(0.f, 0.f, 0.f, 0.f);
           fresh = false;
+          c0 = f.cta_of(at.j * tu);
+          c1 = f.cta_of(at.j * tu + tu - 1);
         }
         const int n = c.item_rows(at.v), s0 = sm.vstart[at.v];
         int from;
@@ -1422,8 +1440,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         const int tb = at.j * tu, te = tb + tu;  // the tile's units
         if (u + visit < min(f.u1, te)) continue;  // more of this tile to come
         fresh = true;
-        if (tb < f.u0 || te > f.u1) {
-          const int c0 = f.cta_of(tb), c1 = f.cta_of(te - 1);
+        if (c0 != c1) {
           auto share = [&](int cta) {
             return reinterpret_cast<float4*>(a.part[1] + (size_t)(2 * cta + (cta == c0)) *
                                                              (kFp4MaxTokens * kTile2)) + lane;
@@ -1506,9 +1523,9 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
           ++oldest;
           return true;
         };
-        TilePos at = f.at(f.u0);
+        TilePos at = f.start;
         const int visit = f.visit();
-        for (int u = f.u0 - f.u0 % visit; u < f.u1; u += visit, f.step(at)) {
+        for (int u = f.u0 - f.ka; u < f.u1; u += visit, f.step(at)) {
           if (!it.next(c, f, false, R, at)) continue;
           while (used + it.rows > R || it.item - oldest >= kItems)
             if (!retire()) goto done;
@@ -1812,6 +1829,7 @@ moe_status moe_fp4_forward(moe_fp4_handle* h, const uint16_t* d_x, const int32_t
   a.stages[1] = p2.stages;
   a.check = (d.flags & MOE_FLAG_CHECK_ROUTES) != 0;
   a.watchdog_test = (d.flags & MOE_FLAG_WATCHDOG_TEST) != 0;
+  a.grid_rcp = (uint32_t)(0x100000000ull / h->grid) + 1;
   a.wait_ns = a.watchdog_test ? 20000000ull : kWaitLimitNs;
   return fp4_launch<true, 1>(h->maps, a, h->grid, p.smem > p2.smem ? p.smem : p2.smem, stream) == cudaSuccess
              ? MOE_OK
@@ -1882,6 +1900,7 @@ moe_status moe_fp4_linear(moe_fp4_handle* h, const uint16_t* d_x, int64_t x_stri
   a.b_bytes[0] = p.b_bytes;
   a.stages[0] = p.stages;
   a.f32 = y_float32 != 0;
+  a.grid_rcp = (uint32_t)(0x100000000ull / h->grid) + 1;
   a.wait_ns = kWaitLimitNs;
   const cudaError_t e = p.nt == 2
                             ? fp4_launch<false, 2>(h->maps, a, h->grid, p.smem, stream)
