@@ -106,10 +106,12 @@ struct Fp4Args {
   uint32_t* ctl;        // [0] barrier, [1] finished CTAs, [2 + 152 p + c] joins of phase p
   float* part[2];       // by phase, [152][2][..]: a CTA's cut tiles, first and last
   int T, E, K;
+  int k_rcp;            // floor(2^16 / K) + 1: quotients of numbers below 128
   // how shared memory is divided: tokens of one operand item (at most 8 NT), bytes of
   // operand rows, places of the ring.  The layer may have a second division (group 0:
   // it has not), of which the routes choose.
   int group[2], b_bytes[2], stages[2];
+  int group_rcp[2];     // as k_rcp
   uint32_t grid_rcp;    // floor(2^32 / CTAs) + 1
   uint64_t wait_ns;     // limit of every wait
   bool check, f32, watchdog_test;
@@ -702,7 +704,7 @@ __device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm, int
     return;
   }
   auto sync = [] { asm volatile("bar.sync 2, 128;" ::: "memory"); };
-  const int R = a.T * a.K;
+  const int R = a.T * a.K, token = tid * a.k_rcp >> 16;
   uint32_t bits = tid < R && (e < -1 || e >= a.E) ? MOE_DEV_ROUTE_RANGE : 0u;
   const bool live = tid < R && e >= 0 && e < a.E;
   const int low = e * kFp4MaxRoutes;
@@ -710,8 +712,10 @@ __device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm, int
   sm.key[tid] = mine;
   sm.first[tid] = 0;
   sync();
-  int pos = 0, within = 0;
+  // routes before this one, with a lower expert, and neither with its expert and token
+  int pos = 0, lower = 0, apart = 0;
   if (live) {
+    const int same = low + token * a.K;
 #pragma unroll 2
     for (int r = 0; r < R; r += 4) {
       const int4 k4 = *reinterpret_cast<const int4*>(&sm.key[r]);
@@ -719,19 +723,21 @@ __device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm, int
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         pos += k[i] < mine;
-        within += k[i] < mine && k[i] >= low;
+        lower += k[i] < low;
+        apart += k[i] < same;
       }
     }
+    const int within = pos - lower;
     if (a.check) {
-      for (int r = tid / a.K * a.K; r < tid; ++r)
-        if (sm.key[r] >= low && sm.key[r] < mine) bits |= MOE_DEV_ROUTE_DUP;
+      if (pos != apart) bits |= MOE_DEV_ROUTE_DUP;
       if (!(fabsf(w) < INFINITY)) bits |= MOE_DEV_ROUTE_NONFINITE;
     }
     sm.route_e[pos] = e;
     sm.route_id[pos] = tid;
-    sm.route_tok[pos] = tid / a.K;
+    sm.route_tok[pos] = token;
     sm.route_w[pos] = w;
-    sm.first[pos] = (within % a.group[0] == 0) | (a.group[1] && within % a.group[1] == 0 ? 2 : 0);
+    auto starts = [&](int i) { return within == (within * a.group_rcp[i] >> 16) * a.group[i]; };
+    sm.first[pos] = (int)starts(0) | (a.group[1] && starts(1) ? 2 : 0);
   }
   bits = __reduce_or_sync(0xFFFFFFFFu, bits);
   const int live_here = __popc(__ballot_sync(0xFFFFFFFFu, live));
@@ -1825,6 +1831,9 @@ moe_status moe_fp4_forward(moe_fp4_handle* h, const uint16_t* d_x, const int32_t
   a.b_bytes[0] = p.b_bytes;
   a.stages[0] = p.stages;
   a.group[1] = p2.group;
+  a.k_rcp = 65536 / d.top_k + 1;
+  a.group_rcp[0] = 65536 / p.group + 1;
+  a.group_rcp[1] = p2.group ? 65536 / p2.group + 1 : 0;
   a.b_bytes[1] = p2.b_bytes;
   a.stages[1] = p2.stages;
   a.check = (d.flags & MOE_FLAG_CHECK_ROUTES) != 0;
