@@ -637,7 +637,10 @@ MOE_API moe_status moe_fp4_linear(moe_fp4_handle* h, const uint16_t* d_x, int64_
                                   struct CUstream_st* stream);
 
 /* moe_fp4_read_status -- the device status word of the handle's latest call
- * (as moe_read_status: copies it on `stream` and synchronises that stream). */
+ * (as moe_read_status: copies it on `stream` and synchronises that stream).
+ * After a wait of the kernel has run out every call reports MOE_DEV_TIMEOUT, its
+ * output undefined, until this function has returned MOE_ERR_DEVICE_TIMEOUT: it
+ * clears the workspace's counters, and the next call is a normal one. */
 MOE_API moe_status moe_fp4_read_status(moe_fp4_handle* h, uint32_t* h_status,
                                        struct CUstream_st* stream);
 /* moe_fp4_destroy -- frees the host handle; NULL is a no-op. */

@@ -58,6 +58,7 @@ namespace mm {
 constexpr int kFp4MaxTokens = 16;
 constexpr int kFp4MaxRoutes = 128;
 constexpr int kFp4Grid = 152;        // one CTA per SM
+constexpr int kCtlPoison = 2 + 2 * kFp4Grid;  // not 0: a wait ran out, the counters may not be at zero
 // The warps' roles.  More service warps than copies need by their number: each
 // wait and each copy is a chain of round trips, and several chains overlap (two
 // copying warps 449 us, four 409, at 16 tokens; one finishing FC1's tiles 36.9, two
@@ -103,7 +104,7 @@ struct Fp4Args {
   uint8_t* h;           // [T*K] records of half values and their block exponents
   void* y;              // the layer's BF16 output, or the linear's
   uint32_t* status;
-  uint32_t* ctl;        // [0] barrier, [1] finished CTAs, [2 + 152 p + c] joins of phase p
+  uint32_t* ctl;        // [0] barrier, [1] warps past it, [2 + 152 p + c] joins of phase p, kCtlPoison
   float* part[2];       // by phase, [152][2][..]: a CTA's cut tiles, first and last
   int T, E, K;
   int k_rcp;            // floor(2^16 / K) + 1: quotients of numbers below 128
@@ -684,9 +685,10 @@ __device__ __forceinline__ bool fill_h(const uint8_t* src, int cols, uint32_t ds
 }
 
 // Sorted routes, and the items: runs of at most `group` tokens of one expert (the
-// linear: groups of tokens).  By the first 128 threads; e, w: the thread's route.
+// linear: groups of tokens).  By the first 128 threads; e, w: the thread's route; bad:
+// status bits that the first CTA's first thread adds.
 template <bool MOE>
-__device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm, int e, float w) {
+__device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm, int e, float w, uint32_t bad) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (!MOE) {
     if (tid == 0) {
@@ -698,7 +700,7 @@ __device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm, int
       sm.vstart[v] = a.T;
       sm.nv = v;
       sm.plan = 0;
-      if (blockIdx.x == 0) atomicExch(a.status, 0u);
+      if (blockIdx.x == 0) atomicExch(a.status, bad);
     }
     if (tid < a.T) sm.route_id[tid] = sm.route_tok[tid] = tid;
     return;
@@ -770,7 +772,7 @@ __device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm, int
     sm.vstart[nv] = sm.warp_live[0] + sm.warp_live[1] + sm.warp_live[2] + sm.warp_live[3];
     // the status word is this call's: the first CTA sets it
     if (blockIdx.x == 0)
-      atomicExch(a.status, sm.warp_bits[0] | sm.warp_bits[1] | sm.warp_bits[2] | sm.warp_bits[3]);
+      atomicExch(a.status, sm.warp_bits[0] | sm.warp_bits[1] | sm.warp_bits[2] | sm.warp_bits[3] | bad);
   }
 }
 
@@ -832,6 +834,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
   }
   int route = -1;
   float route_w = 0.f;
+  uint32_t bad = 0u;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.ctl[kCtlPoison]) bad = MOE_DEV_TIMEOUT;
   if (MOE && threadIdx.x < a.T * a.K) {
     route = a.idx[threadIdx.x];
     route_w = a.w[threadIdx.x];
@@ -847,7 +851,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
   WaitLimit& lim = sm.lim;
   if (warp_id < kWarpLoader) {
     if (threadIdx.x < kFp4MaxRoutes) {
-      build_items<MOE>(a, sm, route, route_w);
+      build_items<MOE>(a, sm, route, route_w, bad);
       asm volatile("bar.sync 2, 128;" ::: "memory");
       if (sm.nv > 0 && lane == 0 && warp_id < (MOE ? 2 : 1))
         sm.phase[warp_id] = Ctx{a, sm, sm.nv}.make_phase(warp_id);
@@ -1562,19 +1566,16 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             if (!retire()) goto done;
       }
     }
-  }
-done:
-  __syncthreads();
-  // the last CTA leaves the counters at zero for the next call
-  if (threadIdx.x == 0) {
-    __threadfence();
-    if (atomicAdd(&a.ctl[1], 1u) == gridDim.x - 1) {
+    // the last warp past the barrier leaves its counter at zero for the next call
+    if (MOE && lane == 0 && atomicAdd(&a.ctl[1], 1u) == kLoaders * gridDim.x - 1) {
       a.ctl[0] = 0u;
       a.ctl[1] = 0u;
-      if (ld_acquire_gpu_u32(a.status) & MOE_DEV_TIMEOUT)
-        for (int i = 0; i < 2 * kFp4Grid; ++i) a.ctl[2 + i] = 0u;
     }
   }
+done:
+  // whoever gave up leaves the counters as they are: every call says so until the host
+  // has read the status and cleared them
+  if (gave_up(lim) && lane == 0) a.ctl[kCtlPoison] = 1u;
 }
 
 // Shared memory of a launch: the operand rows' share, and what is left for the ring.
@@ -1663,7 +1664,7 @@ constexpr size_t kFp4Align = 256;
 constexpr size_t kFp4Ctl = 2048;
 constexpr size_t kFp4Part0 = (size_t)kFp4Grid * 2 * 512 * 4;
 constexpr size_t kFp4Part1 = (size_t)kFp4Grid * 2 * kFp4MaxTokens * kTile2 * 4;
-static_assert((2 + 2 * kFp4Grid) * 4 <= kFp4Ctl, "counters");
+static_assert((kCtlPoison + 1) * 4 <= kFp4Ctl, "counters");
 
 bool fp4_dims_ok(const moe_dims* d) {
   const bool hk = d->hidden >= 128 && d->hidden <= 16384 && d->hidden % 128 == 0;
@@ -1922,7 +1923,11 @@ moe_status moe_fp4_read_status(moe_fp4_handle* h, uint32_t* h_status, struct CUs
   if (cudaMemcpyAsync(h_status, h->status, 4, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
       cudaStreamSynchronize(stream) != cudaSuccess)
     return MOE_ERR_CUDA;
-  if (*h_status & MOE_DEV_TIMEOUT) return MOE_ERR_DEVICE_TIMEOUT;
+  if (*h_status & MOE_DEV_TIMEOUT) {
+    if (cudaMemsetAsync(h->ctl, 0, kFp4Ctl, stream) != cudaSuccess || cudaStreamSynchronize(stream) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    return MOE_ERR_DEVICE_TIMEOUT;
+  }
   return *h_status ? MOE_ERR_BAD_ROUTE : MOE_OK;
 }
 

@@ -36,3 +36,24 @@ def test_waits_expire_with_status_and_context_survives(S, T):  # noqa: F811
                                    good.workspace.data_ptr(), good._ws_bytes,
                                    torch.cuda.current_stream().cuda_stream)
     assert torch.equal(good.forward(x, idx, w), want) and good.read_status() == (0, 0)
+
+
+def test_a_timeout_is_reported_until_it_is_read(S):  # noqa: F811
+    """Calls after one that gave up, on the same workspace, say so too, until the
+    status has been read; then they are normal."""
+    B = S.binding
+    H, I, E, K, T = 1024, 512, 16, 4, 3
+    gen = torch.Generator("cuda").manual_seed(33)
+    p1, p2 = fp4(gen, E, 2 * I, H), fp4(gen, E, H, I)
+    x = torch.randn(T, H, device="cuda", generator=gen).bfloat16()
+    idx, w = routes(gen, T, E, K)
+    want, good = check_layer(S, p1, p2, x, idx, w)
+    bad = S.Fp4MoELayer(H, I, E, K, watchdog_test=True)
+    bad.weights, bad.workspace = good.weights, good.workspace
+    bad.handle = B.moe_fp4_create(H, I, E, K, bad.flags, 16, *(t.data_ptr() for t in bad.weights),
+                                  bad.workspace.data_ptr(), bad._ws_bytes, torch.cuda.current_stream().cuda_stream)
+    bad.forward(x, idx, w)
+    good.forward(x, idx, w)
+    assert good.read_status() == (B.MOE_ERR_DEVICE_TIMEOUT, B.MOE_DEV_TIMEOUT)
+    for _ in range(2):
+        assert torch.equal(good.forward(x, idx, w), want) and good.read_status() == (0, 0)
