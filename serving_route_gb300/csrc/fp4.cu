@@ -37,11 +37,13 @@
 //   * the layer is one cooperative launch: FC1 units, a grid barrier on h, FC2
 //     units.  The weights' copies do not wait at the barrier: the ring fills
 //     with FC2 weights while the last FC1 sums and h are on their way.
-// Where one token's 47.7 us go (H 7168, I 2048, 8 of 256 experts; 29.2 us at the copy
-// rate): tables and the first copies 5.5 us, FC1 to 25, its last sums and the barrier
-// to 28.7, h rows to 30.8, FC2 to 40.5, joining and leaving to 44, the launch.  FC2
+// Where one token's 46.4 us go (H 7168, I 2048, 8 of 256 experts; 29.2 us at the copy
+// rate): tables and the first copies 4.7 us, FC1 to 24, its last sums and the barrier
+// to 28.2, h rows to 30.3, FC2 to 40, joining and leaving to 43, the launch.  FC2
 // there is bound by its products (its first third is in the ring before the barrier
-// opens; sending the rest to L2 ahead made it slower).
+// opens; sending the rest to L2 ahead made it slower).  The linear (4096 x 7168, one
+// token: 7.4 us, 2.4 at the copy rate) is bound by the same start, one tile's products
+// and the launch.
 #include <cudaTypedefs.h>
 
 #include <cstring>
@@ -1635,8 +1637,8 @@ static cudaError_t fp4_launch(const Fp4Maps& maps, const Fp4Args& a, int grid, i
   coop.id = cudaLaunchAttributeCooperative;
   coop.val.cooperative = 1;
   // the layer's CTAs wait for one another (all resident, or the launch fails); the
-  // linear's do not, and its launch and prologue overlap the kernel before (10.2 -> 8.7 us
-  // for 4096 x 7168, T = 1, one after the other)
+  // linear's do not, and its launch and prologue overlap the kernel before (for
+  // 4096 x 7168, T = 1, one after the other, 1.5 us less)
   return launch_k(fp4_stream_kernel<MOE, NT>, dim3(grid), dim3(kFp4Threads), smem, s, !MOE,
                   MOE ? &coop : nullptr, maps, a);
 }
