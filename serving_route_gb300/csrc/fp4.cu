@@ -1104,22 +1104,26 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       const uint8_t* src = m.scales + (in ? lane_row * ng + 32 * k : 0);
       const int n = in ? min(32, ng - 32 * k) : 0;
       const uint32_t to = dst + kCodeBytes + lane * 32;
-      if ((ng & 15) == 0) {
-        cp_async<16>(to, src, n > 0 ? 16 : 0, policy);
-        cp_async<16>(to + 16, n > 16 ? src + 16 : src, n > 16 ? 16 : 0, policy);
-      } else if ((ng & 7) == 0)
-        copy_scale_row<8>(to, src, n, policy);
-      else if ((ng & 3) == 0)
-        copy_scale_row<4>(to, src, n, policy);
-      else {  // rows on odd multiples of two bytes: through registers
+      if ((ng & 3) == 0) {
+        if ((ng & 15) == 0) {
+          cp_async<16>(to, src, n > 0 ? 16 : 0, policy);
+          cp_async<16>(to + 16, n > 16 ? src + 16 : src, n > 16 ? 16 : 0, policy);
+        } else if ((ng & 7) == 0)
+          copy_scale_row<8>(to, src, n, policy);
+        else
+          copy_scale_row<4>(to, src, n, policy);
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+      } else {  // rows on odd multiples of two bytes: through registers
         for (int o = 0; o < 32; o += 4) {
           uint32_t x = 0u;
           if (o < n) x = __ldg(reinterpret_cast<const uint16_t*>(src + o));
           if (o + 2 < n) x |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src + o + 2)) << 16;
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + o), "r"(x) : "memory");
         }
+        // these are ordinary stores, which the arrival of the asynchronous copies does not
+        // order: one that releases them
+        mbar_arrive(bar);
       }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
       slot += kProducers;
       if (slot >= stages) {
         slot -= stages;
