@@ -174,7 +174,8 @@ class MegaMoELayer:
                           topk_idx: torch.Tensor, topk_w: torch.Tensor, stream=None) -> torch.Tensor:
         """forward() of activations in this layer's format, as add_rms_norm(fmt=...) gives
         them: xq uint8 E4M3 codes [T, H], xq_scale uint8 E8M0 bytes [T, H/128] ("mxfp8":
-        [T, H/32]; "per_tensor": None)."""
+        [T, H/32]; "per_tensor": None).  topk_idx, topk_w: contiguous [T, K] (or more rows,
+        of which the first T count)."""
         T = xq.shape[0]
         cols = {"deepseek": self.H // 128, "mxfp8": self.H // 32}.get(self.fmt)
         assert xq.dtype == torch.uint8 and xq.is_cuda and xq.is_contiguous() and tuple(xq.shape) == (T, self.H)
@@ -184,6 +185,8 @@ class MegaMoELayer:
             assert xq_scale.dtype == torch.uint8 and xq_scale.is_cuda and xq_scale.is_contiguous()
             assert tuple(xq_scale.shape) == (T, cols)
         assert topk_idx.dtype == torch.int32 and topk_w.dtype == torch.float32
+        for t in (topk_idx, topk_w):  # dense rows of K, at least T of them: the kernels read T * K
+            assert t.is_cuda and t.is_contiguous() and t.dim() == 2 and t.shape[0] >= T and t.shape[1] == self.K
         B.moe_forward_quantized(self.handle, xq.data_ptr(),
                                 xq_scale.data_ptr() if xq_scale is not None else None,
                                 topk_idx.data_ptr(), topk_w.data_ptr(), T, _stream_ptr(stream))
