@@ -503,7 +503,10 @@ MOE_API moe_status moe_route_noalloc(const int32_t* d_topk_idx, const float* d_t
                                      struct CUstream_st* stream);
 
 /* ------------------------------------------------------------------------
- * Operators around the layer for few tokens.
+ * Operators around the layer for few tokens.  They launch on the current
+ * device: every pointer and the stream of a call are of that device.  The
+ * calls on a moe_fp4_handle refuse another device than the one it was created
+ * on with MOE_ERR_INVALID_ARG.
  * ------------------------------------------------------------------------ */
 
 /*

@@ -1656,7 +1656,7 @@ struct moe_fp4_handle {
   moe_dims dims;         // the layer
   Fp4Matrix m[2];        // the linear: the first
   Fp4Maps maps;
-  int max_tokens, grid;
+  int max_tokens, grid, device;
   uint32_t* status;
   uint32_t* ctl;
   float* part[2];
@@ -1678,6 +1678,13 @@ bool fp4_dims_ok(const moe_dims* d) {
   const bool kk = d->top_k == 1 || d->top_k == 2 || d->top_k == 4 || d->top_k == 6 || d->top_k == 8;
   return hk && ik && kk && d->num_experts >= 1 && d->num_experts <= 1024 &&
          (d->flags & ~(MOE_FLAG_CHECK_ROUTES | MOE_FLAG_WATCHDOG_TEST)) == 0;
+}
+
+// Launches go to the current device: it has to be the one that the weights, the workspace
+// and the kernels' attributes belong to.
+bool elsewhere(const moe_fp4_handle* h) {
+  int dev = -1;
+  return cudaGetDevice(&dev) != cudaSuccess || dev != h->device;
 }
 
 bool misaligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
@@ -1735,6 +1742,7 @@ moe_status fp4_set_up(moe_fp4_handle* h, void* d_workspace, cudaStream_t stream)
     return MOE_ERR_CUDA;
   if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;  // built for sm_103a only
   h->grid = sms < kFp4Grid ? sms : kFp4Grid;
+  h->device = dev;
   const int most = kMaxSmem - (int)sizeof(Fp4Shared) - 1024;
   const void* ks[3] = {(const void*)fp4_stream_kernel<true, 1>, (const void*)fp4_stream_kernel<false, 1>,
                        (const void*)fp4_stream_kernel<false, 2>};
@@ -1807,7 +1815,7 @@ moe_status moe_fp4_forward(moe_fp4_handle* h, const uint16_t* d_x, const int32_t
   if (num_tokens == 0) return MOE_OK;
   if (num_tokens > h->max_tokens) return MOE_ERR_CAPACITY;
   if (!d_x || !d_topk_idx || !d_topk_w || !d_out || misaligned(d_x, 16) ||
-      misaligned(d_topk_idx, 4) || misaligned(d_topk_w, 4) || misaligned(d_out, 16))
+      misaligned(d_topk_idx, 4) || misaligned(d_topk_w, 4) || misaligned(d_out, 16) || elsewhere(h))
     return MOE_ERR_INVALID_ARG;
   const moe_dims& d = h->dims;
   const int budget = fp4_row_budget(1);
@@ -1897,7 +1905,7 @@ moe_status moe_fp4_linear(moe_fp4_handle* h, const uint16_t* d_x, int64_t x_stri
   if (num_tokens > h->max_tokens) return MOE_ERR_CAPACITY;
   const Fp4Matrix& m = h->m[0];
   if (!d_x || !d_y || x_stride < m.cols || x_stride % 8 || misaligned(d_x, 16) ||
-      misaligned(d_y, y_float32 ? 4 : 2))
+      misaligned(d_y, y_float32 ? 4 : 2) || elsewhere(h))
     return MOE_ERR_INVALID_ARG;
   const Fp4Plan p = fp4_plan_linear(m.cols, (int)num_tokens);
   Fp4Args a = {};
@@ -1925,7 +1933,7 @@ moe_status moe_fp4_linear(moe_fp4_handle* h, const uint16_t* d_x, int64_t x_stri
 }
 
 moe_status moe_fp4_read_status(moe_fp4_handle* h, uint32_t* h_status, struct CUstream_st* stream) {
-  if (!h || !h_status) return MOE_ERR_INVALID_ARG;
+  if (!h || !h_status || elsewhere(h)) return MOE_ERR_INVALID_ARG;
   if (cudaMemcpyAsync(h_status, h->status, 4, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
       cudaStreamSynchronize(stream) != cudaSuccess)
     return MOE_ERR_CUDA;

@@ -5,7 +5,9 @@ and streams only; every computation is a kernel of the library.
 
 Given `out` buffers the calls allocate nothing and can be captured in a CUDA
 graph.  Tensors used on another stream than the one they were made on are the
-caller's to order (and to keep alive), as for MegaMoELayer.
+caller's to order (and to keep alive), as for MegaMoELayer.  The kernels run on the
+current device: all tensors (and the stream) of a call are of that device, else it is
+refused.
 """
 from __future__ import annotations
 
@@ -21,9 +23,14 @@ _Q_BLOCK = {"deepseek": 128, "mxfp8": 32}
 _BF16, _F32, _U8, _I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
 
 
-def _stream(stream, like: torch.Tensor) -> int:
-    # the raw handle of the current stream, without making a Stream object of it
-    return torch._C._cuda_getCurrentRawStream(like.get_device()) if stream is None else stream.cuda_stream
+# The current device, which the library launches on (a tensor on the host is on device
+# -1), and the raw handle of its current stream, without making a Stream object of it.
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _given_stream(stream, dev: int) -> int:
+    assert getattr(stream, "device_index", dev) == dev
+    return stream.cuda_stream
 
 
 # The checks below are written out, not shared: at a few microseconds a call
@@ -46,14 +53,15 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
     shape = x.shape
     T, H = shape
     ldx, one = x.stride()
-    assert x.dtype is _BF16 and x.is_cuda and (one == 1 or H == 1)
-    assert weight.dtype is _BF16 and weight.is_cuda and weight.shape == (H,) and weight.is_contiguous()
+    dev = x.get_device()
+    assert x.dtype is _BF16 and dev == _current_device() and (one == 1 or H == 1)
+    assert weight.dtype is _BF16 and weight.get_device() == dev and weight.shape == (H,) and weight.is_contiguous()
     if T <= 1:  # the stride of a single row says nothing
         ldx = H
     res = ldr = 0
     if residual is not None:
         ldr, one = residual.stride()
-        assert residual.dtype is _BF16 and residual.is_cuda and residual.shape == shape
+        assert residual.dtype is _BF16 and residual.get_device() == dev and residual.shape == shape
         assert one == 1 or H == 1
         res = residual.data_ptr()
         if T <= 1:
@@ -72,23 +80,24 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
         out = y, r, q, s
     else:
         y, r, q, s = out
-        assert y is None or (y.dtype is _BF16 and y.is_cuda and y.shape == shape and y.is_contiguous())
+        assert y is None or (y.dtype is _BF16 and y.get_device() == dev and y.shape == shape and y.is_contiguous())
         if residual is None:
             assert r is None
         else:
-            assert r.dtype is _BF16 and r.is_cuda and r.shape == shape and r.is_contiguous()
+            assert r.dtype is _BF16 and r.get_device() == dev and r.shape == shape and r.is_contiguous()
         if fmt is None:
             assert q is None and s is None
         else:
-            assert q.dtype is _U8 and q.is_cuda and q.shape == shape and q.is_contiguous()
+            assert q.dtype is _U8 and q.get_device() == dev and q.shape == shape and q.is_contiguous()
             if block:
-                assert s.dtype is _U8 and s.is_cuda and s.shape == (T, H // block) and s.is_contiguous()
+                assert s.dtype is _U8 and s.get_device() == dev and s.shape == (T, H // block) and s.is_contiguous()
             else:
                 assert s is None
     B.moe_add_rms_norm(x.data_ptr(), ldx, res, ldr, weight.data_ptr(), eps, T, H,
                        0 if r is None else r.data_ptr(), 0 if y is None else y.data_ptr(),
                        0 if q is None else q.data_ptr(), 0 if s is None else s.data_ptr(),
-                       _Q_FORMATS[fmt] if fmt is not None else 0, scale, _stream(stream, x))
+                       _Q_FORMATS[fmt] if fmt is not None else 0, scale,
+                       _current_stream(dev) if stream is None else _given_stream(stream, dev))
     return y, r, q, s
 
 
@@ -105,25 +114,27 @@ def topk_route(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
     T, E = logits.shape
     ld, one = logits.stride()
     bf16 = logits.dtype is _BF16
-    assert (bf16 or logits.dtype is _F32) and logits.is_cuda and (one == 1 or E == 1)
+    dev = logits.get_device()
+    assert (bf16 or logits.dtype is _F32) and dev == _current_device() and (one == 1 or E == 1)
     assert scoring == "softmax" or scoring == "sigmoid"
-    assert bias is None or (bias.dtype is _F32 and bias.is_cuda and bias.shape == (E,) and bias.is_contiguous())
+    assert bias is None or (bias.dtype is _F32 and bias.get_device() == dev and bias.shape == (E,)
+                            and bias.is_contiguous())
     if out is None:
         idx = torch.empty(T, top_k, dtype=_I32, device=logits.device)
         w = torch.empty(T, top_k, dtype=_F32, device=logits.device)
     else:
         idx, w = out
         shape = (T, top_k)
-        assert idx.dtype is _I32 and idx.is_cuda and idx.shape == shape and idx.is_contiguous()
-        assert w.dtype is _F32 and w.is_cuda and w.shape == shape and w.is_contiguous()
+        assert idx.dtype is _I32 and idx.get_device() == dev and idx.shape == shape and idx.is_contiguous()
+        assert w.dtype is _F32 and w.get_device() == dev and w.shape == shape and w.is_contiguous()
     B.moe_topk_route(logits.data_ptr(), bf16, E if T <= 1 else ld, 0 if bias is None else bias.data_ptr(), T, E,
                      top_k, scoring == "sigmoid", num_groups, top_groups, renormalize, scale, idx.data_ptr(),
-                     w.data_ptr(), _stream(stream, logits))
+                     w.data_ptr(), _current_stream(dev) if stream is None else _given_stream(stream, dev))
     return idx, w
 
 
-def _dense(t: torch.Tensor, dtype, shape) -> bool:
-    return t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()
+def _dense(t: torch.Tensor, dtype, shape, dev: int) -> bool:
+    return t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()
 
 
 class _Fp4Handle:
@@ -157,15 +168,18 @@ class Fp4Linear(_Fp4Handle):
                  max_tokens: int = 16, stream=None):
         rows, cols = codes.shape[0], 2 * codes.shape[1]
         n = B.moe_fp4_linear_workspace_query(rows, cols, max_tokens)
-        assert _dense(codes, torch.uint8, (rows, cols // 2))
-        assert _dense(block_scales, torch.uint8, (rows, cols // 16))
-        assert _dense(global_scale, torch.float32, (1,))
+        dev = codes.get_device()
+        assert dev == _current_device()
+        assert _dense(codes, torch.uint8, (rows, cols // 2), dev)
+        assert _dense(block_scales, torch.uint8, (rows, cols // 16), dev)
+        assert _dense(global_scale, torch.float32, (1,), dev)
         self.rows, self.cols, self.max_tokens = rows, cols, max_tokens
         self.weights = (codes, block_scales, global_scale)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=codes.device)
         self.handle = B.moe_fp4_linear_create(rows, cols, max_tokens, codes.data_ptr(),
                                               block_scales.data_ptr(), global_scale.data_ptr(),
-                                              self.workspace.data_ptr(), n, _stream_ptr(stream))
+                                              self.workspace.data_ptr(), n,
+                                              _current_stream(dev) if stream is None else _given_stream(stream, dev))
 
     def forward(self, x: torch.Tensor, out: torch.Tensor | None = None, *,
                 out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
@@ -173,14 +187,16 @@ class Fp4Linear(_Fp4Handle):
         out_dtype (bfloat16 or float32) or in `out`'s type."""
         T, cols = x.shape
         ldx, one = x.stride()
-        assert x.dtype is _BF16 and x.is_cuda and cols == self.cols and one == 1
+        dev = x.get_device()
+        assert x.dtype is _BF16 and dev == _current_device() and cols == self.cols and one == 1
         if out is None:
             assert out_dtype is _BF16 or out_dtype is _F32
             out = torch.empty(T, self.rows, dtype=out_dtype, device=x.device)
         f32 = out.dtype is _F32
-        assert (f32 or out.dtype is _BF16) and out.is_cuda and out.shape == (T, self.rows) and out.is_contiguous()
+        assert (f32 or out.dtype is _BF16) and out.get_device() == dev and out.shape == (T, self.rows)
+        assert out.is_contiguous()
         B.moe_fp4_linear(self.handle, x.data_ptr(), cols if T <= 1 else ldx, T, out.data_ptr(), f32,
-                         _stream(stream, x))
+                         _current_stream(dev) if stream is None else _given_stream(stream, dev))
         return out
 
 
@@ -202,16 +218,19 @@ class Fp4MoELayer(_Fp4Handle):
         """w1 uint8 [E, 2I, H/2] (gate rows, then up rows) with scales uint8 [E, 2I, H/16]
         and float32 [E]; w2 uint8 [E, H, I/2] likewise."""
         E, H, I = self.E, self.H, self.I
-        assert _dense(w1, torch.uint8, (E, 2 * I, H // 2)) and _dense(w2, torch.uint8, (E, H, I // 2))
-        assert _dense(w1_scales, torch.uint8, (E, 2 * I, H // 16))
-        assert _dense(w2_scales, torch.uint8, (E, H, I // 16))
-        assert _dense(w1_global, torch.float32, (E,)) and _dense(w2_global, torch.float32, (E,))
+        dev = w1.get_device()
+        assert dev == _current_device()
+        assert _dense(w1, torch.uint8, (E, 2 * I, H // 2), dev) and _dense(w2, torch.uint8, (E, H, I // 2), dev)
+        assert _dense(w1_scales, torch.uint8, (E, 2 * I, H // 16), dev)
+        assert _dense(w2_scales, torch.uint8, (E, H, I // 16), dev)
+        assert _dense(w1_global, torch.float32, (E,), dev) and _dense(w2_global, torch.float32, (E,), dev)
         self.close()
         self.weights = (w1, w1_scales, w1_global, w2, w2_scales, w2_global)
         self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=w1.device)
         self.handle = B.moe_fp4_create(H, I, E, self.K, self.flags, self.max_tokens,
                                        *(t.data_ptr() for t in self.weights), self.workspace.data_ptr(),
-                                       self._ws_bytes, _stream_ptr(stream))
+                                       self._ws_bytes,
+                                       _current_stream(dev) if stream is None else _given_stream(stream, dev))
 
     def forward(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -220,13 +239,15 @@ class Fp4MoELayer(_Fp4Handle):
             raise B.MoEError(B.MOE_ERR_NOT_BOUND, "moe_fp4_forward")
         shape, routes = x.shape, topk_idx.shape
         T, H = shape
-        assert x.dtype is _BF16 and x.is_cuda and H == self.H and x.is_contiguous()
-        assert topk_idx.dtype is _I32 and topk_idx.is_cuda and routes == (T, self.K) and topk_idx.is_contiguous()
-        assert topk_w.dtype is _F32 and topk_w.is_cuda and topk_w.shape == routes and topk_w.is_contiguous()
+        dev = x.get_device()
+        assert x.dtype is _BF16 and dev == _current_device() and H == self.H and x.is_contiguous()
+        assert topk_idx.dtype is _I32 and topk_idx.get_device() == dev and routes == (T, self.K)
+        assert topk_w.dtype is _F32 and topk_w.get_device() == dev and topk_w.shape == routes
+        assert topk_idx.is_contiguous() and topk_w.is_contiguous()
         if out is None:
             out = torch.empty(T, H, dtype=_BF16, device=x.device)
         else:
-            assert out.dtype is _BF16 and out.is_cuda and out.shape == shape and out.is_contiguous()
+            assert out.dtype is _BF16 and out.get_device() == dev and out.shape == shape and out.is_contiguous()
         B.moe_fp4_forward(self.handle, x.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), T,
-                          out.data_ptr(), _stream(stream, x))
+                          out.data_ptr(), _current_stream(dev) if stream is None else _given_stream(stream, dev))
         return out
