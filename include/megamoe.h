@@ -563,7 +563,7 @@ MOE_API moe_status moe_add_rms_norm(const uint16_t* d_x, int64_t x_stride, const
  * An expert whose logit or bias is -inf is masked; slots that no expert is
  * left for get id -1 and weight 0 (masked slots of the forwards).  A row that
  * holds a NaN gets NaN weights, which the forwards' route checks report.
- * Asynchronous on `stream`; num_tokens 0 is a no-op.  MOE_ERR_UNSUPPORTED:
+ * No overlap of buffers.  Asynchronous on `stream`; num_tokens 0 is a no-op.  MOE_ERR_UNSUPPORTED:
  * num_experts not in 1..1024, top_k not in 1..min(32, num_experts),
  * num_groups not in 1..32 or no divisor of num_experts, top_groups not in
  * 1..num_groups, a bias without sigmoid.  MOE_ERR_INVALID_ARG: a NULL or
@@ -612,7 +612,8 @@ MOE_API moe_status moe_fp4_create(const moe_dims* dims, int64_t max_tokens, cons
  * moe_fp4_forward -- out[t] = sum_k w[t,k] * W2[e] (silu(g) * u), (g; u) =
  * W1[e] x[t], e = topk_idx[t,k].  Inputs and -1 slots as for moe_forward; a
  * token without an active slot gets zeros.  d_out BF16 [num_tokens, hidden].
- * d_x and d_out 16-byte aligned.  An id outside [-1, E) sets
+ * d_x and d_out 16-byte aligned; d_out may be d_x itself (all of x has been
+ * read before the first output is stored), else it overlaps no input.  An id outside [-1, E) sets
  * MOE_DEV_ROUTE_RANGE and its slot is skipped; MOE_FLAG_CHECK_ROUTES adds the
  * duplicate and finite-weight checks.  A token's active ids are distinct: where
  * an expert is named twice its output is undefined.  Asynchronous on `stream`, capturable in
@@ -626,7 +627,8 @@ MOE_API moe_status moe_fp4_forward(moe_fp4_handle* h, const uint16_t* d_x, const
  * moe_fp4_linear -- y = x W^T for 1..16 tokens and one matrix [rows, cols]:
  * d_x BF16 [num_tokens, cols], rows x_stride elements apart (a multiple of 8;
  * 16-byte aligned), d_y [num_tokens, rows] float (y_float32 != 0) or BF16.
- * Any rows up to 2^24; cols a multiple of 32 up to 32768.  Errors as above.
+ * Any rows up to 2^24; cols a multiple of 32 up to 32768.  Errors as above;
+ * MOE_ERR_INVALID_ARG also where d_y overlaps a row of d_x.
  */
 MOE_API moe_status moe_fp4_linear_workspace_query(int32_t rows, int32_t cols, int64_t max_tokens,
                                                   size_t* workspace_bytes);

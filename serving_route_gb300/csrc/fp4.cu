@@ -1907,6 +1907,12 @@ moe_status moe_fp4_linear(moe_fp4_handle* h, const uint16_t* d_x, int64_t x_stri
   if (!d_x || !d_y || x_stride < m.cols || x_stride % 8 || misaligned(d_x, 16) ||
       misaligned(d_y, y_float32 ? 4 : 2) || elsewhere(h))
     return MOE_ERR_INVALID_ARG;
+  // a CTA that has finished stores y while others still read x
+  const uintptr_t y0 = (uintptr_t)d_y, y1 = y0 + (size_t)num_tokens * m.rows * (y_float32 ? 4 : 2);
+  for (int64_t t = 0; t < num_tokens; ++t) {
+    const uintptr_t x0 = (uintptr_t)(d_x + t * x_stride);
+    if (x0 < y1 && y0 < x0 + 2 * (size_t)m.cols) return MOE_ERR_INVALID_ARG;
+  }
   const Fp4Plan p = fp4_plan_linear(m.cols, (int)num_tokens);
   Fp4Args a = {};
   a.m[0] = m;

@@ -184,7 +184,7 @@ class Fp4Linear(_Fp4Handle):
     def forward(self, x: torch.Tensor, out: torch.Tensor | None = None, *,
                 out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
         """x BF16 [T, cols] (rows may be strided by a multiple of 8) -> [T, rows] in
-        out_dtype (bfloat16 or float32) or in `out`'s type."""
+        out_dtype (bfloat16 or float32) or in `out`'s type; `out` may not overlap x."""
         T, cols = x.shape
         ldx, one = x.stride()
         dev = x.get_device()
@@ -234,7 +234,8 @@ class Fp4MoELayer(_Fp4Handle):
 
     def forward(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-        """x BF16 [T, H], topk_idx int32 [T, K] (-1: masked slot), topk_w float32 [T, K] -> BF16 [T, H]."""
+        """x BF16 [T, H], topk_idx int32 [T, K] (-1: masked slot), topk_w float32 [T, K] -> BF16 [T, H].
+        `out` may be x."""
         if self.handle is None:
             raise B.MoEError(B.MOE_ERR_NOT_BOUND, "moe_fp4_forward")
         shape, routes = x.shape, topk_idx.shape
