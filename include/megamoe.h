@@ -562,7 +562,10 @@ MOE_API moe_status moe_add_rms_norm(const uint16_t* d_x, int64_t x_stride, const
  *   d_topk_idx int32 [num_tokens, top_k], d_topk_w float [num_tokens, top_k].
  * An expert whose logit or bias is -inf is masked; slots that no expert is
  * left for get id -1 and weight 0 (masked slots of the forwards).  A row that
- * holds a NaN gets NaN weights, which the forwards' route checks report.
+ * holds a NaN (in its logits or in the bias) gets NaN weights, which the
+ * forwards' route checks report.  Its NaN experts are not chosen either, but
+ * where no other is left the lowest of them takes the first slot, as the
+ * forwards skip slots of id -1.
  * No overlap of buffers.  Asynchronous on `stream`; num_tokens 0 is a no-op.  MOE_ERR_UNSUPPORTED:
  * num_experts not in 1..1024, top_k not in 1..min(32, num_experts),
  * num_groups not in 1..32 or no divisor of num_experts, top_groups not in

@@ -10,7 +10,8 @@
 //   weight:   p of the chosen, divided by their sum (renormalize), times scale.
 //
 // An expert whose logit (or bias) is -inf is masked: it is never chosen, and
-// slots without an expert get id -1 and weight 0, which the layer skips.
+// slots without an expert get id -1 and weight 0, which the layer skips.  Nor is one chosen
+// that holds a NaN, but a row with one has NaN weights and names at least one expert.
 //
 // Every lane holds E / 32 choice values in registers as integers of the same
 // order (0: masked or taken), sorted, so a choice is a warp-wide integer
@@ -242,6 +243,20 @@ __global__ void __launch_bounds__(128) topk_route_kernel(const TopkArgs a) {
         }
       }
       if (lane == k) my = at;
+    }
+
+  // Only NaN (and masked) experts: the first slot names the first one that holds a NaN, so
+  // that its weight is seen; the layer skips slots of -1.
+  if (any_nan && __all_sync(kAll, my < 0))
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const float v = e < a.E ? load_logit<BF16>(a.logits, row + e) : 0.f;
+      const float b = SIGMOID && a.bias && e < a.E ? a.bias[e] : 0.f;
+      const uint32_t who = __ballot_sync(kAll, v != v || b != b);
+      if (who) {
+        if (lane == 0) my = e0 + __ffs(who) - 1;
+        break;
+      }
     }
 
   float p = 0.f;

@@ -110,7 +110,8 @@ def topk_route(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
     "sigmoid" by sigmoid + bias (float32 [E]); weights never hold the bias.
     The choice is limited to the top_groups best of num_groups equal groups (a
     group's score: its largest logit, or the sum of its two largest biased
-    scores).  Logits of -inf mask an expert; slots left over get id -1."""
+    scores).  Logits of -inf mask an expert; slots left over get id -1.
+    A row with a NaN gets NaN weights, and at least one id."""
     T, E = logits.shape
     ld, one = logits.stride()
     bf16 = logits.dtype is _BF16
