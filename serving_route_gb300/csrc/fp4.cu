@@ -499,6 +499,15 @@ __device__ __forceinline__ int row_exponent(float max) {
 
 __device__ __forceinline__ float pow2f(int s) { return __uint_as_float((uint32_t)(s + 127) << 23); }
 
+// A row's scale 2^-s as the product of two normal numbers near its root: sums are multiplied
+// by the first (exactly: they lie between 2^-34 and 2^42, or are 0), the matrix's scale by
+// the second.  The product of the whole 2^-s and the matrix's scale may be subnormal
+// although the result is not (x near 2^-112, say).
+__device__ __forceinline__ float2 root_scales(float rscale) {
+  const uint32_t e = __float_as_uint(rscale), one = 0x3F800000u, root = ((e + one) >> 1) & 0x7F800000u;
+  return make_float2(__uint_as_float(root), __uint_as_float(e - root + one));
+}
+
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 p = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
@@ -1228,7 +1237,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       ItemWalk it;
       TilePos at = f.start;
       int ka = f.ka, n = 0, s0 = 0;
-      float factor[NT][2];
+      float factor[NT][2], factor2[NT][2];
       bool fresh = true;  // a new item since this warp's last tile
       int turn = 0;
       for (int u = f.u0 - ka; u < f.u1; u += f.U, f.step(at)) {
@@ -1299,7 +1308,10 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
               const int col = 8 * nt + 2 * t + o;
-              factor[nt][o] = col < n ? sm.rscale[0][c.row_slot(res, it.pos, R, s0, col)] * gl : 0.f;
+              const float2 f2 =
+                  col < n ? root_scales(sm.rscale[0][c.row_slot(res, it.pos, R, s0, col)]) : make_float2(0.f, 0.f);
+              factor[nt][o] = f2.x;
+              factor2[nt][o] = f2.y * gl;
             }
         }
 #pragma unroll
@@ -1308,8 +1320,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
           for (int o = 0; o < 2; ++o)
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-              acc[m][nt][o] *= factor[nt][o];
-              acc[m][nt][2 + o] *= factor[nt][o];
+              acc[m][nt][o] = acc[m][nt][o] * factor[nt][o] * factor2[nt][o];
+              acc[m][nt][2 + o] = acc[m][nt][2 + o] * factor[nt][o] * factor2[nt][o];
             }
         if (cut) {
           auto share = [&](int cta) {
@@ -1414,12 +1426,14 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         // lane (g, t) holds rows g and g + 8 of tokens 2 t and 2 t + 1: their factors
         // and places in out[token][row], which sums over the tile's items
         const float gl = sm.vglobal[1][at.v];
-        float factor[2] = {0.f, 0.f};
+        float factor[2], factor2[2];
         float* row[2];
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
           const int col = min(2 * t + o, n - 1), s = s0 + col;
-          factor[o] = sm.rscale[1][c.row_slot(false, it.pos, R, s0, col)] * gl * sm.route_w[s];
+          const float2 f2 = root_scales(sm.rscale[1][c.row_slot(false, it.pos, R, s0, col)]);
+          factor[o] = f2.x;
+          factor2[o] = f2.y * gl * sm.route_w[s];
           row[o] = &sm.out[sm.route_tok[s]][g];
         }
 #pragma unroll
@@ -1442,13 +1456,13 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
               auto add = [&](const uint4& p, const uint4& q, int hi) {
                 const uint32_t y = hi ? (o ? p.w : p.z) : (o ? p.y : p.x);
                 const uint32_t z = hi ? (o ? q.w : q.z) : (o ? q.y : q.x);
-                return __uint_as_float(y) + __uint_as_float(z);
+                return (__uint_as_float(y) + __uint_as_float(z)) * factor[o];
               };
               const float r[4] = {to[0], to[8], to[16], to[24]};
-              to[0] = fmaf(factor[o], add(x[0][0], x[1][0], 0), r[0]);
-              to[8] = fmaf(factor[o], add(x[0][0], x[1][0], 1), r[1]);
-              to[16] = fmaf(factor[o], add(x[0][1], x[1][1], 0), r[2]);
-              to[24] = fmaf(factor[o], add(x[0][1], x[1][1], 1), r[3]);
+              to[0] = fmaf(factor2[o], add(x[0][0], x[1][0], 0), r[0]);
+              to[8] = fmaf(factor2[o], add(x[0][0], x[1][0], 1), r[1]);
+              to[16] = fmaf(factor2[o], add(x[0][1], x[1][1], 0), r[2]);
+              to[24] = fmaf(factor2[o], add(x[0][1], x[1][1], 1), r[3]);
             }
         }
         give_back(from, cnt);
