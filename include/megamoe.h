@@ -535,8 +535,8 @@ MOE_API moe_status moe_route_noalloc(const int32_t* d_topk_idx, const float* d_t
  * else MOE_ERR_UNSUPPORTED); multiples of 8 up to 16384 with 16-byte aligned
  * rows take the vector path.  Sums are float.  No other overlap of buffers.
  * Asynchronous on `stream`.  MOE_ERR_INVALID_ARG: a NULL or misaligned
- * pointer, a stride below hidden, eps negative or NaN, a static scale that is
- * not positive and finite.  num_tokens 0 is a no-op.
+ * pointer, a stride below hidden, eps negative, NaN or above 1e30, a static
+ * scale that is not positive and finite.  num_tokens 0 is a no-op.
  */
 MOE_API moe_status moe_add_rms_norm(const uint16_t* d_x, int64_t x_stride, const uint16_t* d_residual,
                                     int64_t residual_stride, const uint16_t* d_weight, float eps,

@@ -16,6 +16,8 @@
 // many rows (8192 x 7168 with 1x128 codes: 77.2 us, 529 MB, 6.85 TB/s: the copy
 // rate) and by one load -> reduce -> store latency chain for few (2.3 us in a
 // stream of calls).
+#include <cfloat>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -277,7 +279,7 @@ extern "C" moe_status moe_add_rms_norm(const uint16_t* d_x, int64_t x_stride,
   float rscale = 1.f;
   if (d_q) {
     if (q_format == MOE_FLAG_PER_TENSOR) {
-      if (!(q_static_scale > 0.f) || q_static_scale > 3.0e38f) return MOE_ERR_INVALID_ARG;
+      if (!(q_static_scale > 0.f) || !(q_static_scale <= FLT_MAX)) return MOE_ERR_INVALID_ARG;
       fmt = 3;
       rscale = 1.f / q_static_scale;
     } else {
