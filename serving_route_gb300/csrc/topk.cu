@@ -17,8 +17,8 @@
 // order (0: masked or taken), sorted, so a choice is a warp-wide integer
 // maximum of the lanes' first ones and a ballot for who has it.  Bytes: the
 // logits once, 8 per chosen expert; for few tokens the chain of top_k choices
-// bounds it (256 experts, 4 of 8 groups, K = 8: 2.6 us in a stream of calls),
-// for many the instructions issued (8192 tokens: 8.4 us, 6.4 without groups, where
+// bounds it (256 experts, 4 of 8 groups, K = 8: 2.5 to 2.8 us in a stream of calls),
+// for many the instructions issued (8192 tokens: 8.8 us, 6.9 without groups, where
 // the bytes alone take 1.3 at 6782 GB/s).
 #include <cfloat>
 
@@ -39,19 +39,16 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
-// (correctly rounded, subnormal scores too: down to l = -88.7, below which exp(-l) is
-// infinite and the score 0)
-__device__ __forceinline__ float sigmoid_score(float l) { return __frcp_rn(1.0f + expf(-l)); }
-
-// The same without the range check of a general quotient (256 experts, 4 of 8 groups: 8192
-// tokens 9.0 us, one 2.5; with the general one 9.15 and 2.8): the hardware's reciprocal and
-// one Newton step (equal to the correctly rounded one for every float from 1 to 2^126:
-// compared on the hardware).  Subnormal results come out as 0, for the caller to do again.
-__device__ __forceinline__ float sigmoid_score_normal(float l) {
-  const float x = 1.0f + expf(-l);
+// 1 / x of x = 1 + exp(-l), by the hardware's reciprocal of x / 8 and one Newton step: equal
+// to the correctly rounded quotient for every float x from 1 on (compared on the hardware;
+// subnormal scores are within one step of it), and not flushed to 0 for l in (-88.7, -87.3) as
+// the reciprocal of x is.  Below that exp(-l) is infinite and the score 0.  (A general quotient
+// with its check of x's range: 8192 tokens of 256 experts, 4 of 8 groups 9.15 us, so 8.8.)
+__device__ __forceinline__ float sigmoid_score(float l) {
+  const float y = fmaf(expf(-l), 0.125f, 0.125f);
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return fmaf(r, fmaf(-fminf(x, FLT_MAX), r, 1.0f), r);  // (x infinite: r = 0)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+  return fmaf(r, fmaf(-fminf(y, FLT_MAX), r, 1.0f), r) * 0.125f;
 }
 
 // Descending, by the odd-even merge network (Batcher 1968): 5, 19, 63, 191 exchanges of
@@ -91,6 +88,20 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
               : reinterpret_cast<const float*>(p)[i];
 }
 
+// A predicated load: from a plain conditional one the compiler may make a branch, and
+// put it behind the scores, where its latency is not hidden (one token 3.1 us, so 2.8).
+__device__ __forceinline__ float load_if(const float* p, bool on) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .pred on;\n\t"
+      "setp.ne.s32 on, %2, 0;\n\t"
+      "mov.f32 %0, 0f00000000;\n\t"
+      "@on ld.global.f32 %0, [%1];\n\t}"
+      : "=f"(v)
+      : "l"(p), "r"((int)on));
+  return v;
+}
+
 // V values per lane: expert 32 i + lane.
 template <int V, bool BF16, bool SIGMOID>
 __global__ void __launch_bounds__(128) topk_route_kernel(const TopkArgs a) {
@@ -107,27 +118,15 @@ __global__ void __launch_bounds__(128) topk_route_kernel(const TopkArgs a) {
   for (int i = 0; i < V; ++i) {  // all loads before the first use
     const int e = 32 * i + lane;
     l[i] = e < a.E ? load_logit<BF16>(a.logits, row + e) : -INFINITY;
-    bias[i] = SIGMOID && a.bias && e < a.E ? a.bias[e] : 0.f;
-  }
-  float score[V];
-  if (SIGMOID) {
-    bool low = false;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      score[i] = sigmoid_score_normal(l[i]);
-      low |= score[i] == 0.f && l[i] > -INFINITY;
-    }
-    if (__any_sync(kAll, low)) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) score[i] = sigmoid_score(l[i]);
-    }
+    bias[i] = SIGMOID ? load_if(a.bias + e, a.bias && e < a.E) : 0.f;
   }
   uint32_t key[V];
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = 32 * i + lane;
-    const float c = SIGMOID ? score[i] + bias[i] : l[i];
+    float c = l[i];
+    if (SIGMOID) c = sigmoid_score(c) + bias[i];
     bad |= c != c;  // also where l is NaN
     key[i] = l[i] > -INFINITY && c > -INFINITY ? order_key(c) : 0u;
     if (kUnique && key[i]) key[i] = (key[i] & 0xFFFF0000u) | (0xFFFFu - e);
