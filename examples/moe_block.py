@@ -6,7 +6,9 @@ choice, routed experts and a shared expert, for a prompt and then token by token
 Few tokens (up to 16) run on the four-bit weights as they are stored, where
 reading them is all the time goes into; a prompt runs on the same weights
 requantised once to 128x128 FP8, and its layer takes the norm's 8-bit output as
-it is.  The few-token step is captured in a CUDA graph.  The weights are random.
+it is.  The few-token step is captured in a CUDA graph.  The weights are random, and
+the gate's are in NVFP4 like the others: a checkpoint that keeps its gate in BF16
+or float multiplies it by other means (y @ gate.t()), as the prompt does here.
 """
 from __future__ import annotations
 

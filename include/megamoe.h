@@ -584,7 +584,9 @@ MOE_API moe_status moe_topk_route(const void* d_logits, int32_t logits_bf16, int
  * [n, rows, cols/2], two E2M1 codes per byte, column 2b in the low nibble of
  * byte b; scales uint8 [n, rows, cols/16], E4M3; global float [n];
  *   v = e2m1(code) * e4m3(scale) * global.
- * Weights stay in four bits, activations in BF16 or better, sums in float.  A
+ * Weights stay in four bits, sums are float.  x keeps BF16's bits down to 2^-32
+ * of its row's largest value (smaller ones are rounded at 2^-40 of it), the
+ * layer's h 11 bits, or it is rounded at 2^-39 of its row's largest value.  A
  * handle binds one layer's or one matrix's device pointers and a workspace
  * that no other handle uses at the same time.
  */
@@ -630,7 +632,10 @@ MOE_API moe_status moe_fp4_forward(moe_fp4_handle* h, const uint16_t* d_x, const
  * moe_fp4_linear -- y = x W^T for 1..16 tokens and one matrix [rows, cols]:
  * d_x BF16 [num_tokens, cols], rows x_stride elements apart (a multiple of 8;
  * 16-byte aligned), d_y [num_tokens, rows] float (y_float32 != 0) or BF16.
- * Any rows up to 2^24; cols a multiple of 32 up to 32768.  Errors as above;
+ * Any rows up to 2^24; cols a multiple of 32 up to 32768.  Whole rows of x stay
+ * in shared memory: where those of all tokens do not fit (above 2048 columns
+ * with 16 tokens, 5120 with 8, 7168 with 6) the matrix is swept two or more
+ * times.  Errors as above;
  * MOE_ERR_INVALID_ARG also where d_y overlaps a row of d_x.
  */
 MOE_API moe_status moe_fp4_linear_workspace_query(int32_t rows, int32_t cols, int64_t max_tokens,

@@ -12,20 +12,23 @@
 // about 42 weights a clock; dequantising them costs one convert and one product
 // per two weights, which is as much again, so the two have to overlap.  Measured
 // for the layer of 256 experts, H 7168, I 2048, 16 tokens (2.52 GB): copies alone
-// 374 us, products alone 374 us, the kernel 385 to 413 us, 6.1 to 6.5 TB/s.
+// 374 us, products alone 374 us, the kernel 385 to 428 us, 5.9 to 6.5 TB/s.
 //   * four code pairs of a 32-bit word become half2 with one hardware convert
 //     each, one half2 product applies the E4M3 scale (6 significant bits: both
 //     exact in half), and m16n8k16 half MMAs with float accumulators take 8
-//     tokens as their N side.  Up to 16 tokens leave a 128-row tensor-memory MMA
-//     nothing to do that would pay for bringing the dequantised weights back to
-//     shared memory; here they go from registers to the tensor cores.  The
+//     tokens as their N side: the weights go from registers to the tensor cores,
+//     which are busy for 7% (linear) to 25% (layer) of the time.  (A tensor-memory
+//     MMA could take them from tensor memory, with 8 or 16 tokens as N, after a
+//     store to it instead of the operand registers: not tried.)  The
 //     checkpoint's order is kept: lane (g, t) owns 128 consecutive columns of
 //     rows g and g + 8, so a 16-byte load of codes feeds eight MMAs of its own,
 //     and x is stored in shared memory in the order in which the lanes need it.
 //   * x (BF16) and h (float) enter as half, each row multiplied by the power of
 //     two that brings its largest value to [2^14, 2^15): for BF16 values exact
 //     down to 2^-32 of the row's largest, below that rounded at 2^-40 of it; h
-//     is rounded to 11 bits.  The inverse is applied to the float sums.
+//     is rounded to 11 bits, or at 2^-39 of its row's largest value where that is
+//     more: half is what the MMA takes, and of BF16 outputs the error against 64 bits
+//     is 0.00167 with it, 0.00166 with a float h.  The inverse is applied to the float sums.
 //   * a place of the shared-memory ring is one consumer warp's unit of work, 32
 //     rows x 512 columns: 8 KB of codes, copied by TMA as stored, and 1 KB of
 //     scales by asynchronous copies (their rows need not be multiples of 16
@@ -37,12 +40,12 @@
 //   * the layer is one cooperative launch: FC1 units, a grid barrier on h, FC2
 //     units.  The weights' copies do not wait at the barrier: the ring fills
 //     with FC2 weights while the last FC1 sums and h are on their way.
-// Where one token's 46.4 us go (H 7168, I 2048, 8 of 256 experts; 29.2 us at the copy
+// Where one token's 46 us go (H 7168, I 2048, 8 of 256 experts; 29.2 us at the copy
 // rate): tables and the first copies 4.7 us, FC1 to 24, its last sums and the barrier
 // to 28.2, h rows to 30.3, FC2 to 40, joining and leaving to 43, the launch.  FC2
 // there is bound by its products (its first third is in the ring before the barrier
 // opens; sending the rest to L2 ahead made it slower).  The linear (4096 x 7168, one
-// token: 7.4 us, 2.4 at the copy rate) is bound by the same start, one tile's products
+// token: 7.5 us, 2.4 at the copy rate) is bound by the same start, one tile's products
 // and the launch.
 #include <cudaTypedefs.h>
 
@@ -86,7 +89,8 @@ constexpr int kUnitBytes = kCodeBytes + kScaleBytes;
 constexpr int kBoxBytes = 16 * 128;  // 16 rows x 256 columns
 constexpr int kItems = 8;            // operand items in flight (rows ring)
 // Ranges are cut within tiles where whole tiles would leave the fullest CTA with more
-// than this many units above the mean: a join takes about 3 us, 15 units of copies
+// than this many units above the mean: a join takes about 3 us, 15 units of copies (one
+// token of H 7168, I 2048; other borders have not been measured)
 constexpr int kCutUnits = 15;
 constexpr int kTile2 = 128;          // output rows of an FC2 tile
 constexpr int kMaxSmem = 232448;
@@ -769,6 +773,7 @@ __device__ __forceinline__ void build_items(const Fp4Args& a, Fp4Shared& sm, int
   // The second division has more places in the ring and takes fewer tokens at a time: an
   // expert with more of them is swept again.  For 16 tokens of 256 experts, H 7168, 16
   // places are 5% faster than 12 (402 and 424 us) and a sweep more is 1% of the products.
+  // (The rule weighs items by that one shape; its border has not been measured.)
   auto items = [&](int i) { return sm.warp_cnt[i][0] + sm.warp_cnt[i][1] + sm.warp_cnt[i][2] + sm.warp_cnt[i][3]; };
   const int plan = a.group[1] && 17 * items(0) >= 16 * items(1), nv = items(plan);
   int v = __popc((plan ? firsts[1] : firsts[0]) & ((1u << lane) - 1u));
@@ -1633,8 +1638,10 @@ static Fp4Plan fp4_plan_layer(int H, int I, int T, int K, int budget) {
 }
 
 // The linear: one sweep over the matrix for up to 16 tokens where their rows
-// fit, else equal groups, each with its own sweep (the second from L2, where
-// the matrix fits there).
+// fit (2048 columns; 8 tokens of 5120, 6 of 7168, 1 of 32768), else equal groups, each
+// with its own sweep (the second from L2, where the matrix fits there).  4096 x 7168:
+// 6 tokens 10.3 us, 7 to 12 (two sweeps) 14.1 to 16.3, 13 to 16 (three) 27.5; 4096 x 4096: 8
+// tokens 8.2, 9 (two) 10.2.
 static Fp4Plan fp4_plan_linear(int cols, int T) {
   Fp4Plan p = {0, 1, 0, 0, 0};
   const int rb = row_bytes(cols, false);

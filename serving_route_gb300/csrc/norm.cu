@@ -42,7 +42,7 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the block; every thread gets it.  red: 33 floats.
+// Sum over the block; every thread gets it.  red: 32 floats, one a warp.
 __device__ __forceinline__ float block_sum(float v, float* red) {
   v = warp_sum(v);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
@@ -245,7 +245,8 @@ static cudaError_t launch_norm(const NormArgs& a, int64_t T, bool vec, cudaStrea
   // few rows: as many threads as a block takes, so that the latency chain is
   // short (7168 columns, one row: 2.3 us, with four vectors a thread 2.6; 2048
   // columns: 1.6 and 2.3); many rows: four vectors a thread, so that several rows
-  // are in flight on an SM (8192 rows: 77 us, with one vector a thread 88)
+  // are in flight on an SM (8192 rows: 77 us, with one vector a thread 88; between one and
+  // 8192 rows neither has been measured, the border is one row an SM)
   if (T <= 152 && nvec <= 1024)
     return launch_k(add_rms_norm_kernel<1, FMT>, dim3((unsigned)T), dim3(threads(1)), 0, s, true, nullptr, a);
   if (T <= 152)

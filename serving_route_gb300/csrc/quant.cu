@@ -183,9 +183,12 @@ __global__ void __launch_bounds__(256, B == 4 ? 4 : 1) quant_dispatch_kernel(
 
 // The dispatch of activations that come quantised (E4M3 codes [T, H], E8M0 bytes
 // [T, H/128], or [T, H/32] under MXFP8, none per-tensor): quant_dispatch's walk and
-// stores without its arithmetic, at half the bytes read.  Unlike there the codes
-// are read after the programmatic wait: the routing kernel's launch may overlap
-// whatever wrote them.  Bound by the K rows written (8192 tokens x 7168, K = 8: 100 us,
+// stores without its arithmetic, at half the bytes read.  All of it comes after the
+// programmatic wait.  The codes need not: the forward's first kernel (routing) is not a
+// programmatic dependent, so whatever wrote the inputs has ended before it
+// starts, which quant_dispatch relies on for its loads of x before the wait and the routing
+// kernels, which do not wait, for topk_idx; loads ahead of the wait have not been
+// measured here.  Bound by the K rows written (8192 tokens x 7168, K = 8: 100 us,
 // quant_dispatch 110; 8 tokens: 6.0 and 8.1).
 template <int FMT>
 __global__ void __launch_bounds__(256) dispatch_quantized_kernel(
