@@ -659,6 +659,123 @@ MOE_API moe_status moe_fp4_read_status(moe_fp4_handle* h, uint32_t* h_status,
 /* moe_fp4_destroy -- frees the host handle; NULL is a no-op. */
 MOE_API void moe_fp4_destroy(moe_fp4_handle* h);
 
+/* ------------------------------------------------------------------------
+ * Dense products beside the layer, for any number of tokens: a linear in the
+ * layer's FP8 format, and a gated feed-forward block (a shared expert, a dense
+ * layer) with its gradients.  Handles as above: they bind device pointers and a
+ * workspace that no other handle uses at the same time, calls of one handle do
+ * not overlap on the GPU, and a call on another device than the handle's is
+ * refused with MOE_ERR_INVALID_ARG.  Calls are asynchronous on `stream`,
+ * allocate nothing and can be captured in a CUDA graph.  num_tokens 0 is a
+ * no-op (but see moe_mlp_backward); MOE_ERR_CAPACITY above max_tokens (at most 2^24).
+ * ------------------------------------------------------------------------ */
+
+typedef struct moe_fp8_linear_handle moe_fp8_linear_handle;
+
+/*
+ * moe_fp8_linear_workspace_query / moe_fp8_linear_create -- one matrix W
+ * [rows, cols] in the layer's default format:
+ *   d_codes   E4M3 [rows, cols], 16-byte aligned; read in place, kept by the
+ *             caller, unchanged, while the handle lives.
+ *   d_scales  float [ceil(rows / 128), cols / 128], one power of two per
+ *             128x128 block (as moe_quantize_weights gives them; rows that are
+ *             no multiple of 128 have a last block of fewer).  Copied.
+ * rows 1 to 2^24; cols a multiple of 128 up to 32768, else
+ * MOE_ERR_UNSUPPORTED.  Creating synchronises `stream`; MOE_ERR_BAD_SCALE
+ * where a scale is no power of two in [2^-127, 2^127].
+ */
+MOE_API moe_status moe_fp8_linear_workspace_query(int32_t rows, int32_t cols, int64_t max_tokens,
+                                                  size_t* workspace_bytes);
+MOE_API moe_status moe_fp8_linear_create(int32_t rows, int32_t cols, int64_t max_tokens,
+                                         const uint8_t* d_codes, const float* d_scales,
+                                         void* d_workspace, size_t workspace_bytes,
+                                         struct CUstream_st* stream, moe_fp8_linear_handle** out);
+
+/*
+ * moe_fp8_linear -- y = xq W^T with x BF16 [num_tokens, cols] (rows x_stride
+ * elements apart, a multiple of 8; 16-byte aligned), each row rounded to E4M3 with one
+ * power-of-two scale per 128 columns: the least 2^e with amax <= 448 * 2^e, e in
+ * [-127, 127], 0 for an all-zero block, as moe_add_rms_norm's.
+ * moe_fp8_linear_quantized -- the same of rows that are so already: d_xq
+ * E4M3 [num_tokens, cols], 16-byte aligned, d_xq_scale E8M0 bytes [num_tokens, cols / 128].
+ * Products and sums are exact to FP32; d_y [num_tokens, rows] float
+ * (y_float32 != 0) or BF16.  MOE_ERR_INVALID_ARG: a NULL or misaligned pointer, a stride
+ * below cols, d_y overlapping the span of the inputs' rows.
+ */
+MOE_API moe_status moe_fp8_linear(moe_fp8_linear_handle* h, const uint16_t* d_x, int64_t x_stride,
+                                  int64_t num_tokens, void* d_y, int32_t y_float32,
+                                  struct CUstream_st* stream);
+MOE_API moe_status moe_fp8_linear_quantized(moe_fp8_linear_handle* h, const uint8_t* d_xq,
+                                            const uint8_t* d_xq_scale, int64_t num_tokens, void* d_y,
+                                            int32_t y_float32, struct CUstream_st* stream);
+
+/* moe_fp8_linear_read_status, moe_mlp_read_status -- the handle's device status
+ * word since it was last read (synchronises `stream`): 0 and MOE_OK, or MOE_DEV_TIMEOUT
+ * and MOE_ERR_DEVICE_TIMEOUT after a bounded wait ran out; the outputs of the calls
+ * since are then undefined, and reading makes the next call a normal one. */
+MOE_API moe_status moe_fp8_linear_read_status(moe_fp8_linear_handle* h, uint32_t* h_status,
+                                              struct CUstream_st* stream);
+/* moe_fp8_linear_destroy, moe_mlp_destroy -- free the host handle; NULL is a no-op. */
+MOE_API void moe_fp8_linear_destroy(moe_fp8_linear_handle* h);
+
+typedef struct moe_mlp_handle moe_mlp_handle;
+
+/* Activations of moe_mlp_create: g / (1 + exp(-g)), and GELU in its tanh form
+ * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2. */
+#define MOE_ACT_SILU 0
+#define MOE_ACT_GELU_TANH 1
+
+/*
+ * moe_mlp_workspace_query / moe_mlp_create -- the block
+ *   y = (act(x Wg^T) * (x Wu^T)) Wd^T
+ * in BF16 (fp16 = 0) or FP16, both as 16-bit patterns:
+ *   d_w1  [2 inter, hidden]: rows [0, inter) gate, rows [inter, 2 inter) up.
+ *   d_w2  [hidden, inter].
+ * Read in place at every call: an optimiser may change them between calls.
+ * hidden and inter are multiples of 8 up to 65536, else MOE_ERR_UNSUPPORTED.
+ * The workspace holds h and the gradients of gate and up, 6 max_tokens inter
+ * bytes, and what few tokens need.
+ */
+MOE_API moe_status moe_mlp_workspace_query(int32_t hidden, int32_t inter, int64_t max_tokens,
+                                           size_t* workspace_bytes);
+MOE_API moe_status moe_mlp_create(int32_t hidden, int32_t inter, int32_t fp16, int32_t activation,
+                                  int64_t max_tokens, const uint16_t* d_w1, const uint16_t* d_w2,
+                                  void* d_workspace, size_t workspace_bytes,
+                                  struct CUstream_st* stream, moe_mlp_handle** out);
+
+/*
+ * moe_mlp_forward -- d_x [num_tokens, hidden], rows x_stride elements apart
+ * (a multiple of 8); d_y [num_tokens, hidden]; d_saved NULL, or gate and up
+ * before the activation [num_tokens, 2 inter] for the backward pass, float
+ * (saved_float32 != 0) or in the block's type.  All 16-byte aligned.  Sums are
+ * FP32, of which act(g) * u is rounded once to the block's type (FP16: its range
+ * holds for it).  d_y may be d_x itself (dense rows), else nothing overlaps
+ * (the span of strided rows counts whole): MOE_ERR_INVALID_ARG.
+ */
+MOE_API moe_status moe_mlp_forward(moe_mlp_handle* h, const uint16_t* d_x, int64_t x_stride,
+                                   int64_t num_tokens, uint16_t* d_y, void* d_saved,
+                                   int32_t saved_float32, struct CUstream_st* stream);
+
+/*
+ * moe_mlp_backward -- from dy [num_tokens, hidden] (rows dy_stride apart) and
+ * the forward's x and saved gate and up:
+ *   dh = dy Wd;  dg = dh * u * act'(g);  du = dh * act(g);
+ *   dx = dg Wg + du Wu;  dW1 = (dg; du)^T x;  dW2 = dy^T (act(g) * u).
+ * d_dx [num_tokens, hidden], d_dw1 [2 inter, hidden], d_dw2 [hidden, inter]:
+ * each may be NULL (not wanted).  d_dx in the block's type; the weights'
+ * gradients in it too, or float (dw_float32 != 0), then with accumulate != 0 added to
+ * what is there.  dg, du and act(g) * u are rounded once to the block's type on the way.
+ * No overlaps, all 16-byte aligned.  num_tokens 0 zeroes the weights' gradients
+ * (accumulate: leaves them).
+ */
+MOE_API moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_stride,
+                                    const uint16_t* d_x, int64_t x_stride, const void* d_saved,
+                                    int32_t saved_float32, int64_t num_tokens, uint16_t* d_dx,
+                                    void* d_dw1, void* d_dw2, int32_t dw_float32, int32_t accumulate,
+                                    struct CUstream_st* stream);
+MOE_API moe_status moe_mlp_read_status(moe_mlp_handle* h, uint32_t* h_status, struct CUstream_st* stream);
+MOE_API void moe_mlp_destroy(moe_mlp_handle* h);
+
 /* moe_destroy -- frees the host handle (lifecycle only; the pages have no
  * passage on it).  Device memory stays the caller's.  NULL is a no-op. */
 MOE_API void moe_destroy(moe_handle* h);

@@ -46,6 +46,9 @@ MOE_FLAG_PER_TENSOR = 0x400
 MOE_FLAG_NO_SWAP_AB = 0x800
 MOE_FLAG_COMBINE_IN_FC2 = 0x1000
 
+MOE_ACT_SILU = 0
+MOE_ACT_GELU_TANH = 1
+
 # every function the header declares (checked against include/megamoe.h by a test)
 API_NAMES = ("moe_workspace_query", "moe_create", "moe_quantize_weights", "moe_quantize_weights_mx",
              "moe_quantize_weights_pt", "moe_requantize_weights_nvfp4", "moe_bind_weights",
@@ -56,7 +59,11 @@ API_NAMES = ("moe_workspace_query", "moe_create", "moe_quantize_weights", "moe_q
              "moe_forward_quantized",
              "moe_fp4_workspace_query", "moe_fp4_create", "moe_fp4_forward",
              "moe_fp4_linear_workspace_query", "moe_fp4_linear_create", "moe_fp4_linear",
-             "moe_fp4_read_status", "moe_fp4_destroy")
+             "moe_fp4_read_status", "moe_fp4_destroy",
+             "moe_fp8_linear_workspace_query", "moe_fp8_linear_create", "moe_fp8_linear",
+             "moe_fp8_linear_quantized", "moe_fp8_linear_read_status", "moe_fp8_linear_destroy",
+             "moe_mlp_workspace_query", "moe_mlp_create", "moe_mlp_forward", "moe_mlp_backward",
+             "moe_mlp_read_status", "moe_mlp_destroy")
 
 
 class moe_dims(ctypes.Structure):
@@ -135,12 +142,24 @@ def lib() -> ctypes.CDLL:
         L.moe_fp4_read_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
         L.moe_fp4_destroy.argtypes = [vp]
         L.moe_fp4_destroy.restype = None
+        L.moe_fp8_linear_workspace_query.argtypes = [i32, i32, i64, psz]
+        L.moe_fp8_linear_create.argtypes = [i32, i32, i64, vp, vp, vp, ctypes.c_size_t, vp, ctypes.POINTER(vp)]
+        L.moe_fp8_linear.argtypes = [vp, vp, i64, i64, vp, i32, vp]
+        L.moe_fp8_linear_quantized.argtypes = [vp, vp, vp, i64, vp, i32, vp]
+        L.moe_mlp_workspace_query.argtypes = [i32, i32, i64, psz]
+        L.moe_mlp_create.argtypes = [i32, i32, i32, i32, i64, vp, vp, vp, ctypes.c_size_t, vp, ctypes.POINTER(vp)]
+        L.moe_mlp_forward.argtypes = [vp, vp, i64, i64, vp, vp, i32, vp]
+        L.moe_mlp_backward.argtypes = [vp, vp, i64, vp, i64, vp, i32, i64, vp, vp, vp, i32, i32, vp]
+        for n in ("fp8_linear", "mlp"):
+            getattr(L, f"moe_{n}_read_status").argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
+            getattr(L, f"moe_{n}_destroy").argtypes = [vp]
+            getattr(L, f"moe_{n}_destroy").restype = None
         L.moe_destroy.argtypes = [vp]
         L.moe_destroy.restype = None
         L.moe_status_str.argtypes = [st]
         L.moe_status_str.restype = ctypes.c_char_p
         for n in API_NAMES:
-            if n not in ("moe_destroy", "moe_status_str", "moe_fp4_destroy"):
+            if n != "moe_status_str" and not n.endswith("_destroy"):
                 getattr(L, n).restype = st
         _lib = L
     return _lib
@@ -336,3 +355,80 @@ def moe_fp4_read_status(h, stream):
 def moe_fp4_destroy(h) -> None:
     if h:
         lib().moe_fp4_destroy(h)
+
+
+def moe_fp8_linear_workspace_query(rows, cols, max_tokens) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_fp8_linear_workspace_query(rows, cols, max_tokens, ctypes.byref(n)),
+           "moe_fp8_linear_workspace_query")
+    return n.value
+
+
+def moe_fp8_linear_create(rows, cols, max_tokens, d_codes, d_scales, d_ws, ws_bytes, stream) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().moe_fp8_linear_create(rows, cols, max_tokens, d_codes, d_scales, d_ws, ws_bytes, stream,
+                                       ctypes.byref(h)), "moe_fp8_linear_create")
+    return h.value
+
+
+def moe_fp8_linear(h, d_x, x_stride, num_tokens, d_y, y_float32, stream) -> None:
+    s = (_lib or lib()).moe_fp8_linear(h, d_x, x_stride, num_tokens, d_y, y_float32, stream)
+    if s:
+        raise MoEError(s, "moe_fp8_linear")
+
+
+def moe_fp8_linear_quantized(h, d_xq, d_xq_scale, num_tokens, d_y, y_float32, stream) -> None:
+    s = (_lib or lib()).moe_fp8_linear_quantized(h, d_xq, d_xq_scale, num_tokens, d_y, y_float32, stream)
+    if s:
+        raise MoEError(s, "moe_fp8_linear_quantized")
+
+
+def moe_fp8_linear_read_status(h, stream):
+    """(status code, device status bits)"""
+    bits = ctypes.c_uint32()
+    s = lib().moe_fp8_linear_read_status(h, ctypes.byref(bits), stream)
+    return s, bits.value
+
+
+def moe_fp8_linear_destroy(h) -> None:
+    if h:
+        lib().moe_fp8_linear_destroy(h)
+
+
+def moe_mlp_workspace_query(hidden, inter, max_tokens) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_mlp_workspace_query(hidden, inter, max_tokens, ctypes.byref(n)), "moe_mlp_workspace_query")
+    return n.value
+
+
+def moe_mlp_create(hidden, inter, fp16, activation, max_tokens, d_w1, d_w2, d_ws, ws_bytes, stream) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().moe_mlp_create(hidden, inter, fp16, activation, max_tokens, d_w1, d_w2, d_ws, ws_bytes, stream,
+                                ctypes.byref(h)), "moe_mlp_create")
+    return h.value
+
+
+def moe_mlp_forward(h, d_x, x_stride, num_tokens, d_y, d_saved, saved_float32, stream) -> None:
+    s = (_lib or lib()).moe_mlp_forward(h, d_x, x_stride, num_tokens, d_y, d_saved, saved_float32, stream)
+    if s:
+        raise MoEError(s, "moe_mlp_forward")
+
+
+def moe_mlp_backward(*args) -> None:
+    """h, d_dy, dy_stride, d_x, x_stride, d_saved, saved_float32, num_tokens, d_dx, d_dw1, d_dw2,
+    dw_float32, accumulate, stream"""
+    s = (_lib or lib()).moe_mlp_backward(*args)
+    if s:
+        raise MoEError(s, "moe_mlp_backward")
+
+
+def moe_mlp_read_status(h, stream):
+    """(status code, device status bits)"""
+    bits = ctypes.c_uint32()
+    s = lib().moe_mlp_read_status(h, ctypes.byref(bits), stream)
+    return s, bits.value
+
+
+def moe_mlp_destroy(h) -> None:
+    if h:
+        lib().moe_mlp_destroy(h)

@@ -1,0 +1,54 @@
+// dense.h -- what the dense products (Fp8Linear, GatedMlp) pass from their calls
+// (dense_api.cu) to their kernels (dense.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace mm {
+
+enum DenseType { kE4M3 = 0, kBF16 = 1, kFP16 = 2 };
+enum DenseAct { kSilu = 0, kGeluTanh = 1 };
+
+// What happens to a product's FP32 sums d[m, n]:
+//   kEpiStore  y[m, n] = d (float or 16 bits; float: added to what is there, if asked)
+//   kEpiGate   n over gate columns, with their up columns: h = act(g) * u, and g, u to
+//              `saved` where it is given
+//   kEpiGrad   d = dh: from the saved g, u -> dg, du (into dgu) and h
+enum DenseEpi { kEpiStore = 0, kEpiGate = 1, kEpiGrad = 2 };
+
+// A[rows, K]: element (r, k) at r * ld + k, or with `mn` at k * ld + r.
+struct DenseOperand {
+  const void* p;
+  int64_t ld;
+  int rows;
+  bool mn;
+};
+
+struct DenseGemm {
+  DenseOperand a, b;       // d[m, n] = sum_k a[m, k] b[n, k]; kEpiGate: b holds 2 N rows, gate then up
+  int M, N, K;
+  DenseType type;
+  DenseEpi epi;
+  DenseAct act;
+  const uint8_t* sa;       // E4M3: E8M0 scales of a's rows [M, K / 128]
+  const uint8_t* sb;       // E4M3: E8M0 scales of b's blocks [ceil(N / 128), K / 128]
+  void* out;               // kEpiStore: y; else h [M, N] (kEpiGrad: or NULL)
+  int64_t ld_out;
+  bool out_f32, accumulate;
+  void* saved;             // [M, 2N]: g, then u
+  bool saved_f32;
+  void* dgu;               // kEpiGrad: [M, 2N]
+  uint32_t* status;
+};
+
+cudaError_t dense_gemm(const DenseGemm& g, cudaStream_t s);
+
+// x BF16 [T, cols] (rows ld elements apart) -> E4M3 codes [T, cols] and E8M0 bytes [T, cols / 128].
+cudaError_t dense_quantize_rows(const uint16_t* x, int64_t ld, int64_t T, int cols, uint8_t* q, uint8_t* s,
+                                cudaStream_t stream);
+// Power-of-two float scales to E8M0 bytes; others set MOE_DEV_BAD_SCALE in *status.
+cudaError_t dense_scales_to_e8m0(const float* s, int64_t n, uint8_t* out, uint32_t* status, cudaStream_t stream);
+
+}  // namespace mm
