@@ -1,6 +1,8 @@
 // dense.cu -- the dense products beside the MoE layer: x W^T in the layer's FP8 format
 // (Fp8Linear) and the products of a gated feed-forward block and of its gradients
 // (GatedMlp).
+#include <cudaTypedefs.h>
+
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -57,13 +59,8 @@ __device__ __forceinline__ float half_bits_to_float(uint32_t b) {
   return __half2float(__ushort_as_half((unsigned short)b));
 }
 
-__device__ __forceinline__ float load16(const void* p, int64_t i, DenseType t) {
-  const uint32_t b = reinterpret_cast<const uint16_t*>(p)[i];
-  return t == kBF16 ? bf16_bits_to_float(b) : half_bits_to_float(b);
-}
-
 __device__ __forceinline__ uint16_t bits16(float v, DenseType t) {
-  return t == kBF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+  return t == kFP16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
 // act(g) and act'(g).  silu = g s(g) with s the logistic function, s + silu (1 - s);
@@ -78,93 +75,610 @@ __device__ __forceinline__ void activate(DenseAct act, float g, float& a, float&
 }
 
 // ------------------------------------------------------------------------- products
-// The simple form: 64 x 64 outputs per block through shared memory, 4 x 4 per thread.
-constexpr int kSimpleK = 16;
+// d[m, n] = sum_k a[m, k] b[n, k] on CTA pairs (tcgen05 cta_group::2): a pair owns a tile of
+// 256 rows x 256 columns, each CTA stages its 128 rows of A and half of B's rows, the
+// leader issues the MMAs and each CTA drains its own 128 rows.  Persistent: pair p takes
+// tiles p, p + pairs, ...; 8 row tiles share a sweep over the columns, so that what
+// runs at one time reads few distinct operand rows.
+//   K-major operands (rows of K)      TMA boxes of 128 rows x 128 bytes.
+//   MN-major operands (K rows of it)  boxes of 64 K rows x 64 elements, two side by
+//                                     side: gradients multiply the stored tensors as they
+//                                     are, nothing is transposed in memory.
+//   E4M3: block-scaled MMAs.  One warp builds the scale atoms (four K blocks of 128
+//   rows) from the rows' and the matrix's E8M0 bytes, a slot ahead of the MMAs.
+// Accumulators: two of 256 TMEM columns in turn.  With scales in TMEM (64 columns) the two
+// overlap by 64 columns, which the epilogue drains first.
+// Warps: 0 loads, 1 MMAs, 2 scales, 4-11 epilogue (two per TMEM lane quadrant, a half
+// of the columns each).
+constexpr int kDThreads = 384;
+constexpr int kDEpiWarps = 8;
+constexpr int kDStages = 6;
+constexpr uint32_t kDBytesA = 16384, kDBytesB = 16384;
+constexpr uint32_t kDStage = kDBytesA + kDBytesB;
+constexpr int kSfSlots = 4;
+constexpr uint32_t kSfSlotBytes = 1536;  // A atom, two B atoms
+constexpr uint32_t kDSmem = kDStages * kDStage + kSfSlots * kSfSlotBytes + 1024;
+constexpr uint32_t kDTmemSf = 448, kDSfCols = 16;
 
-template <bool GATE>
-__global__ void __launch_bounds__(256) dense_simple_kernel(const DenseGemm g) {
-  __shared__ float as[kSimpleK][65], bs[GATE ? 2 : 1][kSimpleK][65];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t m0 = (int64_t)blockIdx.y * 64, n0 = (int64_t)blockIdx.x * 64;
-  const int KB = g.K / 128;
-  auto value = [&](const DenseOperand& o, int64_t r, int k) -> float {
-    if (g.type != kE4M3) return load16(o.p, o.mn ? k * o.ld + r : r * o.ld + k, g.type);
-    const uint8_t c = reinterpret_cast<const uint8_t*>(o.p)[r * o.ld + k];
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-  };
-  float d[GATE ? 2 : 1][4][4] = {}, sum[4][4] = {};
-  for (int k0 = 0; k0 < g.K; k0 += kSimpleK) {
-    for (int i = threadIdx.x; i < 64 * kSimpleK; i += 256) {
-      const int r = i / kSimpleK, k = k0 + i % kSimpleK;
-      as[i % kSimpleK][r] = m0 + r < g.M && k < g.K ? value(g.a, m0 + r, k) : 0.f;
-#pragma unroll
-      for (int h = 0; h < (GATE ? 2 : 1); ++h)
-        bs[h][i % kSimpleK][r] = n0 + r < g.N && k < g.K ? value(g.b, n0 + r + (int64_t)h * g.N, k) : 0.f;
-    }
-    __syncthreads();
-    for (int k = 0; k < kSimpleK; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int h = 0; h < (GATE ? 2 : 1); ++h)
-            d[h][i][j] = fmaf(as[k][ty + 16 * i], bs[h][k][tx + 16 * j], d[h][i][j]);
-    __syncthreads();
-    if (!GATE && g.type == kE4M3 && (k0 + kSimpleK) % 128 == 0)  // a K block's sums, scaled
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-          const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-          if (m < g.M && n < g.N)
-            sum[i][j] += scalbnf(d[0][i][j], (int)g.sa[m * KB + k0 / 128] + g.sb[n / 128 * KB + k0 / 128] - 254);
-          d[0][i][j] = 0.f;
-        }
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      if (!GATE && g.type == kE4M3) d[0][i][j] = sum[i][j];
-      const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= g.M || n >= g.N) continue;
-      const int64_t at = m * g.ld_out + n, gate = m * 2 * g.N + n, up = gate + g.N;
-      if (g.epi == kEpiStore) {
-        float* f = reinterpret_cast<float*>(g.out) + at;
-        if (g.out_f32)
-          *f = g.accumulate ? *f + d[0][i][j] : d[0][i][j];
-        else
-          reinterpret_cast<uint16_t*>(g.out)[at] = bits16(d[0][i][j], g.type == kFP16 ? kFP16 : kBF16);
-        continue;
-      }
-      float a, da;
-      if (GATE) {
-        const float gv = d[0][i][j], uv = d[GATE ? 1 : 0][i][j];
-        activate(g.act, gv, a, da);
-        reinterpret_cast<uint16_t*>(g.out)[at] = bits16(a * uv, g.type);
-        if (g.saved && g.saved_f32) {
-          reinterpret_cast<float*>(g.saved)[gate] = gv;
-          reinterpret_cast<float*>(g.saved)[up] = uv;
-        } else if (g.saved) {
-          reinterpret_cast<uint16_t*>(g.saved)[gate] = bits16(gv, g.type);
-          reinterpret_cast<uint16_t*>(g.saved)[up] = bits16(uv, g.type);
-        }
-      } else {
-        const float gv = g.saved_f32 ? reinterpret_cast<const float*>(g.saved)[gate] : load16(g.saved, gate, g.type);
-        const float uv = g.saved_f32 ? reinterpret_cast<const float*>(g.saved)[up] : load16(g.saved, up, g.type);
-        activate(g.act, gv, a, da);
-        const float dh = d[0][i][j];
-        reinterpret_cast<uint16_t*>(g.dgu)[gate] = bits16(dh * uv * da, g.type);
-        reinterpret_cast<uint16_t*>(g.dgu)[up] = bits16(dh * a, g.type);
-        if (g.out) reinterpret_cast<uint16_t*>(g.out)[at] = bits16(a * uv, g.type);
-      }
-    }
+struct DenseArgs {
+  int M, N, K;
+  int units, mt, nt;       // tiles of 256 rows, of the columns (kEpiGate: 128 h columns)
+  DenseEpi epi;
+  DenseAct act;
+  DenseType type;
+  const uint8_t *sa, *sb;
+  void* out;
+  int64_t ld_out;
+  bool out_f32, accumulate, vec, wide;  // vec: columns in pieces of 8, 16-byte stores; wide: 32-byte stores
+  void* saved;
+  bool saved_f32;
+  void* dgu;
+  uint32_t* status;
+};
+
+// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle: 64 elements
+// (128 bytes) per K row, 8 K rows 1024 bytes apart from the next 8 (stride offset), the
+// next 64 elements one box of 64 K rows further (leading offset).
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(8192u >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
 }
 
-cudaError_t dense_gemm(const DenseGemm& g, cudaStream_t s) {
-  const dim3 grid((g.N + 63) / 64, (g.M + 63) / 64);
-  if (g.epi == kEpiGate)
-    dense_simple_kernel<true><<<grid, 256, 0, s>>>(g);
-  else
-    dense_simple_kernel<false><<<grid, 256, 0, s>>>(g);
-  return cudaGetLastError();
+// Instruction descriptor of kind::f16: FP32 sums (bits 4-5), A and B FP16 (0) or BF16 (1) at
+// bits 7-9 and 10-12, MN-major operands bits 15 and 16, N >> 3, M >> 4.
+__host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool bf16, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)a_mn << 15) |
+         ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tc_mma_16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, DenseType t) {
+  if (t != kFP16) return pack_bf16x2(lo, hi);
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+__device__ __forceinline__ void unpack16(uint32_t v, DenseType t, float& lo, float& hi) {
+  lo = t == kFP16 ? half_bits_to_float(v & 0xFFFFu) : bf16_bits_to_float(v & 0xFFFFu);
+  hi = t == kFP16 ? half_bits_to_float(v >> 16) : bf16_bits_to_float(v >> 16);
+}
+
+// Stores and loads of a row's 32 consecutive columns from c on, of which those below n
+// exist.  16-byte pieces where n is a multiple of 8 (`vec`), 32-byte ones where the row
+// allows it (`wide`).
+__device__ __forceinline__ void store32_16(void* base, int64_t at, int c, int n, const float (&v)[32], DenseType t,
+                                           bool vec, bool wide) {
+  uint16_t* p = reinterpret_cast<uint16_t*>(base) + at;
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 16) {
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = pack16(v[i + 2 * j], v[i + 2 * j + 1], t);
+      if (wide && c + i + 16 <= n) {
+        st_global_v8(p + i, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+      } else {
+        if (c + i < n) *reinterpret_cast<uint4*>(p + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (c + i + 8 < n) *reinterpret_cast<uint4*>(p + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (c + i < n) p[i] = bits16(v[i], t);
+  }
+}
+
+__device__ __forceinline__ void store32_f32(void* base, int64_t at, int c, int n, const float (&v)[32], bool vec,
+                                            bool wide) {
+  float* p = reinterpret_cast<float*>(base) + at;
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      if (c + i >= n) break;
+      if (wide) {
+        st_global_v8(p + i, __float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
+                     __float_as_uint(v[i + 3]), __float_as_uint(v[i + 4]), __float_as_uint(v[i + 5]),
+                     __float_as_uint(v[i + 6]), __float_as_uint(v[i + 7]));
+      } else {
+        *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        *reinterpret_cast<float4*>(p + i + 4) = make_float4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (c + i < n) p[i] = v[i];
+  }
+}
+
+// (n a multiple of 8)
+__device__ __forceinline__ void load32(const void* base, int64_t at, int c, int n, bool f32, DenseType t,
+                                       float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    if (c + i >= n) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i + j] = 0.f;
+    } else if (f32) {
+      const float4 a = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + at + i);
+      const float4 b = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + at + i + 4);
+      v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
+      v[i + 4] = b.x, v[i + 5] = b.y, v[i + 6] = b.z, v[i + 7] = b.w;
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + at + i);
+      unpack16(a.x, t, v[i], v[i + 1]);
+      unpack16(a.y, t, v[i + 2], v[i + 3]);
+      unpack16(a.z, t, v[i + 4], v[i + 5]);
+      unpack16(a.w, t, v[i + 6], v[i + 7]);
+    }
+  }
+}
+
+// Four K blocks' scale bytes of one row (0 past the last block).
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t row, int KB, int q) {
+  const uint8_t* p = s + row * KB + 4 * q;
+  if ((KB & 3) == 0 && ((uintptr_t)s & 3) == 0) return *reinterpret_cast<const uint32_t*>(p);
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (4 * q + j < KB) w |= (uint32_t)p[j] << (8 * j);
+  return w;
+}
+
+template <bool F8, bool AMN, bool BMN, DenseEpi EPI>
+__global__ void __launch_bounds__(kDThreads, 1)
+    dense_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const DenseArgs g) {
+  extern __shared__ uint8_t dsmem[];
+  __shared__ __align__(8) uint64_t full_bar[kDStages], empty_bar[kDStages];
+  __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2], drain_bar;
+  __shared__ __align__(8) uint64_t sff_bar[kSfSlots], sfe_bar[kSfSlots];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sfbase = sbase + kDStages * kDStage;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair0 = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kDStages; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&accf_bar[i]), 1);
+      mbar_init(smem_u32(&acce_bar[i]), 2 * kDEpiWarps);
+    }
+    for (int i = 0; i < kSfSlots; ++i) {
+      mbar_init(smem_u32(&sff_bar[i]), 2);
+      mbar_init(smem_u32(&sfe_bar[i]), 1);
+    }
+    mbar_init(smem_u32(&drain_bar), 1);
+    abort_sh = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tmA);
+    prefetch_tensormap(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&tmem_base_sh), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  volatile int* abort = &abort_sh;
+  pdl_wait();
+
+  constexpr int kStep = F8 ? 128 : 64;  // elements of K per stage: 128 bytes
+  constexpr int kRowM = 8;              // row tiles of one sweep
+  const int KB = (g.K + kStep - 1) / kStep;
+  auto tile = [&](int u, int& m, int& n) {
+    const int band = u / (kRowM * g.nt), r = u - band * kRowM * g.nt;
+    const int rows = min(kRowM, g.mt - band * kRowM);
+    n = r / rows;
+    m = band * kRowM + (r - n * rows);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, last_parity = 0;
+    for (int u = pair0; u < g.units && !*abort; u += pairs) {
+      int m, n;
+      tile(u, m, n);
+      const int ra = m * 256 + (int)rank * 128;
+      // kEpiGate: the leader stages the gate rows, its peer the up rows
+      const int rb = EPI == kEpiGate ? n * 128 + (rank ? g.N : 0) : n * 256 + (int)rank * 128;
+      bool ok = true;
+      for (int kb = 0; kb < KB; ++kb) {
+        if (!mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort, g.status)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t st = sbase + stage * kDStage;
+          const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
+          if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * kDStage);
+          if (AMN) {
+            tma_load_2d_pair(st, &tmA, fb, ra, kb * kStep);
+            tma_load_2d_pair(st + 8192, &tmA, fb, ra + 64, kb * kStep);
+          } else {
+            tma_load_2d_pair(st, &tmA, fb, kb * kStep, ra);
+          }
+          if (BMN) {
+            tma_load_2d_pair(st + kDBytesA, &tmB, fb, rb, kb * kStep);
+            tma_load_2d_pair(st + kDBytesA + 8192, &tmB, fb, rb + 64, kb * kStep);
+          } else {
+            tma_load_2d_pair(st + kDBytesA, &tmB, fb, kb * kStep, rb);
+          }
+        }
+        __syncwarp();
+        issued |= 1u << stage;
+        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == kDStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+    }
+    // Every copy has landed before the CTAs leave (the leader's barriers count both CTAs'
+    // bytes); after an abort the peer also gives its last copies 100 us.
+    if (!leader && lane == 0 && *abort) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 100000ull) {
+      }
+    }
+    if (lane == 0 && leader) {
+      for (int s = 0; s < kDStages; ++s) {
+        if (!(issued & (1u << s))) continue;
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(smem_u32(&full_bar[s]), (last_parity >> s) & 1u) &&
+               globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0 && leader) {
+      const uint32_t idesc0 = F8 ? idesc_mxf8_e4m3(256, 256) : idesc_16(256, 256, g.type == kBF16, AMN, BMN);
+      int stage = 0;
+      uint32_t phase = 0, group = 0;
+      auto probe = [&](int s, uint32_t ph) { return mbar_test_wait_cluster(smem_u32(&full_bar[s]), ph); };
+      bool ready = probe(0, 0);
+      int i = 0;  // tiles so far
+      for (int u = pair0; u < g.units; u += pairs, ++i) {
+        const int b = i & 1;
+        // E4M3: every warp has left the tile before last, and the tile before the columns
+        // that both buffers have; else the tile before last
+        const bool free = F8 ? mbar_wait<true>(smem_u32(&acce_bar[0]), (i & 1) ^ 1u, abort, g.status)
+                             : mbar_wait<true>(smem_u32(&acce_bar[b]), ((i >> 1) & 1) ^ 1u, abort, g.status);
+        if (!free) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + (b ? (F8 ? 192u : 256u) : 0u);
+        bool ok = true;
+        uint32_t sf = 0, slot = 0;
+        for (int kb = 0; kb < KB; ++kb) {
+          const uint32_t j = (uint32_t)kb & 3u;
+          if (F8 && j == 0) {
+            slot = group & (kSfSlots - 1);
+            if (!mbar_wait<true>(smem_u32(&sff_bar[slot]), (group / kSfSlots) & 1u, abort, g.status)) {
+              ok = false;
+              break;
+            }
+            ++group;
+          }
+          if (!ready && !mbar_wait_slow<true>(smem_u32(&full_bar[stage]), phase, abort, g.status, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = sbase + stage * kDStage;
+          if constexpr (F8) {
+            if (j == 0) {
+              sf = tmem + kDTmemSf + slot * kDSfCols;
+              const uint32_t sp = sfbase + slot * kSfSlotBytes;
+              tc_cp_sf_atom_pair(sf, sdesc_sf_atom(sp));
+              tc_cp_sf_atom_pair(sf + 8, sdesc_sf_atom(sp + 512));
+              tc_cp_sf_atom_pair(sf + 12, sdesc_sf_atom(sp + 1024));
+            }
+          }
+          const uint64_t ad = AMN ? sdesc_mn_sw128(st) : sdesc_k_sw128(st);
+          const uint64_t bd = BMN ? sdesc_mn_sw128(st + kDBytesA) : sdesc_k_sw128(st + kDBytesA);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t add = (kb | k) != 0 ? 1u : 0u;
+            // 32 bytes along K inside the swizzle atom, or 16 K rows of 128 bytes
+            const uint64_t da = ad + (AMN ? 128 : 2) * k, db = bd + (BMN ? 128 : 2) * k;
+            if constexpr (F8)
+              tc_mma_mxf8_pair(acc, da, db, idesc0 | (j << 4) | (j << 29), sf, sf + 8, add);
+            else
+              tc_mma_16_pair(acc, da, db, idesc0, add);
+          }
+          const int done_stage = stage;
+          if (++stage == kDStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          ready = probe(stage, phase);
+          tc_commit_pair_multicast(smem_u32(&empty_bar[done_stage]), 0x3);
+          if (F8 && (j == 3 || kb == KB - 1)) tc_commit_pair_multicast(smem_u32(&sfe_bar[slot]), 0x3);
+        }
+        if (!ok) break;
+        tc_commit_pair_multicast(smem_u32(&accf_bar[b]), 0x3);
+      }
+      tc_commit_pair(smem_u32(&drain_bar));
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_u32(&drain_bar), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+      }
+    }
+    __syncwarp();
+  } else if (F8 && warp == 2) {
+    // ------------------------------------------------------------ scales
+    // Lane l holds the words of rows l, l + 32, l + 64, l + 96: 16 consecutive bytes of an
+    // atom.  Rows past M have no scale (their sums are not stored).
+    const int KQ = (KB + 3) / 4, NB = (g.N + 127) / 128;
+    uint32_t group = 0;
+    for (int u = pair0; u < g.units && !*abort; u += pairs) {
+      int m, n;
+      tile(u, m, n);
+      const int64_t ra = (int64_t)m * 256 + rank * 128 + lane;
+      const int nb = 2 * n, nb1 = min(nb + 1, NB - 1);
+      bool ok = true;
+      auto words = [&](int q, uint32_t (&w)[6]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = ra + 32 * i < g.M ? scale_word(g.sa, ra + 32 * i, KB, q) : 0u;
+        w[4] = scale_word(g.sb, nb, KB, q);
+        w[5] = scale_word(g.sb, nb1, KB, q);
+      };
+      uint32_t w[6];
+      words(0, w);
+      for (int q = 0; q < KQ; ++q, ++group) {
+        const uint32_t slot = group & (kSfSlots - 1);
+        if (!mbar_wait(smem_u32(&sfe_bar[slot]), ((group / kSfSlots) & 1u) ^ 1u, abort, g.status)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sp = smem + kDStages * kDStage + slot * kSfSlotBytes + lane * 16;
+        *reinterpret_cast<uint4*>(sp) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(sp + 512) = make_uint4(w[4], w[4], w[4], w[4]);
+        *reinterpret_cast<uint4*>(sp + 1024) = make_uint4(w[5], w[5], w[5], w[5]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sff_bar[slot]), 0));
+        if (q + 1 < KQ) words(q + 1, w);
+      }
+      if (!ok) break;
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t tlane = tmem + ((uint32_t)(q * 32) << 16);
+    int i = 0;
+    for (int u = pair0; u < g.units; u += pairs, ++i) {
+      int m, n;
+      tile(u, m, n);
+      const int b = i & 1;
+      const int64_t row = (int64_t)m * 256 + rank * 128 + q * 32 + lane;
+      const bool live = row < g.M;
+      if (!mbar_wait(smem_u32(&accf_bar[b]), (i >> 1) & 1, abort, g.status)) break;
+      tc_fence_after();
+      const uint32_t acc = tlane + (b ? (F8 ? 192u : 256u) : 0u);
+      auto release = [&](int bar) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acce_bar[bar]), 0));
+      };
+      if constexpr (EPI == kEpiStore) {
+        // the columns that both buffers have are the first one's last 64 and the second
+        // one's first: their half drains them first, the other half has left the tile before
+        const int c0 = half * 128, n0 = n * 256 + c0;
+        if (F8 && half == b) release(0);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const int cc = F8 && b == 0 ? (c ^ 2) * 32 : c * 32;
+          uint32_t r[32];
+          tmem_ld32(acc + c0 + cc, r);
+          tmem_ld_wait();
+          if (F8 ? (c == 1 && half != b) : c == 3) release(F8 ? 0 : b);
+          const int col = n0 + cc;
+          if (!live || col >= g.N) continue;
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+          const int64_t at = row * g.ld_out + col;
+          if (g.out_f32) {
+            if (g.accumulate) {
+              float old[32];
+              load32(g.out, at, col, g.N, true, g.type, old);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] += old[k];
+            }
+            store32_f32(g.out, at, col, g.N, v, g.vec, g.wide);
+          } else {
+            store32_16(g.out, at, col, g.N, v, g.type, g.vec, g.wide);
+          }
+        }
+      } else if constexpr (EPI == kEpiGate) {
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          const int cc = half * 64 + c * 32, col = n * 128 + cc;
+          uint32_t rg[32], ru[32];
+          tmem_ld32(acc + cc, rg);
+          tmem_ld32(acc + 128 + cc, ru);
+          tmem_ld_wait();
+          if (c == 1) release(b);
+          if (!live || col >= g.N) continue;
+          float gv[32], uv[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) gv[k] = __uint_as_float(rg[k]), uv[k] = __uint_as_float(ru[k]);
+          if (g.saved) {
+            const int64_t at = row * 2 * g.N + col;
+            if (g.saved_f32) {
+              store32_f32(g.saved, at, col, g.N, gv, true, g.wide);
+              store32_f32(g.saved, at + g.N, col, g.N, uv, true, g.wide);
+            } else {
+              store32_16(g.saved, at, col, g.N, gv, g.type, true, g.wide);
+              store32_16(g.saved, at + g.N, col, g.N, uv, g.type, true, g.wide);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            float a, da;
+            activate(g.act, gv[k], a, da);
+            uv[k] *= a;
+          }
+          store32_16(g.out, row * g.ld_out + col, col, g.N, uv, g.type, true, g.wide);
+        }
+      } else {
+        const int c0 = half * 128;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const int col = n * 256 + c0 + c * 32;
+          const bool on = live && col < g.N;
+          const int64_t at = row * 2 * g.N + col;
+          float gv[32], uv[32];
+          if (on) {
+            load32(g.saved, at, col, g.N, g.saved_f32, g.type, gv);
+            load32(g.saved, at + g.N, col, g.N, g.saved_f32, g.type, uv);
+          }
+          uint32_t r[32];
+          tmem_ld32(acc + c0 + c * 32, r);
+          tmem_ld_wait();
+          if (c == 3) release(b);
+          if (!on) continue;
+          float hv[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float dh = __uint_as_float(r[k]);
+            float a, da;
+            activate(g.act, gv[k], a, da);
+            hv[k] = a * uv[k];
+            gv[k] = dh * uv[k] * da;
+            uv[k] = dh * a;
+          }
+          store32_16(g.dgu, at, col, g.N, gv, g.type, true, g.wide);
+          store32_16(g.dgu, at + g.N, col, g.N, uv, g.type, true, g.wide);
+          if (g.out) store32_16(g.out, row * g.ld_out + col, col, g.N, hv, g.type, true, g.wide);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  pdl_trigger();
+  cluster_sync_all();  // neither CTA frees TMEM the pair still uses
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------- launches
+static bool encode_map(CUtensorMap* map, const DenseOperand& o, int K, DenseType t, int box_rows) {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return false;
+    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  const cuuint64_t es = t == kE4M3 ? 1 : 2;
+  const cuuint64_t dims[2] = {(cuuint64_t)(o.mn ? o.rows : K), (cuuint64_t)(o.mn ? K : o.rows)};
+  const cuuint64_t strides[1] = {(cuuint64_t)o.ld * es};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)(o.mn ? 64 : box_rows)};
+  const cuuint32_t one[2] = {1, 1};
+  return fn(map,
+            t == kE4M3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+            : t == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            2, const_cast<void*>(o.p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool F8, bool AMN, bool BMN, DenseEpi EPI>
+static cudaError_t launch_pair(const CUtensorMap& a, const CUtensorMap& b, const DenseArgs& g, int ctas,
+                               cudaStream_t s) {
+  cudaLaunchAttribute c;
+  c.id = cudaLaunchAttributeClusterDimension;
+  c.val.clusterDim.x = 2;
+  c.val.clusterDim.y = 1;
+  c.val.clusterDim.z = 1;
+  return launch_k(dense_pair_kernel<F8, AMN, BMN, EPI>, dim3(ctas), dim3(kDThreads), kDSmem, s, true, &c, a, b, g);
+}
+
+cudaError_t dense_set_attributes() {
+  const void* ks[6] = {(const void*)dense_pair_kernel<true, false, false, kEpiStore>,
+                       (const void*)dense_pair_kernel<false, false, false, kEpiGate>,
+                       (const void*)dense_pair_kernel<false, false, false, kEpiStore>,
+                       (const void*)dense_pair_kernel<false, false, true, kEpiGrad>,
+                       (const void*)dense_pair_kernel<false, false, true, kEpiStore>,
+                       (const void*)dense_pair_kernel<false, true, true, kEpiStore>};
+  for (const void* k : ks) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
+  CUtensorMap a, b;
+  if (!encode_map(&a, g.a, g.K, g.type, 128) || !encode_map(&b, g.b, g.K, g.type, 128)) return cudaErrorInvalidValue;
+  DenseArgs d = {};
+  d.M = g.M;
+  d.N = g.N;
+  d.K = g.K;
+  d.mt = (g.M + 255) / 256;
+  d.nt = g.epi == kEpiGate ? (g.N + 127) / 128 : (g.N + 255) / 256;
+  d.units = d.mt * d.nt;
+  d.epi = g.epi;
+  d.act = g.act;
+  d.type = g.type;
+  d.sa = g.sa;
+  d.sb = g.sb;
+  d.out = g.out;
+  d.ld_out = g.ld_out;
+  d.out_f32 = g.out_f32;
+  d.accumulate = g.accumulate;
+  d.saved = g.saved;
+  d.saved_f32 = g.saved_f32;
+  d.dgu = g.dgu;
+  d.status = g.status;
+  const uintptr_t at = (uintptr_t)g.out | (uintptr_t)g.saved | (uintptr_t)g.dgu;
+  d.vec = g.N % 8 == 0 && at % 16 == 0;
+  d.wide = d.vec && g.N % 16 == 0 && at % 32 == 0;
+  const int pairs = d.units < sms / 2 ? d.units : sms / 2;
+  if (g.type == kE4M3) return launch_pair<true, false, false, kEpiStore>(a, b, d, 2 * pairs, s);
+  if (g.epi == kEpiGate) return launch_pair<false, false, false, kEpiGate>(a, b, d, 2 * pairs, s);
+  if (g.epi == kEpiGrad) return launch_pair<false, false, true, kEpiGrad>(a, b, d, 2 * pairs, s);
+  if (g.a.mn) return launch_pair<false, true, true, kEpiStore>(a, b, d, 2 * pairs, s);
+  if (g.b.mn) return launch_pair<false, false, true, kEpiStore>(a, b, d, 2 * pairs, s);
+  return launch_pair<false, false, false, kEpiStore>(a, b, d, 2 * pairs, s);
 }
 
 }  // namespace mm

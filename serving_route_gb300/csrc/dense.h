@@ -43,7 +43,8 @@ struct DenseGemm {
   uint32_t* status;
 };
 
-cudaError_t dense_gemm(const DenseGemm& g, cudaStream_t s);
+cudaError_t dense_set_attributes();  // of the kernels, on the current device
+cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s);
 
 // x BF16 [T, cols] (rows ld elements apart) -> E4M3 codes [T, cols] and E8M0 bytes [T, cols / 128].
 cudaError_t dense_quantize_rows(const uint16_t* x, int64_t ld, int64_t T, int cols, uint8_t* q, uint8_t* s,

@@ -9,7 +9,7 @@
 using namespace mm;
 
 struct moe_fp8_linear_handle {
-  int rows, cols, device;
+  int rows, cols, device, sms;
   int64_t max_tokens;
   const uint8_t* codes;
   uint32_t* status;
@@ -19,7 +19,7 @@ struct moe_fp8_linear_handle {
 };
 
 struct moe_mlp_handle {
-  int hidden, inter, device;
+  int hidden, inter, device, sms;
   DenseType type;
   DenseAct act;
   int64_t max_tokens;
@@ -38,15 +38,16 @@ size_t up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 uint8_t* aligned(void* p) { return reinterpret_cast<uint8_t*>(((uintptr_t)p + kAlign - 1) / kAlign * kAlign); }
 bool off(const void* p, size_t a) { return !p || (uintptr_t)p % a != 0; }
 
-moe_status this_device(int* device) {
+moe_status this_device(int* device, int* sms) {
   int dev = 0, major = 0, minor = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return MOE_ERR_CUDA;
   if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;  // built for sm_103a only
   *device = dev;
-  return MOE_OK;
+  return dense_set_attributes() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // Launches go to the current device: it has to be the handle's.
@@ -114,7 +115,7 @@ moe_status linear_run(moe_fp8_linear_handle* h, const uint8_t* xq, const uint8_t
   g.ld_out = h->rows;
   g.out_f32 = f32;
   g.status = h->status;
-  return dense_gemm(g, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return dense_gemm(g, h->sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 bool mlp_dims_ok(int32_t hidden, int32_t inter) {
@@ -142,8 +143,8 @@ moe_status moe_fp8_linear_create(int32_t rows, int32_t cols, int64_t max_tokens,
   if (st != MOE_OK) return st;
   if (off(d_codes, 16) || off(d_scales, 4) || off(d_workspace, 16)) return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
-  int dev = 0;
-  if ((st = this_device(&dev)) != MOE_OK) return st;
+  int dev = 0, sms = 0;
+  if ((st = this_device(&dev, &sms)) != MOE_OK) return st;
   const LinearLayout l(rows, cols, max_tokens);
   uint8_t* b = aligned(d_workspace);
   uint32_t* status = reinterpret_cast<uint32_t*>(b);
@@ -160,6 +161,7 @@ moe_status moe_fp8_linear_create(int32_t rows, int32_t cols, int64_t max_tokens,
   h->rows = rows;
   h->cols = cols;
   h->device = dev;
+  h->sms = sms;
   h->max_tokens = max_tokens;
   h->codes = d_codes;
   h->status = status;
@@ -222,8 +224,8 @@ moe_status moe_mlp_create(int32_t hidden, int32_t inter, int32_t fp16, int32_t a
   if (activation != MOE_ACT_SILU && activation != MOE_ACT_GELU_TANH) return MOE_ERR_UNSUPPORTED;
   if (off(d_w1, 16) || off(d_w2, 16) || off(d_workspace, 16)) return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
-  int dev = 0;
-  if ((st = this_device(&dev)) != MOE_OK) return st;
+  int dev = 0, sms = 0;
+  if ((st = this_device(&dev, &sms)) != MOE_OK) return st;
   const MlpLayout l(inter, max_tokens);
   uint8_t* b = aligned(d_workspace);
   if (cudaMemsetAsync(b, 0, kAlign, stream) != cudaSuccess) return MOE_ERR_CUDA;
@@ -233,6 +235,7 @@ moe_status moe_mlp_create(int32_t hidden, int32_t inter, int32_t fp16, int32_t a
   h->hidden = hidden;
   h->inter = inter;
   h->device = dev;
+  h->sms = sms;
   h->type = fp16 ? kFP16 : kBF16;
   h->act = activation == MOE_ACT_SILU ? kSilu : kGeluTanh;
   h->max_tokens = max_tokens;
@@ -272,7 +275,7 @@ moe_status moe_mlp_forward(moe_mlp_handle* h, const uint16_t* d_x, int64_t x_str
   g.saved = d_saved;
   g.saved_f32 = saved_float32 != 0;
   g.status = h->status;
-  if (dense_gemm(g, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  if (dense_gemm(g, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
   DenseGemm d = {};
   d.a = {h->h, I, (int)num_tokens, false};
   d.b = {h->w2, I, H, false};
@@ -284,7 +287,7 @@ moe_status moe_mlp_forward(moe_mlp_handle* h, const uint16_t* d_x, int64_t x_str
   d.out = d_y;
   d.ld_out = H;
   d.status = h->status;
-  return dense_gemm(d, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return dense_gemm(d, h->sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_stride, const uint16_t* d_x,
@@ -329,7 +332,7 @@ moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_
   g.saved_f32 = saved_float32 != 0;
   g.dgu = h->dgu;
   g.status = h->status;
-  if (dense_gemm(g, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  if (dense_gemm(g, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
   DenseGemm d = {};
   d.type = h->type;
   d.epi = kEpiStore;
@@ -342,7 +345,7 @@ moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_
     d.K = 2 * I;
     d.out = d_dx;
     d.ld_out = H;
-    if (dense_gemm(d, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dense_gemm(d, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
   }
   d.out_f32 = dw_float32 != 0;
   d.accumulate = accumulate != 0;
@@ -354,7 +357,7 @@ moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_
     d.N = H;
     d.out = d_dw1;
     d.ld_out = H;
-    if (dense_gemm(d, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dense_gemm(d, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
   }
   if (d_dw2) {  // dy^T h
     d.a = {d_dy, dy_stride, H, true};
@@ -363,7 +366,7 @@ moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_
     d.N = I;
     d.out = d_dw2;
     d.ld_out = I;
-    if (dense_gemm(d, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dense_gemm(d, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
   }
   return MOE_OK;
 }
