@@ -3,10 +3,7 @@
 // (GatedMlp).
 #include <cudaTypedefs.h>
 
-#include <cuda_fp16.h>
-
-#include "common.cuh"
-#include "dense.h"
+#include "dense.cuh"
 
 namespace mm {
 
@@ -16,6 +13,8 @@ namespace mm {
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* x, int64_t ld, int64_t blocks, int kb,
                                                             uint8_t* q, uint8_t* s) {
   const int lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
   for (int64_t b = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); b < blocks; b += (int64_t)gridDim.x * 8) {
     const int64_t t = b / kb;
     const int c = (int)(b - t * kb);
@@ -36,8 +35,8 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* x, i
 cudaError_t dense_quantize_rows(const uint16_t* x, int64_t ld, int64_t T, int cols, uint8_t* q, uint8_t* s,
                                 cudaStream_t stream) {
   const int64_t blocks = T * (cols / 128), ctas = (blocks + 7) / 8;
-  quantize_rows_kernel<<<(int)(ctas < 152 * 8 ? ctas : 152 * 8), 256, 0, stream>>>(x, ld, blocks, cols / 128, q, s);
-  return cudaGetLastError();
+  return launch_k(quantize_rows_kernel, dim3((unsigned)(ctas < 152 * 8 ? ctas : 152 * 8)), dim3(256), 0, stream, true,
+                  nullptr, x, ld, blocks, cols / 128, q, s);
 }
 
 __global__ void scales_to_e8m0_kernel(const float* s, int64_t n, uint8_t* out, uint32_t* status) {
@@ -52,26 +51,6 @@ __global__ void scales_to_e8m0_kernel(const float* s, int64_t n, uint8_t* out, u
 cudaError_t dense_scales_to_e8m0(const float* s, int64_t n, uint8_t* out, uint32_t* status, cudaStream_t stream) {
   scales_to_e8m0_kernel<<<(int)((n + 255) / 256 < 1024 ? (n + 255) / 256 : 1024), 256, 0, stream>>>(s, n, out, status);
   return cudaGetLastError();
-}
-
-// ------------------------------------------------------------------------- values
-__device__ __forceinline__ float half_bits_to_float(uint32_t b) {
-  return __half2float(__ushort_as_half((unsigned short)b));
-}
-
-__device__ __forceinline__ uint16_t bits16(float v, DenseType t) {
-  return t == kFP16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-
-// act(g) and act'(g).  silu = g s(g) with s the logistic function, s + silu (1 - s);
-// gelu (tanh form) = g s(2z), z = sqrt(2/pi) (g + 0.044715 g^3), as tanh z = 2 s(2z) - 1.
-__device__ __forceinline__ void activate(DenseAct act, float g, float& a, float& d) {
-  const float z = act == kSilu ? g : g * (1.5957691216f + 0.0713548163f * g * g);
-  const float dz = act == kSilu ? 1.0f : 1.5957691216f + 0.2140644488f * g * g;
-  const float s = __fdividef(1.0f, 1.0f + __expf(-z));
-  const float t = s * (1.0f - s);
-  a = g * s;
-  d = s + (t == 0.f ? 0.f : g * t * dz);  // (far out dz may be infinite)
 }
 
 // ------------------------------------------------------------------------- products
@@ -100,42 +79,6 @@ constexpr uint32_t kSfSlotBytes = 1536;  // A atom, two B atoms
 constexpr uint32_t kDSmem = kDStages * kDStage + kSfSlots * kSfSlotBytes + 1024;
 constexpr uint32_t kDTmemSf = 448, kDSfCols = 16;
 
-struct DenseArgs {
-  int M, N, K;
-  int units, mt, nt;       // tiles of 256 rows, of the columns (kEpiGate: 128 h columns)
-  DenseEpi epi;
-  DenseAct act;
-  DenseType type;
-  const uint8_t *sa, *sb;
-  void* out;
-  int64_t ld_out;
-  bool out_f32, accumulate, vec, wide;  // vec: columns in pieces of 8, 16-byte stores; wide: 32-byte stores
-  void* saved;
-  bool saved_f32;
-  void* dgu;
-  uint32_t* status;
-};
-
-// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle: 64 elements
-// (128 bytes) per K row, 8 K rows 1024 bytes apart from the next 8 (stride offset), the
-// next 64 elements one box of 64 K rows further (leading offset).
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(8192u >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
-// Instruction descriptor of kind::f16: FP32 sums (bits 4-5), A and B FP16 (0) or BF16 (1) at
-// bits 7-9 and 10-12, MN-major operands bits 15 and 16, N >> 3, M >> 4.
-__host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool bf16, bool a_mn, bool b_mn) {
-  return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)a_mn << 15) |
-         ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
 __device__ __forceinline__ void tc_mma_16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                uint32_t accumulate) {
   asm volatile(
@@ -144,17 +87,6 @@ __device__ __forceinline__ void tc_mma_16_pair(uint32_t d_tmem, uint64_t adesc, 
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, DenseType t) {
-  if (t != kFP16) return pack_bf16x2(lo, hi);
-  const __half2 p = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
-
-__device__ __forceinline__ void unpack16(uint32_t v, DenseType t, float& lo, float& hi) {
-  lo = t == kFP16 ? half_bits_to_float(v & 0xFFFFu) : bf16_bits_to_float(v & 0xFFFFu);
-  hi = t == kFP16 ? half_bits_to_float(v >> 16) : bf16_bits_to_float(v >> 16);
 }
 
 // Stores and loads of a row's 32 consecutive columns from c on, of which those below n
@@ -227,17 +159,6 @@ __device__ __forceinline__ void load32(const void* base, int64_t at, int c, int 
       unpack16(a.w, t, v[i + 6], v[i + 7]);
     }
   }
-}
-
-// Four K blocks' scale bytes of one row (0 past the last block).
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t row, int KB, int q) {
-  const uint8_t* p = s + row * KB + 4 * q;
-  if ((KB & 3) == 0 && ((uintptr_t)s & 3) == 0) return *reinterpret_cast<const uint32_t*>(p);
-  uint32_t w = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (4 * q + j < KB) w |= (uint32_t)p[j] << (8 * j);
-  return w;
 }
 
 template <bool F8, bool AMN, bool BMN, DenseEpi EPI>
@@ -643,12 +564,11 @@ cudaError_t dense_set_attributes() {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDSmem);
     if (e != cudaSuccess) return e;
   }
-  return cudaSuccess;
+  return dense_split_set_attributes();
 }
 
 cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
   CUtensorMap a, b;
-  if (!encode_map(&a, g.a, g.K, g.type, 128) || !encode_map(&b, g.b, g.K, g.type, 128)) return cudaErrorInvalidValue;
   DenseArgs d = {};
   d.M = g.M;
   d.N = g.N;
@@ -672,6 +592,15 @@ cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
   const uintptr_t at = (uintptr_t)g.out | (uintptr_t)g.saved | (uintptr_t)g.dgu;
   d.vec = g.N % 8 == 0 && at % 16 == 0;
   d.wide = d.vec && g.N % 16 == 0 && at % 32 == 0;
+  if (g.M <= 256) {
+    DenseSplit p = dense_split_plan(g, sms);
+    p.early = g.early;
+    if (!encode_map(&a, g.a, g.K, g.type, p.NT) ||
+        !encode_map(&b, g.b, g.K, g.type, g.epi == kEpiGate ? 64 : 128))
+      return cudaErrorInvalidValue;
+    return dense_split_launch(a, b, g, d, p, s);
+  }
+  if (!encode_map(&a, g.a, g.K, g.type, 128) || !encode_map(&b, g.b, g.K, g.type, 128)) return cudaErrorInvalidValue;
   const int pairs = d.units < sms / 2 ? d.units : sms / 2;
   if (g.type == kE4M3) return launch_pair<true, false, false, kEpiStore>(a, b, d, 2 * pairs, s);
   if (g.epi == kEpiGate) return launch_pair<false, false, false, kEpiGate>(a, b, d, 2 * pairs, s);

@@ -41,6 +41,7 @@ struct DenseGemm {
   bool saved_f32;
   void* dgu;               // kEpiGrad: [M, 2N]
   uint32_t* status;
+  bool early;              // the kernel before in the stream is of the same call and does not write b
 };
 
 cudaError_t dense_set_attributes();  // of the kernels, on the current device

@@ -100,7 +100,7 @@ struct MlpLayout {
 };
 
 moe_status linear_run(moe_fp8_linear_handle* h, const uint8_t* xq, const uint8_t* xs, int64_t T, void* y, bool f32,
-                      cudaStream_t s) {
+                      bool early, cudaStream_t s) {
   DenseGemm g = {};
   g.a = {xq, h->cols, (int)T, false};
   g.b = {h->codes, h->cols, h->rows, false};
@@ -114,6 +114,7 @@ moe_status linear_run(moe_fp8_linear_handle* h, const uint8_t* xq, const uint8_t
   g.out = y;
   g.ld_out = h->rows;
   g.out_f32 = f32;
+  g.early = early;
   g.status = h->status;
   return dense_gemm(g, h->sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -183,7 +184,7 @@ moe_status moe_fp8_linear(moe_fp8_linear_handle* h, const uint16_t* d_x, int64_t
   if (x.meets(Span(d_y, num_tokens, h->rows, h->rows, y_float32 ? 4 : 2))) return MOE_ERR_INVALID_ARG;
   if (dense_quantize_rows(d_x, x_stride, num_tokens, h->cols, h->xq, h->xs, stream) != cudaSuccess)
     return MOE_ERR_CUDA;
-  return linear_run(h, h->xq, h->xs, num_tokens, d_y, y_float32 != 0, stream);
+  return linear_run(h, h->xq, h->xs, num_tokens, d_y, y_float32 != 0, true, stream);
 }
 
 moe_status moe_fp8_linear_quantized(moe_fp8_linear_handle* h, const uint8_t* d_xq, const uint8_t* d_xq_scale,
@@ -196,7 +197,7 @@ moe_status moe_fp8_linear_quantized(moe_fp8_linear_handle* h, const uint8_t* d_x
   if (y.meets(Span(d_xq, num_tokens, h->cols, h->cols, 1)) ||
       y.meets(Span(d_xq_scale, num_tokens, h->cols / 128, h->cols / 128, 1)))
     return MOE_ERR_INVALID_ARG;
-  return linear_run(h, d_xq, d_xq_scale, num_tokens, d_y, y_float32 != 0, stream);
+  return linear_run(h, d_xq, d_xq_scale, num_tokens, d_y, y_float32 != 0, false, stream);
 }
 
 moe_status moe_fp8_linear_read_status(moe_fp8_linear_handle* h, uint32_t* h_status, struct CUstream_st* stream) {
@@ -286,6 +287,7 @@ moe_status moe_mlp_forward(moe_mlp_handle* h, const uint16_t* d_x, int64_t x_str
   d.epi = kEpiStore;
   d.out = d_y;
   d.ld_out = H;
+  d.early = true;
   d.status = h->status;
   return dense_gemm(d, h->sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -345,8 +347,10 @@ moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_
     d.K = 2 * I;
     d.out = d_dx;
     d.ld_out = H;
+    d.early = true;  // the weights, unlike x and h below
     if (dense_gemm(d, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
   }
+  d.early = false;
   d.out_f32 = dw_float32 != 0;
   d.accumulate = accumulate != 0;
   d.K = T;

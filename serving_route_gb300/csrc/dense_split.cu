@@ -1,0 +1,443 @@
+// dense_split.cu -- the dense products where a few tiles cannot fill the GPU: few tokens,
+// small matrices.
+//
+// d^T[n, m] = sum_k b[n, k] a[m, k]: 128 rows of B (the weights) are the MMA's M operand and
+// NT <= 256 rows of A (the tokens, a multiple of 16) its N operand, so a K block of a tile
+// costs 16 KB of weights and 128 NT bytes of tokens.  What bounds these products is the
+// weights' time, so every SM has to stream its share of them: the K blocks of a tile
+// are split over a cluster of up to 8 CTAs, each of which sums its share in tensor
+// memory.  The shares meet in the cluster's shared memory: every CTA leaves its FP32 sums in its
+// own, and after one cluster barrier each finishes every s-th token of the tile, adding
+// the shares in the order of the CTAs.  No workspace, no counters, no order that changes.
+// Two CTAs per SM (up to 128 tokens) overlap one's join with the other's stream.
+// Warps: 0 loads, 1 MMAs, 2 scales, 4-7 drain the accumulator (thread = weight row); all
+// eight finish tokens (a lane has consecutive columns, so stores are whole lines).
+#include "dense.cuh"
+
+namespace mm {
+
+constexpr int kSpThreads = 256;
+constexpr int kSpWarps = kSpThreads / 32;
+constexpr int kSpMaxStages = 8;
+constexpr uint32_t kSpW = 16384;            // 128 weight rows x 128 bytes
+constexpr uint32_t kSpSfBytes = 1536;       // weights' atom, two token atoms
+constexpr int kSpSfSlots = 4;
+constexpr uint32_t kSpSfCols = 16;
+
+__device__ __forceinline__ void tc_mma_16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float2 ld_cluster_v2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// C consecutive columns of a row, of which those below n exist; whole where `vec`
+// (n a multiple of C, rows on C elements' boundaries).
+template <int C>
+__device__ __forceinline__ void store_few(void* base, int64_t at, int c, int n, const float (&v)[C], bool f32,
+                                          DenseType t, bool vec) {
+  if (f32) {
+    float* p = reinterpret_cast<float*>(base) + at;
+    if (vec) {
+      if (c >= n) return;
+      if constexpr (C == 4)
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      else
+        *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (c + i < n) p[i] = v[i];
+    }
+    return;
+  }
+  uint16_t* p = reinterpret_cast<uint16_t*>(base) + at;
+  if (vec) {
+    if (c >= n) return;
+    if constexpr (C == 4)
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack16(v[0], v[1], t), pack16(v[2], v[3], t));
+    else
+      *reinterpret_cast<uint32_t*>(p) = pack16(v[0], v[1], t);
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (c + i < n) p[i] = bits16(v[i], t);
+  }
+}
+
+// (n a multiple of 4)
+__device__ __forceinline__ float4 load_four(const void* base, int64_t at, bool f32, DenseType t) {
+  if (f32) return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + at);
+  const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(base) + at);
+  float4 v;
+  unpack16(w.x, t, v.x, v.y);
+  unpack16(w.y, t, v.z, v.w);
+  return v;
+}
+
+template <bool F8, bool AMN, bool BMN, DenseEpi EPI>
+__global__ void __launch_bounds__(kSpThreads, 2)
+    dense_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const DenseArgs g, const DenseSplit p) {
+  extern __shared__ uint8_t dsmem[];
+  __shared__ __align__(8) uint64_t full_bar[kSpMaxStages], empty_bar[kSpMaxStages];
+  __shared__ __align__(8) uint64_t accf_bar, sff_bar[kSpSfSlots], sfe_bar[kSpSfSlots];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t stage_bytes = kSpW + (uint32_t)p.NT * 128u;
+  uint8_t* sf_smem = smem + p.stages * stage_bytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    for (int i = 0; i < kSpSfSlots; ++i) {
+      mbar_init(smem_u32(&sff_bar[i]), 1);
+      mbar_init(smem_u32(&sfe_bar[i]), 1);
+    }
+    mbar_init(smem_u32(&accf_bar), 1);
+    abort_sh = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tmA);
+    prefetch_tensormap(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_base_sh), p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  volatile int* abort = &abort_sh;
+
+  constexpr int kStep = F8 ? 128 : 64;
+  const int KB = (g.K + kStep - 1) / kStep;
+  const int unit = blockIdx.x / p.split;
+  const int jt = unit / p.tt, m0 = (unit - jt * p.tt) * p.NT;  // weight tile, first token
+  const int tokens = min(p.NT, g.M - m0);
+  const int kb0 = (int)((int64_t)rank * KB / p.split), kb1 = (int)((int64_t)(rank + 1) * KB / p.split);
+  const int n = kb1 - kb0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    auto weights = [&](int i, int st) {
+      const uint32_t dst = sbase + st * stage_bytes, fb = smem_u32(&full_bar[st]);
+      const int k = (kb0 + i) * kStep;
+      if (EPI == kEpiGate) {  // 64 gate rows, then their 64 up rows
+        tma_load_2d(dst, &tmB, fb, k, jt * 64);
+        tma_load_2d(dst + 8192, &tmB, fb, k, g.N + jt * 64);
+      } else if (BMN) {
+        tma_load_2d(dst, &tmB, fb, jt * 128, k);
+        tma_load_2d(dst + 8192, &tmB, fb, jt * 128 + 64, k);
+      } else {
+        tma_load_2d(dst, &tmB, fb, k, jt * 128);
+      }
+    };
+    auto rows = [&](int i, int st) {
+      const uint32_t dst = sbase + st * stage_bytes + kSpW, fb = smem_u32(&full_bar[st]);
+      const int k = (kb0 + i) * kStep;
+      if (AMN) {
+        for (int c = 0; c < p.NT; c += 64) tma_load_2d(dst + c * 128, &tmA, fb, m0 + c, k);
+      } else {
+        tma_load_2d(dst, &tmA, fb, k, m0);
+      }
+    };
+    // The kernel before wrote the tokens, but not the weights (`early`): their copies do
+    // not wait for it.
+    const int pre = p.early ? min(p.stages, n) : 0;
+    if (lane == 0) {
+      for (int i = 0; i < pre; ++i) {
+        mbar_arrive_expect_tx(smem_u32(&full_bar[i]), stage_bytes);
+        weights(i, i);
+      }
+    }
+    pdl_wait();
+    pdl_trigger();
+    int issued = pre;
+    if (lane == 0) {
+      for (int i = 0; i < pre; ++i) rows(i, i);
+      for (int i = pre; i < n; ++i) {
+        const int st = i % p.stages;
+        if (!mbar_wait(smem_u32(&empty_bar[st]), ((i / p.stages) & 1) ^ 1, abort, g.status)) break;
+        mbar_arrive_expect_tx(smem_u32(&full_bar[st]), stage_bytes);
+        weights(i, st);
+        rows(i, st);
+        issued = i + 1;
+      }
+      // every copy has landed before the CTA leaves
+      for (int i = max(0, issued - p.stages); i < issued; ++i) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(smem_u32(&full_bar[i % p.stages]), (i / p.stages) & 1) &&
+               globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    pdl_wait();
+    pdl_trigger();
+  }
+  if (warp == 1) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      const uint32_t idesc0 =
+          F8 ? idesc_mxf8_e4m3(128, 16) - (2u << 17) + ((uint32_t)(p.NT >> 3) << 17)
+             : idesc_16(128, 0, g.type == kBF16, BMN, AMN) + ((uint32_t)(p.NT >> 3) << 17);
+      uint32_t sf = 0, slot = 0, group = 0;
+      for (int i = 0; i < n; ++i) {
+        const int st = i % p.stages;
+        const uint32_t j = (uint32_t)(kb0 + i) & 3u;
+        if (F8 && (j == 0 || i == 0)) {
+          slot = group & (kSpSfSlots - 1);
+          if (!mbar_wait(smem_u32(&sff_bar[slot]), (group / kSpSfSlots) & 1u, abort, g.status)) break;
+          ++group;
+        }
+        if (!mbar_wait(smem_u32(&full_bar[st]), (i / p.stages) & 1, abort, g.status)) break;
+        tc_fence_after();
+        const uint32_t wa = sbase + st * stage_bytes, ra = wa + kSpW;
+        if constexpr (F8) {
+          if (j == 0 || i == 0) {
+            sf = tmem + p.NT + slot * kSpSfCols;
+            const uint32_t sp = smem_u32(sf_smem) + slot * kSpSfBytes;
+            tc_cp_sf_atom(sf, sdesc_sf_atom(sp));
+            tc_cp_sf_atom(sf + 8, sdesc_sf_atom(sp + 512));
+            if (p.NT > 128) tc_cp_sf_atom(sf + 12, sdesc_sf_atom(sp + 1024));
+          }
+        }
+        const uint64_t wd = BMN ? sdesc_mn_sw128(wa) : sdesc_k_sw128(wa);
+        const uint64_t rd = AMN ? sdesc_mn_sw128(ra) : sdesc_k_sw128(ra);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t add = (i | k) != 0 ? 1u : 0u;
+          if constexpr (F8)
+            tc_mma_mxf8(tmem, wd + 2 * k, rd + 2 * k, idesc0 | (j << 4) | (j << 29), sf, sf + 8, add);
+          else
+            tc_mma_16(tmem, wd + (BMN ? 128 : 2) * k, rd + (AMN ? 128 : 2) * k, idesc0, add);
+        }
+        tc_commit(smem_u32(&empty_bar[st]));
+        if (F8 && (j == 3 || i == n - 1)) tc_commit(smem_u32(&sfe_bar[slot]));
+      }
+      tc_commit(smem_u32(&accf_bar));
+    }
+    __syncwarp();
+  } else if (F8 && warp == 2) {
+    // ------------------------------------------------------------ scales
+    // Lane l holds the words of rows l, l + 32, l + 64, l + 96 of an atom; a weight tile
+    // is one block of the matrix, all its rows have the same word.
+    const int64_t r0 = m0 + lane;
+    auto words = [&](int q, uint32_t (&w)[9]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = lane + 32 * i < tokens ? scale_word(g.sa, r0 + 32 * i, KB, q) : 0u;
+      w[8] = scale_word(g.sb, jt, KB, q);
+    };
+    uint32_t w[9];
+    const int q0 = kb0 >> 2, q1 = (kb1 + 3) >> 2;
+    words(q0, w);
+    for (int q = q0; q < q1; ++q) {
+      const uint32_t group = q - q0, slot = group & (kSpSfSlots - 1);
+      if (!mbar_wait(smem_u32(&sfe_bar[slot]), ((group / kSpSfSlots) & 1u) ^ 1u, abort, g.status)) break;
+      uint8_t* sp = sf_smem + slot * kSpSfBytes + lane * 16;
+      *reinterpret_cast<uint4*>(sp) = make_uint4(w[8], w[8], w[8], w[8]);
+      *reinterpret_cast<uint4*>(sp + 512) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (p.NT > 128) *reinterpret_cast<uint4*>(sp + 1024) = make_uint4(w[4], w[5], w[6], w[7]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sff_bar[slot]));
+      if (q + 1 < q1) words(q + 1, w);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ sums to shared memory
+    // sums[token][row], over the ring: all its copies have been multiplied.
+    const int q = warp & 3;
+    const bool ok = mbar_wait(smem_u32(&accf_bar), 0, abort, g.status);
+    if (ok && !*abort) {
+      tc_fence_after();
+      float* sums = reinterpret_cast<float*>(smem) + q * 32 + lane;
+      for (int c = 0; c < tokens; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sums[(c + k) * 128] = __uint_as_float(r[k]);
+      }
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  if (p.split > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+
+  // -------------------------------------------------------------- finish tokens
+  // This CTA's tokens are rank, rank + split, ...; a warp takes one at a time.
+  for (int t = rank + p.split * warp; t < tokens; t += p.split * kSpWarps) {
+    const int64_t m = m0 + t;
+    if constexpr (EPI == kEpiGate) {
+      const uint32_t at = sbase + (uint32_t)t * 512u + lane * 8u;
+      float gv[2] = {0.f, 0.f}, uv[2] = {0.f, 0.f};
+#pragma unroll 4
+      for (int c = 0; c < p.split; ++c) {
+        const uint32_t a = mapa_shared(at, c);
+        const float2 x = ld_cluster_v2(a), y = ld_cluster_v2(a + 256);
+        gv[0] += x.x, gv[1] += x.y, uv[0] += y.x, uv[1] += y.y;
+      }
+      const int col = jt * 64 + 2 * lane;
+      if (col >= g.N) continue;
+      if (g.saved) {
+        const int64_t s = m * 2 * g.N + col;
+        store_few(g.saved, s, col, g.N, gv, g.saved_f32, g.type, true);
+        store_few(g.saved, s + g.N, col, g.N, uv, g.saved_f32, g.type, true);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float a, da;
+        activate(g.act, gv[i], a, da);
+        uv[i] *= a;
+      }
+      store_few(g.out, m * g.ld_out + col, col, g.N, uv, false, g.type, true);
+    } else {
+      const uint32_t at = sbase + (uint32_t)t * 512u + lane * 16u;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int c = 0; c < p.split; ++c) {
+        const float4 x = ld_cluster_v4(mapa_shared(at, c));
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+      }
+      const int col = jt * 128 + 4 * lane;
+      if (col >= g.N) continue;
+      if constexpr (EPI == kEpiStore) {
+        const int64_t o = m * g.ld_out + col;
+        if (g.accumulate) {  // (float, whole vectors)
+          const float4 old = load_four(g.out, o, true, g.type);
+          v[0] += old.x, v[1] += old.y, v[2] += old.z, v[3] += old.w;
+        }
+        store_few(g.out, o, col, g.N, v, g.out_f32, g.type, g.vec);
+      } else {
+        const int64_t s = m * 2 * g.N + col;
+        const float4 gs = load_four(g.saved, s, g.saved_f32, g.type);
+        const float4 us = load_four(g.saved, s + g.N, g.saved_f32, g.type);
+        const float gv[4] = {gs.x, gs.y, gs.z, gs.w}, uv[4] = {us.x, us.y, us.z, us.w};
+        float dg[4], du[4], hv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float a, da;
+          activate(g.act, gv[i], a, da);
+          hv[i] = a * uv[i];
+          dg[i] = v[i] * uv[i] * da;
+          du[i] = v[i] * a;
+        }
+        store_few(g.dgu, s, col, g.N, dg, false, g.type, true);
+        store_few(g.dgu, s + g.N, col, g.N, du, false, g.type, true);
+        if (g.out) store_few(g.out, m * g.ld_out + col, col, g.N, hv, false, g.type, true);
+      }
+    }
+  }
+  if (p.split > 1) cluster_sync_all();  // the others have read this CTA's sums
+}
+
+template <bool F8, bool AMN, bool BMN, DenseEpi EPI>
+static cudaError_t launch_split(const CUtensorMap& a, const CUtensorMap& b, const DenseArgs& g, const DenseSplit& p,
+                                cudaStream_t s) {
+  cudaLaunchAttribute c;
+  c.id = cudaLaunchAttributeClusterDimension;
+  c.val.clusterDim.x = p.split;
+  c.val.clusterDim.y = 1;
+  c.val.clusterDim.z = 1;
+  return launch_k(dense_split_kernel<F8, AMN, BMN, EPI>, dim3((unsigned)(p.split * p.tt * p.rt)), dim3(kSpThreads),
+                  p.smem, s, true, &c, a, b, g, p);
+}
+
+cudaError_t dense_split_set_attributes() {
+  const void* ks[6] = {(const void*)dense_split_kernel<true, false, false, kEpiStore>,
+                       (const void*)dense_split_kernel<false, false, false, kEpiGate>,
+                       (const void*)dense_split_kernel<false, false, false, kEpiStore>,
+                       (const void*)dense_split_kernel<false, false, true, kEpiGrad>,
+                       (const void*)dense_split_kernel<false, false, true, kEpiStore>,
+                       (const void*)dense_split_kernel<false, true, true, kEpiStore>};
+  for (const void* k : ks) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpMaxSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+// How a product is divided: tokens in equal tiles of at most 256, one or two CTAs per
+// SM by what their tiles take of shared and tensor memory, and as many shares of K as fill
+// them.
+DenseSplit dense_split_plan(const DenseGemm& g, int sms) {
+  DenseSplit p = {};
+  const int unit = g.a.mn ? 64 : 16;
+  p.tt = (g.M + 255) / 256;
+  p.NT = ((g.M + p.tt - 1) / p.tt + unit - 1) / unit * unit;
+  p.tt = (g.M + p.NT - 1) / p.NT;
+  p.rt = g.epi == kEpiGate ? (g.N + 63) / 64 : (g.N + 127) / 128;
+  const bool f8 = g.type == kE4M3;
+  const int cols = p.NT + (f8 ? kSpSfSlots * kSpSfCols : 0);
+  p.tmem_cols = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
+  const int per_sm = p.NT <= 128 ? 2 : 1;  // (2 x 256 columns; above 76 KB each, so never three)
+  const uint32_t stage = kSpW + p.NT * 128, fixed = kSpSfSlots * kSpSfBytes + 1024;
+  const uint32_t room = per_sm == 2 ? 114 * 1024 : kSpMaxSmem;
+  p.stages = (int)((room - fixed) / stage);
+  if (p.stages > kSpMaxStages) p.stages = kSpMaxStages;
+  p.smem = p.stages * stage + fixed;
+  const int KB = (g.K + (f8 ? 127 : 63)) / (f8 ? 128 : 64);
+  const int64_t tiles = (int64_t)p.tt * p.rt;
+  int64_t split = (int64_t)sms * per_sm / tiles;
+  if (split > KB / 2) split = KB / 2;
+  p.split = split < 1 ? 1 : split > 8 ? 8 : (int)split;
+  return p;
+}
+
+cudaError_t dense_split_launch(const CUtensorMap& a, const CUtensorMap& b, const DenseGemm& g, const DenseArgs& d,
+                               const DenseSplit& p, cudaStream_t s) {
+  if (g.type == kE4M3) return launch_split<true, false, false, kEpiStore>(a, b, d, p, s);
+  if (g.epi == kEpiGate) return launch_split<false, false, false, kEpiGate>(a, b, d, p, s);
+  if (g.epi == kEpiGrad) return launch_split<false, false, true, kEpiGrad>(a, b, d, p, s);
+  if (g.a.mn) return launch_split<false, true, true, kEpiStore>(a, b, d, p, s);
+  if (g.b.mn) return launch_split<false, false, true, kEpiStore>(a, b, d, p, s);
+  return launch_split<false, false, false, kEpiStore>(a, b, d, p, s);
+}
+
+}  // namespace mm
