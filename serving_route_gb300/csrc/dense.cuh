@@ -59,6 +59,29 @@ DenseSplit dense_split_plan(const DenseGemm& g, int sms);
 cudaError_t dense_split_launch(const CUtensorMap& a, const CUtensorMap& b, const DenseGemm& g, const DenseArgs& d,
                                const DenseSplit& p, cudaStream_t s);
 
+// One lane of a converged warp.  The loops that issue copies and MMAs are run by whole warps
+// and their instructions by the elected lane, so that descriptors stay in uniform
+// registers: from one lane's branch every MMA took 76 clocks to issue.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0u;
+}
+
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity));
+}
+
+// Bounded wait of a whole warp: all of its lanes go on, or none.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait<CLUSTER>(bar, parity, abort, status));
+}
+
 // Shared-memory descriptor of an MN-major operand with the 128-byte swizzle: 64 elements
 // (128 bytes) per K row, 8 K rows 1024 bytes apart from the next 8 (stride offset), the
 // next 64 elements one box of 64 K rows further (leading offset).

@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     // The kernel before wrote the tokens, but not the weights (`early`): their copies do
     // not wait for it.
     const int pre = p.early ? min(p.stages, n) : 0;
-    if (lane == 0) {
+    const bool one = elect_one();
+    if (one) {
       for (int i = 0; i < pre; ++i) {
         mbar_arrive_expect_tx(smem_u32(&full_bar[i]), stage_bytes);
         weights(i, i);
@@ -189,23 +190,28 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     }
     pdl_wait();
     pdl_trigger();
-    int issued = pre;
-    if (lane == 0) {
+    if (one)
       for (int i = 0; i < pre; ++i) rows(i, i);
-      for (int i = pre; i < n; ++i) {
-        const int st = i % p.stages;
-        if (!mbar_wait(smem_u32(&empty_bar[st]), ((i / p.stages) & 1) ^ 1, abort, g.status)) break;
+    int st = pre == p.stages ? 0 : pre, issued = pre;
+    uint32_t ph = pre == p.stages ? 0u : 1u;  // parity of the wait for an empty place
+    for (int i = pre; i < n; ++i) {
+      if (!warp_wait(smem_u32(&empty_bar[st]), ph, abort, g.status)) break;
+      if (one) {
         mbar_arrive_expect_tx(smem_u32(&full_bar[st]), stage_bytes);
         weights(i, st);
         rows(i, st);
-        issued = i + 1;
       }
-      // every copy has landed before the CTA leaves
-      for (int i = max(0, issued - p.stages); i < issued; ++i) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(smem_u32(&full_bar[i % p.stages]), (i / p.stages) & 1) &&
-               globaltimer_ns() - t0 < kWaitLimitNs) {
-        }
+      issued = i + 1;
+      if (++st == p.stages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+    // every copy has landed before the CTA leaves
+    for (int i = max(0, issued - p.stages); i < issued; ++i) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_u32(&full_bar[i % p.stages]), (i / p.stages) & 1) &&
+             globaltimer_ns() - t0 < kWaitLimitNs) {
       }
     }
     __syncwarp();
@@ -215,33 +221,35 @@ __global__ void __launch_bounds__(kSpThreads, 2)
   }
   if (warp == 1) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      const uint32_t idesc0 =
-          F8 ? idesc_mxf8_e4m3(128, 16) - (2u << 17) + ((uint32_t)(p.NT >> 3) << 17)
-             : idesc_16(128, 0, g.type == kBF16, BMN, AMN) + ((uint32_t)(p.NT >> 3) << 17);
-      uint32_t sf = 0, slot = 0, group = 0;
-      for (int i = 0; i < n; ++i) {
-        const int st = i % p.stages;
-        const uint32_t j = (uint32_t)(kb0 + i) & 3u;
-        if (F8 && (j == 0 || i == 0)) {
-          slot = group & (kSpSfSlots - 1);
-          if (!mbar_wait(smem_u32(&sff_bar[slot]), (group / kSpSfSlots) & 1u, abort, g.status)) break;
-          ++group;
+    const bool one = elect_one();
+    const uint32_t idesc0 = F8 ? idesc_mxf8_e4m3(128, 0) + ((uint32_t)(p.NT >> 3) << 17)
+                               : idesc_16(128, 0, g.type == kBF16, BMN, AMN) + ((uint32_t)(p.NT >> 3) << 17);
+    uint32_t sf = 0, slot = 0, group = 0;
+    // (the next place is probed while this one's MMAs run)
+    int st = 0;
+    uint32_t ph = 0;
+    bool ready = warp_test(smem_u32(&full_bar[0]), 0);
+    for (int i = 0; i < n; ++i) {
+      const uint32_t j = (uint32_t)(kb0 + i) & 3u;
+      const bool fresh = F8 && (j == 0 || i == 0);
+      if (fresh) {
+        slot = group & (kSpSfSlots - 1);
+        if (!warp_wait(smem_u32(&sff_bar[slot]), (group / kSpSfSlots) & 1u, abort, g.status)) break;
+        ++group;
+        sf = tmem + p.NT + slot * kSpSfCols;
+      }
+      if (!ready && !warp_wait(smem_u32(&full_bar[st]), ph, abort, g.status)) break;
+      tc_fence_after();
+      const uint32_t wa = sbase + st * stage_bytes, ra = wa + kSpW;
+      const uint64_t wd = BMN ? sdesc_mn_sw128(wa) : sdesc_k_sw128(wa);
+      const uint64_t rd = AMN ? sdesc_mn_sw128(ra) : sdesc_k_sw128(ra);
+      if (one) {
+        if (fresh) {
+          const uint32_t sp = smem_u32(sf_smem) + slot * kSpSfBytes;
+          tc_cp_sf_atom(sf, sdesc_sf_atom(sp));
+          tc_cp_sf_atom(sf + 8, sdesc_sf_atom(sp + 512));
+          if (p.NT > 128) tc_cp_sf_atom(sf + 12, sdesc_sf_atom(sp + 1024));
         }
-        if (!mbar_wait(smem_u32(&full_bar[st]), (i / p.stages) & 1, abort, g.status)) break;
-        tc_fence_after();
-        const uint32_t wa = sbase + st * stage_bytes, ra = wa + kSpW;
-        if constexpr (F8) {
-          if (j == 0 || i == 0) {
-            sf = tmem + p.NT + slot * kSpSfCols;
-            const uint32_t sp = smem_u32(sf_smem) + slot * kSpSfBytes;
-            tc_cp_sf_atom(sf, sdesc_sf_atom(sp));
-            tc_cp_sf_atom(sf + 8, sdesc_sf_atom(sp + 512));
-            if (p.NT > 128) tc_cp_sf_atom(sf + 12, sdesc_sf_atom(sp + 1024));
-          }
-        }
-        const uint64_t wd = BMN ? sdesc_mn_sw128(wa) : sdesc_k_sw128(wa);
-        const uint64_t rd = AMN ? sdesc_mn_sw128(ra) : sdesc_k_sw128(ra);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t add = (i | k) != 0 ? 1u : 0u;
@@ -253,8 +261,13 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         tc_commit(smem_u32(&empty_bar[st]));
         if (F8 && (j == 3 || i == n - 1)) tc_commit(smem_u32(&sfe_bar[slot]));
       }
-      tc_commit(smem_u32(&accf_bar));
+      if (++st == p.stages) {
+        st = 0;
+        ph ^= 1u;
+      }
+      ready = warp_test(smem_u32(&full_bar[st]), ph);
     }
+    if (one) tc_commit(smem_u32(&accf_bar));
     __syncwarp();
   } else if (F8 && warp == 2) {
     // ------------------------------------------------------------ scales
