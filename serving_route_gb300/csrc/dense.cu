@@ -223,9 +223,10 @@ __global__ void __launch_bounds__(kDThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
+    const bool one = elect_one();
     int stage = 0;
     uint32_t phase = 0, issued = 0, last_parity = 0;
-    for (int u = pair0; u < g.units && !*abort; u += pairs) {
+    for (int u = pair0; u < g.units && !__any_sync(0xFFFFFFFFu, *abort); u += pairs) {
       int m, n;
       tile(u, m, n);
       const int ra = m * 256 + (int)rank * 128;
@@ -233,13 +234,13 @@ __global__ void __launch_bounds__(kDThreads, 1)
       const int rb = EPI == kEpiGate ? n * 128 + (rank ? g.N : 0) : n * 256 + (int)rank * 128;
       bool ok = true;
       for (int kb = 0; kb < KB; ++kb) {
-        if (!mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort, g.status)) {
+        if (!warp_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort, g.status)) {
           ok = false;
           break;
         }
-        if (lane == 0) {
-          const uint32_t st = sbase + stage * kDStage;
-          const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
+        const uint32_t st = sbase + stage * kDStage;
+        const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
+        if (one) {
           if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * kDStage);
           if (AMN) {
             tma_load_2d_pair(st, &tmA, fb, ra, kb * kStep);
@@ -254,7 +255,6 @@ __global__ void __launch_bounds__(kDThreads, 1)
             tma_load_2d_pair(st + kDBytesA, &tmB, fb, kb * kStep, rb);
           }
         }
-        __syncwarp();
         issued |= 1u << stage;
         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == kDStages) {
@@ -266,12 +266,12 @@ __global__ void __launch_bounds__(kDThreads, 1)
     }
     // Every copy has landed before the CTAs leave (the leader's barriers count both CTAs'
     // bytes); after an abort the peer also gives its last copies 100 us.
-    if (!leader && lane == 0 && *abort) {
+    if (!leader && *abort) {
       const uint64_t t0 = globaltimer_ns();
       while (globaltimer_ns() - t0 < 100000ull) {
       }
     }
-    if (lane == 0 && leader) {
+    if (leader) {
       for (int s = 0; s < kDStages; ++s) {
         if (!(issued & (1u << s))) continue;
         const uint64_t t0 = globaltimer_ns();
@@ -283,20 +283,22 @@ __global__ void __launch_bounds__(kDThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0 && leader) {
+    if (leader) {
+      const bool one = elect_one();
       const uint32_t idesc0 = F8 ? idesc_mxf8_e4m3(256, 256) : idesc_16(256, 256, g.type == kBF16, AMN, BMN);
       int stage = 0;
       uint32_t phase = 0, group = 0;
-      auto probe = [&](int s, uint32_t ph) { return mbar_test_wait_cluster(smem_u32(&full_bar[s]), ph); };
+      // (the next stage is probed while this one's MMAs run)
+      auto probe = [&](int s, uint32_t ph) {
+        return (bool)__all_sync(0xFFFFFFFFu, mbar_test_wait_cluster(smem_u32(&full_bar[s]), ph));
+      };
       bool ready = probe(0, 0);
       int i = 0;  // tiles so far
       for (int u = pair0; u < g.units; u += pairs, ++i) {
         const int b = i & 1;
         // E4M3: every warp has left the tile before last, and the tile before the columns
         // that both buffers have; else the tile before last
-        const bool free = F8 ? mbar_wait<true>(smem_u32(&acce_bar[0]), (i & 1) ^ 1u, abort, g.status)
-                             : mbar_wait<true>(smem_u32(&acce_bar[b]), ((i >> 1) & 1) ^ 1u, abort, g.status);
-        if (!free) break;
+        if (!warp_wait<true>(smem_u32(&acce_bar[F8 ? 0 : b]), ((F8 ? i : i >> 1) & 1) ^ 1u, abort, g.status)) break;
         tc_fence_after();
         const uint32_t acc = tmem + (b ? (F8 ? 192u : 256u) : 0u);
         bool ok = true;
@@ -305,52 +307,51 @@ __global__ void __launch_bounds__(kDThreads, 1)
           const uint32_t j = (uint32_t)kb & 3u;
           if (F8 && j == 0) {
             slot = group & (kSfSlots - 1);
-            if (!mbar_wait<true>(smem_u32(&sff_bar[slot]), (group / kSfSlots) & 1u, abort, g.status)) {
+            if (!warp_wait<true>(smem_u32(&sff_bar[slot]), (group / kSfSlots) & 1u, abort, g.status)) {
               ok = false;
               break;
             }
             ++group;
+            sf = tmem + kDTmemSf + slot * kDSfCols;
           }
-          if (!ready && !mbar_wait_slow<true>(smem_u32(&full_bar[stage]), phase, abort, g.status, kWaitLimitNs)) {
+          if (!ready && !warp_wait<true>(smem_u32(&full_bar[stage]), phase, abort, g.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t st = sbase + stage * kDStage;
-          if constexpr (F8) {
-            if (j == 0) {
-              sf = tmem + kDTmemSf + slot * kDSfCols;
+          const uint64_t ad = AMN ? sdesc_mn_sw128(st) : sdesc_k_sw128(st);
+          const uint64_t bd = BMN ? sdesc_mn_sw128(st + kDBytesA) : sdesc_k_sw128(st + kDBytesA);
+          if (one) {
+            if (F8 && j == 0) {
               const uint32_t sp = sfbase + slot * kSfSlotBytes;
               tc_cp_sf_atom_pair(sf, sdesc_sf_atom(sp));
               tc_cp_sf_atom_pair(sf + 8, sdesc_sf_atom(sp + 512));
               tc_cp_sf_atom_pair(sf + 12, sdesc_sf_atom(sp + 1024));
             }
-          }
-          const uint64_t ad = AMN ? sdesc_mn_sw128(st) : sdesc_k_sw128(st);
-          const uint64_t bd = BMN ? sdesc_mn_sw128(st + kDBytesA) : sdesc_k_sw128(st + kDBytesA);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t add = (kb | k) != 0 ? 1u : 0u;
-            // 32 bytes along K inside the swizzle atom, or 16 K rows of 128 bytes
-            const uint64_t da = ad + (AMN ? 128 : 2) * k, db = bd + (BMN ? 128 : 2) * k;
-            if constexpr (F8)
-              tc_mma_mxf8_pair(acc, da, db, idesc0 | (j << 4) | (j << 29), sf, sf + 8, add);
-            else
-              tc_mma_16_pair(acc, da, db, idesc0, add);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t add = (kb | k) != 0 ? 1u : 0u;
+              // 32 bytes along K inside the swizzle atom, or 16 K rows of 128 bytes
+              const uint64_t da = ad + (AMN ? 128 : 2) * k, db = bd + (BMN ? 128 : 2) * k;
+              if constexpr (F8)
+                tc_mma_mxf8_pair(acc, da, db, idesc0 | (j << 4) | (j << 29), sf, sf + 8, add);
+              else
+                tc_mma_16_pair(acc, da, db, idesc0, add);
+            }
+            tc_commit_pair_multicast(smem_u32(&empty_bar[stage]), 0x3);
+            if (F8 && (j == 3 || kb == KB - 1)) tc_commit_pair_multicast(smem_u32(&sfe_bar[slot]), 0x3);
           }
-          const int done_stage = stage;
           if (++stage == kDStages) {
             stage = 0;
             phase ^= 1u;
           }
           ready = probe(stage, phase);
-          tc_commit_pair_multicast(smem_u32(&empty_bar[done_stage]), 0x3);
-          if (F8 && (j == 3 || kb == KB - 1)) tc_commit_pair_multicast(smem_u32(&sfe_bar[slot]), 0x3);
         }
         if (!ok) break;
-        tc_commit_pair_multicast(smem_u32(&accf_bar[b]), 0x3);
+        if (one) tc_commit_pair_multicast(smem_u32(&accf_bar[b]), 0x3);
       }
-      tc_commit_pair(smem_u32(&drain_bar));
+      if (one) tc_commit_pair(smem_u32(&drain_bar));
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(smem_u32(&drain_bar), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
       }
