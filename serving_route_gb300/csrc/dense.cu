@@ -71,12 +71,20 @@ cudaError_t dense_scales_to_e8m0(const float* s, int64_t n, uint8_t* out, uint32
 // of the columns each).
 constexpr int kDThreads = 384;
 constexpr int kDEpiWarps = 8;
-constexpr int kDStages = 6;
+constexpr int kDStages = 5;  // (with 6: 1% less time, with 4: 8% more; the fifth's room goes to the epilogue)
 constexpr uint32_t kDBytesA = 16384, kDBytesB = 16384;
 constexpr uint32_t kDStage = kDBytesA + kDBytesB;
 constexpr int kSfSlots = 4;
 constexpr uint32_t kSfSlotBytes = 1536;  // A atom, two B atoms
-constexpr uint32_t kDSmem = kDStages * kDStage + kSfSlots * kSfSlotBytes + 1024;
+// Epilogue: per warp 32 rows x 128 bytes once (E4M3) or twice, through which sums and
+// operands pass between thread = row and whole lines of memory.
+template <bool F8>
+struct PairSmem {
+  static constexpr uint32_t kSf = kDStages * kDStage;
+  static constexpr uint32_t kEpi = kSf + (F8 ? kSfSlots * kSfSlotBytes : 0u);
+  static constexpr uint32_t kEpiWarp = F8 ? 4096u : 8192u;
+  static constexpr uint32_t kBytes = kEpi + kDEpiWarps * kEpiWarp + 1024u;
+};
 constexpr uint32_t kDTmemSf = 448, kDSfCols = 16;
 
 __device__ __forceinline__ void tc_mma_16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -89,76 +97,120 @@ __device__ __forceinline__ void tc_mma_16_pair(uint32_t d_tmem, uint64_t adesc, 
       : "memory");
 }
 
-// Stores and loads of a row's 32 consecutive columns from c on, of which those below n
-// exist.  16-byte pieces where n is a multiple of 8 (`vec`), 32-byte ones where the row
-// allows it (`wide`).
-__device__ __forceinline__ void store32_16(void* base, int64_t at, int c, int n, const float (&v)[32], DenseType t,
-                                           bool vec, bool wide) {
-  uint16_t* p = reinterpret_cast<uint16_t*>(base) + at;
-  if (vec) {
+// A warp's 32 rows x 128 bytes (or 64) in shared memory, in 16-byte pieces whose place is
+// changed by the row, so that neither a thread's pieces of its row nor eight lanes' of one row
+// meet in a bank.  Thread = row writes and reads pieces; memory is written and read
+// eight (four) lanes to a row, whole lines at a time.  (Straight from the threads, 32 rows an
+// instruction, the gradient's epilogue took 14 us of a 256 x 256 tile, most of it the
+// load and store unit's time for 32 lines each.)
+template <int BYTES>
+__device__ __forceinline__ uint32_t piece_at(uint32_t buf, int row, int c) {
+  return BYTES == 128 ? buf + row * 128 + ((c ^ (row & 7)) << 4) : buf + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void sts_piece(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds_piece(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// This thread's 32 values to its row: floats (128 bytes), or 16 bits from piece `first` on.
+__device__ __forceinline__ void put_f32(uint32_t buf, int row, const float (&v)[32]) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 16) {
-      uint32_t w[8];
+  for (int c = 0; c < 8; ++c)
+    sts_piece(piece_at<128>(buf, row, c), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+              __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+}
+
+template <int BYTES>
+__device__ __forceinline__ void put_16(uint32_t buf, int row, int first, const float (&v)[32], DenseType t) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = pack16(v[i + 2 * j], v[i + 2 * j + 1], t);
-      if (wide && c + i + 16 <= n) {
-        st_global_v8(p + i, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
-      } else {
-        if (c + i < n) *reinterpret_cast<uint4*>(p + i) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (c + i + 8 < n) *reinterpret_cast<uint4*>(p + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-      }
+  for (int c = 0; c < 4; ++c)
+    sts_piece(piece_at<BYTES>(buf, row, first + c), pack16(v[8 * c], v[8 * c + 1], t),
+              pack16(v[8 * c + 2], v[8 * c + 3], t), pack16(v[8 * c + 4], v[8 * c + 5], t),
+              pack16(v[8 * c + 6], v[8 * c + 7], t));
+}
+
+// The buffer's rows to dst (rows `pitch` bytes apart), `rows` of them and `bytes` of each
+// (whole pieces).  ADD: floats, added to what is there.
+template <int BYTES, bool ADD = false>
+__device__ __forceinline__ void flush(uint32_t buf, uint8_t* dst, int64_t pitch, int rows, int bytes, int lane) {
+  constexpr int kLanes = BYTES / 16, kRows = 32 / kLanes;
+  const int r0 = lane / kLanes, c = lane % kLanes;
+  if (16 * c >= bytes) return;
+#pragma unroll
+  for (int i = 0; i < 32; i += kRows) {
+    const int r = i + r0;
+    if (r >= rows) break;
+    uint4 v = lds_piece(piece_at<BYTES>(buf, r, c));
+    uint4* p = reinterpret_cast<uint4*>(dst + r * pitch + 16 * c);
+    if (ADD) {
+      const float4 o = *reinterpret_cast<const float4*>(p);
+      v.x = __float_as_uint(__uint_as_float(v.x) + o.x);
+      v.y = __float_as_uint(__uint_as_float(v.y) + o.y);
+      v.z = __float_as_uint(__uint_as_float(v.z) + o.z);
+      v.w = __float_as_uint(__uint_as_float(v.w) + o.w);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (c + i < n) p[i] = bits16(v[i], t);
+    *p = v;
   }
 }
 
-__device__ __forceinline__ void store32_f32(void* base, int64_t at, int c, int n, const float (&v)[32], bool vec,
-                                            bool wide) {
-  float* p = reinterpret_cast<float*>(base) + at;
-  if (vec) {
+// The same where rows begin anywhere: an element per lane.
+template <typename E>
+__device__ __forceinline__ void flush_elements(const uint8_t* buf, E* dst, int64_t ld, int rows, int cols, int lane) {
+  constexpr int kPer = 16 / sizeof(E);
+  for (int r = 0; r < rows; ++r)
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-      if (c + i >= n) break;
-      if (wide) {
-        st_global_v8(p + i, __float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
-                     __float_as_uint(v[i + 3]), __float_as_uint(v[i + 4]), __float_as_uint(v[i + 5]),
-                     __float_as_uint(v[i + 6]), __float_as_uint(v[i + 7]));
-      } else {
-        *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        *reinterpret_cast<float4*>(p + i + 4) = make_float4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
-      }
-    }
+    for (int c = lane; c < (int)(128 / sizeof(E)); c += 32)
+      if (c < cols)
+        dst[r * ld + c] = *reinterpret_cast<const E*>(buf + r * 128 + (((c / kPer) ^ (r & 7)) << 4) + c % kPer * sizeof(E));
+}
+
+// 32 columns of saved gate or up, asynchronously, zeros past the rows and columns.
+__device__ __forceinline__ void fetch_saved(uint32_t buf, const uint8_t* src, int64_t pitch, int rows, int bytes, bool f32,
+                                            int lane) {
+  auto copy = [&](uint32_t at, int r, int c) {
+    const bool in = r < rows && 16 * c < bytes;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(in ? src + r * pitch + 16 * c : src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+  };
+  if (f32) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) copy(piece_at<128>(buf, i + lane / 8, lane % 8), i + lane / 8, lane % 8);
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (c + i < n) p[i] = v[i];
+    for (int i = 0; i < 32; i += 8) copy(piece_at<64>(buf, i + lane / 4, lane % 4), i + lane / 4, lane % 4);
   }
 }
 
-// (n a multiple of 8)
-__device__ __forceinline__ void load32(const void* base, int64_t at, int c, int n, bool f32, DenseType t,
-                                       float (&v)[32]) {
+__device__ __forceinline__ void get_saved(uint32_t buf, int row, bool f32, DenseType t, float (&v)[32]) {
+  if (f32) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    if (c + i >= n) {
+    for (int c = 0; c < 8; ++c) {
+      const uint4 w = lds_piece(piece_at<128>(buf, row, c));
+      v[4 * c] = __uint_as_float(w.x), v[4 * c + 1] = __uint_as_float(w.y);
+      v[4 * c + 2] = __uint_as_float(w.z), v[4 * c + 3] = __uint_as_float(w.w);
+    }
+  } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i + j] = 0.f;
-    } else if (f32) {
-      const float4 a = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + at + i);
-      const float4 b = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + at + i + 4);
-      v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
-      v[i + 4] = b.x, v[i + 5] = b.y, v[i + 6] = b.z, v[i + 7] = b.w;
-    } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + at + i);
-      unpack16(a.x, t, v[i], v[i + 1]);
-      unpack16(a.y, t, v[i + 2], v[i + 3]);
-      unpack16(a.z, t, v[i + 4], v[i + 5]);
-      unpack16(a.w, t, v[i + 6], v[i + 7]);
+    for (int c = 0; c < 4; ++c) {
+      const uint4 w = lds_piece(piece_at<64>(buf, row, c));
+      unpack16(w.x, t, v[8 * c], v[8 * c + 1]);
+      unpack16(w.y, t, v[8 * c + 2], v[8 * c + 3]);
+      unpack16(w.z, t, v[8 * c + 4], v[8 * c + 5]);
+      unpack16(w.w, t, v[8 * c + 6], v[8 * c + 7]);
     }
   }
+}
+
+__device__ __forceinline__ void as_floats(const uint32_t (&r)[32], float (&v)[32]) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
 }
 
 template <bool F8, bool AMN, bool BMN, DenseEpi EPI>
@@ -174,7 +226,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t sfbase = sbase + kDStages * kDStage;
+  const uint32_t sfbase = sbase + PairSmem<F8>::kSf;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -383,7 +435,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
           ok = false;
           break;
         }
-        uint8_t* sp = smem + kDStages * kDStage + slot * kSfSlotBytes + lane * 16;
+        uint8_t* sp = smem + PairSmem<F8>::kSf + slot * kSfSlotBytes + lane * 16;
         *reinterpret_cast<uint4*>(sp) = make_uint4(w[0], w[1], w[2], w[3]);
         *reinterpret_cast<uint4*>(sp + 512) = make_uint4(w[4], w[4], w[4], w[4]);
         *reinterpret_cast<uint4*>(sp + 1024) = make_uint4(w[5], w[5], w[5], w[5]);
@@ -398,14 +450,27 @@ __global__ void __launch_bounds__(kDThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t tlane = tmem + ((uint32_t)(q * 32) << 16);
+    const uint32_t epi = PairSmem<F8>::kEpi + (uint32_t)(warp - 4) * PairSmem<F8>::kEpiWarp;
+    const uint32_t buf = sbase + epi;
     int i = 0;
     for (int u = pair0; u < g.units; u += pairs, ++i) {
       int m, n;
       tile(u, m, n);
       const int b = i & 1;
-      const int64_t row = (int64_t)m * 256 + rank * 128 + q * 32 + lane;
-      const bool live = row < g.M;
-      if (!mbar_wait(smem_u32(&accf_bar[b]), (i >> 1) & 1, abort, g.status)) break;
+      const int64_t row0 = (int64_t)m * 256 + rank * 128 + q * 32;
+      const int rows = (int)max((int64_t)0, min((int64_t)32, g.M - row0));  // of this warp
+      const int ss = g.saved_f32 ? 4 : 2;
+      uint8_t* saved = reinterpret_cast<uint8_t*>(g.saved) + row0 * 2 * g.N * ss;
+      const int64_t saved_pitch = (int64_t)2 * g.N * ss;
+      auto fetch = [&](int up, int col) {  // gate to the first buffer, up to the second
+        fetch_saved(buf + 4096 * up, saved + ((int64_t)up * g.N + col) * ss, saved_pitch, rows, (g.N - col) * ss,
+                    g.saved_f32, lane);
+      };
+      if constexpr (EPI == kEpiGrad) {
+        fetch(0, n * 256 + half * 128);
+        fetch(1, n * 256 + half * 128);
+      }
+      if (!warp_wait(smem_u32(&accf_bar[b]), (i >> 1) & 1, abort, g.status)) break;
       tc_fence_after();
       const uint32_t acc = tlane + (b ? (F8 ? 192u : 256u) : 0u);
       auto release = [&](int bar) {
@@ -416,54 +481,77 @@ __global__ void __launch_bounds__(kDThreads, 1)
       if constexpr (EPI == kEpiStore) {
         // the columns that both buffers have are the first one's last 64 and the second
         // one's first: their half drains them first, the other half has left the tile before
-        const int c0 = half * 128, n0 = n * 256 + c0;
         if (F8 && half == b) release(0);
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const int cc = F8 && b == 0 ? (c ^ 2) * 32 : c * 32;
-          uint32_t r[32];
-          tmem_ld32(acc + c0 + cc, r);
+        for (int p = 0; p < 2; ++p) {
+          const int cc = half * 128 + (F8 && b == 0 ? p ^ 1 : p) * 64, col = n * 256 + cc, cols = g.N - col;
+          uint32_t r[2][32];
+          tmem_ld32(acc + cc, r[0]);
+          tmem_ld32(acc + cc + 32, r[1]);
           tmem_ld_wait();
-          if (F8 ? (c == 1 && half != b) : c == 3) release(F8 ? 0 : b);
-          const int col = n0 + cc;
-          if (!live || col >= g.N) continue;
+          if (F8 ? p == 0 && half != b : p == 1) release(F8 ? 0 : b);
+          if (rows == 0 || cols <= 0) continue;
           float v[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
-          const int64_t at = row * g.ld_out + col;
           if (g.out_f32) {
-            if (g.accumulate) {
-              float old[32];
-              load32(g.out, at, col, g.N, true, g.type, old);
+            float* out = reinterpret_cast<float*>(g.out) + row0 * g.ld_out + col;
 #pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] += old[k];
+            for (int h = 0; h < 2; ++h) {
+              as_floats(r[h], v);
+              __syncwarp();
+              put_f32(buf, lane, v);
+              __syncwarp();
+              uint8_t* dst = reinterpret_cast<uint8_t*>(out + 32 * h);
+              const int left = cols - 32 * h;
+              if (!g.vec)
+                flush_elements(smem + epi, out + 32 * h, g.ld_out, rows, left, lane);
+              else if (g.accumulate)
+                flush<128, true>(buf, dst, g.ld_out * 4, rows, left * 4, lane);
+              else
+                flush<128>(buf, dst, g.ld_out * 4, rows, left * 4, lane);
             }
-            store32_f32(g.out, at, col, g.N, v, g.vec, g.wide);
           } else {
-            store32_16(g.out, at, col, g.N, v, g.type, g.vec, g.wide);
+            __syncwarp();
+            as_floats(r[0], v);
+            put_16<128>(buf, lane, 0, v, g.type);
+            as_floats(r[1], v);
+            put_16<128>(buf, lane, 4, v, g.type);
+            __syncwarp();
+            uint16_t* out = reinterpret_cast<uint16_t*>(g.out) + row0 * g.ld_out + col;
+            if (g.vec)
+              flush<128>(buf, reinterpret_cast<uint8_t*>(out), g.ld_out * 2, rows, cols * 2, lane);
+            else
+              flush_elements(smem + epi, out, g.ld_out, rows, cols, lane);
           }
         }
       } else if constexpr (EPI == kEpiGate) {
+        const int col0 = n * 128 + half * 64;
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
-          const int cc = half * 64 + c * 32, col = n * 128 + cc;
+          const int cc = half * 64 + c * 32, col = col0 + c * 32;
           uint32_t rg[32], ru[32];
           tmem_ld32(acc + cc, rg);
           tmem_ld32(acc + 128 + cc, ru);
           tmem_ld_wait();
           if (c == 1) release(b);
-          if (!live || col >= g.N) continue;
           float gv[32], uv[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) gv[k] = __uint_as_float(rg[k]), uv[k] = __uint_as_float(ru[k]);
-          if (g.saved) {
-            const int64_t at = row * 2 * g.N + col;
+          as_floats(rg, gv);
+          as_floats(ru, uv);
+          if (g.saved && rows && col < g.N) {
+            __syncwarp();
+            const int bytes = (g.N - col) * ss;
+            uint8_t* dst = saved + (int64_t)col * ss;
             if (g.saved_f32) {
-              store32_f32(g.saved, at, col, g.N, gv, true, g.wide);
-              store32_f32(g.saved, at + g.N, col, g.N, uv, true, g.wide);
+              put_f32(buf, lane, gv);
+              put_f32(buf + 4096, lane, uv);
+              __syncwarp();
+              flush<128>(buf, dst, saved_pitch, rows, bytes, lane);
+              flush<128>(buf + 4096, dst + (int64_t)g.N * 4, saved_pitch, rows, bytes, lane);
             } else {
-              store32_16(g.saved, at, col, g.N, gv, g.type, true, g.wide);
-              store32_16(g.saved, at + g.N, col, g.N, uv, g.type, true, g.wide);
+              put_16<64>(buf, lane, 0, gv, g.type);
+              put_16<64>(buf + 4096, lane, 0, uv, g.type);
+              __syncwarp();
+              flush<64>(buf, dst, saved_pitch, rows, bytes, lane);
+              flush<64>(buf + 4096, dst + (int64_t)g.N * 2, saved_pitch, rows, bytes, lane);
             }
           }
 #pragma unroll
@@ -472,25 +560,32 @@ __global__ void __launch_bounds__(kDThreads, 1)
             activate(g.act, gv[k], a, da);
             uv[k] *= a;
           }
-          store32_16(g.out, row * g.ld_out + col, col, g.N, uv, g.type, true, g.wide);
+          if (rows && col < g.N) {
+            __syncwarp();
+            put_16<64>(buf, lane, 0, uv, g.type);
+            __syncwarp();
+            flush<64>(buf, reinterpret_cast<uint8_t*>(g.out) + (row0 * g.ld_out + col) * 2, g.ld_out * 2, rows,
+                      (g.N - col) * 2, lane);
+          }
         }
       } else {
-        const int c0 = half * 128;
+        // The saved gate and up of the next 32 columns are under way while these are
+        // finished: up at once, gate when its buffer, which dg and du and then h leave
+        // through, is free.
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          const int col = n * 256 + c0 + c * 32;
-          const bool on = live && col < g.N;
-          const int64_t at = row * 2 * g.N + col;
+          const int col = n * 256 + half * 128 + c * 32;
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncwarp();
           float gv[32], uv[32];
-          if (on) {
-            load32(g.saved, at, col, g.N, g.saved_f32, g.type, gv);
-            load32(g.saved, at + g.N, col, g.N, g.saved_f32, g.type, uv);
-          }
+          get_saved(buf, lane, g.saved_f32, g.type, gv);
+          get_saved(buf + 4096, lane, g.saved_f32, g.type, uv);
+          __syncwarp();
+          if (c < 3) fetch(1, col + 32);
           uint32_t r[32];
-          tmem_ld32(acc + c0 + c * 32, r);
+          tmem_ld32(acc + half * 128 + c * 32, r);
           tmem_ld_wait();
           if (c == 3) release(b);
-          if (!on) continue;
           float hv[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
@@ -501,12 +596,28 @@ __global__ void __launch_bounds__(kDThreads, 1)
             gv[k] = dh * uv[k] * da;
             uv[k] = dh * a;
           }
-          store32_16(g.dgu, at, col, g.N, gv, g.type, true, g.wide);
-          store32_16(g.dgu, at + g.N, col, g.N, uv, g.type, true, g.wide);
-          if (g.out) store32_16(g.out, row * g.ld_out + col, col, g.N, hv, g.type, true, g.wide);
+          if (rows && col < g.N) {
+            const int bytes = (g.N - col) * 2;
+            put_16<64>(buf, lane, 0, gv, g.type);
+            put_16<64>(buf + 2048, lane, 0, uv, g.type);
+            __syncwarp();
+            uint8_t* dst = reinterpret_cast<uint8_t*>(g.dgu) + (row0 * 2 * g.N + col) * 2;
+            flush<64>(buf, dst, (int64_t)4 * g.N, rows, bytes, lane);
+            flush<64>(buf + 2048, dst + (int64_t)2 * g.N, (int64_t)4 * g.N, rows, bytes, lane);
+            if (g.out) {
+              __syncwarp();
+              put_16<64>(buf, lane, 0, hv, g.type);
+              __syncwarp();
+              flush<64>(buf, reinterpret_cast<uint8_t*>(g.out) + (row0 * g.ld_out + col) * 2, g.ld_out * 2, rows, bytes,
+                        lane);
+            }
+          }
+          __syncwarp();
+          if (c < 3) fetch(0, col + 32);
         }
       }
     }
+    if (EPI == kEpiGrad) asm volatile("cp.async.wait_all;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -551,7 +662,7 @@ static cudaError_t launch_pair(const CUtensorMap& a, const CUtensorMap& b, const
   c.val.clusterDim.x = 2;
   c.val.clusterDim.y = 1;
   c.val.clusterDim.z = 1;
-  return launch_k(dense_pair_kernel<F8, AMN, BMN, EPI>, dim3(ctas), dim3(kDThreads), kDSmem, s, true, &c, a, b, g);
+  return launch_k(dense_pair_kernel<F8, AMN, BMN, EPI>, dim3(ctas), dim3(kDThreads), PairSmem<F8>::kBytes, s, true, &c, a, b, g);
 }
 
 cudaError_t dense_set_attributes() {
@@ -561,8 +672,9 @@ cudaError_t dense_set_attributes() {
                        (const void*)dense_pair_kernel<false, false, true, kEpiGrad>,
                        (const void*)dense_pair_kernel<false, false, true, kEpiStore>,
                        (const void*)dense_pair_kernel<false, true, true, kEpiStore>};
-  for (const void* k : ks) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDSmem);
+  for (int i = 0; i < 6; ++i) {
+    const uint32_t bytes = i ? PairSmem<false>::kBytes : PairSmem<true>::kBytes;
+    const cudaError_t e = cudaFuncSetAttribute(ks[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
   }
   return dense_split_set_attributes();
@@ -592,7 +704,6 @@ cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
   d.status = g.status;
   const uintptr_t at = (uintptr_t)g.out | (uintptr_t)g.saved | (uintptr_t)g.dgu;
   d.vec = g.N % 8 == 0 && at % 16 == 0;
-  d.wide = d.vec && g.N % 16 == 0 && at % 32 == 0;
   if (g.M <= 256) {
     DenseSplit p = dense_split_plan(g, sms);
     p.early = g.early;

@@ -38,7 +38,7 @@ struct DenseArgs {
   const uint8_t *sa, *sb;
   void* out;
   int64_t ld_out;
-  bool out_f32, accumulate, vec, wide;  // vec: columns in pieces of 8, 16-byte stores; wide: 32-byte stores
+  bool out_f32, accumulate, vec;  // vec: columns in pieces of 8, rows on 16-byte boundaries
   void* saved;
   bool saved_f32;
   void* dgu;
