@@ -554,12 +554,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
               flush<64>(buf + 4096, dst + (int64_t)g.N * 2, saved_pitch, rows, bytes, lane);
             }
           }
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float a, da;
-            activate(g.act, gv[k], a, da);
-            uv[k] *= a;
-          }
+          gate_values(g.act, gv, uv);
           if (rows && col < g.N) {
             __syncwarp();
             put_16<64>(buf, lane, 0, uv, g.type);
@@ -587,15 +582,8 @@ __global__ void __launch_bounds__(kDThreads, 1)
           tmem_ld_wait();
           if (c == 3) release(b);
           float hv[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float dh = __uint_as_float(r[k]);
-            float a, da;
-            activate(g.act, gv[k], a, da);
-            hv[k] = a * uv[k];
-            gv[k] = dh * uv[k] * da;
-            uv[k] = dh * a;
-          }
+          as_floats(r, hv);
+          gradient_values(g.act, hv, gv, uv);
           if (rows && col < g.N) {
             const int bytes = (g.N - col) * 2;
             put_16<64>(buf, lane, 0, gv, g.type);

@@ -343,12 +343,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         store_few(g.saved, s, col, g.N, gv, g.saved_f32, g.type, true);
         store_few(g.saved, s + g.N, col, g.N, uv, g.saved_f32, g.type, true);
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float a, da;
-        activate(g.act, gv[i], a, da);
-        uv[i] *= a;
-      }
+      gate_values(g.act, gv, uv);
       store_few(g.out, m * g.ld_out + col, col, g.N, uv, false, g.type, true);
     } else {
       const uint32_t at = sbase + (uint32_t)t * 512u + lane * 16u;
@@ -371,19 +366,11 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         const int64_t s = m * 2 * g.N + col;
         const float4 gs = load_four(g.saved, s, g.saved_f32, g.type);
         const float4 us = load_four(g.saved, s + g.N, g.saved_f32, g.type);
-        const float gv[4] = {gs.x, gs.y, gs.z, gs.w}, uv[4] = {us.x, us.y, us.z, us.w};
-        float dg[4], du[4], hv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float a, da;
-          activate(g.act, gv[i], a, da);
-          hv[i] = a * uv[i];
-          dg[i] = v[i] * uv[i] * da;
-          du[i] = v[i] * a;
-        }
-        store_few(g.dgu, s, col, g.N, dg, false, g.type, true);
-        store_few(g.dgu, s + g.N, col, g.N, du, false, g.type, true);
-        if (g.out) store_few(g.out, m * g.ld_out + col, col, g.N, hv, false, g.type, true);
+        float gv[4] = {gs.x, gs.y, gs.z, gs.w}, uv[4] = {us.x, us.y, us.z, us.w};
+        gradient_values(g.act, v, gv, uv);
+        store_few(g.dgu, s, col, g.N, gv, false, g.type, true);
+        store_few(g.dgu, s + g.N, col, g.N, uv, false, g.type, true);
+        if (g.out) store_few(g.out, m * g.ld_out + col, col, g.N, v, false, g.type, true);
       }
     }
   }
