@@ -55,18 +55,20 @@ cudaError_t dense_scales_to_e8m0(const float* s, int64_t n, uint8_t* out, uint32
 
 // ------------------------------------------------------------------------- products
 // d[m, n] = sum_k a[m, k] b[n, k] on CTA pairs (tcgen05 cta_group::2): a pair owns a tile of
-// 256 rows x 256 columns, each CTA stages its 128 rows of A and half of B's rows, the
+// 256 rows x BN columns, each CTA stages its 128 rows of A and half of B's rows, the
 // leader issues the MMAs and each CTA drains its own 128 rows.  Persistent: pair p takes
-// tiles p, p + pairs, ...; 8 row tiles share a sweep over the columns, so that what
-// runs at one time reads few distinct operand rows.
-//   K-major operands (rows of K)      TMA boxes of 128 rows x 128 bytes.
+// tiles p, p + pairs, ... of up to three products (the gradients of a block's input and
+// weights need only what one kernel before them wrote, and fill each other's last wave);
+// 8 row tiles share a sweep over the columns, so that what runs at one time reads few
+// distinct operand rows.  BN is 256, or 192, 128, 64 where the tiles are few (pair_columns).
+//   K-major operands (rows of K)      TMA boxes of rows x 128 bytes.
 //   MN-major operands (K rows of it)  boxes of 64 K rows x 64 elements, two side by
 //                                     side: gradients multiply the stored tensors as they
 //                                     are, nothing is transposed in memory.
 //   E4M3: block-scaled MMAs.  One warp builds the scale atoms (four K blocks of 128
 //   rows) from the rows' and the matrix's E8M0 bytes, a slot ahead of the MMAs.
-// Accumulators: two of 256 TMEM columns in turn.  With scales in TMEM (64 columns) the two
-// overlap by 64 columns, which the epilogue drains first.
+// Accumulators: two of up to 256 TMEM columns in turn.  With scales in TMEM (64 columns) two
+// of 256 overlap by 64 columns, which the epilogue drains first.
 // Warps: 0 loads, 1 MMAs, 2 scales, 4-11 epilogue (two per TMEM lane quadrant, a half
 // of the columns each).
 constexpr int kDThreads = 384;
@@ -213,10 +215,32 @@ __device__ __forceinline__ void as_floats(const uint32_t (&r)[32], float (&v)[32
   for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
 }
 
-template <bool F8, bool AMN, bool BMN, DenseEpi EPI>
-__global__ void __launch_bounds__(kDThreads, 1)
-    dense_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      const DenseArgs g) {
+struct PairProblem {
+  CUtensorMap a, b;
+  int M, N, K;
+  int mt, nt, end;         // tiles of 256 rows, of columns; units of this product and those before
+  bool amn, bmn;
+  bool out_f32, accumulate, vec;  // vec: columns in pieces of 8, rows on 16-byte boundaries
+  void* out;
+  int64_t ld_out;
+};
+
+constexpr int kPairProblems = 3;
+
+struct PairArgs {
+  PairProblem p[kPairProblems];
+  int BN, units;
+  DenseAct act;
+  DenseType type;
+  const uint8_t *sa, *sb;
+  void* saved;
+  bool saved_f32;
+  void* dgu;
+  uint32_t* status;
+};
+
+template <bool F8, DenseEpi EPI>
+__global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_constant__ PairArgs g) {
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full_bar[kDStages], empty_bar[kDStages];
   __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2], drain_bar;
@@ -248,8 +272,8 @@ __global__ void __launch_bounds__(kDThreads, 1)
     mbar_init(smem_u32(&drain_bar), 1);
     abort_sh = 0;
     fence_mbar_init();
-    prefetch_tensormap(&tmA);
-    prefetch_tensormap(&tmB);
+    prefetch_tensormap(&g.p[0].a);
+    prefetch_tensormap(&g.p[0].b);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(&tmem_base_sh), 512);
@@ -265,12 +289,21 @@ __global__ void __launch_bounds__(kDThreads, 1)
 
   constexpr int kStep = F8 ? 128 : 64;  // elements of K per stage: 128 bytes
   constexpr int kRowM = 8;              // row tiles of one sweep
-  const int KB = (g.K + kStep - 1) / kStep;
-  auto tile = [&](int u, int& m, int& n) {
-    const int band = u / (kRowM * g.nt), r = u - band * kRowM * g.nt;
-    const int rows = min(kRowM, g.mt - band * kRowM);
+  const int BN = g.BN, hb = BN / 2;     // (kEpiGate: hb columns of h, their gate and up)
+  const bool overlap = F8 && BN > 192;  // the accumulators share columns
+  const uint32_t acc_next = F8 ? 192u : 256u;
+  // unit u -> product, row and column tile
+  auto tile = [&](int u, int& m, int& n) -> const PairProblem& {
+    int i = 0;
+    if (!F8 && EPI == kEpiStore)
+      while (u >= g.p[i].end) ++i;
+    const PairProblem& p = g.p[i];
+    if (i) u -= g.p[i - 1].end;
+    const int band = u / (kRowM * p.nt), r = u - band * kRowM * p.nt;
+    const int rows = min(kRowM, p.mt - band * kRowM);
     n = r / rows;
     m = band * kRowM + (r - n * rows);
+    return p;
   };
 
   if (warp == 0) {
@@ -280,10 +313,13 @@ __global__ void __launch_bounds__(kDThreads, 1)
     uint32_t phase = 0, issued = 0, last_parity = 0;
     for (int u = pair0; u < g.units && !__any_sync(0xFFFFFFFFu, *abort); u += pairs) {
       int m, n;
-      tile(u, m, n);
+      const PairProblem& p = tile(u, m, n);
+      const int KB = (p.K + kStep - 1) / kStep;
+      const bool amn = p.amn, bmn = p.bmn;
       const int ra = m * 256 + (int)rank * 128;
       // kEpiGate: the leader stages the gate rows, its peer the up rows
-      const int rb = EPI == kEpiGate ? n * 128 + (rank ? g.N : 0) : n * 256 + (int)rank * 128;
+      const int rb = EPI == kEpiGate ? n * hb + (rank ? p.N : 0) : n * BN + (int)rank * hb;
+      const uint32_t bytes = 2 * (kDBytesA + (bmn ? (hb + 63) / 64 * 8192 : hb * 128));
       bool ok = true;
       for (int kb = 0; kb < KB; ++kb) {
         if (!warp_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort, g.status)) {
@@ -293,18 +329,18 @@ __global__ void __launch_bounds__(kDThreads, 1)
         const uint32_t st = sbase + stage * kDStage;
         const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
         if (one) {
-          if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * kDStage);
-          if (AMN) {
-            tma_load_2d_pair(st, &tmA, fb, ra, kb * kStep);
-            tma_load_2d_pair(st + 8192, &tmA, fb, ra + 64, kb * kStep);
+          if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), bytes);
+          if (!F8 && amn) {
+            tma_load_2d_pair(st, &p.a, fb, ra, kb * kStep);
+            tma_load_2d_pair(st + 8192, &p.a, fb, ra + 64, kb * kStep);
           } else {
-            tma_load_2d_pair(st, &tmA, fb, kb * kStep, ra);
+            tma_load_2d_pair(st, &p.a, fb, kb * kStep, ra);
           }
-          if (BMN) {
-            tma_load_2d_pair(st + kDBytesA, &tmB, fb, rb, kb * kStep);
-            tma_load_2d_pair(st + kDBytesA + 8192, &tmB, fb, rb + 64, kb * kStep);
+          if (!F8 && bmn) {
+            tma_load_2d_pair(st + kDBytesA, &p.b, fb, rb, kb * kStep);
+            if (hb > 64) tma_load_2d_pair(st + kDBytesA + 8192, &p.b, fb, rb + 64, kb * kStep);
           } else {
-            tma_load_2d_pair(st + kDBytesA, &tmB, fb, kb * kStep, rb);
+            tma_load_2d_pair(st + kDBytesA, &p.b, fb, kb * kStep, rb);
           }
         }
         issued |= 1u << stage;
@@ -337,7 +373,8 @@ __global__ void __launch_bounds__(kDThreads, 1)
     // ------------------------------------------------------------ MMAs
     if (leader) {
       const bool one = elect_one();
-      const uint32_t idesc0 = F8 ? idesc_mxf8_e4m3(256, 256) : idesc_16(256, 256, g.type == kBF16, AMN, BMN);
+      const uint32_t idesc1 = (F8 ? idesc_mxf8_e4m3(256, 0) : idesc_16(256, 0, g.type == kBF16, false, false)) |
+                              ((uint32_t)(BN >> 3) << 17);
       int stage = 0;
       uint32_t phase = 0, group = 0;
       // (the next stage is probed while this one's MMAs run)
@@ -347,12 +384,19 @@ __global__ void __launch_bounds__(kDThreads, 1)
       bool ready = probe(0, 0);
       int i = 0;  // tiles so far
       for (int u = pair0; u < g.units; u += pairs, ++i) {
+        int m, n;
+        const PairProblem& p = tile(u, m, n);
+        const int KB = (p.K + kStep - 1) / kStep;
+        const bool amn = !F8 && p.amn, bmn = !F8 && p.bmn;
+        const uint32_t idesc0 = idesc1 | ((uint32_t)amn << 15) | ((uint32_t)bmn << 16);
+        const uint64_t step_a = amn ? 128 : 2, step_b = bmn ? 128 : 2;  // 16 K rows, or 32 bytes of a row
         const int b = i & 1;
-        // E4M3: every warp has left the tile before last, and the tile before the columns
+        // overlapping: every warp has left the tile before last, and the tile before the columns
         // that both buffers have; else the tile before last
-        if (!warp_wait<true>(smem_u32(&acce_bar[F8 ? 0 : b]), ((F8 ? i : i >> 1) & 1) ^ 1u, abort, g.status)) break;
+        if (!warp_wait<true>(smem_u32(&acce_bar[overlap ? 0 : b]), ((overlap ? i : i >> 1) & 1) ^ 1u, abort, g.status))
+          break;
         tc_fence_after();
-        const uint32_t acc = tmem + (b ? (F8 ? 192u : 256u) : 0u);
+        const uint32_t acc = tmem + (b ? acc_next : 0u);
         bool ok = true;
         uint32_t sf = 0, slot = 0;
         for (int kb = 0; kb < KB; ++kb) {
@@ -372,8 +416,8 @@ __global__ void __launch_bounds__(kDThreads, 1)
           }
           tc_fence_after();
           const uint32_t st = sbase + stage * kDStage;
-          const uint64_t ad = AMN ? sdesc_mn_sw128(st) : sdesc_k_sw128(st);
-          const uint64_t bd = BMN ? sdesc_mn_sw128(st + kDBytesA) : sdesc_k_sw128(st + kDBytesA);
+          const uint64_t ad = amn ? sdesc_mn_sw128(st) : sdesc_k_sw128(st);
+          const uint64_t bd = bmn ? sdesc_mn_sw128(st + kDBytesA) : sdesc_k_sw128(st + kDBytesA);
           if (one) {
             if (F8 && j == 0) {
               const uint32_t sp = sfbase + slot * kSfSlotBytes;
@@ -384,8 +428,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t add = (kb | k) != 0 ? 1u : 0u;
-              // 32 bytes along K inside the swizzle atom, or 16 K rows of 128 bytes
-              const uint64_t da = ad + (AMN ? 128 : 2) * k, db = bd + (BMN ? 128 : 2) * k;
+              const uint64_t da = ad + step_a * k, db = bd + step_b * k;
               if constexpr (F8)
                 tc_mma_mxf8_pair(acc, da, db, idesc0 | (j << 4) | (j << 29), sf, sf + 8, add);
               else
@@ -413,32 +456,33 @@ __global__ void __launch_bounds__(kDThreads, 1)
     // ------------------------------------------------------------ scales
     // Lane l holds the words of rows l, l + 32, l + 64, l + 96: 16 consecutive bytes of an
     // atom.  Rows past M have no scale (their sums are not stored).
-    const int KQ = (KB + 3) / 4, NB = (g.N + 127) / 128;
+    const PairProblem& p = g.p[0];
+    const int KB = p.K / kStep, KQ = (KB + 3) / 4, NB = (p.N + 127) / 128;
     uint32_t group = 0;
-    for (int u = pair0; u < g.units && !*abort; u += pairs) {
+    for (int u = pair0; u < g.units && !__any_sync(0xFFFFFFFFu, *abort); u += pairs) {
       int m, n;
       tile(u, m, n);
       const int64_t ra = (int64_t)m * 256 + rank * 128 + lane;
-      const int nb = 2 * n, nb1 = min(nb + 1, NB - 1);
       bool ok = true;
-      auto words = [&](int q, uint32_t (&w)[6]) {
+      auto words = [&](int q, uint32_t (&w)[12]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = ra + 32 * i < g.M ? scale_word(g.sa, ra + 32 * i, KB, q) : 0u;
-        w[4] = scale_word(g.sb, nb, KB, q);
-        w[5] = scale_word(g.sb, nb1, KB, q);
+        for (int i = 0; i < 4; ++i) w[i] = ra + 32 * i < p.M ? scale_word(g.sa, ra + 32 * i, KB, q) : 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)  // 32 columns are of one block of the matrix
+          w[4 + i] = 32 * i < BN ? scale_word(g.sb, min((n * BN + 32 * i) / 128, NB - 1), KB, q) : 0u;
       };
-      uint32_t w[6];
+      uint32_t w[12];
       words(0, w);
       for (int q = 0; q < KQ; ++q, ++group) {
         const uint32_t slot = group & (kSfSlots - 1);
-        if (!mbar_wait(smem_u32(&sfe_bar[slot]), ((group / kSfSlots) & 1u) ^ 1u, abort, g.status)) {
+        if (!warp_wait(smem_u32(&sfe_bar[slot]), ((group / kSfSlots) & 1u) ^ 1u, abort, g.status)) {
           ok = false;
           break;
         }
         uint8_t* sp = smem + PairSmem<F8>::kSf + slot * kSfSlotBytes + lane * 16;
         *reinterpret_cast<uint4*>(sp) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(sp + 512) = make_uint4(w[4], w[4], w[4], w[4]);
-        *reinterpret_cast<uint4*>(sp + 1024) = make_uint4(w[5], w[5], w[5], w[5]);
+        *reinterpret_cast<uint4*>(sp + 512) = make_uint4(w[4], w[5], w[6], w[7]);
+        *reinterpret_cast<uint4*>(sp + 1024) = make_uint4(w[8], w[9], w[10], w[11]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sff_bar[slot]), 0));
@@ -455,24 +499,24 @@ __global__ void __launch_bounds__(kDThreads, 1)
     int i = 0;
     for (int u = pair0; u < g.units; u += pairs, ++i) {
       int m, n;
-      tile(u, m, n);
-      const int b = i & 1;
-      const int64_t row0 = (int64_t)m * 256 + rank * 128 + q * 32;
-      const int rows = (int)max((int64_t)0, min((int64_t)32, g.M - row0));  // of this warp
+      const PairProblem& p = tile(u, m, n);
+      const int N = p.N, b = i & 1;
+      const int64_t row0 = (int64_t)m * 256 + rank * 128 + q * 32, ld = p.ld_out;
+      const int rows = (int)max((int64_t)0, min((int64_t)32, p.M - row0));  // of this warp
       const int ss = g.saved_f32 ? 4 : 2;
-      uint8_t* saved = reinterpret_cast<uint8_t*>(g.saved) + row0 * 2 * g.N * ss;
-      const int64_t saved_pitch = (int64_t)2 * g.N * ss;
+      uint8_t* saved = reinterpret_cast<uint8_t*>(g.saved) + row0 * 2 * N * ss;
+      const int64_t saved_pitch = (int64_t)2 * N * ss;
       auto fetch = [&](int up, int col) {  // gate to the first buffer, up to the second
-        fetch_saved(buf + 4096 * up, saved + ((int64_t)up * g.N + col) * ss, saved_pitch, rows, (g.N - col) * ss,
-                    g.saved_f32, lane);
+        fetch_saved(buf + 4096 * up, saved + ((int64_t)up * N + col) * ss, saved_pitch, rows, (N - col) * ss, g.saved_f32,
+                    lane);
       };
       if constexpr (EPI == kEpiGrad) {
-        fetch(0, n * 256 + half * 128);
-        fetch(1, n * 256 + half * 128);
+        fetch(0, n * BN + half * hb);
+        fetch(1, n * BN + half * hb);
       }
       if (!warp_wait(smem_u32(&accf_bar[b]), (i >> 1) & 1, abort, g.status)) break;
       tc_fence_after();
-      const uint32_t acc = tlane + (b ? (F8 ? 192u : 256u) : 0u);
+      const uint32_t acc = tlane + (b ? acc_next : 0u);
       auto release = [&](int bar) {
         tc_fence_before();
         __syncwarp();
@@ -481,86 +525,93 @@ __global__ void __launch_bounds__(kDThreads, 1)
       if constexpr (EPI == kEpiStore) {
         // the columns that both buffers have are the first one's last 64 and the second
         // one's first: their half drains them first, the other half has left the tile before
-        if (F8 && half == b) release(0);
+        if (overlap && half == b) release(0);
+        const int groups = (hb + 63) / 64;
 #pragma unroll 1
-        for (int p = 0; p < 2; ++p) {
-          const int cc = half * 128 + (F8 && b == 0 ? p ^ 1 : p) * 64, col = n * 256 + cc, cols = g.N - col;
+        for (int k = 0; k < groups; ++k) {
+          const int cc = half * hb + (overlap && b == 0 ? k ^ 1 : k) * 64, width = min(64, half * hb + hb - cc);
+          const int col = n * BN + cc, cols = min(width, N - col);
           uint32_t r[2][32];
           tmem_ld32(acc + cc, r[0]);
-          tmem_ld32(acc + cc + 32, r[1]);
+          if (width > 32) tmem_ld32(acc + cc + 32, r[1]);
           tmem_ld_wait();
-          if (F8 ? p == 0 && half != b : p == 1) release(F8 ? 0 : b);
+          if (overlap ? k == 0 && half != b : k == groups - 1) release(overlap ? 0 : b);
           if (rows == 0 || cols <= 0) continue;
           float v[32];
-          if (g.out_f32) {
-            float* out = reinterpret_cast<float*>(g.out) + row0 * g.ld_out + col;
+          if (p.out_f32) {
+            float* out = reinterpret_cast<float*>(p.out) + row0 * ld + col;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+              const int left = cols - 32 * h;
+              if (left <= 0) break;
               as_floats(r[h], v);
               __syncwarp();
               put_f32(buf, lane, v);
               __syncwarp();
               uint8_t* dst = reinterpret_cast<uint8_t*>(out + 32 * h);
-              const int left = cols - 32 * h;
-              if (!g.vec)
-                flush_elements(smem + epi, out + 32 * h, g.ld_out, rows, left, lane);
-              else if (g.accumulate)
-                flush<128, true>(buf, dst, g.ld_out * 4, rows, left * 4, lane);
+              if (!p.vec)
+                flush_elements(smem + epi, out + 32 * h, ld, rows, left, lane);
+              else if (p.accumulate)
+                flush<128, true>(buf, dst, ld * 4, rows, left * 4, lane);
               else
-                flush<128>(buf, dst, g.ld_out * 4, rows, left * 4, lane);
+                flush<128>(buf, dst, ld * 4, rows, left * 4, lane);
             }
           } else {
             __syncwarp();
             as_floats(r[0], v);
             put_16<128>(buf, lane, 0, v, g.type);
-            as_floats(r[1], v);
-            put_16<128>(buf, lane, 4, v, g.type);
+            if (width > 32) {
+              as_floats(r[1], v);
+              put_16<128>(buf, lane, 4, v, g.type);
+            }
             __syncwarp();
-            uint16_t* out = reinterpret_cast<uint16_t*>(g.out) + row0 * g.ld_out + col;
-            if (g.vec)
-              flush<128>(buf, reinterpret_cast<uint8_t*>(out), g.ld_out * 2, rows, cols * 2, lane);
+            uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + row0 * ld + col;
+            if (p.vec)
+              flush<128>(buf, reinterpret_cast<uint8_t*>(out), ld * 2, rows, cols * 2, lane);
             else
-              flush_elements(smem + epi, out, g.ld_out, rows, cols, lane);
+              flush_elements(smem + epi, out, ld, rows, cols, lane);
           }
         }
       } else if constexpr (EPI == kEpiGate) {
-        const int col0 = n * 128 + half * 64;
+        // 32 columns at a time, in turn by the two halves
+        const int chunks = hb / 32;
+        if (half >= chunks) release(b);
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          const int cc = half * 64 + c * 32, col = col0 + c * 32;
+        for (int c = half; c < chunks; c += 2) {
+          const int cc = c * 32, col = n * hb + cc;
           uint32_t rg[32], ru[32];
           tmem_ld32(acc + cc, rg);
-          tmem_ld32(acc + 128 + cc, ru);
+          tmem_ld32(acc + hb + cc, ru);
           tmem_ld_wait();
-          if (c == 1) release(b);
+          if (c + 2 >= chunks) release(b);
           float gv[32], uv[32];
           as_floats(rg, gv);
           as_floats(ru, uv);
-          if (g.saved && rows && col < g.N) {
+          if (g.saved && rows && col < N) {
             __syncwarp();
-            const int bytes = (g.N - col) * ss;
+            const int bytes = (N - col) * ss;
             uint8_t* dst = saved + (int64_t)col * ss;
             if (g.saved_f32) {
               put_f32(buf, lane, gv);
               put_f32(buf + 4096, lane, uv);
               __syncwarp();
               flush<128>(buf, dst, saved_pitch, rows, bytes, lane);
-              flush<128>(buf + 4096, dst + (int64_t)g.N * 4, saved_pitch, rows, bytes, lane);
+              flush<128>(buf + 4096, dst + (int64_t)N * 4, saved_pitch, rows, bytes, lane);
             } else {
               put_16<64>(buf, lane, 0, gv, g.type);
               put_16<64>(buf + 4096, lane, 0, uv, g.type);
               __syncwarp();
               flush<64>(buf, dst, saved_pitch, rows, bytes, lane);
-              flush<64>(buf + 4096, dst + (int64_t)g.N * 2, saved_pitch, rows, bytes, lane);
+              flush<64>(buf + 4096, dst + (int64_t)N * 2, saved_pitch, rows, bytes, lane);
             }
           }
           gate_values(g.act, gv, uv);
-          if (rows && col < g.N) {
+          if (rows && col < N) {
             __syncwarp();
             put_16<64>(buf, lane, 0, uv, g.type);
             __syncwarp();
-            flush<64>(buf, reinterpret_cast<uint8_t*>(g.out) + (row0 * g.ld_out + col) * 2, g.ld_out * 2, rows,
-                      (g.N - col) * 2, lane);
+            flush<64>(buf, reinterpret_cast<uint8_t*>(p.out) + (row0 * ld + col) * 2, ld * 2, rows,
+                      (N - col) * 2, lane);
           }
         }
       } else {
@@ -568,40 +619,40 @@ __global__ void __launch_bounds__(kDThreads, 1)
         // finished: up at once, gate when its buffer, which dg and du and then h leave
         // through, is free.
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const int col = n * 256 + half * 128 + c * 32;
+        for (int c = 0; c < hb / 32; ++c) {
+          const int col = n * BN + half * hb + c * 32;
           asm volatile("cp.async.wait_all;" ::: "memory");
           __syncwarp();
           float gv[32], uv[32];
           get_saved(buf, lane, g.saved_f32, g.type, gv);
           get_saved(buf + 4096, lane, g.saved_f32, g.type, uv);
           __syncwarp();
-          if (c < 3) fetch(1, col + 32);
+          if (c < hb / 32 - 1) fetch(1, col + 32);
           uint32_t r[32];
-          tmem_ld32(acc + half * 128 + c * 32, r);
+          tmem_ld32(acc + half * hb + c * 32, r);
           tmem_ld_wait();
-          if (c == 3) release(b);
+          if (c == hb / 32 - 1) release(b);
           float hv[32];
           as_floats(r, hv);
           gradient_values(g.act, hv, gv, uv);
-          if (rows && col < g.N) {
-            const int bytes = (g.N - col) * 2;
+          if (rows && col < N) {
+            const int bytes = (N - col) * 2;
             put_16<64>(buf, lane, 0, gv, g.type);
             put_16<64>(buf + 2048, lane, 0, uv, g.type);
             __syncwarp();
-            uint8_t* dst = reinterpret_cast<uint8_t*>(g.dgu) + (row0 * 2 * g.N + col) * 2;
-            flush<64>(buf, dst, (int64_t)4 * g.N, rows, bytes, lane);
-            flush<64>(buf + 2048, dst + (int64_t)2 * g.N, (int64_t)4 * g.N, rows, bytes, lane);
-            if (g.out) {
+            uint8_t* dst = reinterpret_cast<uint8_t*>(g.dgu) + (row0 * 2 * N + col) * 2;
+            flush<64>(buf, dst, (int64_t)4 * N, rows, bytes, lane);
+            flush<64>(buf + 2048, dst + (int64_t)2 * N, (int64_t)4 * N, rows, bytes, lane);
+            if (p.out) {
               __syncwarp();
               put_16<64>(buf, lane, 0, hv, g.type);
               __syncwarp();
-              flush<64>(buf, reinterpret_cast<uint8_t*>(g.out) + (row0 * g.ld_out + col) * 2, g.ld_out * 2, rows, bytes,
+              flush<64>(buf, reinterpret_cast<uint8_t*>(p.out) + (row0 * ld + col) * 2, ld * 2, rows, bytes,
                         lane);
             }
           }
           __syncwarp();
-          if (c < 3) fetch(0, col + 32);
+          if (c < hb / 32 - 1) fetch(0, col + 32);
         }
       }
     }
@@ -642,25 +693,21 @@ static bool encode_map(CUtensorMap* map, const DenseOperand& o, int K, DenseType
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool F8, bool AMN, bool BMN, DenseEpi EPI>
-static cudaError_t launch_pair(const CUtensorMap& a, const CUtensorMap& b, const DenseArgs& g, int ctas,
-                               cudaStream_t s) {
+template <bool F8, DenseEpi EPI>
+static cudaError_t launch_pair(const PairArgs& g, int pairs, cudaStream_t s) {
   cudaLaunchAttribute c;
   c.id = cudaLaunchAttributeClusterDimension;
   c.val.clusterDim.x = 2;
   c.val.clusterDim.y = 1;
   c.val.clusterDim.z = 1;
-  return launch_k(dense_pair_kernel<F8, AMN, BMN, EPI>, dim3(ctas), dim3(kDThreads), PairSmem<F8>::kBytes, s, true, &c, a, b, g);
+  return launch_k(dense_pair_kernel<F8, EPI>, dim3(2 * (g.units < pairs ? g.units : pairs)), dim3(kDThreads),
+                  PairSmem<F8>::kBytes, s, true, &c, g);
 }
 
 cudaError_t dense_set_attributes() {
-  const void* ks[6] = {(const void*)dense_pair_kernel<true, false, false, kEpiStore>,
-                       (const void*)dense_pair_kernel<false, false, false, kEpiGate>,
-                       (const void*)dense_pair_kernel<false, false, false, kEpiStore>,
-                       (const void*)dense_pair_kernel<false, false, true, kEpiGrad>,
-                       (const void*)dense_pair_kernel<false, false, true, kEpiStore>,
-                       (const void*)dense_pair_kernel<false, true, true, kEpiStore>};
-  for (int i = 0; i < 6; ++i) {
+  const void* ks[4] = {(const void*)dense_pair_kernel<true, kEpiStore>, (const void*)dense_pair_kernel<false, kEpiStore>,
+                       (const void*)dense_pair_kernel<false, kEpiGate>, (const void*)dense_pair_kernel<false, kEpiGrad>};
+  for (int i = 0; i < 4; ++i) {
     const uint32_t bytes = i ? PairSmem<false>::kBytes : PairSmem<true>::kBytes;
     const cudaError_t e = cudaFuncSetAttribute(ks[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
@@ -668,16 +715,82 @@ cudaError_t dense_set_attributes() {
   return dense_split_set_attributes();
 }
 
-cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
+// The tiles' columns: the width whose fullest pair has the least to do.
+static int pair_columns(const DenseGemm* g, int count, int pairs) {
+  int best = 256;
+  double least = 0;
+  for (int BN = 256; BN >= 64; BN -= 64) {
+    double most = 0;
+    for (int p = 0; p < pairs; ++p) {
+      double load = 0;
+      int64_t first = 0;
+      for (int i = 0; i < count; ++i) {
+        const int64_t cols = g[i].epi == kEpiGate ? BN / 2 : BN;
+        const int64_t units = ((g[i].M + 255) / 256) * ((g[i].N + cols - 1) / cols);
+        const int KB = (g[i].K + (g[i].type == kE4M3 ? 127 : 63)) / (g[i].type == kE4M3 ? 128 : 64);
+        const int64_t mine = (first + units - p + pairs - 1) / pairs - (first - p + pairs - 1) / pairs;
+        load += (double)mine * (KB * (0.08 + 0.2 * BN / 256) + 0.4);
+        first += units;
+      }
+      if (load > most) most = load;
+    }
+    most += 3.0 * BN / 256;  // the last tile's epilogue
+    if (BN == 256 || most < least) {
+      least = most;
+      best = BN;
+    }
+  }
+  return best;
+}
+
+static cudaError_t pair_gemm(const DenseGemm* g, int count, int sms, cudaStream_t s) {
+  PairArgs d = {};
+  const int pairs = sms / 2, BN = pair_columns(g, count, pairs);
+  d.BN = BN;
+  for (int i = 0; i < count; ++i) {
+    PairProblem& p = d.p[i];
+    if (!encode_map(&p.a, g[i].a, g[i].K, g[i].type, 128) || !encode_map(&p.b, g[i].b, g[i].K, g[i].type, BN / 2))
+      return cudaErrorInvalidValue;
+    p.M = g[i].M;
+    p.N = g[i].N;
+    p.K = g[i].K;
+    const int cols = g[i].epi == kEpiGate ? BN / 2 : BN;
+    p.mt = (p.M + 255) / 256;
+    p.nt = (p.N + cols - 1) / cols;
+    d.units += p.mt * p.nt;
+    p.end = d.units;
+    p.amn = g[i].a.mn;
+    p.bmn = g[i].b.mn;
+    p.out_f32 = g[i].out_f32;
+    p.accumulate = g[i].accumulate;
+    p.vec = p.N % 8 == 0 && (uintptr_t)g[i].out % 16 == 0;
+    p.out = g[i].out;
+    p.ld_out = g[i].ld_out;
+  }
+  d.act = g->act;
+  d.type = g->type;
+  d.sa = g->sa;
+  d.sb = g->sb;
+  d.saved = g->saved;
+  d.saved_f32 = g->saved_f32;
+  d.dgu = g->dgu;
+  d.status = g->status;
+  if (g->type == kE4M3) return launch_pair<true, kEpiStore>(d, pairs, s);
+  if (g->epi == kEpiGate) return launch_pair<false, kEpiGate>(d, pairs, s);
+  if (g->epi == kEpiGrad) return launch_pair<false, kEpiGrad>(d, pairs, s);
+  return launch_pair<false, kEpiStore>(d, pairs, s);
+}
+
+static cudaError_t split_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
   CUtensorMap a, b;
+  DenseSplit p = dense_split_plan(g, sms);
+  p.early = g.early;
+  if (!encode_map(&a, g.a, g.K, g.type, p.NT) || !encode_map(&b, g.b, g.K, g.type, g.epi == kEpiGate ? 64 : 128))
+    return cudaErrorInvalidValue;
   DenseArgs d = {};
   d.M = g.M;
   d.N = g.N;
   d.K = g.K;
-  d.mt = (g.M + 255) / 256;
-  d.nt = g.epi == kEpiGate ? (g.N + 127) / 128 : (g.N + 255) / 256;
-  d.units = d.mt * d.nt;
-  d.epi = g.epi;
   d.act = g.act;
   d.type = g.type;
   d.sa = g.sa;
@@ -690,24 +803,16 @@ cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
   d.saved_f32 = g.saved_f32;
   d.dgu = g.dgu;
   d.status = g.status;
-  const uintptr_t at = (uintptr_t)g.out | (uintptr_t)g.saved | (uintptr_t)g.dgu;
-  d.vec = g.N % 8 == 0 && at % 16 == 0;
-  if (g.M <= 256) {
-    DenseSplit p = dense_split_plan(g, sms);
-    p.early = g.early;
-    if (!encode_map(&a, g.a, g.K, g.type, p.NT) ||
-        !encode_map(&b, g.b, g.K, g.type, g.epi == kEpiGate ? 64 : 128))
-      return cudaErrorInvalidValue;
-    return dense_split_launch(a, b, g, d, p, s);
-  }
-  if (!encode_map(&a, g.a, g.K, g.type, 128) || !encode_map(&b, g.b, g.K, g.type, 128)) return cudaErrorInvalidValue;
-  const int pairs = d.units < sms / 2 ? d.units : sms / 2;
-  if (g.type == kE4M3) return launch_pair<true, false, false, kEpiStore>(a, b, d, 2 * pairs, s);
-  if (g.epi == kEpiGate) return launch_pair<false, false, false, kEpiGate>(a, b, d, 2 * pairs, s);
-  if (g.epi == kEpiGrad) return launch_pair<false, false, true, kEpiGrad>(a, b, d, 2 * pairs, s);
-  if (g.a.mn) return launch_pair<false, true, true, kEpiStore>(a, b, d, 2 * pairs, s);
-  if (g.b.mn) return launch_pair<false, false, true, kEpiStore>(a, b, d, 2 * pairs, s);
-  return launch_pair<false, false, false, kEpiStore>(a, b, d, 2 * pairs, s);
+  d.vec = g.N % 8 == 0 && (uintptr_t)g.out % 16 == 0;
+  return dense_split_launch(a, b, g, d, p, s);
+}
+
+cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
+  return g.M <= 256 ? split_gemm(g, sms, s) : pair_gemm(&g, 1, sms, s);
+}
+
+cudaError_t dense_gemms(const DenseGemm* g, int count, int sms, cudaStream_t s) {
+  return pair_gemm(g, count, sms, s);
 }
 
 }  // namespace mm

@@ -123,8 +123,6 @@ __device__ __forceinline__ void gradient_values(DenseAct act, float (&dh)[N], fl
 
 struct DenseArgs {
   int M, N, K;
-  int units, mt, nt;       // tiles of 256 rows, of the columns (kEpiGate: 128 h columns)
-  DenseEpi epi;
   DenseAct act;
   DenseType type;
   const uint8_t *sa, *sb;

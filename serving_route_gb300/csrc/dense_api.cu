@@ -335,44 +335,28 @@ moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_
   g.dgu = h->dgu;
   g.status = h->status;
   if (dense_gemm(g, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
-  DenseGemm d = {};
-  d.type = h->type;
-  d.epi = kEpiStore;
-  d.status = h->status;
-  if (d_dx) {  // dx = dgu W1
-    d.a = {h->dgu, 2 * I, T, false};
-    d.b = {h->w1, H, H, true};
-    d.M = T;
-    d.N = H;
-    d.K = 2 * I;
-    d.out = d_dx;
-    d.ld_out = H;
-    d.early = true;  // the weights, unlike x and h below
-    if (dense_gemm(d, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
-  }
-  d.early = false;
-  d.out_f32 = dw_float32 != 0;
-  d.accumulate = accumulate != 0;
-  d.K = T;
-  if (d_dw1) {  // dgu^T x
-    d.a = {h->dgu, 2 * I, 2 * I, true};
-    d.b = {d_x, x_stride, H, true};
-    d.M = 2 * I;
-    d.N = H;
-    d.out = d_dw1;
-    d.ld_out = H;
-    if (dense_gemm(d, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
-  }
-  if (d_dw2) {  // dy^T h
-    d.a = {d_dy, dy_stride, H, true};
-    d.b = {h->h, I, I, true};
-    d.M = H;
-    d.N = I;
-    d.out = d_dw2;
-    d.ld_out = I;
-    if (dense_gemm(d, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
-  }
-  return MOE_OK;
+  // what these read the product above has written, or the caller
+  DenseGemm d[3] = {};
+  int count = 0;
+  auto add = [&](DenseOperand a, DenseOperand b, int M, int N, int K, void* out, bool weights) {
+    DenseGemm& p = d[count++];
+    p.a = a;
+    p.b = b;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.type = h->type;
+    p.epi = kEpiStore;
+    p.out = out;
+    p.ld_out = N;
+    p.out_f32 = weights && dw_float32;
+    p.accumulate = weights && accumulate;
+    p.status = h->status;
+  };
+  if (d_dx) add({h->dgu, 2 * I, T, false}, {h->w1, H, H, true}, T, H, 2 * I, d_dx, false);            // dgu W1
+  if (d_dw1) add({h->dgu, 2 * I, 2 * I, true}, {d_x, x_stride, H, true}, 2 * I, H, T, d_dw1, true);   // dgu^T x
+  if (d_dw2) add({d_dy, dy_stride, H, true}, {h->h, I, I, true}, H, I, T, d_dw2, true);               // dy^T h
+  return !count || dense_gemms(d, count, h->sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_mlp_read_status(moe_mlp_handle* h, uint32_t* h_status, struct CUstream_st* stream) {
