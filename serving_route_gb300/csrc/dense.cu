@@ -715,37 +715,40 @@ cudaError_t dense_set_attributes() {
   return dense_split_set_attributes();
 }
 
-// The tiles' columns: the width whose fullest pair has the least to do.
-static int pair_columns(const DenseGemm* g, int count, int pairs) {
-  int best = 256;
+// The tiles' columns: the width with which the fullest pair has the least to do, and its time in
+// microseconds.  By what was measured (one K block of 128 bytes 0.25 us with 64 or 128
+// columns, 0.30 with 256; start, first copies and last tile 4.6 us with 128 columns, 5.8 with
+// 256, with gate and gradient up to 8): 512 x 4096 x 2048 in E4M3 9.3 us with 128 columns, 10.0
+// with 256; 1021 x 4096 x 7168 46 and 25.
+static double pair_columns(const DenseGemm* g, int count, int pairs, int* columns) {
   double least = 0;
   for (int BN = 256; BN >= 64; BN -= 64) {
-    double most = 0;
-    for (int p = 0; p < pairs; ++p) {
-      double load = 0;
-      int64_t first = 0;
-      for (int i = 0; i < count; ++i) {
-        const int64_t cols = g[i].epi == kEpiGate ? BN / 2 : BN;
-        const int64_t units = ((g[i].M + 255) / 256) * ((g[i].N + cols - 1) / cols);
-        const int KB = (g[i].K + (g[i].type == kE4M3 ? 127 : 63)) / (g[i].type == kE4M3 ? 128 : 64);
-        const int64_t mine = (first + units - p + pairs - 1) / pairs - (first - p + pairs - 1) / pairs;
-        load += (double)mine * (KB * (0.08 + 0.2 * BN / 256) + 0.4);
-        first += units;
-      }
-      if (load > most) most = load;
+    const double w = BN / 256.0, block = 0.24 + 0.06 * w * w;
+    double sum = 0, one = 0;
+    int64_t units = 0;
+    for (int i = 0; i < count; ++i) {
+      const int cols = g[i].epi == kEpiGate ? BN / 2 : BN;
+      const int64_t n = (int64_t)((g[i].M + 255) / 256) * ((g[i].N + cols - 1) / cols);
+      const int KB = (g[i].K + (g[i].type == kE4M3 ? 127 : 63)) / (g[i].type == kE4M3 ? 128 : 64);
+      const double us = KB * block + 0.4;
+      units += n;
+      sum += n * us;
+      if (us > one) one = us;
     }
-    most += 3.0 * BN / 256;  // the last tile's epilogue
-    if (BN == 256 || most < least) {
-      least = most;
-      best = BN;
+    // one product: whole waves; several: their sum, and half a tile that does not fill up
+    double us = count == 1 ? (double)((units + pairs - 1) / pairs) * one : sum / pairs + 0.5 * one;
+    if (us < one) us = one;
+    us += 3.4 + (g->epi == kEpiStore ? 2.4 : 5.0) * w;
+    if (BN == 256 || us < least) {
+      least = us;
+      *columns = BN;
     }
   }
-  return best;
+  return least;
 }
 
-static cudaError_t pair_gemm(const DenseGemm* g, int count, int sms, cudaStream_t s) {
+static cudaError_t pair_gemm(const DenseGemm* g, int count, int BN, int pairs, cudaStream_t s) {
   PairArgs d = {};
-  const int pairs = sms / 2, BN = pair_columns(g, count, pairs);
   d.BN = BN;
   for (int i = 0; i < count; ++i) {
     PairProblem& p = d.p[i];
@@ -781,9 +784,8 @@ static cudaError_t pair_gemm(const DenseGemm* g, int count, int sms, cudaStream_
   return launch_pair<false, kEpiStore>(d, pairs, s);
 }
 
-static cudaError_t split_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
+static cudaError_t split_gemm(const DenseGemm& g, DenseSplit p, cudaStream_t s) {
   CUtensorMap a, b;
-  DenseSplit p = dense_split_plan(g, sms);
   p.early = g.early;
   if (!encode_map(&a, g.a, g.K, g.type, p.NT) || !encode_map(&b, g.b, g.K, g.type, g.epi == kEpiGate ? 64 : 128))
     return cudaErrorInvalidValue;
@@ -807,12 +809,22 @@ static cudaError_t split_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
   return dense_split_launch(a, b, g, d, p, s);
 }
 
+// Which kernel: the one that the measured times above say is faster; beyond 16 tiles of 128
+// tokens that is always the pair's.
 cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
-  return g.M <= 256 ? split_gemm(g, sms, s) : pair_gemm(&g, 1, sms, s);
+  int BN = 256;
+  const double pair_us = pair_columns(&g, 1, sms / 2, &BN);
+  if (g.M <= 16 * kSpMaxTokens) {
+    const DenseSplit p = dense_split_plan(g, sms);
+    if (p.us < pair_us) return split_gemm(g, p, s);
+  }
+  return pair_gemm(&g, 1, BN, sms / 2, s);
 }
 
 cudaError_t dense_gemms(const DenseGemm* g, int count, int sms, cudaStream_t s) {
-  return pair_gemm(g, count, sms, s);
+  int BN = 256;
+  pair_columns(g, count, sms / 2, &BN);
+  return pair_gemm(g, count, BN, sms / 2, s);
 }
 
 }  // namespace mm

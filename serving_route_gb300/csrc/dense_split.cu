@@ -2,14 +2,14 @@
 // small matrices.
 //
 // d^T[n, m] = sum_k b[n, k] a[m, k]: 128 rows of B (the weights) are the MMA's M operand and
-// NT <= 256 rows of A (the tokens, a multiple of 16) its N operand, so a K block of a tile
+// NT <= 128 rows of A (the tokens, a multiple of 16) its N operand, so a K block of a tile
 // costs 16 KB of weights and 128 NT bytes of tokens.  What bounds these products is the
 // weights' time, so every SM has to stream its share of them: the K blocks of a tile
 // are split over a cluster of up to 8 CTAs, each of which sums its share in tensor
 // memory.  The shares meet in the cluster's shared memory: every CTA leaves its FP32 sums in its
 // own, and after one cluster barrier each finishes every s-th token of the tile, adding
 // the shares in the order of the CTAs.  No workspace, no counters, no order that changes.
-// Two CTAs per SM (up to 128 tokens) overlap one's join with the other's stream.
+// Two CTAs per SM overlap one's join with the other's stream.
 // Warps: 0 loads, 1 MMAs, 2 scales, 4-7 drain the accumulator (thread = weight row); all
 // eight finish tokens (a lane has consecutive columns, so stores are whole lines).
 #include "dense.cuh"
@@ -20,7 +20,7 @@ constexpr int kSpThreads = 256;
 constexpr int kSpWarps = kSpThreads / 32;
 constexpr int kSpMaxStages = 8;
 constexpr uint32_t kSpW = 16384;            // 128 weight rows x 128 bytes
-constexpr uint32_t kSpSfBytes = 1536;       // weights' atom, two token atoms
+constexpr uint32_t kSpSfBytes = 1024;       // weights' atom, tokens' atom
 constexpr int kSpSfSlots = 4;
 constexpr uint32_t kSpSfCols = 16;
 
@@ -248,7 +248,6 @@ __global__ void __launch_bounds__(kSpThreads, 2)
           const uint32_t sp = smem_u32(sf_smem) + slot * kSpSfBytes;
           tc_cp_sf_atom(sf, sdesc_sf_atom(sp));
           tc_cp_sf_atom(sf + 8, sdesc_sf_atom(sp + 512));
-          if (p.NT > 128) tc_cp_sf_atom(sf + 12, sdesc_sf_atom(sp + 1024));
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -274,21 +273,20 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     // Lane l holds the words of rows l, l + 32, l + 64, l + 96 of an atom; a weight tile
     // is one block of the matrix, all its rows have the same word.
     const int64_t r0 = m0 + lane;
-    auto words = [&](int q, uint32_t (&w)[9]) {
+    auto words = [&](int q, uint32_t (&w)[5]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = lane + 32 * i < tokens ? scale_word(g.sa, r0 + 32 * i, KB, q) : 0u;
-      w[8] = scale_word(g.sb, jt, KB, q);
+      for (int i = 0; i < 4; ++i) w[i] = lane + 32 * i < tokens ? scale_word(g.sa, r0 + 32 * i, KB, q) : 0u;
+      w[4] = scale_word(g.sb, jt, KB, q);
     };
-    uint32_t w[9];
+    uint32_t w[5];
     const int q0 = kb0 >> 2, q1 = (kb1 + 3) >> 2;
     words(q0, w);
     for (int q = q0; q < q1; ++q) {
       const uint32_t group = q - q0, slot = group & (kSpSfSlots - 1);
       if (!mbar_wait(smem_u32(&sfe_bar[slot]), ((group / kSpSfSlots) & 1u) ^ 1u, abort, g.status)) break;
       uint8_t* sp = sf_smem + slot * kSpSfBytes + lane * 16;
-      *reinterpret_cast<uint4*>(sp) = make_uint4(w[8], w[8], w[8], w[8]);
+      *reinterpret_cast<uint4*>(sp) = make_uint4(w[4], w[4], w[4], w[4]);
       *reinterpret_cast<uint4*>(sp + 512) = make_uint4(w[0], w[1], w[2], w[3]);
-      if (p.NT > 128) *reinterpret_cast<uint4*>(sp + 1024) = make_uint4(w[4], w[5], w[6], w[7]);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sff_bar[slot]));
@@ -303,9 +301,20 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     if (ok && !*abort) {
       tc_fence_after();
       float* sums = reinterpret_cast<float*>(smem) + q * 32 + lane;
-      for (int c = 0; c < tokens; c += 16) {
+      const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+      int c = 0;
+      for (; c + 16 < tokens; c += 32) {
+        uint32_t r[2][16];
+        tmem_ld16(lanes + c, r[0]);
+        tmem_ld16(lanes + c + 16, r[1]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          sums[(c + k) * 128] = __uint_as_float(r[k / 16][k % 16]);
+      }
+      if (c < tokens) {
         uint32_t r[16];
-        tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, r);
+        tmem_ld16(lanes + c, r);
         tmem_ld_wait();
 #pragma unroll
         for (int k = 0; k < 16; ++k) sums[(c + k) * 128] = __uint_as_float(r[k]);
@@ -324,54 +333,75 @@ __global__ void __launch_bounds__(kSpThreads, 2)
   }
 
   // -------------------------------------------------------------- finish tokens
-  // This CTA's tokens are rank, rank + split, ...; a warp takes one at a time.
-  for (int t = rank + p.split * warp; t < tokens; t += p.split * kSpWarps) {
-    const int64_t m = m0 + t;
-    if constexpr (EPI == kEpiGate) {
-      const uint32_t at = sbase + (uint32_t)t * 512u + lane * 8u;
-      float gv[2] = {0.f, 0.f}, uv[2] = {0.f, 0.f};
-#pragma unroll 4
-      for (int c = 0; c < p.split; ++c) {
-        const uint32_t a = mapa_shared(at, c);
-        const float2 x = ld_cluster_v2(a), y = ld_cluster_v2(a + 256);
-        gv[0] += x.x, gv[1] += x.y, uv[0] += y.x, uv[1] += y.y;
+  // This CTA's tokens are rank, rank + split, ...: `mine` of them, in turn the warps'.  A warp
+  // takes up to four at a time, whose loads overlap.
+  const int mine = (tokens - rank + p.split - 1) / p.split;
+  const int col = EPI == kEpiGate ? jt * 64 + 2 * lane : jt * 128 + 4 * lane;
+  auto finish = [&](int i0, auto together) {
+    constexpr int kN = decltype(together)::value;
+    // a token's sums: columns 4 lane .. 4 lane + 3, or (kEpiGate) gate and up of h columns
+    // 2 lane, 2 lane + 1
+    uint32_t at[kN];
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+      at[j] = sbase + (uint32_t)(rank + p.split * (i0 + kSpWarps * j)) * 512u + lane * (EPI == kEpiGate ? 8u : 16u);
+    float v[kN][4] = {};
+#pragma unroll(kN == 1 ? 4 : 2)
+    for (int c = 0; c < p.split; ++c)
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const uint32_t a = mapa_shared(at[j], c);
+        float4 x;
+        if constexpr (EPI == kEpiGate) {
+          const float2 gx = ld_cluster_v2(a), ux = ld_cluster_v2(a + 256);
+          x = make_float4(gx.x, gx.y, ux.x, ux.y);
+        } else {
+          x = ld_cluster_v4(a);
+        }
+        v[j][0] += x.x, v[j][1] += x.y, v[j][2] += x.z, v[j][3] += x.w;
       }
-      const int col = jt * 64 + 2 * lane;
-      if (col >= g.N) continue;
-      if (g.saved) {
-        const int64_t s = m * 2 * g.N + col;
-        store_few(g.saved, s, col, g.N, gv, g.saved_f32, g.type, true);
-        store_few(g.saved, s + g.N, col, g.N, uv, g.saved_f32, g.type, true);
-      }
-      gate_values(g.act, gv, uv);
-      store_few(g.out, m * g.ld_out + col, col, g.N, uv, false, g.type, true);
-    } else {
-      const uint32_t at = sbase + (uint32_t)t * 512u + lane * 16u;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-      for (int c = 0; c < p.split; ++c) {
-        const float4 x = ld_cluster_v4(mapa_shared(at, c));
-        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-      }
-      const int col = jt * 128 + 4 * lane;
-      if (col >= g.N) continue;
-      if constexpr (EPI == kEpiStore) {
-        const int64_t o = m * g.ld_out + col;
+    if (col >= g.N) return;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const int64_t m = m0 + rank + p.split * (i0 + kSpWarps * j);
+      const int64_t o = m * g.ld_out + col, s = m * 2 * g.N + col;
+      if constexpr (EPI == kEpiGate) {
+        const float gv[2] = {v[j][0], v[j][1]};
+        float uv[2] = {v[j][2], v[j][3]};
+        if (g.saved) {
+          store_few(g.saved, s, col, g.N, gv, g.saved_f32, g.type, true);
+          store_few(g.saved, s + g.N, col, g.N, uv, g.saved_f32, g.type, true);
+        }
+        gate_values(g.act, gv, uv);
+        store_few(g.out, o, col, g.N, uv, false, g.type, true);
+      } else if constexpr (EPI == kEpiStore) {
         if (g.accumulate) {  // (float, whole vectors)
           const float4 old = load_four(g.out, o, true, g.type);
-          v[0] += old.x, v[1] += old.y, v[2] += old.z, v[3] += old.w;
+          v[j][0] += old.x, v[j][1] += old.y, v[j][2] += old.z, v[j][3] += old.w;
         }
-        store_few(g.out, o, col, g.N, v, g.out_f32, g.type, g.vec);
+        store_few(g.out, o, col, g.N, v[j], g.out_f32, g.type, g.vec);
       } else {
-        const int64_t s = m * 2 * g.N + col;
         const float4 gs = load_four(g.saved, s, g.saved_f32, g.type);
         const float4 us = load_four(g.saved, s + g.N, g.saved_f32, g.type);
         float gv[4] = {gs.x, gs.y, gs.z, gs.w}, uv[4] = {us.x, us.y, us.z, us.w};
-        gradient_values(g.act, v, gv, uv);
+        gradient_values(g.act, v[j], gv, uv);
         store_few(g.dgu, s, col, g.N, gv, false, g.type, true);
         store_few(g.dgu, s + g.N, col, g.N, uv, false, g.type, true);
-        if (g.out) store_few(g.out, m * g.ld_out + col, col, g.N, v, false, g.type, true);
+        if (g.out) store_few(g.out, o, col, g.N, v[j], false, g.type, true);
       }
+    }
+  };
+  for (int i = warp; i < mine;) {
+    const int left = (mine - i + kSpWarps - 1) / kSpWarps;  // tokens of this warp
+    if (left >= 4) {
+      finish(i, std::integral_constant<int, 4>{});
+      i += 4 * kSpWarps;
+    } else if (left >= 2) {
+      finish(i, std::integral_constant<int, 2>{});
+      i += 2 * kSpWarps;
+    } else {
+      finish(i, std::integral_constant<int, 1>{});
+      i += kSpWarps;
     }
   }
   if (p.split > 1) cluster_sync_all();  // the others have read this CTA's sums
@@ -403,31 +433,53 @@ cudaError_t dense_split_set_attributes() {
   return cudaSuccess;
 }
 
-// How a product is divided: tokens in equal tiles of at most 256, one or two CTAs per
-// SM by what their tiles take of shared and tensor memory, and as many shares of K as fill
-// them.
+// How a product is divided: tokens in equal tiles of at most 64 or 128, two CTAs per SM, K
+// in 1, 2, 4 or 8 shares (others did not do better: clusters of them fill the GPU's parts
+// unevenly).  By microseconds as measured (E4M3, 4096 x 7168, 32 tiles of 128 rows; K split by
+// 1 / 2 / 4 / 8): 1 token 18.4 / 11.1 / 7.4 / 6.8, 64 tokens 20.1 / 12.4 / 8.8 / 9.7, 128
+// tokens 22.5 / 14.2 / 11.1 / 14.0.  A K block of 128 bytes takes 0.26 us and more with
+// many tokens; start, drain and finish 3.4 us and 17 ns a token; the join through other CTAs'
+// shared memory 10 or 30 ns a token for 4 or 8 shares; where SMs have two CTAs each of
+// these takes longer.
 DenseSplit dense_split_plan(const DenseGemm& g, int sms) {
-  DenseSplit p = {};
-  const int unit = g.a.mn ? 64 : 16;
-  p.tt = (g.M + 255) / 256;
-  p.NT = ((g.M + p.tt - 1) / p.tt + unit - 1) / unit * unit;
-  p.tt = (g.M + p.NT - 1) / p.NT;
-  p.rt = g.epi == kEpiGate ? (g.N + 63) / 64 : (g.N + 127) / 128;
+  DenseSplit best = {};
   const bool f8 = g.type == kE4M3;
-  const int cols = p.NT + (f8 ? kSpSfSlots * kSpSfCols : 0);
-  p.tmem_cols = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
-  const int per_sm = p.NT <= 128 ? 2 : 1;  // (2 x 256 columns; above 76 KB each, so never three)
-  const uint32_t stage = kSpW + p.NT * 128, fixed = kSpSfSlots * kSpSfBytes + 1024;
-  const uint32_t room = per_sm == 2 ? 114 * 1024 : kSpMaxSmem;
-  p.stages = (int)((room - fixed) / stage);
-  if (p.stages > kSpMaxStages) p.stages = kSpMaxStages;
-  p.smem = p.stages * stage + fixed;
+  const int unit = g.a.mn ? 64 : 16;
   const int KB = (g.K + (f8 ? 127 : 63)) / (f8 ? 128 : 64);
-  const int64_t tiles = (int64_t)p.tt * p.rt;
-  int64_t split = (int64_t)sms * per_sm / tiles;
-  if (split > KB / 2) split = KB / 2;
-  p.split = split < 1 ? 1 : split > 8 ? 8 : (int)split;
-  return p;
+  const double stream_us = (double)g.N * g.K * (f8 ? 1 : 2) * (g.epi == kEpiGate ? 2 : 1) / 6.5e6;
+  for (int most = 64; most <= kSpMaxTokens; most *= 2) {
+    if (most > 64 && g.M <= most / 2) break;
+    DenseSplit p = {};
+    p.tt = (g.M + most - 1) / most;
+    p.NT = ((g.M + p.tt - 1) / p.tt + unit - 1) / unit * unit;
+    p.tt = (g.M + p.NT - 1) / p.NT;
+    p.rt = g.epi == kEpiGate ? (g.N + 63) / 64 : (g.N + 127) / 128;
+    const int64_t tiles = (int64_t)p.tt * p.rt;
+    for (int split = 1; split <= 8 && split <= KB; split *= 2) {
+      const int64_t ctas = tiles * split;
+      const bool shared = ctas > sms;
+      const double waves = (double)((ctas + 2 * sms - 1) / (2 * sms));
+      double block = 0.255 + 0.0004 * p.NT, join = p.NT * (split == 8 ? 0.03 : split == 4 ? 0.01 : 0.0);
+      double us = 3.4 + 0.017 * p.NT;
+      if (shared) block *= 1.13 + 0.003 * p.NT, join *= 1.6, us += 0.012 * p.NT;
+      us *= 0.5 + 0.5 * waves;  // (one's end overlaps another's start)
+      const double stream = block * ((KB + split - 1) / split) * waves;
+      us += join + (stream > stream_us ? stream : stream_us);
+      if (best.split && us >= best.us) continue;
+      best = p;
+      best.split = split;
+      best.us = us;
+    }
+  }
+  const int cols = best.NT + (f8 ? kSpSfSlots * (int)kSpSfCols : 0);
+  best.tmem_cols = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
+  // two CTAs per SM (above 76 KB each and with at most 256 columns, so never three, and
+  // two always find their tensor memory)
+  const uint32_t stage = kSpW + best.NT * 128, fixed = kSpSfSlots * kSpSfBytes + 1024;
+  best.stages = (int)((kSpMaxSmem - fixed) / stage);
+  if (best.stages > kSpMaxStages) best.stages = kSpMaxStages;
+  best.smem = best.stages * stage + fixed;
+  return best;
 }
 
 cudaError_t dense_split_launch(const CUtensorMap& a, const CUtensorMap& b, const DenseGemm& g, const DenseArgs& d,
