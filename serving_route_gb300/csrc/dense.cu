@@ -1,6 +1,8 @@
 // dense.cu -- the dense products beside the MoE layer: x W^T in the layer's FP8 format
 // (Fp8Linear) and the products of a gated feed-forward block and of its gradients
 // (GatedMlp).
+#include <algorithm>
+
 #include <cudaTypedefs.h>
 
 #include "dense.cuh"
@@ -56,9 +58,9 @@ cudaError_t dense_scales_to_e8m0(const float* s, int64_t n, uint8_t* out, uint32
 // ------------------------------------------------------------------------- products
 // d[m, n] = sum_k a[m, k] b[n, k] on CTA pairs (tcgen05 cta_group::2): a pair owns a tile of
 // 256 rows x BN columns, each CTA stages its 128 rows of A and half of B's rows, the
-// leader issues the MMAs and each CTA drains its own 128 rows.  Persistent: pair p takes
-// tiles p, p + pairs, ... of up to three products (the gradients of a block's input and
-// weights need only what one kernel before them wrote, and fill each other's last wave);
+// leader issues the MMAs and each CTA drains its own 128 rows.  Persistent: the pairs take
+// tiles in turn (PairArgs), of up to three products: the gradients of a block's input and
+// weights need only what one kernel before them wrote, and fill each other's last wave;
 // 8 row tiles share a sweep over the columns, so that what runs at one time reads few
 // distinct operand rows.  BN is 256, or 192, 128, 64 where the tiles are few (pair_columns).
 //   K-major operands (rows of K)      TMA boxes of rows x 128 bytes.
@@ -69,7 +71,7 @@ cudaError_t dense_scales_to_e8m0(const float* s, int64_t n, uint8_t* out, uint32
 //   rows) from the rows' and the matrix's E8M0 bytes, a slot ahead of the MMAs.
 // Accumulators: two of up to 256 TMEM columns in turn.  With scales in TMEM (64 columns) two
 // of 256 overlap by 64 columns, which the epilogue drains first.
-// Warps: 0 loads, 1 MMAs, 2 scales, 4-11 epilogue (two per TMEM lane quadrant, a half
+// Warps: 0 and 3 loads, 1 MMAs, 2 scales, 4-11 epilogue (two per TMEM lane quadrant, a half
 // of the columns each).
 constexpr int kDThreads = 384;
 constexpr int kDEpiWarps = 8;
@@ -227,9 +229,13 @@ struct PairProblem {
 
 constexpr int kPairProblems = 3;
 
+// The pairs take the `heavy` first tiles, those of the products with the longest K, in turn: pair
+// p tiles p, p + pairs, ...; `more` pairs then have one more of them than the others, which take
+// `light` of the remaining tiles each to be even, and the rest goes round again.
 struct PairArgs {
   PairProblem p[kPairProblems];
   int BN, units;
+  int heavy, more, light;
   DenseAct act;
   DenseType type;
   const uint8_t *sa, *sb;
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kDStages; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&full_bar[s]), 2);  // A and B
       mbar_init(smem_u32(&empty_bar[s]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -292,6 +298,20 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
   const int BN = g.BN, hb = BN / 2;     // (kEpiGate: hb columns of h, their gate and up)
   const bool overlap = F8 && BN > 192;  // the accumulators share columns
   const uint32_t acc_next = F8 ? 192u : 256u;
+  // the i-th unit of this pair, or `units`
+  auto unit = [&](int i) {
+    if (F8 || EPI != kEpiStore) return min(pair0 + i * pairs, g.units);
+    int u = pair0 + i * pairs;
+    if (u < g.heavy) return u;
+    i -= (g.heavy - pair0 + pairs - 1) / pairs;  // those it had of the heavy ones
+    const int others = pairs - g.more;
+    if (pair0 >= g.more) {
+      if (i < g.light) return min(g.heavy + pair0 - g.more + i * others, g.units);
+      i -= g.light;
+    }
+    const int first = pair0 - g.more + (pair0 < g.more ? pairs : 0);
+    return min(g.heavy + g.light * others + first + i * pairs, g.units);
+  };
   // unit u -> product, row and column tile
   auto tile = [&](int u, int& m, int& n) -> const PairProblem& {
     int i = 0;
@@ -306,42 +326,37 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
     return p;
   };
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ loads
-    const bool one = elect_one();
+    // A warp for each operand; both CTAs' copies of it complete on the leader's barrier.
+    const bool one = elect_one(), is_b = warp == 3;
     int stage = 0;
     uint32_t phase = 0, issued = 0, last_parity = 0;
-    for (int u = pair0; u < g.units && !__any_sync(0xFFFFFFFFu, *abort); u += pairs) {
+    for (int i = 0, u; (u = unit(i)) < g.units && !__any_sync(0xFFFFFFFFu, *abort); ++i) {
       int m, n;
       const PairProblem& p = tile(u, m, n);
       const int KB = (p.K + kStep - 1) / kStep;
-      const bool amn = p.amn, bmn = p.bmn;
-      const int ra = m * 256 + (int)rank * 128;
+      const CUtensorMap* map = is_b ? &p.b : &p.a;
+      const bool mn = !F8 && (is_b ? p.bmn : p.amn);
       // kEpiGate: the leader stages the gate rows, its peer the up rows
-      const int rb = EPI == kEpiGate ? n * hb + (rank ? p.N : 0) : n * BN + (int)rank * hb;
-      const uint32_t bytes = 2 * (kDBytesA + (bmn ? (hb + 63) / 64 * 8192 : hb * 128));
+      const int row = !is_b             ? m * 256 + (int)rank * 128
+                      : EPI == kEpiGate ? n * hb + (rank ? p.N : 0)
+                                        : n * BN + (int)rank * hb;
+      const int height = is_b ? hb : 128;
+      const bool two = mn && height > 64;
+      const uint32_t bytes = 2 * (mn ? (two ? 16384u : 8192u) : height * 128u), at = sbase + (is_b ? kDBytesA : 0u);
       bool ok = true;
       for (int kb = 0; kb < KB; ++kb) {
         if (!warp_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort, g.status)) {
           ok = false;
           break;
         }
-        const uint32_t st = sbase + stage * kDStage;
+        const uint32_t st = at + stage * kDStage;
         const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
         if (one) {
           if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), bytes);
-          if (!F8 && amn) {
-            tma_load_2d_pair(st, &p.a, fb, ra, kb * kStep);
-            tma_load_2d_pair(st + 8192, &p.a, fb, ra + 64, kb * kStep);
-          } else {
-            tma_load_2d_pair(st, &p.a, fb, kb * kStep, ra);
-          }
-          if (!F8 && bmn) {
-            tma_load_2d_pair(st + kDBytesA, &p.b, fb, rb, kb * kStep);
-            if (hb > 64) tma_load_2d_pair(st + kDBytesA + 8192, &p.b, fb, rb + 64, kb * kStep);
-          } else {
-            tma_load_2d_pair(st + kDBytesA, &p.b, fb, kb * kStep, rb);
-          }
+          tma_load_2d_pair(st, map, fb, mn ? row : kb * kStep, mn ? kb * kStep : row);
+          if (two) tma_load_2d_pair(st + 8192, map, fb, row + 64, kb * kStep);
         }
         issued |= 1u << stage;
         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
@@ -353,19 +368,17 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
       if (!ok) break;
     }
     // Every copy has landed before the CTAs leave (the leader's barriers count both CTAs'
-    // bytes); after an abort the peer also gives its last copies 100 us.
-    if (!leader && *abort) {
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 100000ull) {
-      }
-    }
+    // bytes); after an abort, when some may not have come, they get 100 us.
+    const uint64_t t0 = globaltimer_ns();
     if (leader) {
       for (int s = 0; s < kDStages; ++s) {
         if (!(issued & (1u << s))) continue;
-        const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(smem_u32(&full_bar[s]), (last_parity >> s) & 1u) &&
-               globaltimer_ns() - t0 < kWaitLimitNs) {
+               globaltimer_ns() - t0 < (*abort ? 100000ull : kWaitLimitNs)) {
         }
+      }
+    } else if (*abort) {
+      while (globaltimer_ns() - t0 < 100000ull) {
       }
     }
     __syncwarp();
@@ -382,8 +395,7 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
         return (bool)__all_sync(0xFFFFFFFFu, mbar_test_wait_cluster(smem_u32(&full_bar[s]), ph));
       };
       bool ready = probe(0, 0);
-      int i = 0;  // tiles so far
-      for (int u = pair0; u < g.units; u += pairs, ++i) {
+      for (int i = 0, u; (u = unit(i)) < g.units; ++i) {
         int m, n;
         const PairProblem& p = tile(u, m, n);
         const int KB = (p.K + kStep - 1) / kStep;
@@ -459,7 +471,7 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
     const PairProblem& p = g.p[0];
     const int KB = p.K / kStep, KQ = (KB + 3) / 4, NB = (p.N + 127) / 128;
     uint32_t group = 0;
-    for (int u = pair0; u < g.units && !__any_sync(0xFFFFFFFFu, *abort); u += pairs) {
+    for (int t = 0, u; (u = unit(t)) < g.units && !__any_sync(0xFFFFFFFFu, *abort); ++t) {
       int m, n;
       tile(u, m, n);
       const int64_t ra = (int64_t)m * 256 + rank * 128 + lane;
@@ -496,8 +508,7 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
     const uint32_t tlane = tmem + ((uint32_t)(q * 32) << 16);
     const uint32_t epi = PairSmem<F8>::kEpi + (uint32_t)(warp - 4) * PairSmem<F8>::kEpiWarp;
     const uint32_t buf = sbase + epi;
-    int i = 0;
-    for (int u = pair0; u < g.units; u += pairs, ++i) {
+    for (int i = 0, u; (u = unit(i)) < g.units; ++i) {
       int m, n;
       const PairProblem& p = tile(u, m, n);
       const int N = p.N, b = i & 1;
@@ -770,6 +781,11 @@ static cudaError_t pair_gemm(const DenseGemm* g, int count, int BN, int pairs, c
     p.out = g[i].out;
     p.ld_out = g[i].ld_out;
   }
+  // (the products come with the longest K first)
+  const int ctas = d.units < pairs ? d.units : pairs;
+  for (int i = 0; i < count && g[i].K == g[0].K; ++i) d.heavy = d.p[i].end;
+  d.more = d.heavy % ctas;
+  d.light = count > 1 && d.heavy < d.units ? (g[0].K + g[count - 1].K / 2) / g[count - 1].K : 0;
   d.act = g->act;
   d.type = g->type;
   d.sa = g->sa;
@@ -821,7 +837,8 @@ cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
   return pair_gemm(&g, 1, BN, sms / 2, s);
 }
 
-cudaError_t dense_gemms(const DenseGemm* g, int count, int sms, cudaStream_t s) {
+cudaError_t dense_gemms(DenseGemm* g, int count, int sms, cudaStream_t s) {
+  std::stable_sort(g, g + count, [](const DenseGemm& a, const DenseGemm& b) { return a.K > b.K; });
   int BN = 256;
   pair_columns(g, count, sms / 2, &BN);
   return pair_gemm(g, count, BN, sms / 2, s);

@@ -164,11 +164,8 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0u;
 }
 
-__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity));
-}
-
-// Bounded wait of a whole warp: all of its lanes go on, or none.
+// Bounded wait of a whole warp: all of its lanes go on, or none.  One lane polls: with all
+// of them the polling of a few warps slowed the others down.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
   return __all_sync(0xFFFFFFFFu, mbar_wait<CLUSTER>(bar, parity, abort, status));

@@ -46,8 +46,9 @@ struct DenseGemm {
 
 cudaError_t dense_set_attributes();  // of the kernels, on the current device
 cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s);
-// Up to three products of 16-bit operands (kEpiStore), of which none reads what another writes, in one launch.
-cudaError_t dense_gemms(const DenseGemm* g, int count, int sms, cudaStream_t s);
+// Up to three products of 16-bit operands (kEpiStore), of which none reads what another writes, in one launch
+// (sorts them).
+cudaError_t dense_gemms(DenseGemm* g, int count, int sms, cudaStream_t s);
 
 // x BF16 [T, cols] (rows ld elements apart) -> E4M3 codes [T, cols] and E8M0 bytes [T, cols / 128].
 cudaError_t dense_quantize_rows(const uint16_t* x, int64_t ld, int64_t T, int cols, uint8_t* q, uint8_t* s,

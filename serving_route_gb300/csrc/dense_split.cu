@@ -10,7 +10,7 @@
 // own, and after one cluster barrier each finishes every s-th token of the tile, adding
 // the shares in the order of the CTAs.  No workspace, no counters, no order that changes.
 // Two CTAs per SM overlap one's join with the other's stream.
-// Warps: 0 loads, 1 MMAs, 2 scales, 4-7 drain the accumulator (thread = weight row); all
+// Warps: 0 and 3 loads, 1 MMAs, 2 scales, 4-7 drain the accumulator (thread = weight row); all
 // eight finish tokens (a lane has consecutive columns, so stores are whole lines).
 #include "dense.cuh"
 
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&full_bar[s]), 2);  // weights and tokens
       mbar_init(smem_u32(&empty_bar[s]), 1);
     }
     for (int i = 0; i < kSpSfSlots; ++i) {
@@ -154,70 +154,60 @@ __global__ void __launch_bounds__(kSpThreads, 2)
   const int kb0 = (int)((int64_t)rank * KB / p.split), kb1 = (int)((int64_t)(rank + 1) * KB / p.split);
   const int n = kb1 - kb0;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ loads
-    auto weights = [&](int i, int st) {
-      const uint32_t dst = sbase + st * stage_bytes, fb = smem_u32(&full_bar[st]);
-      const int k = (kb0 + i) * kStep;
-      if (EPI == kEpiGate) {  // 64 gate rows, then their 64 up rows
-        tma_load_2d(dst, &tmB, fb, k, jt * 64);
-        tma_load_2d(dst + 8192, &tmB, fb, k, g.N + jt * 64);
-      } else if (BMN) {
-        tma_load_2d(dst, &tmB, fb, jt * 128, k);
-        tma_load_2d(dst + 8192, &tmB, fb, jt * 128 + 64, k);
-      } else {
-        tma_load_2d(dst, &tmB, fb, k, jt * 128);
-      }
-    };
-    auto rows = [&](int i, int st) {
-      const uint32_t dst = sbase + st * stage_bytes + kSpW, fb = smem_u32(&full_bar[st]);
-      const int k = (kb0 + i) * kStep;
-      if (AMN) {
-        for (int c = 0; c < p.NT; c += 64) tma_load_2d(dst + c * 128, &tmA, fb, m0 + c, k);
-      } else {
-        tma_load_2d(dst, &tmA, fb, k, m0);
-      }
-    };
-    // The kernel before wrote the tokens, but not the weights (`early`): their copies do
-    // not wait for it.
-    const int pre = p.early ? min(p.stages, n) : 0;
-    const bool one = elect_one();
-    if (one) {
-      for (int i = 0; i < pre; ++i) {
-        mbar_arrive_expect_tx(smem_u32(&full_bar[i]), stage_bytes);
-        weights(i, i);
-      }
-    }
+  // The kernel before in the stream wrote the tokens, but not the weights where they are
+  // `early`: their first loads do not wait for it.  (Beyond those the warp would only poll for
+  // empty places, at the cost of the CTAs that still run.)
+  if (warp != 0 || !p.early) {
     pdl_wait();
-    pdl_trigger();
-    if (one)
-      for (int i = 0; i < pre; ++i) rows(i, i);
-    int st = pre == p.stages ? 0 : pre, issued = pre;
-    uint32_t ph = pre == p.stages ? 0u : 1u;  // parity of the wait for an empty place
-    for (int i = pre; i < n; ++i) {
-      if (!warp_wait(smem_u32(&empty_bar[st]), ph, abort, g.status)) break;
-      if (one) {
-        mbar_arrive_expect_tx(smem_u32(&full_bar[st]), stage_bytes);
-        weights(i, st);
-        rows(i, st);
+    pdl_trigger();  // (any thread's counts for the CTA: not before its wait)
+  }
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------------ loads
+    // A warp for the weights, one for the tokens: wait, arrival and copy are a chain of
+    // some 350 clocks a K block with both in one.
+    const bool one = elect_one(), tokens_warp = warp == 3;
+    const uint32_t bytes = tokens_warp ? (uint32_t)p.NT * 128u : kSpW;
+    int st = 0, i = 0;
+    uint32_t ph = 1u;
+    for (; i < n; ++i) {
+      if (i >= p.stages) {  // (the first places are free)
+        if (i == p.stages && warp == 0 && p.early) pdl_wait();
+        if (!warp_wait(smem_u32(&empty_bar[st]), ph, abort, g.status)) break;
       }
-      issued = i + 1;
+      if (one) {
+        const uint32_t dst = sbase + st * stage_bytes + (tokens_warp ? kSpW : 0u), fb = smem_u32(&full_bar[st]);
+        const int k = (kb0 + i) * kStep;
+        mbar_arrive_expect_tx(fb, bytes);
+        if (tokens_warp) {
+          if (AMN) {
+            for (int c = 0; c < p.NT; c += 64) tma_load_2d(dst + c * 128, &tmA, fb, m0 + c, k);
+          } else {
+            tma_load_2d(dst, &tmA, fb, k, m0);
+          }
+        } else if (EPI == kEpiGate) {  // 64 gate rows, then their 64 up rows
+          tma_load_2d(dst, &tmB, fb, k, jt * 64);
+          tma_load_2d(dst + 8192, &tmB, fb, k, g.N + jt * 64);
+        } else if (BMN) {
+          tma_load_2d(dst, &tmB, fb, jt * 128, k);
+          tma_load_2d(dst + 8192, &tmB, fb, jt * 128 + 64, k);
+        } else {
+          tma_load_2d(dst, &tmB, fb, k, jt * 128);
+        }
+      }
       if (++st == p.stages) {
         st = 0;
         ph ^= 1u;
       }
     }
-    // every copy has landed before the CTA leaves
-    for (int i = max(0, issued - p.stages); i < issued; ++i) {
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(smem_u32(&full_bar[i % p.stages]), (i / p.stages) & 1) &&
-             globaltimer_ns() - t0 < kWaitLimitNs) {
+    if (i <= p.stages && warp == 0 && p.early) pdl_wait();
+    // Every copy has landed before the CTA leaves; after an abort, when one of the two may not
+    // have come, they get 100 us.
+    const uint64_t t0 = globaltimer_ns();
+    for (int k = max(0, i - p.stages); k < i; ++k)
+      while (!mbar_try_wait(smem_u32(&full_bar[k % p.stages]), (k / p.stages) & 1) &&
+             globaltimer_ns() - t0 < (*abort ? 100000ull : kWaitLimitNs)) {
       }
-    }
     __syncwarp();
-  } else {
-    pdl_wait();
-    pdl_trigger();
   }
   if (warp == 1) {
     // ------------------------------------------------------------ MMAs
@@ -228,7 +218,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     // (the next place is probed while this one's MMAs run)
     int st = 0;
     uint32_t ph = 0;
-    bool ready = warp_test(smem_u32(&full_bar[0]), 0);
+    bool ready = __all_sync(0xFFFFFFFFu, mbar_test_wait(smem_u32(&full_bar[0]), 0));
     for (int i = 0; i < n; ++i) {
       const uint32_t j = (uint32_t)(kb0 + i) & 3u;
       const bool fresh = F8 && (j == 0 || i == 0);
@@ -264,7 +254,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         st = 0;
         ph ^= 1u;
       }
-      ready = warp_test(smem_u32(&full_bar[st]), ph);
+      ready = __all_sync(0xFFFFFFFFu, mbar_test_wait(smem_u32(&full_bar[st]), ph));
     }
     if (one) tc_commit(smem_u32(&accf_bar));
     __syncwarp();
@@ -283,7 +273,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     words(q0, w);
     for (int q = q0; q < q1; ++q) {
       const uint32_t group = q - q0, slot = group & (kSpSfSlots - 1);
-      if (!mbar_wait(smem_u32(&sfe_bar[slot]), ((group / kSpSfSlots) & 1u) ^ 1u, abort, g.status)) break;
+      if (!warp_wait(smem_u32(&sfe_bar[slot]), ((group / kSpSfSlots) & 1u) ^ 1u, abort, g.status)) break;
       uint8_t* sp = sf_smem + slot * kSpSfBytes + lane * 16;
       *reinterpret_cast<uint4*>(sp) = make_uint4(w[4], w[4], w[4], w[4]);
       *reinterpret_cast<uint4*>(sp + 512) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -297,7 +287,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     // ------------------------------------------------------------ sums to shared memory
     // sums[token][row], over the ring: all its copies have been multiplied.
     const int q = warp & 3;
-    const bool ok = mbar_wait(smem_u32(&accf_bar), 0, abort, g.status);
+    const bool ok = warp_wait(smem_u32(&accf_bar), 0, abort, g.status);
     if (ok && !*abort) {
       tc_fence_after();
       float* sums = reinterpret_cast<float*>(smem) + q * 32 + lane;
@@ -437,8 +427,8 @@ cudaError_t dense_split_set_attributes() {
 // in 1, 2, 4 or 8 shares (others did not do better: clusters of them fill the GPU's parts
 // unevenly).  By microseconds as measured (E4M3, 4096 x 7168, 32 tiles of 128 rows; K split by
 // 1 / 2 / 4 / 8): 1 token 18.4 / 11.1 / 7.4 / 6.8, 64 tokens 20.1 / 12.4 / 8.8 / 9.7, 128
-// tokens 22.5 / 14.2 / 11.1 / 14.0.  A K block of 128 bytes takes 0.26 us and more with
-// many tokens; start, drain and finish 3.4 us and 17 ns a token; the join through other CTAs'
+// tokens 22.5 / 14.2 / 11.1 / 14.0.  A K block of 128 bytes takes 0.27 us, 0.39 with 128
+// tokens; start, drain and finish 3.4 us and 17 ns a token; the join through other CTAs'
 // shared memory 10 or 30 ns a token for 4 or 8 shares; where SMs have two CTAs each of
 // these takes longer.
 DenseSplit dense_split_plan(const DenseGemm& g, int sms) {
@@ -446,7 +436,7 @@ DenseSplit dense_split_plan(const DenseGemm& g, int sms) {
   const bool f8 = g.type == kE4M3;
   const int unit = g.a.mn ? 64 : 16;
   const int KB = (g.K + (f8 ? 127 : 63)) / (f8 ? 128 : 64);
-  const double stream_us = (double)g.N * g.K * (f8 ? 1 : 2) * (g.epi == kEpiGate ? 2 : 1) / 6.5e6;
+  const double bytes = (double)g.N * g.K * (f8 ? 1 : 2) * (g.epi == kEpiGate ? 2 : 1) * 1e-6;
   for (int most = 64; most <= kSpMaxTokens; most *= 2) {
     if (most > 64 && g.M <= most / 2) break;
     DenseSplit p = {};
@@ -459,10 +449,12 @@ DenseSplit dense_split_plan(const DenseGemm& g, int sms) {
       const int64_t ctas = tiles * split;
       const bool shared = ctas > sms;
       const double waves = (double)((ctas + 2 * sms - 1) / (2 * sms));
-      double block = 0.255 + 0.0004 * p.NT, join = p.NT * (split == 8 ? 0.03 : split == 4 ? 0.01 : 0.0);
+      double block = 0.25 + 0.0011 * p.NT, join = p.NT * (split == 8 ? 0.03 : split == 4 ? 0.01 : 0.0);
       double us = 3.4 + 0.017 * p.NT;
       if (shared) block *= 1.13 + 0.003 * p.NT, join *= 1.6, us += 0.012 * p.NT;
       us *= 0.5 + 0.5 * waves;  // (one's end overlaps another's start)
+      // (fewer CTAs have less in flight than the memory needs)
+      const double rate = ctas < 144 ? 0.045 * ctas : 6.5, stream_us = bytes / rate;
       const double stream = block * ((KB + split - 1) / split) * waves;
       us += join + (stream > stream_us ? stream : stream_us);
       if (best.split && us >= best.us) continue;
