@@ -13,7 +13,7 @@ namespace mm {
 // One warp per 128 columns of a row: amax, the least power of two that brings it to at
 // most 448, codes.  x * 2^-e is exact (but below E4M3's range, where it rounds once).
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* x, int64_t ld, int64_t blocks, int kb,
-                                                            uint8_t* q, uint8_t* s) {
+                                                            int pitch, uint8_t* q, uint8_t* s) {
   const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* x, i
     const float inv = pow2_neg(e);
     *reinterpret_cast<uint32_t*>(q + b * 128 + lane * 4) =
         e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-    if (lane == 0) s[b] = (uint8_t)(e + 127);
+    if (lane == 0) s[t * pitch + c] = (uint8_t)(e + 127);
   }
 }
 
@@ -38,20 +38,24 @@ cudaError_t dense_quantize_rows(const uint16_t* x, int64_t ld, int64_t T, int co
                                 cudaStream_t stream) {
   const int64_t blocks = T * (cols / 128), ctas = (blocks + 7) / 8;
   return launch_k(quantize_rows_kernel, dim3((unsigned)(ctas < 152 * 8 ? ctas : 152 * 8)), dim3(256), 0, stream, true,
-                  nullptr, x, ld, blocks, cols / 128, q, s);
+                  nullptr, x, ld, blocks, cols / 128, scale_pitch(cols), q, s);
 }
 
-__global__ void scales_to_e8m0_kernel(const float* s, int64_t n, uint8_t* out, uint32_t* status) {
+__global__ void scales_to_e8m0_kernel(const float* s, int64_t n, int cols, int pitch, uint8_t* out,
+                                      uint32_t* status) {
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
     const uint32_t b = __float_as_uint(s[i]);
     const bool ok = b == 0x00400000u || ((b & 0x807FFFFFu) == 0u && b != 0u && b < 0x7F800000u);
     if (!ok) record_status(status, MOE_DEV_BAD_SCALE);
-    out[i] = (uint8_t)(b >> 23);  // 2^-127, subnormal, is byte 0
+    out[i / cols * pitch + i % cols] = (uint8_t)(b >> 23);  // 2^-127, subnormal, is byte 0
   }
 }
 
-cudaError_t dense_scales_to_e8m0(const float* s, int64_t n, uint8_t* out, uint32_t* status, cudaStream_t stream) {
-  scales_to_e8m0_kernel<<<(int)((n + 255) / 256 < 1024 ? (n + 255) / 256 : 1024), 256, 0, stream>>>(s, n, out, status);
+cudaError_t dense_scales_to_e8m0(const float* s, int64_t rows, int cols, int pitch, uint8_t* out, uint32_t* status,
+                                 cudaStream_t stream) {
+  const int64_t n = rows * cols;
+  scales_to_e8m0_kernel<<<(int)((n + 255) / 256 < 1024 ? (n + 255) / 256 : 1024), 256, 0, stream>>>(s, n, cols, pitch,
+                                                                                                out, status);
   return cudaGetLastError();
 }
 
@@ -143,35 +147,53 @@ __device__ __forceinline__ void put_16(uint32_t buf, int row, int first, const f
 // (whole pieces).  ADD: floats, added to what is there.
 template <int BYTES, bool ADD = false>
 __device__ __forceinline__ void flush(uint32_t buf, uint8_t* dst, int64_t pitch, int rows, int bytes, int lane) {
-  constexpr int kLanes = BYTES / 16, kRows = 32 / kLanes;
+  constexpr int kLanes = BYTES / 16, kRows = 32 / kLanes, kN = 32 / kRows;
   const int r0 = lane / kLanes, c = lane % kLanes;
-  if (16 * c >= bytes) return;
+  uint4 v[kN];  // (all read before the first is written: the reads' latency once)
 #pragma unroll
-  for (int i = 0; i < 32; i += kRows) {
-    const int r = i + r0;
-    if (r >= rows) break;
-    uint4 v = lds_piece(piece_at<BYTES>(buf, r, c));
-    uint4* p = reinterpret_cast<uint4*>(dst + r * pitch + 16 * c);
-    if (ADD) {
-      const float4 o = *reinterpret_cast<const float4*>(p);
-      v.x = __float_as_uint(__uint_as_float(v.x) + o.x);
-      v.y = __float_as_uint(__uint_as_float(v.y) + o.y);
-      v.z = __float_as_uint(__uint_as_float(v.z) + o.z);
-      v.w = __float_as_uint(__uint_as_float(v.w) + o.w);
+  for (int i = 0; i < kN; ++i) v[i] = lds_piece(piece_at<BYTES>(buf, i * kRows + r0, c));
+  if (16 * c >= bytes) return;
+  uint4* p = reinterpret_cast<uint4*>(dst + r0 * pitch + 16 * c);
+  const int64_t step = kRows * pitch / 16;
+  if (ADD) {
+    float4 o[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (i * kRows + r0 < rows) o[i] = *reinterpret_cast<const float4*>(p + i * step);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      v[i].x = __float_as_uint(__uint_as_float(v[i].x) + o[i].x);
+      v[i].y = __float_as_uint(__uint_as_float(v[i].y) + o[i].y);
+      v[i].z = __float_as_uint(__uint_as_float(v[i].z) + o[i].z);
+      v[i].w = __float_as_uint(__uint_as_float(v[i].w) + o[i].w);
     }
-    *p = v;
   }
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+    if (i * kRows + r0 < rows) p[i * step] = v[i];
 }
 
 // The same where rows begin anywhere: an element per lane.
 template <typename E>
 __device__ __forceinline__ void flush_elements(const uint8_t* buf, E* dst, int64_t ld, int rows, int cols, int lane) {
-  constexpr int kPer = 16 / sizeof(E);
-  for (int r = 0; r < rows; ++r)
+  constexpr int kPer = 16 / sizeof(E), kCols = 128 / sizeof(E) / 32;
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    E v[8][kCols];
 #pragma unroll
-    for (int c = lane; c < (int)(128 / sizeof(E)); c += 32)
-      if (c < cols)
-        dst[r * ld + c] = *reinterpret_cast<const E*>(buf + r * 128 + (((c / kPer) ^ (r & 7)) << 4) + c % kPer * sizeof(E));
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) {
+        const int c = lane + 32 * k;
+        v[r][k] = *reinterpret_cast<const E*>(buf + (r0 + r) * 128 + (((c / kPer) ^ r) << 4) + c % kPer * sizeof(E));
+      }
+    E* p = dst + r0 * ld + lane;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int k = 0; k < kCols; ++k)
+        if (r0 + r < rows && lane + 32 * k < cols) p[r * ld + 32 * k] = v[r][k];
+  }
 }
 
 // 32 columns of saved gate or up, asynchronously, zeros past the rows and columns.
@@ -239,6 +261,7 @@ struct PairArgs {
   DenseAct act;
   DenseType type;
   const uint8_t *sa, *sb;
+  int sa_pitch, sb_pitch;
   void* saved;
   bool saved_f32;
   void* dgu;
@@ -470,37 +493,49 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
     // atom.  Rows past M have no scale (their sums are not stored).
     const PairProblem& p = g.p[0];
     const int KB = p.K / kStep, KQ = (KB + 3) / 4, NB = (p.N + 127) / 128;
-    uint32_t group = 0;
-    for (int t = 0, u; (u = unit(t)) < g.units && !__any_sync(0xFFFFFFFFu, *abort); ++t) {
-      int m, n;
-      tile(u, m, n);
-      const int64_t ra = (int64_t)m * 256 + rank * 128 + lane;
-      bool ok = true;
-      auto words = [&](int q, uint32_t (&w)[12]) {
+    // The words of the next two groups of four K blocks are under way while one is written: a
+    // load's time is that of a group's MMAs.
+    struct Words {
+      uint32_t w[4], b[3];  // of the rows, and of the up to three blocks that the columns are of
+      int first;            // the tile's first column in its block, in groups of 32; -1: past the last tile
+    } even, odd;
+    int t = 0, q = 0, m = 0, n = 0, u = unit(0);
+    if (u < g.units) tile(u, m, n);
+    auto load = [&](Words& x) {
+      x.first = u < g.units ? n * BN % 128 / 32 : -1;
+      if (u >= g.units) return;
+      scale_words(g.sa, (int64_t)m * 256 + rank * 128 + lane, p.M, g.sa_pitch, KB, q, x.w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = ra + 32 * i < p.M ? scale_word(g.sa, ra + 32 * i, KB, q) : 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)  // 32 columns are of one block of the matrix
-          w[4 + i] = 32 * i < BN ? scale_word(g.sb, min((n * BN + 32 * i) / 128, NB - 1), KB, q) : 0u;
-      };
-      uint32_t w[12];
-      words(0, w);
-      for (int q = 0; q < KQ; ++q, ++group) {
-        const uint32_t slot = group & (kSfSlots - 1);
-        if (!warp_wait(smem_u32(&sfe_bar[slot]), ((group / kSfSlots) & 1u) ^ 1u, abort, g.status)) {
-          ok = false;
-          break;
-        }
-        uint8_t* sp = smem + PairSmem<F8>::kSf + slot * kSfSlotBytes + lane * 16;
-        *reinterpret_cast<uint4*>(sp) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(sp + 512) = make_uint4(w[4], w[5], w[6], w[7]);
-        *reinterpret_cast<uint4*>(sp + 1024) = make_uint4(w[8], w[9], w[10], w[11]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sff_bar[slot]), 0));
-        if (q + 1 < KQ) words(q + 1, w);
+      for (int i = 0; i < 3; ++i) x.b[i] = block_word(g.sb, min(n * BN / 128 + i, NB - 1), g.sb_pitch, q);
+      if (++q == KQ) {
+        q = 0;
+        if ((u = unit(++t)) < g.units) tile(u, m, n);
       }
-      if (!ok) break;
+    };
+    uint32_t group = 0;
+    auto emit = [&](const Words& x) {
+      const uint32_t slot = group & (kSfSlots - 1);
+      if (x.first < 0 || !warp_wait(smem_u32(&sfe_bar[slot]), ((group / kSfSlots) & 1u) ^ 1u, abort, g.status))
+        return false;
+      uint32_t c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = i + x.first < 4 ? x.b[0] : i + x.first < 8 ? x.b[1] : x.b[2];
+      uint8_t* sp = smem + PairSmem<F8>::kSf + slot * kSfSlotBytes + lane * 16;
+      *reinterpret_cast<uint4*>(sp) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+      *reinterpret_cast<uint4*>(sp + 512) = make_uint4(c[0], c[1], c[2], c[3]);
+      *reinterpret_cast<uint4*>(sp + 1024) = make_uint4(c[4], c[5], c[6], c[7]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sff_bar[slot]), 0));
+      ++group;
+      return true;
+    };
+    load(even);
+    load(odd);
+    while (emit(even)) {
+      load(even);
+      if (!emit(odd)) break;
+      load(odd);
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
@@ -790,6 +825,8 @@ static cudaError_t pair_gemm(const DenseGemm* g, int count, int BN, int pairs, c
   d.type = g->type;
   d.sa = g->sa;
   d.sb = g->sb;
+  d.sa_pitch = g->sa_pitch;
+  d.sb_pitch = scale_pitch(g->K);
   d.saved = g->saved;
   d.saved_f32 = g->saved_f32;
   d.dgu = g->dgu;
@@ -813,6 +850,8 @@ static cudaError_t split_gemm(const DenseGemm& g, DenseSplit p, cudaStream_t s) 
   d.type = g.type;
   d.sa = g.sa;
   d.sb = g.sb;
+  d.sa_pitch = g.sa_pitch;
+  d.sb_pitch = scale_pitch(g.K);
   d.out = g.out;
   d.ld_out = g.ld_out;
   d.out_f32 = g.out_f32;

@@ -126,6 +126,7 @@ struct DenseArgs {
   DenseAct act;
   DenseType type;
   const uint8_t *sa, *sb;
+  int sa_pitch, sb_pitch;
   void* out;
   int64_t ld_out;
   bool out_f32, accumulate, vec;  // vec: columns in pieces of 8, rows on 16-byte boundaries
@@ -202,15 +203,36 @@ __device__ __forceinline__ void unpack16(uint32_t v, DenseType t, float& lo, flo
   hi = t == kFP16 ? half_bits_to_float(v >> 16) : bf16_bits_to_float(v >> 16);
 }
 
-// Four K blocks' scale bytes of one row (0 past the last block).
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t row, int KB, int q) {
-  const uint8_t* p = s + row * KB + 4 * q;
-  if ((KB & 3) == 0 && ((uintptr_t)s & 3) == 0) return *reinterpret_cast<const uint32_t*>(p);
-  uint32_t w = 0;
+// Four K blocks' scale bytes of four rows, r, r + 32, r + 64, r + 96 (rows `pitch` bytes apart;
+// past the last of `rows` rows the last one's, past the last block anything).  Aligned words
+// only, all asked for before one is used: where rows begin within words, two for each row, of
+// which the second is the first again unless it holds a byte of the row.  (Not
+// by the read-only path: the kernel before may write them while this one has begun.)
+__device__ __forceinline__ void scale_words(const uint8_t* s, int64_t r, int64_t rows, int pitch, int KB, int q,
+                                            uint32_t (&w)[4]) {
+  const uint8_t* p[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (4 * q + j < KB) w |= (uint32_t)p[j] << (8 * j);
-  return w;
+  for (int i = 0; i < 4; ++i) p[i] = s + min(r + 32 * i, rows - 1) * pitch + 4 * q;
+  if (((uintptr_t)s & 3) == 0 && (pitch & 3) == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(p[i]);
+    return;
+  }
+  uint32_t off[4], lo[4], hi[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    off[i] = (uint32_t)(uintptr_t)p[i] & 3u;
+    const uint32_t* a = reinterpret_cast<const uint32_t*>(p[i] - off[i]);
+    lo[i] = *a;
+    hi[i] = a[off[i] && 4 * q + 4 - (int)off[i] < KB ? 1 : 0];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(lo[i], hi[i], 8 * off[i]);
+}
+
+// The same of one block of the matrix (whole words).
+__device__ __forceinline__ uint32_t block_word(const uint8_t* s, int64_t block, int pitch, int q) {
+  return __ldg(reinterpret_cast<const uint32_t*>(s + block * pitch) + q);
 }
 
 }  // namespace mm

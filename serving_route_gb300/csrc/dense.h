@@ -32,8 +32,9 @@ struct DenseGemm {
   DenseType type;
   DenseEpi epi;
   DenseAct act;
-  const uint8_t* sa;       // E4M3: E8M0 scales of a's rows [M, K / 128]
-  const uint8_t* sb;       // E4M3: E8M0 scales of b's blocks [ceil(N / 128), K / 128]
+  const uint8_t* sa;       // E4M3: E8M0 scales of a's rows [M, K / 128], rows sa_pitch bytes apart
+  const uint8_t* sb;       // E4M3: E8M0 scales of b's blocks [ceil(N / 128), scale_pitch(K)]
+  int sa_pitch;
   void* out;               // kEpiStore: y; else h [M, N] (kEpiGrad: or NULL)
   int64_t ld_out;
   bool out_f32, accumulate;
@@ -50,10 +51,13 @@ cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s);
 // (sorts them).
 cudaError_t dense_gemms(DenseGemm* g, int count, int sms, cudaStream_t s);
 
-// x BF16 [T, cols] (rows ld elements apart) -> E4M3 codes [T, cols] and E8M0 bytes [T, cols / 128].
+// Bytes from one row of E8M0 scales to the next where the library lays them out: whole words.
+constexpr int scale_pitch(int K) { return (K / 128 + 3) / 4 * 4; }
+// x BF16 [T, cols] (rows ld elements apart) -> E4M3 codes [T, cols] and E8M0 bytes [T, scale_pitch(cols)].
 cudaError_t dense_quantize_rows(const uint16_t* x, int64_t ld, int64_t T, int cols, uint8_t* q, uint8_t* s,
                                 cudaStream_t stream);
-// Power-of-two float scales to E8M0 bytes; others set MOE_DEV_BAD_SCALE in *status.
-cudaError_t dense_scales_to_e8m0(const float* s, int64_t n, uint8_t* out, uint32_t* status, cudaStream_t stream);
+// Power-of-two float scales [rows, cols] to E8M0 bytes (rows pitch apart); others set MOE_DEV_BAD_SCALE in *status.
+cudaError_t dense_scales_to_e8m0(const float* s, int64_t rows, int cols, int pitch, uint8_t* out, uint32_t* status,
+                                 cudaStream_t stream);
 
 }  // namespace mm

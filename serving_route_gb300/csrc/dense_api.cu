@@ -84,9 +84,9 @@ struct LinearLayout {
   size_t sb, xq, xs, bytes;
   LinearLayout(int rows, int cols, int64_t T) {
     sb = kAlign;
-    xq = sb + up((size_t)((rows + 127) / 128) * (cols / 128));
+    xq = sb + up((size_t)((rows + 127) / 128) * scale_pitch(cols));
     xs = xq + up((size_t)T * cols);
-    bytes = xs + up((size_t)T * (cols / 128)) + kAlign;
+    bytes = xs + up((size_t)T * scale_pitch(cols)) + kAlign;
   }
 };
 
@@ -100,7 +100,7 @@ struct MlpLayout {
 };
 
 moe_status linear_run(moe_fp8_linear_handle* h, const uint8_t* xq, const uint8_t* xs, int64_t T, void* y, bool f32,
-                      bool early, cudaStream_t s) {
+                      bool early, cudaStream_t s) {  // early: x was quantised within the call
   DenseGemm g = {};
   g.a = {xq, h->cols, (int)T, false};
   g.b = {h->codes, h->cols, h->rows, false};
@@ -111,6 +111,7 @@ moe_status linear_run(moe_fp8_linear_handle* h, const uint8_t* xq, const uint8_t
   g.epi = kEpiStore;
   g.sa = xs;
   g.sb = h->sb;
+  g.sa_pitch = early ? scale_pitch(h->cols) : h->cols / 128;
   g.out = y;
   g.ld_out = h->rows;
   g.out_f32 = f32;
@@ -151,7 +152,7 @@ moe_status moe_fp8_linear_create(int32_t rows, int32_t cols, int64_t max_tokens,
   uint32_t* status = reinterpret_cast<uint32_t*>(b);
   uint32_t bits = 0;
   if (cudaMemsetAsync(b, 0, kAlign, stream) != cudaSuccess ||
-      dense_scales_to_e8m0(d_scales, (int64_t)((rows + 127) / 128) * (cols / 128), b + l.sb, status, stream) !=
+      dense_scales_to_e8m0(d_scales, (rows + 127) / 128, cols / 128, scale_pitch(cols), b + l.sb, status, stream) !=
           cudaSuccess ||
       read_word(status, &bits, stream) != MOE_OK)
     return MOE_ERR_CUDA;

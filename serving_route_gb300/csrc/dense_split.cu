@@ -262,26 +262,33 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     // ------------------------------------------------------------ scales
     // Lane l holds the words of rows l, l + 32, l + 64, l + 96 of an atom; a weight tile
     // is one block of the matrix, all its rows have the same word.
-    const int64_t r0 = m0 + lane;
-    auto words = [&](int q, uint32_t (&w)[5]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = lane + 32 * i < tokens ? scale_word(g.sa, r0 + 32 * i, KB, q) : 0u;
-      w[4] = scale_word(g.sb, jt, KB, q);
+    struct Words {
+      uint32_t w[4], b;
+    } even;
+    const int q1 = (kb1 + 3) >> 2;
+    int q = kb0 >> 2;
+    auto load = [&](Words& x) {
+      if (q >= q1) return;
+      scale_words(g.sa, m0 + lane, g.M, g.sa_pitch, KB, q, x.w);
+      x.b = block_word(g.sb, jt, g.sb_pitch, q++);
     };
-    uint32_t w[5];
-    const int q0 = kb0 >> 2, q1 = (kb1 + 3) >> 2;
-    words(q0, w);
-    for (int q = q0; q < q1; ++q) {
-      const uint32_t group = q - q0, slot = group & (kSpSfSlots - 1);
-      if (!warp_wait(smem_u32(&sfe_bar[slot]), ((group / kSpSfSlots) & 1u) ^ 1u, abort, g.status)) break;
+    uint32_t group = 0;
+    const uint32_t groups = q1 - q;
+    auto emit = [&](const Words& x) {
+      const uint32_t slot = group & (kSpSfSlots - 1);
+      if (group == groups || !warp_wait(smem_u32(&sfe_bar[slot]), ((group / kSpSfSlots) & 1u) ^ 1u, abort, g.status))
+        return false;
       uint8_t* sp = sf_smem + slot * kSpSfBytes + lane * 16;
-      *reinterpret_cast<uint4*>(sp) = make_uint4(w[4], w[4], w[4], w[4]);
-      *reinterpret_cast<uint4*>(sp + 512) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(sp) = make_uint4(x.b, x.b, x.b, x.b);
+      *reinterpret_cast<uint4*>(sp + 512) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sff_bar[slot]));
-      if (q + 1 < q1) words(q + 1, w);
-    }
+      ++group;
+      return true;
+    };
+    load(even);
+    while (emit(even)) load(even);
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ sums to shared memory
