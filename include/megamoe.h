@@ -665,7 +665,9 @@ MOE_API void moe_fp4_destroy(moe_fp4_handle* h);
  * layer) with its gradients.  Handles as above: they bind device pointers and a
  * workspace that no other handle uses at the same time, calls of one handle do
  * not overlap on the GPU, and a call on another device than the handle's is
- * refused with MOE_ERR_INVALID_ARG.  Calls are asynchronous on `stream`,
+ * refused with MOE_ERR_INVALID_ARG.  flags: 0, or MOE_FLAG_WATCHDOG_TEST (every wait
+ * of the kernels is bounded by 1 s; here by 20 ms, and each kernel withholds one of its
+ * copies, so that the calls record MOE_DEV_TIMEOUT).  Calls are asynchronous on `stream`,
  * allocate nothing and can be captured in a CUDA graph.  num_tokens 0 is a
  * no-op (but see moe_mlp_backward); MOE_ERR_CAPACITY above max_tokens (at most 2^24).
  * ------------------------------------------------------------------------ */
@@ -686,8 +688,8 @@ typedef struct moe_fp8_linear_handle moe_fp8_linear_handle;
  */
 MOE_API moe_status moe_fp8_linear_workspace_query(int32_t rows, int32_t cols, int64_t max_tokens,
                                                   size_t* workspace_bytes);
-MOE_API moe_status moe_fp8_linear_create(int32_t rows, int32_t cols, int64_t max_tokens,
-                                         const uint8_t* d_codes, const float* d_scales,
+MOE_API moe_status moe_fp8_linear_create(int32_t rows, int32_t cols, uint32_t flags,
+                                         int64_t max_tokens, const uint8_t* d_codes, const float* d_scales,
                                          void* d_workspace, size_t workspace_bytes,
                                          struct CUstream_st* stream, moe_fp8_linear_handle** out);
 
@@ -739,7 +741,7 @@ typedef struct moe_mlp_handle moe_mlp_handle;
 MOE_API moe_status moe_mlp_workspace_query(int32_t hidden, int32_t inter, int64_t max_tokens,
                                            size_t* workspace_bytes);
 MOE_API moe_status moe_mlp_create(int32_t hidden, int32_t inter, int32_t fp16, int32_t activation,
-                                  int64_t max_tokens, const uint16_t* d_w1, const uint16_t* d_w2,
+                                  uint32_t flags, int64_t max_tokens, const uint16_t* d_w1, const uint16_t* d_w2,
                                   void* d_workspace, size_t workspace_bytes,
                                   struct CUstream_st* stream, moe_mlp_handle** out);
 

@@ -143,11 +143,12 @@ def lib() -> ctypes.CDLL:
         L.moe_fp4_destroy.argtypes = [vp]
         L.moe_fp4_destroy.restype = None
         L.moe_fp8_linear_workspace_query.argtypes = [i32, i32, i64, psz]
-        L.moe_fp8_linear_create.argtypes = [i32, i32, i64, vp, vp, vp, ctypes.c_size_t, vp, ctypes.POINTER(vp)]
+        L.moe_fp8_linear_create.argtypes = [i32, i32, u32, i64, vp, vp, vp, ctypes.c_size_t, vp, ctypes.POINTER(vp)]
         L.moe_fp8_linear.argtypes = [vp, vp, i64, i64, vp, i32, vp]
         L.moe_fp8_linear_quantized.argtypes = [vp, vp, vp, i64, vp, i32, vp]
         L.moe_mlp_workspace_query.argtypes = [i32, i32, i64, psz]
-        L.moe_mlp_create.argtypes = [i32, i32, i32, i32, i64, vp, vp, vp, ctypes.c_size_t, vp, ctypes.POINTER(vp)]
+        L.moe_mlp_create.argtypes = [i32, i32, i32, i32, u32, i64, vp, vp, vp, ctypes.c_size_t, vp,
+                                     ctypes.POINTER(vp)]
         L.moe_mlp_forward.argtypes = [vp, vp, i64, i64, vp, vp, i32, vp]
         L.moe_mlp_backward.argtypes = [vp, vp, i64, vp, i64, vp, i32, i64, vp, vp, vp, i32, i32, vp]
         for n in ("fp8_linear", "mlp"):
@@ -364,9 +365,9 @@ def moe_fp8_linear_workspace_query(rows, cols, max_tokens) -> int:
     return n.value
 
 
-def moe_fp8_linear_create(rows, cols, max_tokens, d_codes, d_scales, d_ws, ws_bytes, stream) -> int:
+def moe_fp8_linear_create(rows, cols, flags, max_tokens, d_codes, d_scales, d_ws, ws_bytes, stream) -> int:
     h = ctypes.c_void_p()
-    _check(lib().moe_fp8_linear_create(rows, cols, max_tokens, d_codes, d_scales, d_ws, ws_bytes, stream,
+    _check(lib().moe_fp8_linear_create(rows, cols, flags, max_tokens, d_codes, d_scales, d_ws, ws_bytes, stream,
                                        ctypes.byref(h)), "moe_fp8_linear_create")
     return h.value
 
@@ -401,9 +402,9 @@ def moe_mlp_workspace_query(hidden, inter, max_tokens) -> int:
     return n.value
 
 
-def moe_mlp_create(hidden, inter, fp16, activation, max_tokens, d_w1, d_w2, d_ws, ws_bytes, stream) -> int:
+def moe_mlp_create(hidden, inter, fp16, activation, flags, max_tokens, d_w1, d_w2, d_ws, ws_bytes, stream) -> int:
     h = ctypes.c_void_p()
-    _check(lib().moe_mlp_create(hidden, inter, fp16, activation, max_tokens, d_w1, d_w2, d_ws, ws_bytes, stream,
+    _check(lib().moe_mlp_create(hidden, inter, fp16, activation, flags, max_tokens, d_w1, d_w2, d_ws, ws_bytes, stream,
                                 ctypes.byref(h)), "moe_mlp_create")
     return h.value
 

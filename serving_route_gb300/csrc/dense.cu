@@ -266,6 +266,8 @@ struct PairArgs {
   bool saved_f32;
   void* dgu;
   uint32_t* status;
+  uint64_t wait_ns;  // limit of every wait
+  bool withhold;     // a test: one copy is never made, so that a wait runs out
 };
 
 template <bool F8, DenseEpi EPI>
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
       const uint32_t bytes = 2 * (mn ? (two ? 16384u : 8192u) : height * 128u), at = sbase + (is_b ? kDBytesA : 0u);
       bool ok = true;
       for (int kb = 0; kb < KB; ++kb) {
-        if (!warp_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort, g.status)) {
+        if (!warp_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort, g.status, g.wait_ns)) {
           ok = false;
           break;
         }
@@ -378,8 +380,11 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
         const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
         if (one) {
           if (leader) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), bytes);
-          tma_load_2d_pair(st, map, fb, mn ? row : kb * kStep, mn ? kb * kStep : row);
-          if (two) tma_load_2d_pair(st + 8192, map, fb, row + 64, kb * kStep);
+          // (withheld: the leader expects the bytes all the same)
+          if (!g.withhold || !is_b || blockIdx.x != 1 || i != 0 || kb != KB - 1) {
+            tma_load_2d_pair(st, map, fb, mn ? row : kb * kStep, mn ? kb * kStep : row);
+            if (two) tma_load_2d_pair(st + 8192, map, fb, row + 64, kb * kStep);
+          }
         }
         issued |= 1u << stage;
         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
       for (int s = 0; s < kDStages; ++s) {
         if (!(issued & (1u << s))) continue;
         while (!mbar_try_wait(smem_u32(&full_bar[s]), (last_parity >> s) & 1u) &&
-               globaltimer_ns() - t0 < (*abort ? 100000ull : kWaitLimitNs)) {
+               globaltimer_ns() - t0 < (*abort ? 100000ull : g.wait_ns)) {
         }
       }
     } else if (*abort) {
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
         const int b = i & 1;
         // overlapping: every warp has left the tile before last, and the tile before the columns
         // that both buffers have; else the tile before last
-        if (!warp_wait<true>(smem_u32(&acce_bar[overlap ? 0 : b]), ((overlap ? i : i >> 1) & 1) ^ 1u, abort, g.status))
+        if (!warp_wait<true>(smem_u32(&acce_bar[overlap ? 0 : b]), ((overlap ? i : i >> 1) & 1) ^ 1u, abort, g.status, g.wait_ns))
           break;
         tc_fence_after();
         const uint32_t acc = tmem + (b ? acc_next : 0u);
@@ -438,14 +443,14 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
           const uint32_t j = (uint32_t)kb & 3u;
           if (F8 && j == 0) {
             slot = group & (kSfSlots - 1);
-            if (!warp_wait<true>(smem_u32(&sff_bar[slot]), (group / kSfSlots) & 1u, abort, g.status)) {
+            if (!warp_wait<true>(smem_u32(&sff_bar[slot]), (group / kSfSlots) & 1u, abort, g.status, g.wait_ns)) {
               ok = false;
               break;
             }
             ++group;
             sf = tmem + kDTmemSf + slot * kDSfCols;
           }
-          if (!ready && !warp_wait<true>(smem_u32(&full_bar[stage]), phase, abort, g.status)) {
+          if (!ready && !warp_wait<true>(smem_u32(&full_bar[stage]), phase, abort, g.status, g.wait_ns)) {
             ok = false;
             break;
           }
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
       }
       if (one) tc_commit_pair(smem_u32(&drain_bar));
       const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(smem_u32(&drain_bar), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+      while (!mbar_try_wait(smem_u32(&drain_bar), 0) && globaltimer_ns() - t0 < g.wait_ns) {
       }
     }
     __syncwarp();
@@ -515,7 +520,7 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
     uint32_t group = 0;
     auto emit = [&](const Words& x) {
       const uint32_t slot = group & (kSfSlots - 1);
-      if (x.first < 0 || !warp_wait(smem_u32(&sfe_bar[slot]), ((group / kSfSlots) & 1u) ^ 1u, abort, g.status))
+      if (x.first < 0 || !warp_wait(smem_u32(&sfe_bar[slot]), ((group / kSfSlots) & 1u) ^ 1u, abort, g.status, g.wait_ns))
         return false;
       uint32_t c[8];
 #pragma unroll
@@ -560,7 +565,7 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
         fetch(0, n * BN + half * hb);
         fetch(1, n * BN + half * hb);
       }
-      if (!warp_wait(smem_u32(&accf_bar[b]), (i >> 1) & 1, abort, g.status)) break;
+      if (!warp_wait(smem_u32(&accf_bar[b]), (i >> 1) & 1, abort, g.status, g.wait_ns)) break;
       tc_fence_after();
       const uint32_t acc = tlane + (b ? acc_next : 0u);
       auto release = [&](int bar) {
@@ -715,6 +720,8 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------------- launches
+constexpr uint64_t kWithheldNs = 20000000ull;  // the limit under the watchdog's test
+
 static bool encode_map(CUtensorMap* map, const DenseOperand& o, int K, DenseType t, int box_rows) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
@@ -831,6 +838,8 @@ static cudaError_t pair_gemm(const DenseGemm* g, int count, int BN, int pairs, c
   d.saved_f32 = g->saved_f32;
   d.dgu = g->dgu;
   d.status = g->status;
+  d.wait_ns = g->withhold ? kWithheldNs : kWaitLimitNs;
+  d.withhold = g->withhold;
   if (g->type == kE4M3) return launch_pair<true, kEpiStore>(d, pairs, s);
   if (g->epi == kEpiGate) return launch_pair<false, kEpiGate>(d, pairs, s);
   if (g->epi == kEpiGrad) return launch_pair<false, kEpiGrad>(d, pairs, s);
@@ -860,6 +869,8 @@ static cudaError_t split_gemm(const DenseGemm& g, DenseSplit p, cudaStream_t s) 
   d.saved_f32 = g.saved_f32;
   d.dgu = g.dgu;
   d.status = g.status;
+  d.wait_ns = g.withhold ? kWithheldNs : kWaitLimitNs;
+  d.withhold = g.withhold;
   d.vec = g.N % 8 == 0 && (uintptr_t)g.out % 16 == 0;
   return dense_split_launch(a, b, g, d, p, s);
 }

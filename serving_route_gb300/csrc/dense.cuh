@@ -134,6 +134,8 @@ struct DenseArgs {
   bool saved_f32;
   void* dgu;
   uint32_t* status;
+  uint64_t wait_ns;  // limit of every wait
+  bool withhold;     // a test: one copy is never made, so that a wait runs out
 };
 
 // A product on clusters that share K (dense_split.cu).
@@ -168,8 +170,9 @@ __device__ __forceinline__ bool elect_one() {
 // Bounded wait of a whole warp: all of its lanes go on, or none.  One lane polls: with all
 // of them the polling of a few warps slowed the others down.
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait<CLUSTER>(bar, parity, abort, status));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status,
+                                          uint64_t limit_ns) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait<CLUSTER>(bar, parity, abort, status, limit_ns));
 }
 
 // Shared-memory descriptor of an MN-major operand with the 128-byte swizzle: 64 elements

@@ -42,6 +42,7 @@ struct DenseGemm {
   bool saved_f32;
   void* dgu;               // kEpiGrad: [M, 2N]
   uint32_t* status;
+  bool withhold;           // a test of the waits: one copy is never made
   bool early;              // the kernel before in the stream is of the same call and does not write b
 };
 

@@ -11,6 +11,7 @@ using namespace mm;
 struct moe_fp8_linear_handle {
   int rows, cols, device, sms;
   int64_t max_tokens;
+  bool withhold;
   const uint8_t* codes;
   uint32_t* status;
   uint8_t* sb;   // E8M0 scales of the weight blocks
@@ -23,6 +24,7 @@ struct moe_mlp_handle {
   DenseType type;
   DenseAct act;
   int64_t max_tokens;
+  bool withhold;
   const void *w1, *w2;
   uint32_t* status;
   void* h;       // [max_tokens, inter]
@@ -117,6 +119,7 @@ moe_status linear_run(moe_fp8_linear_handle* h, const uint8_t* xq, const uint8_t
   g.out_f32 = f32;
   g.early = early;
   g.status = h->status;
+  g.withhold = h->withhold;
   return dense_gemm(g, h->sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -135,7 +138,7 @@ moe_status moe_fp8_linear_workspace_query(int32_t rows, int32_t cols, int64_t ma
   return MOE_OK;
 }
 
-moe_status moe_fp8_linear_create(int32_t rows, int32_t cols, int64_t max_tokens, const uint8_t* d_codes,
+moe_status moe_fp8_linear_create(int32_t rows, int32_t cols, uint32_t flags, int64_t max_tokens, const uint8_t* d_codes,
                                  const float* d_scales, void* d_workspace, size_t workspace_bytes,
                                  struct CUstream_st* stream, moe_fp8_linear_handle** out) {
   if (!out) return MOE_ERR_INVALID_ARG;
@@ -143,6 +146,7 @@ moe_status moe_fp8_linear_create(int32_t rows, int32_t cols, int64_t max_tokens,
   size_t need = 0;
   moe_status st = moe_fp8_linear_workspace_query(rows, cols, max_tokens, &need);
   if (st != MOE_OK) return st;
+  if (flags & ~MOE_FLAG_WATCHDOG_TEST) return MOE_ERR_UNSUPPORTED;
   if (off(d_codes, 16) || off(d_scales, 4) || off(d_workspace, 16)) return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
   int dev = 0, sms = 0;
@@ -165,6 +169,7 @@ moe_status moe_fp8_linear_create(int32_t rows, int32_t cols, int64_t max_tokens,
   h->device = dev;
   h->sms = sms;
   h->max_tokens = max_tokens;
+  h->withhold = (flags & MOE_FLAG_WATCHDOG_TEST) != 0;
   h->codes = d_codes;
   h->status = status;
   h->sb = b + l.sb;
@@ -215,15 +220,15 @@ moe_status moe_mlp_workspace_query(int32_t hidden, int32_t inter, int64_t max_to
   return MOE_OK;
 }
 
-moe_status moe_mlp_create(int32_t hidden, int32_t inter, int32_t fp16, int32_t activation, int64_t max_tokens,
-                          const uint16_t* d_w1, const uint16_t* d_w2, void* d_workspace, size_t workspace_bytes,
+moe_status moe_mlp_create(int32_t hidden, int32_t inter, int32_t fp16, int32_t activation, uint32_t flags,
+                          int64_t max_tokens, const uint16_t* d_w1, const uint16_t* d_w2, void* d_workspace, size_t workspace_bytes,
                           struct CUstream_st* stream, moe_mlp_handle** out) {
   if (!out) return MOE_ERR_INVALID_ARG;
   *out = nullptr;
   size_t need = 0;
   moe_status st = moe_mlp_workspace_query(hidden, inter, max_tokens, &need);
   if (st != MOE_OK) return st;
-  if (activation != MOE_ACT_SILU && activation != MOE_ACT_GELU_TANH) return MOE_ERR_UNSUPPORTED;
+  if ((activation != MOE_ACT_SILU && activation != MOE_ACT_GELU_TANH) || (flags & ~MOE_FLAG_WATCHDOG_TEST)) return MOE_ERR_UNSUPPORTED;
   if (off(d_w1, 16) || off(d_w2, 16) || off(d_workspace, 16)) return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
   int dev = 0, sms = 0;
@@ -241,6 +246,7 @@ moe_status moe_mlp_create(int32_t hidden, int32_t inter, int32_t fp16, int32_t a
   h->type = fp16 ? kFP16 : kBF16;
   h->act = activation == MOE_ACT_SILU ? kSilu : kGeluTanh;
   h->max_tokens = max_tokens;
+  h->withhold = (flags & MOE_FLAG_WATCHDOG_TEST) != 0;
   h->w1 = d_w1;
   h->w2 = d_w2;
   h->status = reinterpret_cast<uint32_t*>(b);
@@ -277,6 +283,7 @@ moe_status moe_mlp_forward(moe_mlp_handle* h, const uint16_t* d_x, int64_t x_str
   g.saved = d_saved;
   g.saved_f32 = saved_float32 != 0;
   g.status = h->status;
+  g.withhold = h->withhold;
   if (dense_gemm(g, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
   DenseGemm d = {};
   d.a = {h->h, I, (int)num_tokens, false};
@@ -290,6 +297,7 @@ moe_status moe_mlp_forward(moe_mlp_handle* h, const uint16_t* d_x, int64_t x_str
   d.ld_out = H;
   d.early = true;
   d.status = h->status;
+  d.withhold = h->withhold;
   return dense_gemm(d, h->sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -335,6 +343,7 @@ moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_
   g.saved_f32 = saved_float32 != 0;
   g.dgu = h->dgu;
   g.status = h->status;
+  g.withhold = h->withhold;
   if (dense_gemm(g, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
   // what these read the product above has written, or the caller
   DenseGemm d[3] = {};
@@ -353,6 +362,7 @@ moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_
     p.out_f32 = weights && dw_float32;
     p.accumulate = weights && accumulate;
     p.status = h->status;
+    p.withhold = h->withhold;
   };
   if (d_dx) add({h->dgu, 2 * I, T, false}, {h->w1, H, H, true}, T, H, 2 * I, d_dx, false);            // dgu W1
   if (d_dw1) add({h->dgu, 2 * I, 2 * I, true}, {d_x, x_stride, H, true}, 2 * I, H, T, d_dw1, true);   // dgu^T x

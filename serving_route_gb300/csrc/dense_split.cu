@@ -172,13 +172,15 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     for (; i < n; ++i) {
       if (i >= p.stages) {  // (the first places are free)
         if (i == p.stages && warp == 0 && p.early) pdl_wait();
-        if (!warp_wait(smem_u32(&empty_bar[st]), ph, abort, g.status)) break;
+        if (!warp_wait(smem_u32(&empty_bar[st]), ph, abort, g.status, g.wait_ns)) break;
       }
       if (one) {
         const uint32_t dst = sbase + st * stage_bytes + (tokens_warp ? kSpW : 0u), fb = smem_u32(&full_bar[st]);
         const int k = (kb0 + i) * kStep;
         mbar_arrive_expect_tx(fb, bytes);
-        if (tokens_warp) {
+        if (g.withhold && tokens_warp && blockIdx.x == 0 && i == n - 1) {
+          // the bytes never come
+        } else if (tokens_warp) {
           if (AMN) {
             for (int c = 0; c < p.NT; c += 64) tma_load_2d(dst + c * 128, &tmA, fb, m0 + c, k);
           } else {
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     const uint64_t t0 = globaltimer_ns();
     for (int k = max(0, i - p.stages); k < i; ++k)
       while (!mbar_try_wait(smem_u32(&full_bar[k % p.stages]), (k / p.stages) & 1) &&
-             globaltimer_ns() - t0 < (*abort ? 100000ull : kWaitLimitNs)) {
+             globaltimer_ns() - t0 < (*abort ? 100000ull : g.wait_ns)) {
       }
     __syncwarp();
   }
@@ -224,11 +226,11 @@ __global__ void __launch_bounds__(kSpThreads, 2)
       const bool fresh = F8 && (j == 0 || i == 0);
       if (fresh) {
         slot = group & (kSpSfSlots - 1);
-        if (!warp_wait(smem_u32(&sff_bar[slot]), (group / kSpSfSlots) & 1u, abort, g.status)) break;
+        if (!warp_wait(smem_u32(&sff_bar[slot]), (group / kSpSfSlots) & 1u, abort, g.status, g.wait_ns)) break;
         ++group;
         sf = tmem + p.NT + slot * kSpSfCols;
       }
-      if (!ready && !warp_wait(smem_u32(&full_bar[st]), ph, abort, g.status)) break;
+      if (!ready && !warp_wait(smem_u32(&full_bar[st]), ph, abort, g.status, g.wait_ns)) break;
       tc_fence_after();
       const uint32_t wa = sbase + st * stage_bytes, ra = wa + kSpW;
       const uint64_t wd = BMN ? sdesc_mn_sw128(wa) : sdesc_k_sw128(wa);
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     const uint32_t groups = q1 - q;
     auto emit = [&](const Words& x) {
       const uint32_t slot = group & (kSpSfSlots - 1);
-      if (group == groups || !warp_wait(smem_u32(&sfe_bar[slot]), ((group / kSpSfSlots) & 1u) ^ 1u, abort, g.status))
+      if (group == groups || !warp_wait(smem_u32(&sfe_bar[slot]), ((group / kSpSfSlots) & 1u) ^ 1u, abort, g.status, g.wait_ns))
         return false;
       uint8_t* sp = sf_smem + slot * kSpSfBytes + lane * 16;
       *reinterpret_cast<uint4*>(sp) = make_uint4(x.b, x.b, x.b, x.b);
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     // ------------------------------------------------------------ sums to shared memory
     // sums[token][row], over the ring: all its copies have been multiplied.
     const int q = warp & 3;
-    const bool ok = warp_wait(smem_u32(&accf_bar), 0, abort, g.status);
+    const bool ok = warp_wait(smem_u32(&accf_bar), 0, abort, g.status, g.wait_ns);
     if (ok && !*abort) {
       tc_fence_after();
       float* sums = reinterpret_cast<float*>(smem) + q * 32 + lane;

@@ -52,7 +52,8 @@ class Fp8Linear(_Handle):
 
     _destroy = staticmethod(B.moe_fp8_linear_destroy)
 
-    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, *, max_tokens: int, stream=None):
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, *, max_tokens: int, watchdog_test: bool = False,
+                 stream=None):
         rows, cols = codes.shape
         n = B.moe_fp8_linear_workspace_query(rows, cols, max_tokens)
         dev = codes.get_device()
@@ -62,7 +63,8 @@ class Fp8Linear(_Handle):
         self.rows, self.cols, self.max_tokens = rows, cols, max_tokens
         self.codes = codes
         self.workspace = torch.empty(n, dtype=_U8, device=codes.device)
-        self.handle = B.moe_fp8_linear_create(rows, cols, max_tokens, codes.data_ptr(), scales.data_ptr(),
+        self.handle = B.moe_fp8_linear_create(rows, cols, B.MOE_FLAG_WATCHDOG_TEST if watchdog_test else 0,
+                                              max_tokens, codes.data_ptr(), scales.data_ptr(),
                                               self.workspace.data_ptr(), n,
                                               _current_stream(dev) if stream is None else _given_stream(stream, dev))
 
@@ -117,7 +119,7 @@ class GatedMlp(_Handle):
     _destroy = staticmethod(B.moe_mlp_destroy)
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, *, max_tokens: int, activation: str = "silu",
-                 stream=None):
+                 watchdog_test: bool = False, stream=None):
         H, I = w2.shape
         assert activation in _ACTS
         n = B.moe_mlp_workspace_query(H, I, max_tokens)
@@ -127,7 +129,8 @@ class GatedMlp(_Handle):
         self.H, self.I, self.max_tokens, self.dtype = H, I, max_tokens, dtype
         self.weights = (w1, w2)
         self.workspace = torch.empty(n, dtype=_U8, device=w1.device)
-        self.handle = B.moe_mlp_create(H, I, dtype is _F16, _ACTS[activation], max_tokens, w1.data_ptr(),
+        self.handle = B.moe_mlp_create(H, I, dtype is _F16, _ACTS[activation],
+                                       B.MOE_FLAG_WATCHDOG_TEST if watchdog_test else 0, max_tokens, w1.data_ptr(),
                                        w2.data_ptr(), self.workspace.data_ptr(), n,
                                        _current_stream(dev) if stream is None else _given_stream(stream, dev))
 
