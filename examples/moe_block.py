@@ -6,7 +6,7 @@ choice, routed experts and a shared expert, for a prompt and then token by token
 Few tokens (up to 16) run on the four-bit weights as they are stored, where
 reading them is all the time goes into; a prompt runs on the same weights
 requantised once to 128x128 FP8, and its layer takes the norm's 8-bit output as
-it is.  The few-token step is captured in a CUDA graph.  The weights are random, and
+it is, and its shared expert is one gated feed-forward block.  The few-token step is captured in a CUDA graph.  The weights are random, and
 the gate's are in NVFP4 like the others: a checkpoint that keeps its gate in BF16
 or float multiplies it by other means (y @ gate.t()), as the prompt does here.
 """
@@ -63,9 +63,10 @@ class MoEBlock:
         self.many = S.MegaMoELayer(hidden, inter, experts, top_k, max_rows=max_prompt, fuse_fc1=True)
         self.many.bind_weights(*S.MegaMoELayer.requantize_weights_nvfp4(*self.w1),
                                *S.MegaMoELayer.requantize_weights_nvfp4(*self.w2))
-        self.gate_bf16, self.up_bf16, self.down_bf16 = (
+        self.gate_bf16, up_bf16, down_bf16 = (
             dequantize(*w, dtype=torch.float32)[0].bfloat16()
             for w in (self.gate_w, self.shared_w1, self.shared_w2))
+        self.shared = S.GatedMlp(up_bf16, down_bf16, max_tokens=max_prompt)
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor):
         """(block output, new residual), BF16 [T, H]."""
@@ -74,12 +75,16 @@ class MoEBlock:
         logits = self.gate.forward(y, out_dtype=torch.float32) if few else (y @ self.gate_bf16.t()).float()
         idx, w = S.topk_route(logits, self.K, bias=self.bias, **self.route_args)
         out = self.few.forward(y, idx, w) if few else self.many.forward_quantized(q, s, idx, w)
-        g, u = (self.up.forward(y) if few else y @ self.up_bf16.t()).split(self.I, -1)
-        h = torch.nn.functional.silu(g) * u
-        return out + (self.down.forward(h) if few else h @ self.down_bf16.t()), r
+        if not few:
+            return out + self.shared.forward(y), r
+        g, u = self.up.forward(y).split(self.I, -1)
+        return out + self.down.forward(torch.nn.functional.silu(g) * u), r
 
     def status(self, few: bool):
-        return (self.few if few else self.many).read_status()
+        if few:
+            return self.few.read_status()
+        status = self.many.read_status()
+        return status if status != (0, 0) else self.shared.read_status()
 
     def forward_plain(self, x, residual, idx, w):
         """The same in float64, with the experts idx and weights w."""
