@@ -849,7 +849,7 @@ static cudaError_t pair_gemm(const DenseGemm* g, int count, int BN, int pairs, c
 static cudaError_t split_gemm(const DenseGemm& g, DenseSplit p, cudaStream_t s) {
   CUtensorMap a, b;
   p.early = g.early;
-  if (!encode_map(&a, g.a, g.K, g.type, p.NT) || !encode_map(&b, g.b, g.K, g.type, g.epi == kEpiGate ? 64 : 128))
+  if ((!g.x && !encode_map(&a, g.a, g.K, g.type, p.NT)) || !encode_map(&b, g.b, g.K, g.type, g.epi == kEpiGate ? 64 : 128))
     return cudaErrorInvalidValue;
   DenseArgs d = {};
   d.M = g.M;
@@ -861,6 +861,8 @@ static cudaError_t split_gemm(const DenseGemm& g, DenseSplit p, cudaStream_t s) 
   d.sb = g.sb;
   d.sa_pitch = g.sa_pitch;
   d.sb_pitch = scale_pitch(g.K);
+  d.x = g.x;
+  d.ldx = g.ldx;
   d.out = g.out;
   d.ld_out = g.ld_out;
   d.out_f32 = g.out_f32;
@@ -882,7 +884,7 @@ cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
   const double pair_us = pair_columns(&g, 1, sms / 2, &BN);
   if (g.M <= 16 * kSpMaxTokens) {
     const DenseSplit p = dense_split_plan(g, sms);
-    if (p.us < pair_us) return split_gemm(g, p, s);
+    if (p.us < pair_us || g.x) return split_gemm(g, p, s);
   }
   return pair_gemm(&g, 1, BN, sms / 2, s);
 }

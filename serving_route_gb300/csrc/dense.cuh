@@ -127,6 +127,8 @@ struct DenseArgs {
   DenseType type;
   const uint8_t *sa, *sb;
   int sa_pitch, sb_pitch;
+  const uint16_t* x;  // the tokens in BF16 (quantised on the way), rows ldx elements apart
+  int64_t ldx;
   void* out;
   int64_t ld_out;
   bool out_f32, accumulate, vec;  // vec: columns in pieces of 8, rows on 16-byte boundaries

@@ -8,6 +8,8 @@
 
 namespace mm {
 
+constexpr int kFusedTokens = 16;
+
 enum DenseType { kE4M3 = 0, kBF16 = 1, kFP16 = 2 };
 enum DenseAct { kSilu = 0, kGeluTanh = 1 };
 
@@ -35,6 +37,8 @@ struct DenseGemm {
   const uint8_t* sa;       // E4M3: E8M0 scales of a's rows [M, K / 128], rows sa_pitch bytes apart
   const uint8_t* sb;       // E4M3: E8M0 scales of b's blocks [ceil(N / 128), scale_pitch(K)]
   int sa_pitch;
+  const uint16_t* x;       // E4M3, up to kFusedTokens rows: a in BF16 instead, quantised on the way
+  int64_t ldx;
   void* out;               // kEpiStore: y; else h [M, N] (kEpiGrad: or NULL)
   int64_t ld_out;
   bool out_f32, accumulate;

@@ -101,26 +101,21 @@ struct MlpLayout {
   }
 };
 
-moe_status linear_run(moe_fp8_linear_handle* h, const uint8_t* xq, const uint8_t* xs, int64_t T, void* y, bool f32,
-                      bool early, cudaStream_t s) {  // early: x was quantised within the call
+DenseGemm linear_product(const moe_fp8_linear_handle* h, int64_t T, void* y, bool f32) {
   DenseGemm g = {};
-  g.a = {xq, h->cols, (int)T, false};
   g.b = {h->codes, h->cols, h->rows, false};
   g.M = (int)T;
   g.N = h->rows;
   g.K = h->cols;
   g.type = kE4M3;
   g.epi = kEpiStore;
-  g.sa = xs;
   g.sb = h->sb;
-  g.sa_pitch = early ? scale_pitch(h->cols) : h->cols / 128;
   g.out = y;
   g.ld_out = h->rows;
   g.out_f32 = f32;
-  g.early = early;
   g.status = h->status;
   g.withhold = h->withhold;
-  return dense_gemm(g, h->sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return g;
 }
 
 bool mlp_dims_ok(int32_t hidden, int32_t inter) {
@@ -188,9 +183,19 @@ moe_status moe_fp8_linear(moe_fp8_linear_handle* h, const uint16_t* d_x, int64_t
     return MOE_ERR_INVALID_ARG;
   const Span x(d_x, num_tokens, x_stride, h->cols, 2);
   if (x.meets(Span(d_y, num_tokens, h->rows, h->rows, y_float32 ? 4 : 2))) return MOE_ERR_INVALID_ARG;
-  if (dense_quantize_rows(d_x, x_stride, num_tokens, h->cols, h->xq, h->xs, stream) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  return linear_run(h, h->xq, h->xs, num_tokens, d_y, y_float32 != 0, true, stream);
+  DenseGemm g = linear_product(h, num_tokens, d_y, y_float32 != 0);
+  if (num_tokens <= kFusedTokens) {
+    g.x = d_x;
+    g.ldx = x_stride;
+  } else {
+    if (dense_quantize_rows(d_x, x_stride, num_tokens, h->cols, h->xq, h->xs, stream) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    g.a = {h->xq, h->cols, (int)num_tokens, false};
+    g.sa = h->xs;
+    g.sa_pitch = scale_pitch(h->cols);
+    g.early = true;
+  }
+  return dense_gemm(g, h->sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_fp8_linear_quantized(moe_fp8_linear_handle* h, const uint8_t* d_xq, const uint8_t* d_xq_scale,
@@ -203,7 +208,11 @@ moe_status moe_fp8_linear_quantized(moe_fp8_linear_handle* h, const uint8_t* d_x
   if (y.meets(Span(d_xq, num_tokens, h->cols, h->cols, 1)) ||
       y.meets(Span(d_xq_scale, num_tokens, h->cols / 128, h->cols / 128, 1)))
     return MOE_ERR_INVALID_ARG;
-  return linear_run(h, d_xq, d_xq_scale, num_tokens, d_y, y_float32 != 0, false, stream);
+  DenseGemm g = linear_product(h, num_tokens, d_y, y_float32 != 0);
+  g.a = {d_xq, h->cols, (int)num_tokens, false};
+  g.sa = d_xq_scale;
+  g.sa_pitch = h->cols / 128;
+  return dense_gemm(g, h->sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_fp8_linear_read_status(moe_fp8_linear_handle* h, uint32_t* h_status, struct CUstream_st* stream) {

@@ -10,6 +10,9 @@
 // own, and after one cluster barrier each finishes every s-th token of the tile, adding
 // the shares in the order of the CTAs.  No workspace, no counters, no order that changes.
 // Two CTAs per SM overlap one's join with the other's stream.
+// FUSE (E4M3, up to 16 tokens): the tokens come in BF16 and the CTAs quantise what they need of
+// them themselves, a warp for each ring place, straight into it: a kernel less before the
+// stream (4096 x 7168, one token: 8.6 -> 7.2 us), for 16 x 256 bytes a K block from L2.
 // Warps: 0 and 3 loads, 1 MMAs, 2 scales, 4-7 drain the accumulator (thread = weight row); all
 // eight finish tokens (a lane has consecutive columns, so stores are whole lines).
 #include "dense.cuh"
@@ -23,6 +26,7 @@ constexpr uint32_t kSpW = 16384;            // 128 weight rows x 128 bytes
 constexpr uint32_t kSpSfBytes = 1024;       // weights' atom, tokens' atom
 constexpr int kSpSfSlots = 4;
 constexpr uint32_t kSpSfCols = 16;
+constexpr int kSpFusedSlots = 7;  // more than ring places: a slot's MMAs are done when it comes again
 
 __device__ __forceinline__ void tc_mma_16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {
@@ -104,7 +108,45 @@ __device__ __forceinline__ float4 load_four(const void* base, int64_t at, bool f
   return v;
 }
 
-template <bool F8, bool AMN, bool BMN, DenseEpi EPI>
+// One K block of up to 16 tokens from BF16 to E4M3 with a power-of-two scale, as
+// quantize_rows_kernel's: to `rows` as TMA's 128-byte swizzle would leave it, and the scales to
+// an atom whose four bytes are alike.  Two lanes to a token, 64 columns each.
+__device__ __forceinline__ void quantize_block(const uint16_t* x, int64_t ld, int tokens, uint32_t rows, uint32_t atom) {
+  const int lane = threadIdx.x & 31, t = lane >> 1, h = lane & 1;
+  uint4 v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = t < tokens ? *reinterpret_cast<const uint4*>(x + t * ld + h * 64 + i * 8) : make_uint4(0u, 0u, 0u, 0u);
+  uint32_t m = v[0].x & 0x7FFF7FFFu;  // the larger of each pair's halves (a NaN only where all are)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[k] & 0x7FFF7FFFu));
+  }
+  asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(__shfl_xor_sync(0xFFFFFFFFu, m, 1)));
+  const int e = pow2_scale_exp(fmaxf(bf16_bits_to_float(m & 0xFFFFu), bf16_bits_to_float(m >> 16)));
+  const float inv = pow2_neg(e);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 u = v[2 * c + i];
+      q[2 * i] = e4m3x4(bf16_bits_to_float(u.x & 0xFFFFu) * inv, bf16_bits_to_float(u.x >> 16) * inv,
+                        bf16_bits_to_float(u.y & 0xFFFFu) * inv, bf16_bits_to_float(u.y >> 16) * inv);
+      q[2 * i + 1] = e4m3x4(bf16_bits_to_float(u.z & 0xFFFFu) * inv, bf16_bits_to_float(u.z >> 16) * inv,
+                            bf16_bits_to_float(u.w & 0xFFFFu) * inv, bf16_bits_to_float(u.w >> 16) * inv);
+    }
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(rows + t * 128 + (((4 * h + c) ^ (t & 7)) << 4)),
+                 "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3])
+                 : "memory");
+  }
+  if (h == 0)
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(atom + t * 16), "r"((uint32_t)(e + 127) * 0x01010101u) : "memory");
+}
+
+template <bool F8, bool AMN, bool BMN, DenseEpi EPI, bool FUSE>
 __global__ void __launch_bounds__(kSpThreads, 2)
     dense_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const DenseArgs g, const DenseSplit p) {
@@ -116,7 +158,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t stage_bytes = kSpW + (uint32_t)p.NT * 128u;
+  const uint32_t stage_bytes = kSpW + (uint32_t)p.NT * 128u + (FUSE ? kSpSfBytes : 0u);
   uint8_t* sf_smem = smem + p.stages * stage_bytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
@@ -161,7 +203,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     pdl_wait();
     pdl_trigger();  // (any thread's counts for the CTA: not before its wait)
   }
-  if (warp == 0 || warp == 3) {
+  if (warp == 0 || (warp == 3 && !FUSE)) {
     // ------------------------------------------------------------ loads
     // A warp for the weights, one for the tokens: wait, arrival and copy are a chain of
     // some 350 clocks a K block with both in one.
@@ -211,6 +253,24 @@ __global__ void __launch_bounds__(kSpThreads, 2)
       }
     __syncwarp();
   }
+  if (FUSE && warp >= 2) {
+    // ------------------------------------------------------------ tokens, quantised here
+    // A ring place is one warp's: a wait for its next use but one would take the parity of the
+    // use before for it.
+    const int st = warp - 2;
+    uint32_t ph = 1u;
+    for (int i = st; i < n && st < p.stages; i += p.stages, ph ^= 1u) {
+      if (i >= p.stages && !warp_wait(smem_u32(&empty_bar[st]), ph, abort, g.status, g.wait_ns)) break;
+      const uint32_t rows = sbase + st * stage_bytes + kSpW, atoms = rows + (uint32_t)p.NT * 128u;
+      const uint32_t b = g.sb[(int64_t)jt * g.sb_pitch + kb0 + i] * 0x01010101u;  // one for the tile's weights
+      quantize_block(g.x + m0 * g.ldx + (kb0 + i) * kStep, g.ldx, tokens, rows, atoms + 512u);
+      asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(atoms + lane * 16), "r"(b) : "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && !(g.withhold && blockIdx.x == 0 && i == n - 1)) mbar_arrive(smem_u32(&full_bar[st]));
+    }
+    __syncwarp();
+  }
   if (warp == 1) {
     // ------------------------------------------------------------ MMAs
     const bool one = elect_one();
@@ -223,7 +283,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     bool ready = __all_sync(0xFFFFFFFFu, mbar_test_wait(smem_u32(&full_bar[0]), 0));
     for (int i = 0; i < n; ++i) {
       const uint32_t j = (uint32_t)(kb0 + i) & 3u;
-      const bool fresh = F8 && (j == 0 || i == 0);
+      const bool fresh = F8 && !FUSE && (j == 0 || i == 0);
       if (fresh) {
         slot = group & (kSpSfSlots - 1);
         if (!warp_wait(smem_u32(&sff_bar[slot]), (group / kSpSfSlots) & 1u, abort, g.status, g.wait_ns)) break;
@@ -235,8 +295,12 @@ __global__ void __launch_bounds__(kSpThreads, 2)
       const uint32_t wa = sbase + st * stage_bytes, ra = wa + kSpW;
       const uint64_t wd = BMN ? sdesc_mn_sw128(wa) : sdesc_k_sw128(wa);
       const uint64_t rd = AMN ? sdesc_mn_sw128(ra) : sdesc_k_sw128(ra);
+      if (FUSE) sf = tmem + p.NT + (uint32_t)(i % kSpFusedSlots) * kSpSfCols;
       if (one) {
-        if (fresh) {
+        if (FUSE) {  // scales with every K block
+          tc_cp_sf_atom(sf, sdesc_sf_atom(ra + p.NT * 128));
+          tc_cp_sf_atom(sf + 8, sdesc_sf_atom(ra + p.NT * 128 + 512));
+        } else if (fresh) {
           const uint32_t sp = smem_u32(sf_smem) + slot * kSpSfBytes;
           tc_cp_sf_atom(sf, sdesc_sf_atom(sp));
           tc_cp_sf_atom(sf + 8, sdesc_sf_atom(sp + 512));
@@ -245,12 +309,12 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         for (int k = 0; k < 4; ++k) {
           const uint32_t add = (i | k) != 0 ? 1u : 0u;
           if constexpr (F8)
-            tc_mma_mxf8(tmem, wd + 2 * k, rd + 2 * k, idesc0 | (j << 4) | (j << 29), sf, sf + 8, add);
+            tc_mma_mxf8(tmem, wd + 2 * k, rd + 2 * k, FUSE ? idesc0 : idesc0 | (j << 4) | (j << 29), sf, sf + 8, add);
           else
             tc_mma_16(tmem, wd + (BMN ? 128 : 2) * k, rd + (AMN ? 128 : 2) * k, idesc0, add);
         }
         tc_commit(smem_u32(&empty_bar[st]));
-        if (F8 && (j == 3 || i == n - 1)) tc_commit(smem_u32(&sfe_bar[slot]));
+        if (F8 && !FUSE && (j == 3 || i == n - 1)) tc_commit(smem_u32(&sfe_bar[slot]));
       }
       if (++st == p.stages) {
         st = 0;
@@ -260,7 +324,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     }
     if (one) tc_commit(smem_u32(&accf_bar));
     __syncwarp();
-  } else if (F8 && warp == 2) {
+  } else if (F8 && !FUSE && warp == 2) {
     // ------------------------------------------------------------ scales
     // Lane l holds the words of rows l, l + 32, l + 64, l + 96 of an atom; a weight tile
     // is one block of the matrix, all its rows have the same word.
@@ -363,7 +427,8 @@ __global__ void __launch_bounds__(kSpThreads, 2)
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const int64_t m = m0 + rank + p.split * (i0 + kSpWarps * j);
-      const int64_t o = m * g.ld_out + col, s = m * 2 * g.N + col;
+      const int64_t o = m * g.ld_out + col;
+      [[maybe_unused]] const int64_t s = m * 2 * g.N + col;
       if constexpr (EPI == kEpiGate) {
         const float gv[2] = {v[j][0], v[j][1]};
         float uv[2] = {v[j][2], v[j][3]};
@@ -406,7 +471,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
   if (p.split > 1) cluster_sync_all();  // the others have read this CTA's sums
 }
 
-template <bool F8, bool AMN, bool BMN, DenseEpi EPI>
+template <bool F8, bool AMN, bool BMN, DenseEpi EPI, bool FUSE = false>
 static cudaError_t launch_split(const CUtensorMap& a, const CUtensorMap& b, const DenseArgs& g, const DenseSplit& p,
                                 cudaStream_t s) {
   cudaLaunchAttribute c;
@@ -414,17 +479,18 @@ static cudaError_t launch_split(const CUtensorMap& a, const CUtensorMap& b, cons
   c.val.clusterDim.x = p.split;
   c.val.clusterDim.y = 1;
   c.val.clusterDim.z = 1;
-  return launch_k(dense_split_kernel<F8, AMN, BMN, EPI>, dim3((unsigned)(p.split * p.tt * p.rt)), dim3(kSpThreads),
+  return launch_k(dense_split_kernel<F8, AMN, BMN, EPI, FUSE>, dim3((unsigned)(p.split * p.tt * p.rt)), dim3(kSpThreads),
                   p.smem, s, true, &c, a, b, g, p);
 }
 
 cudaError_t dense_split_set_attributes() {
-  const void* ks[6] = {(const void*)dense_split_kernel<true, false, false, kEpiStore>,
-                       (const void*)dense_split_kernel<false, false, false, kEpiGate>,
-                       (const void*)dense_split_kernel<false, false, false, kEpiStore>,
-                       (const void*)dense_split_kernel<false, false, true, kEpiGrad>,
-                       (const void*)dense_split_kernel<false, false, true, kEpiStore>,
-                       (const void*)dense_split_kernel<false, true, true, kEpiStore>};
+  const void* ks[7] = {(const void*)dense_split_kernel<true, false, false, kEpiStore, true>,
+                       (const void*)dense_split_kernel<true, false, false, kEpiStore, false>,
+                       (const void*)dense_split_kernel<false, false, false, kEpiGate, false>,
+                       (const void*)dense_split_kernel<false, false, false, kEpiStore, false>,
+                       (const void*)dense_split_kernel<false, false, true, kEpiGrad, false>,
+                       (const void*)dense_split_kernel<false, false, true, kEpiStore, false>,
+                       (const void*)dense_split_kernel<false, true, true, kEpiStore, false>};
   for (const void* k : ks) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpMaxSmem);
     if (e != cudaSuccess) return e;
@@ -472,19 +538,20 @@ DenseSplit dense_split_plan(const DenseGemm& g, int sms) {
       best.us = us;
     }
   }
-  const int cols = best.NT + (f8 ? kSpSfSlots * (int)kSpSfCols : 0);
+  const int cols = best.NT + (g.x ? kSpFusedSlots : f8 ? kSpSfSlots : 0) * (int)kSpSfCols;
   best.tmem_cols = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
   // two CTAs per SM (above 76 KB each and with at most 256 columns, so never three, and
   // two always find their tensor memory)
-  const uint32_t stage = kSpW + best.NT * 128, fixed = kSpSfSlots * kSpSfBytes + 1024;
+  const uint32_t stage = kSpW + best.NT * 128 + (g.x ? kSpSfBytes : 0u), fixed = kSpSfSlots * kSpSfBytes + 1024;
   best.stages = (int)((kSpMaxSmem - fixed) / stage);
-  if (best.stages > kSpMaxStages) best.stages = kSpMaxStages;
+  if (best.stages > (g.x ? kSpFusedSlots - 1 : kSpMaxStages)) best.stages = g.x ? kSpFusedSlots - 1 : kSpMaxStages;
   best.smem = best.stages * stage + fixed;
   return best;
 }
 
 cudaError_t dense_split_launch(const CUtensorMap& a, const CUtensorMap& b, const DenseGemm& g, const DenseArgs& d,
                                const DenseSplit& p, cudaStream_t s) {
+  if (g.x) return launch_split<true, false, false, kEpiStore, true>(b, b, d, p, s);
   if (g.type == kE4M3) return launch_split<true, false, false, kEpiStore>(a, b, d, p, s);
   if (g.epi == kEpiGate) return launch_split<false, false, false, kEpiGate>(a, b, d, p, s);
   if (g.epi == kEpiGrad) return launch_split<false, false, true, kEpiGrad>(a, b, d, p, s);

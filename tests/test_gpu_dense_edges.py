@@ -180,3 +180,23 @@ def test_linear_values_of_every_code(S):
         nan = want.isnan()
         # a NaN code makes its whole row one (0 * NaN); the others are single products
         assert torch.equal(y[~nan.any(1)], want[~nan.any(1)]) and y[nan.any(1)].isnan().all()
+
+
+@pytest.mark.parametrize("T", [1, 7, 16])
+@pytest.mark.parametrize("rows,cols", [(4096, 7168), (20000, 3968), (130, 32768), (9000, 16384)])
+def test_linear_few_tokens_long_rows(S, T, rows, cols):
+    """Many K blocks for each CTA: the ring goes round several times."""
+    codes, scales = weights8(rows, cols, seed=60)
+    lin = S.Fp8Linear(codes, scales, max_tokens=T)
+    x = rand(T, cols, seed=61)
+    xq, xs = ref.quantize_rows(x)
+    got = lin.forward(x)
+    ref.check(got, ref.linear(xq, xs, codes, scales, BF))
+    assert torch.equal(got, lin.forward_quantized(xq, xs))
+
+
+@pytest.mark.parametrize("T", [1, 12])
+@pytest.mark.parametrize("H,I", [(16384, 4096), (4096, 20000)])
+def test_mlp_few_tokens_long_rows(S, T, H, I):
+    w1, w2, x, mlp = mlp_case(S, T, H, I, BF, "silu", seed=70)
+    ref.check(mlp.forward(x), ref.forward(x, w1, w2, "silu", BF))
