@@ -286,11 +286,12 @@ constexpr int kPairProblems = 3;
 
 // The pairs take the `heavy` first tiles, those of the products with the longest K, in turn: pair
 // p tiles p, p + pairs, ...; `more` pairs then have one more of them than the others, which take
-// `light` of the remaining tiles each to be even, and the rest goes round again.
+// `light` of the remaining tiles each to be even, and the rest goes round again, from pair
+// `rest` on, the first that has less to do.
 struct PairArgs {
   PairProblem p[kPairProblems];
   int BN, units;
-  int heavy, more, light;
+  int heavy, more, light, rest;
   DenseAct act;
   DenseType type;
   const uint8_t *sa, *sb;
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
       if (i < g.light) return min(g.heavy + pair0 - g.more + i * others, g.units);
       i -= g.light;
     }
-    const int first = pair0 - g.more + (pair0 < g.more ? pairs : 0);
+    const int first = pair0 - g.rest + (pair0 < g.rest ? pairs : 0);
     return min(g.heavy + g.light * others + first + i * pairs, g.units);
   };
   // unit u -> product, row and column tile
@@ -861,6 +862,7 @@ static cudaError_t pair_gemm(const DenseGemm* g, int count, int BN, int pairs, c
   for (int i = 0; i < count && g[i].K == g[0].K; ++i) d.heavy = d.p[i].end;
   d.more = d.heavy % ctas;
   d.light = count > 1 && d.heavy < d.units ? (g[0].K + g[count - 1].K / 2) / g[count - 1].K : 0;
+  d.rest = (int64_t)d.light * g[count - 1].K > g[0].K ? 0 : d.more;
   d.act = g->act;
   d.type = g->type;
   d.sa = g->sa;
