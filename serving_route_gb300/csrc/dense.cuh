@@ -146,10 +146,12 @@ struct DenseSplit {
   int split, stages;     // CTAs that share a tile's K, ring places
   uint32_t tmem_cols, smem;
   bool early;            // the weights' first copies need not wait for the kernel before
+  bool alone;            // at most one CTA per SM
   double us;             // its time by the model below
 };
 constexpr int kSpMaxTokens = 128;
-constexpr int kSpMaxSmem = 112 * 1024;  // two CTAs, with what each has besides, in 228 KB
+constexpr int kSpMaxSmem = 104 * 1024;   // two CTAs, with what each has besides, in 228 KB
+constexpr int kSpAloneSmem = 117248;     // two do not fit
 
 cudaError_t dense_split_set_attributes();
 DenseSplit dense_split_plan(const DenseGemm& g, int sms);
