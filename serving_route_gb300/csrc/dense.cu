@@ -1,7 +1,7 @@
 // dense.cu -- the dense products beside the MoE layer: x W^T in the layer's FP8 format
 // (Fp8Linear) and the products of a gated feed-forward block and of its gradients
 // (GatedMlp).
-#include <algorithm>
+#include <utility>
 
 #include <cudaTypedefs.h>
 
@@ -901,7 +901,6 @@ static cudaError_t split_gemm(const DenseGemm& g, DenseSplit p, cudaStream_t s) 
   d.out = g.out;
   d.ld_out = g.ld_out;
   d.out_f32 = g.out_f32;
-  d.accumulate = g.accumulate;
   d.saved = g.saved;
   d.saved_f32 = g.saved_f32;
   d.dgu = g.dgu;
@@ -925,7 +924,8 @@ cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
 }
 
 cudaError_t dense_gemms(DenseGemm* g, int count, int sms, cudaStream_t s) {
-  std::stable_sort(g, g + count, [](const DenseGemm& a, const DenseGemm& b) { return a.K > b.K; });
+  for (int i = 1; i < count; ++i)  // the longest K first
+    for (int j = i; j > 0 && g[j].K > g[j - 1].K; --j) std::swap(g[j], g[j - 1]);
   int BN = 256;
   pair_columns(g, count, sms / 2, &BN);
   return pair_gemm(g, count, BN, sms / 2, s);

@@ -146,10 +146,12 @@ __device__ __forceinline__ void quantize_block(const uint16_t* x, int64_t ld, in
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(atom + t * 16), "r"((uint32_t)(e + 127) * 0x01010101u) : "memory");
 }
 
-template <bool F8, bool AMN, bool BMN, DenseEpi EPI, bool FUSE>
+// (kEpiGrad multiplies W2 [K, N] as it lies: MN-major.)
+template <bool F8, DenseEpi EPI, bool FUSE>
 __global__ void __launch_bounds__(kSpThreads, 2)
     dense_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const DenseArgs g, const DenseSplit p) {
+  constexpr bool BMN = EPI == kEpiGrad;
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full_bar[kSpMaxStages], empty_bar[kSpMaxStages];
   __shared__ __align__(8) uint64_t accf_bar, sff_bar[kSpSfSlots], sfe_bar[kSpSfSlots];
@@ -223,11 +225,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         if (g.withhold && tokens_warp && blockIdx.x == 0 && i == n - 1) {
           // the bytes never come
         } else if (tokens_warp) {
-          if (AMN) {
-            for (int c = 0; c < p.NT; c += 64) tma_load_2d(dst + c * 128, &tmA, fb, m0 + c, k);
-          } else {
-            tma_load_2d(dst, &tmA, fb, k, m0);
-          }
+          tma_load_2d(dst, &tmA, fb, k, m0);
         } else if (EPI == kEpiGate) {  // 64 gate rows, then their 64 up rows
           tma_load_2d(dst, &tmB, fb, k, jt * 64);
           tma_load_2d(dst + 8192, &tmB, fb, k, g.N + jt * 64);
@@ -275,7 +273,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     // ------------------------------------------------------------ MMAs
     const bool one = elect_one();
     const uint32_t idesc0 = F8 ? idesc_mxf8_e4m3(128, 0) + ((uint32_t)(p.NT >> 3) << 17)
-                               : idesc_16(128, 0, g.type == kBF16, BMN, AMN) + ((uint32_t)(p.NT >> 3) << 17);
+                               : idesc_16(128, 0, g.type == kBF16, BMN, false) + ((uint32_t)(p.NT >> 3) << 17);
     uint32_t sf = 0, slot = 0, group = 0;
     // (the next place is probed while this one's MMAs run)
     int st = 0;
@@ -294,7 +292,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
       tc_fence_after();
       const uint32_t wa = sbase + st * stage_bytes, ra = wa + kSpW;
       const uint64_t wd = BMN ? sdesc_mn_sw128(wa) : sdesc_k_sw128(wa);
-      const uint64_t rd = AMN ? sdesc_mn_sw128(ra) : sdesc_k_sw128(ra);
+      const uint64_t rd = sdesc_k_sw128(ra);
       if (FUSE) sf = tmem + p.NT + (uint32_t)(i % kSpFusedSlots) * kSpSfCols;
       if (one) {
         if (FUSE) {  // scales with every K block
@@ -311,7 +309,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
           if constexpr (F8)
             tc_mma_mxf8(tmem, wd + 2 * k, rd + 2 * k, FUSE ? idesc0 : idesc0 | (j << 4) | (j << 29), sf, sf + 8, add);
           else
-            tc_mma_16(tmem, wd + (BMN ? 128 : 2) * k, rd + (AMN ? 128 : 2) * k, idesc0, add);
+            tc_mma_16(tmem, wd + (BMN ? 128 : 2) * k, rd + 2 * k, idesc0, add);
         }
         tc_commit(smem_u32(&empty_bar[st]));
         if (F8 && !FUSE && (j == 3 || i == n - 1)) tc_commit(smem_u32(&sfe_bar[slot]));
@@ -439,10 +437,6 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         gate_values(g.act, gv, uv);
         store_few(g.out, o, col, g.N, uv, false, g.type, true);
       } else if constexpr (EPI == kEpiStore) {
-        if (g.accumulate) {  // (float, whole vectors)
-          const float4 old = load_four(g.out, o, true, g.type);
-          v[j][0] += old.x, v[j][1] += old.y, v[j][2] += old.z, v[j][3] += old.w;
-        }
         store_few(g.out, o, col, g.N, v[j], g.out_f32, g.type, g.vec);
       } else {
         const float4 gs = load_four(g.saved, s, g.saved_f32, g.type);
@@ -471,7 +465,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
   if (p.split > 1) cluster_sync_all();  // the others have read this CTA's sums
 }
 
-template <bool F8, bool AMN, bool BMN, DenseEpi EPI, bool FUSE = false>
+template <bool F8, DenseEpi EPI, bool FUSE = false>
 static cudaError_t launch_split(const CUtensorMap& a, const CUtensorMap& b, const DenseArgs& g, const DenseSplit& p,
                                 cudaStream_t s) {
   cudaLaunchAttribute c;
@@ -479,18 +473,16 @@ static cudaError_t launch_split(const CUtensorMap& a, const CUtensorMap& b, cons
   c.val.clusterDim.x = p.split;
   c.val.clusterDim.y = 1;
   c.val.clusterDim.z = 1;
-  return launch_k(dense_split_kernel<F8, AMN, BMN, EPI, FUSE>, dim3((unsigned)(p.split * p.tt * p.rt)), dim3(kSpThreads),
+  return launch_k(dense_split_kernel<F8, EPI, FUSE>, dim3((unsigned)(p.split * p.tt * p.rt)), dim3(kSpThreads),
                   p.smem, s, true, &c, a, b, g, p);
 }
 
 cudaError_t dense_split_set_attributes() {
-  const void* ks[7] = {(const void*)dense_split_kernel<true, false, false, kEpiStore, true>,
-                       (const void*)dense_split_kernel<true, false, false, kEpiStore, false>,
-                       (const void*)dense_split_kernel<false, false, false, kEpiGate, false>,
-                       (const void*)dense_split_kernel<false, false, false, kEpiStore, false>,
-                       (const void*)dense_split_kernel<false, false, true, kEpiGrad, false>,
-                       (const void*)dense_split_kernel<false, false, true, kEpiStore, false>,
-                       (const void*)dense_split_kernel<false, true, true, kEpiStore, false>};
+  const void* ks[5] = {(const void*)dense_split_kernel<true, kEpiStore, true>,
+                       (const void*)dense_split_kernel<true, kEpiStore, false>,
+                       (const void*)dense_split_kernel<false, kEpiStore, false>,
+                       (const void*)dense_split_kernel<false, kEpiGate, false>,
+                       (const void*)dense_split_kernel<false, kEpiGrad, false>};
   for (const void* k : ks) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpAloneSmem);
     if (e != cudaSuccess) return e;
@@ -509,14 +501,13 @@ cudaError_t dense_split_set_attributes() {
 DenseSplit dense_split_plan(const DenseGemm& g, int sms) {
   DenseSplit best = {};
   const bool f8 = g.type == kE4M3;
-  const int unit = g.a.mn ? 64 : 16;
   const int KB = (g.K + (f8 ? 127 : 63)) / (f8 ? 128 : 64);
   const double bytes = (double)g.N * g.K * (f8 ? 1 : 2) * (g.epi == kEpiGate ? 2 : 1) * 1e-6;
   for (int most = 64; most <= kSpMaxTokens; most *= 2) {
     if (most > 64 && g.M <= most / 2) break;
     DenseSplit p = {};
     p.tt = (g.M + most - 1) / most;
-    p.NT = ((g.M + p.tt - 1) / p.tt + unit - 1) / unit * unit;
+    p.NT = ((g.M + p.tt - 1) / p.tt + 15) / 16 * 16;
     p.tt = (g.M + p.NT - 1) / p.NT;
     p.rt = g.epi == kEpiGate ? (g.N + 63) / 64 : (g.N + 127) / 128;
     const int64_t tiles = (int64_t)p.tt * p.rt;
@@ -556,13 +547,11 @@ DenseSplit dense_split_plan(const DenseGemm& g, int sms) {
 
 cudaError_t dense_split_launch(const CUtensorMap& a, const CUtensorMap& b, const DenseGemm& g, const DenseArgs& d,
                                const DenseSplit& p, cudaStream_t s) {
-  if (g.x) return launch_split<true, false, false, kEpiStore, true>(b, b, d, p, s);
-  if (g.type == kE4M3) return launch_split<true, false, false, kEpiStore>(a, b, d, p, s);
-  if (g.epi == kEpiGate) return launch_split<false, false, false, kEpiGate>(a, b, d, p, s);
-  if (g.epi == kEpiGrad) return launch_split<false, false, true, kEpiGrad>(a, b, d, p, s);
-  if (g.a.mn) return launch_split<false, true, true, kEpiStore>(a, b, d, p, s);
-  if (g.b.mn) return launch_split<false, false, true, kEpiStore>(a, b, d, p, s);
-  return launch_split<false, false, false, kEpiStore>(a, b, d, p, s);
+  if (g.x) return launch_split<true, kEpiStore, true>(b, b, d, p, s);
+  if (g.type == kE4M3) return launch_split<true, kEpiStore>(a, b, d, p, s);
+  if (g.epi == kEpiGate) return launch_split<false, kEpiGate>(a, b, d, p, s);
+  if (g.epi == kEpiGrad) return launch_split<false, kEpiGrad>(a, b, d, p, s);
+  return launch_split<false, kEpiStore>(a, b, d, p, s);
 }
 
 }  // namespace mm
