@@ -452,11 +452,9 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
                               ((uint32_t)(BN >> 3) << 17);
       int stage = 0;
       uint32_t phase = 0, group = 0;
-      // (the next stage is probed while this one's MMAs run)
-      auto probe = [&](int s, uint32_t ph) {
-        return (bool)__all_sync(0xFFFFFFFFu, mbar_test_wait_cluster(smem_u32(&full_bar[s]), ph));
-      };
-      bool ready = probe(0, 0);
+      // The next stage is probed between this one's MMAs and their commit, and the answer looked
+      // at a K block later.
+      bool ready = mbar_test_wait_cluster(smem_u32(&full_bar[0]), 0);
       for (int i = 0, u; (u = unit(i)) < g.units; ++i) {
         int m, n;
         const PairProblem& p = tile(u, m, n);
@@ -484,7 +482,8 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
             ++group;
             sf = tmem + kDTmemSf + slot * kDSfCols;
           }
-          if (!ready && !warp_wait<true>(smem_u32(&full_bar[stage]), phase, abort, g.status, g.wait_ns)) {
+          if (!__all_sync(0xFFFFFFFFu, ready) &&
+              !warp_wait<true>(smem_u32(&full_bar[stage]), phase, abort, g.status, g.wait_ns)) {
             ok = false;
             break;
           }
@@ -508,14 +507,17 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
               else
                 tc_mma_16_pair(acc, da, db, idesc0, add);
             }
-            tc_commit_pair_multicast(smem_u32(&empty_bar[stage]), 0x3);
-            if (F8 && (j == 3 || kb == KB - 1)) tc_commit_pair_multicast(smem_u32(&sfe_bar[slot]), 0x3);
           }
+          const uint32_t done = smem_u32(&empty_bar[stage]);
           if (++stage == kDStages) {
             stage = 0;
             phase ^= 1u;
           }
-          ready = probe(stage, phase);
+          ready = mbar_test_wait_cluster(smem_u32(&full_bar[stage]), phase);
+          if (one) {
+            tc_commit_pair_multicast(done, 0x3);
+            if (F8 && (j == 3 || kb == KB - 1)) tc_commit_pair_multicast(smem_u32(&sfe_bar[slot]), 0x3);
+          }
         }
         if (!ok) break;
         if (one) tc_commit_pair_multicast(smem_u32(&accf_bar[b]), 0x3);

@@ -275,10 +275,10 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     const uint32_t idesc0 = F8 ? idesc_mxf8_e4m3(128, 0) + ((uint32_t)(p.NT >> 3) << 17)
                                : idesc_16(128, 0, g.type == kBF16, BMN, false) + ((uint32_t)(p.NT >> 3) << 17);
     uint32_t sf = 0, slot = 0, group = 0;
-    // (the next place is probed while this one's MMAs run)
+    // (the next place is probed between this one's MMAs and their commit)
     int st = 0;
     uint32_t ph = 0;
-    bool ready = __all_sync(0xFFFFFFFFu, mbar_test_wait(smem_u32(&full_bar[0]), 0));
+    bool ready = mbar_test_wait(smem_u32(&full_bar[0]), 0);
     for (int i = 0; i < n; ++i) {
       const uint32_t j = (uint32_t)(kb0 + i) & 3u;
       const bool fresh = F8 && !FUSE && (j == 0 || i == 0);
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         ++group;
         sf = tmem + p.NT + slot * kSpSfCols;
       }
-      if (!ready && !warp_wait(smem_u32(&full_bar[st]), ph, abort, g.status, g.wait_ns)) break;
+      if (!__all_sync(0xFFFFFFFFu, ready) && !warp_wait(smem_u32(&full_bar[st]), ph, abort, g.status, g.wait_ns)) break;
       tc_fence_after();
       const uint32_t wa = sbase + st * stage_bytes, ra = wa + kSpW;
       const uint64_t wd = BMN ? sdesc_mn_sw128(wa) : sdesc_k_sw128(wa);
@@ -311,14 +311,17 @@ __global__ void __launch_bounds__(kSpThreads, 2)
           else
             tc_mma_16(tmem, wd + (BMN ? 128 : 2) * k, rd + 2 * k, idesc0, add);
         }
-        tc_commit(smem_u32(&empty_bar[st]));
-        if (F8 && !FUSE && (j == 3 || i == n - 1)) tc_commit(smem_u32(&sfe_bar[slot]));
       }
+      const uint32_t done = smem_u32(&empty_bar[st]);
       if (++st == p.stages) {
         st = 0;
         ph ^= 1u;
       }
-      ready = __all_sync(0xFFFFFFFFu, mbar_test_wait(smem_u32(&full_bar[st]), ph));
+      ready = mbar_test_wait(smem_u32(&full_bar[st]), ph);
+      if (one) {
+        tc_commit(done);
+        if (F8 && !FUSE && (j == 3 || i == n - 1)) tc_commit(smem_u32(&sfe_bar[slot]));
+      }
     }
     if (one) tc_commit(smem_u32(&accf_bar));
     __syncwarp();
