@@ -114,7 +114,7 @@ class GatedMlp(_Handle):
     w1 [2I, H] (gate rows, then up rows), w2 [H, I], of one type, on the GPU; H and I
     multiples of 8.  activation: "silu", or "gelu" in its tanh form.  The object keeps
     the weights, which every call reads where they are (an optimiser may change them in
-    place), and its own workspace of 6 max_tokens I bytes and what few tokens need."""
+    place), and its own workspace of 6 max_tokens I bytes."""
 
     _destroy = staticmethod(B.moe_mlp_destroy)
 
