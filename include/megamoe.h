@@ -700,7 +700,8 @@ MOE_API moe_status moe_fp8_linear_create(int32_t rows, int32_t cols, uint32_t fl
  * [-127, 127], 0 for an all-zero block, as moe_add_rms_norm's.
  * moe_fp8_linear_quantized -- the same of rows that are so already: d_xq
  * E4M3 [num_tokens, cols], 16-byte aligned, d_xq_scale E8M0 bytes [num_tokens, cols / 128].
- * Products and sums are exact to FP32; d_y [num_tokens, rows] float
+ * Products are exact, sums FP32, which the tensor cores truncate at every step (measured
+ * in norm: 2e-7 of y at 1408 columns, 1e-6 at 7168); d_y [num_tokens, rows] float
  * (y_float32 != 0) or BF16.  MOE_ERR_INVALID_ARG: a NULL or misaligned pointer, a stride
  * below cols, d_y overlapping the span of the inputs' rows.
  */
