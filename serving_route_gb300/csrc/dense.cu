@@ -805,14 +805,15 @@ cudaError_t dense_set_attributes() {
 }
 
 // The tiles' columns: the width with which the fullest pair has the least to do, and its time in
-// microseconds.  By what was measured (one K block of 128 bytes 0.25 us with 64 or 128
-// columns, 0.30 with 256; start, first copies and last tile 4.6 us with 128 columns, 5.8 with
-// 256, with gate and gradient up to 8): 512 x 4096 x 2048 in E4M3 9.3 us with 128 columns, 10.0
-// with 256; 1021 x 4096 x 7168 46 and 25.
+// microseconds.  Fitted, as the split kernel's, to the times of 90 E4M3 products (1 to 8192
+// tokens, 64 to 8192 weight rows, K from 128 to 7168) in each width and split: one K block of 128
+// bytes 0.31 us with 64 columns, 0.35 with 256; start, first copies and last tile 4.2 and 5.4
+// us, 2.6 more with gate and gradient.  512 x 4096 x 2048 takes 9.3 us with 128 columns, 10.0
+// with 256; 1021 x 4096 x 7168 46 and 25; 8192 x 256 x 7168 26.6.
 static double pair_columns(const DenseGemm* g, int count, int pairs, int* columns) {
   double least = 0;
   for (int BN = 256; BN >= 64; BN -= 64) {
-    const double w = BN / 256.0, block = 0.24 + 0.06 * w * w;
+    const double w = BN / 256.0, block = 0.31 + 0.04 * w * w;
     double sum = 0, one = 0;
     int64_t units = 0;
     for (int i = 0; i < count; ++i) {
@@ -827,7 +828,11 @@ static double pair_columns(const DenseGemm* g, int count, int pairs, int* column
     // one product: whole waves; several: their sum, and half a tile that does not fill up
     double us = count == 1 ? (double)((units + pairs - 1) / pairs) * one : sum / pairs + 0.5 * one;
     if (us < one) us = one;
-    us += 3.4 + (g->epi == kEpiStore ? 2.4 : 5.0) * w;
+    // a few tiles of long rows wait for memory: 2.9 TB/s, 100 GB/s for a pair
+    const double mb = count == 1 ? ((double)g->M + g->N) * g->K * (g->type == kE4M3 ? 1e-6 : 2e-6) : 0;
+    const double rate = units < 29 ? 0.1 * units : 2.9;
+    if (us < mb / rate) us = mb / rate;
+    us += 3.8 + (g->epi == kEpiStore ? 1.6 : 4.2) * w;
     if (BN == 256 || us < least) {
       least = us;
       *columns = BN;
@@ -913,15 +918,12 @@ static cudaError_t split_gemm(const DenseGemm& g, DenseSplit p, cudaStream_t s) 
   return dense_split_launch(a, b, g, d, p, s);
 }
 
-// Which kernel: the one that the measured times above say is faster; beyond 16 tiles of 128
-// tokens that is always the pair's.
+// Which kernel: the one that the measured times above say is faster.
 cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
   int BN = 256;
   const double pair_us = pair_columns(&g, 1, sms / 2, &BN);
-  if (g.M <= 16 * kSpMaxTokens) {
-    const DenseSplit p = dense_split_plan(g, sms);
-    if (p.us < pair_us || g.x) return split_gemm(g, p, s);
-  }
+  const DenseSplit p = dense_split_plan(g, sms);
+  if (p.us < pair_us || g.x) return split_gemm(g, p, s);
   return pair_gemm(&g, 1, BN, sms / 2, s);
 }
 

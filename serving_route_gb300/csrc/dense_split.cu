@@ -497,15 +497,17 @@ cudaError_t dense_split_set_attributes() {
 // in 1, 2, 4 or 8 shares (others did not do better: clusters of them fill the GPU's parts
 // unevenly).  By microseconds as measured (E4M3, 4096 x 7168, 32 tiles of 128 rows; K split by
 // 1 / 2 / 4 / 8): 1 token 18.4 / 11.1 / 7.4 / 6.8, 64 tokens 20.1 / 12.4 / 8.8 / 9.7, 128
-// tokens 22.5 / 14.2 / 11.1 / 14.0.  A K block of 128 bytes takes 0.26 us, 0.35 with 128
-// tokens; start, drain and finish 3.4 us and 17 ns a token; the join through other CTAs'
-// shared memory 10 or 30 ns a token for 4 or 8 shares; where SMs have two CTAs each of
-// these takes longer.
+// tokens 22.5 / 14.2 / 11.1 / 14.0.  A K block of 128 bytes takes 0.25 us, 0.32 with 128
+// tokens; start, drain and finish 2.8 us and 18 ns a token; the join through other CTAs'
+// shared memory 5 or 9 ns a token for 4 or 8 shares; where SMs have two CTAs each of
+// these takes longer, and so do joining and finishing gate and up.  Over 90 sizes
+// (pair_columns) the choice by these figures and the pair's takes 0.3% longer than the best one,
+// over 70 gated blocks 1.2%.
 DenseSplit dense_split_plan(const DenseGemm& g, int sms) {
   DenseSplit best = {};
   const bool f8 = g.type == kE4M3;
   const int KB = (g.K + (f8 ? 127 : 63)) / (f8 ? 128 : 64);
-  const double bytes = (double)g.N * g.K * (f8 ? 1 : 2) * (g.epi == kEpiGate ? 2 : 1) * 1e-6;
+  const double bytes = ((double)g.N * (g.epi == kEpiGate ? 2 : 1) + g.M) * g.K * (f8 ? 1e-6 : 2e-6);
   for (int most = 64; most <= kSpMaxTokens; most *= 2) {
     if (most > 64 && g.M <= most / 2) break;
     DenseSplit p = {};
@@ -518,9 +520,10 @@ DenseSplit dense_split_plan(const DenseGemm& g, int sms) {
       const int64_t ctas = tiles * split;
       const bool shared = ctas > sms;
       const double waves = (double)((ctas + 2 * sms - 1) / (2 * sms));
-      double block = 0.25 + 0.0008 * p.NT, join = p.NT * (split == 8 ? 0.03 : split == 4 ? 0.01 : 0.0);
-      double us = 3.4 + 0.017 * p.NT;
-      if (shared) block *= 1.13 + 0.0045 * p.NT, join *= 1.6, us += 0.012 * p.NT;
+      double block = 0.24 + 0.0006 * p.NT, join = p.NT * (split == 8 ? 0.009 : split == 4 ? 0.0055 : 0.0);
+      double us = 2.8 + 0.018 * p.NT;
+      if (shared) block *= 1.11 + 0.0016 * p.NT, join *= 1.9, us += 0.023 * p.NT;
+      if (g.epi == kEpiGate) us += (shared ? 0.03 : 0.02) * p.NT, join += split > 1 ? 1.0 : 0.0;
       us *= 0.5 + 0.5 * waves;  // (one's end overlaps another's start)
       // (fewer CTAs have less in flight than the memory needs)
       const double rate = ctas < 144 ? 0.045 * ctas : 6.5, stream_us = bytes / rate;
