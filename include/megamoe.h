@@ -703,7 +703,7 @@ MOE_API moe_status moe_fp8_linear_create(int32_t rows, int32_t cols, uint32_t fl
  * Products are exact, sums FP32, which the tensor cores truncate at every step (measured
  * in norm: 2e-7 of y at 1408 columns, 1e-6 at 7168); d_y [num_tokens, rows] float
  * (y_float32 != 0) or BF16.  MOE_ERR_INVALID_ARG: a NULL or misaligned pointer, a stride
- * below cols, d_y overlapping the span of the inputs' rows.
+ * below cols, d_y overlapping the codes or the span of the inputs' rows.
  */
 MOE_API moe_status moe_fp8_linear(moe_fp8_linear_handle* h, const uint16_t* d_x, int64_t x_stride,
                                   int64_t num_tokens, void* d_y, int32_t y_float32,
@@ -752,7 +752,7 @@ MOE_API moe_status moe_mlp_create(int32_t hidden, int32_t inter, int32_t fp16, i
  * before the activation [num_tokens, 2 inter] for the backward pass, float
  * (saved_float32 != 0) or in the block's type.  All 16-byte aligned.  Sums are
  * FP32, of which act(g) * u is rounded once to the block's type (FP16: its range
- * holds for it).  d_y may be d_x itself (dense rows), else nothing overlaps
+ * holds for it).  d_y may be d_x itself (dense rows), else no output overlaps anything
  * (the span of strided rows counts whole): MOE_ERR_INVALID_ARG.
  */
 MOE_API moe_status moe_mlp_forward(moe_mlp_handle* h, const uint16_t* d_x, int64_t x_stride,
@@ -768,7 +768,7 @@ MOE_API moe_status moe_mlp_forward(moe_mlp_handle* h, const uint16_t* d_x, int64
  * each may be NULL (not wanted).  d_dx in the block's type; the weights'
  * gradients in it too, or float (dw_float32 != 0), then with accumulate != 0 added to
  * what is there.  dg, du and act(g) * u are rounded once to the block's type on the way.
- * No overlaps, all 16-byte aligned.  num_tokens 0 zeroes the weights' gradients
+ * No output overlaps anything, all 16-byte aligned.  num_tokens 0 zeroes the weights' gradients
  * (accumulate: leaves them).
  */
 MOE_API moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_stride,

@@ -181,8 +181,9 @@ moe_status moe_fp8_linear(moe_fp8_linear_handle* h, const uint16_t* d_x, int64_t
   if (num_tokens > h->max_tokens) return MOE_ERR_CAPACITY;
   if (off(d_x, 16) || off(d_y, y_float32 ? 4 : 2) || x_stride < h->cols || x_stride % 8 || elsewhere(h->device))
     return MOE_ERR_INVALID_ARG;
-  const Span x(d_x, num_tokens, x_stride, h->cols, 2);
-  if (x.meets(Span(d_y, num_tokens, h->rows, h->rows, y_float32 ? 4 : 2))) return MOE_ERR_INVALID_ARG;
+  const Span y(d_y, num_tokens, h->rows, h->rows, y_float32 ? 4 : 2);
+  if (y.meets(Span(d_x, num_tokens, x_stride, h->cols, 2)) || y.meets(Span(h->codes, h->rows, h->cols, h->cols, 1)))
+    return MOE_ERR_INVALID_ARG;
   DenseGemm g = linear_product(h, num_tokens, d_y, y_float32 != 0);
   if (num_tokens <= kFusedTokens) {
     g.x = d_x;
@@ -206,7 +207,8 @@ moe_status moe_fp8_linear_quantized(moe_fp8_linear_handle* h, const uint8_t* d_x
   if (off(d_xq, 16) || !d_xq_scale || off(d_y, y_float32 ? 4 : 2) || elsewhere(h->device)) return MOE_ERR_INVALID_ARG;
   const Span y(d_y, num_tokens, h->rows, h->rows, y_float32 ? 4 : 2);
   if (y.meets(Span(d_xq, num_tokens, h->cols, h->cols, 1)) ||
-      y.meets(Span(d_xq_scale, num_tokens, h->cols / 128, h->cols / 128, 1)))
+      y.meets(Span(d_xq_scale, num_tokens, h->cols / 128, h->cols / 128, 1)) ||
+      y.meets(Span(h->codes, h->rows, h->cols, h->cols, 1)))
     return MOE_ERR_INVALID_ARG;
   DenseGemm g = linear_product(h, num_tokens, d_y, y_float32 != 0);
   g.a = {d_xq, h->cols, (int)num_tokens, false};
@@ -275,9 +277,11 @@ moe_status moe_mlp_forward(moe_mlp_handle* h, const uint16_t* d_x, int64_t x_str
       elsewhere(h->device))
     return MOE_ERR_INVALID_ARG;
   const Span x(d_x, num_tokens, x_stride, H, 2), y(d_y, num_tokens, H, H, 2),
-      saved(d_saved, num_tokens, 2 * I, 2 * I, saved_float32 ? 4 : 2);
+      saved(d_saved, num_tokens, 2 * I, 2 * I, saved_float32 ? 4 : 2), w1(h->w1, 2 * I, H, H, 2), w2(h->w2, H, I, I, 2);
   // y is stored after all of x has been read: it may be x itself
-  if (saved.meets(x) || saved.meets(y) || (x.meets(y) && !(d_x == d_y && x_stride == H))) return MOE_ERR_INVALID_ARG;
+  if (saved.meets(x) || saved.meets(y) || (x.meets(y) && !(d_x == d_y && x_stride == H)) || y.meets(w1) || y.meets(w2) ||
+      saved.meets(w1) || saved.meets(w2))
+    return MOE_ERR_INVALID_ARG;
   DenseGemm g = {};
   g.a = {d_x, x_stride, (int)num_tokens, false};
   g.b = {h->w1, H, 2 * I, false};
@@ -328,8 +332,9 @@ moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_
   if (off(d_dy, 16) || off(d_x, 16) || off(d_saved, 16) || (d_dx && off(d_dx, 16)) || dy_stride < H ||
       dy_stride % 8 || x_stride < H || x_stride % 8)
     return MOE_ERR_INVALID_ARG;
-  const Span in[3] = {Span(d_dy, T, dy_stride, H, 2), Span(d_x, T, x_stride, H, 2),
-                      Span(d_saved, T, 2 * I, 2 * I, saved_float32 ? 4 : 2)};
+  const Span in[5] = {Span(d_dy, T, dy_stride, H, 2), Span(d_x, T, x_stride, H, 2),
+                      Span(d_saved, T, 2 * I, 2 * I, saved_float32 ? 4 : 2), Span(h->w1, 2 * I, H, H, 2),
+                      Span(h->w2, H, I, I, 2)};
   const Span out[3] = {Span(d_dx, T, H, H, 2), Span(d_dw1, 2 * I, H, H, ds), Span(d_dw2, H, I, I, ds)};
   for (int i = 0; i < 3; ++i) {
     for (const Span& s : in)

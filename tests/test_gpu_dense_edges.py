@@ -153,7 +153,7 @@ def test_mlp_tiles_of_every_width(S, T, H, I):
 @pytest.mark.parametrize("rows", [63, 190, 193, 450, 1100, 3333, 9000])
 @pytest.mark.parametrize("cols", [128, 640, 1664])
 def test_linear_tiles_of_every_width(S, rows, cols):
-    """2100 rows: the pair kernel, its tiles' columns across blocks of the matrix, scale rows of
+    """2100 tokens: tiles' columns across blocks of the matrix, scale rows of
     every alignment, from views at odd addresses too."""
     T = 2100
     codes, scales = weights8(rows, cols, seed=50)
@@ -200,3 +200,52 @@ def test_linear_few_tokens_long_rows(S, T, rows, cols):
 def test_mlp_few_tokens_long_rows(S, T, H, I):
     w1, w2, x, mlp = mlp_case(S, T, H, I, BF, "silu", seed=70)
     ref.check(mlp.forward(x), ref.forward(x, w1, w2, "silu", BF))
+
+
+@pytest.mark.parametrize("T,rows,cols", [(4911, 136, 128), (6439, 136, 128), (4890, 16, 1536), (2076, 136, 3968),
+                                         (6840, 536, 1536), (2585, 784, 128)])
+def test_linear_many_tokens_few_rows(S, T, rows, cols):
+    """A few tiles of the matrix for dozens of tiles of tokens: narrow pairs, and splits."""
+    codes, scales = weights8(rows, cols, seed=80)
+    lin = S.Fp8Linear(codes, scales, max_tokens=T)
+    x = rand(T, cols, seed=81)
+    xq, xs = ref.quantize_rows(x)
+    got = lin.forward(x, out_dtype=F32)
+    ref.check(got, ref.linear(xq, xs, codes, scales, F32))
+    assert torch.equal(got, lin.forward_quantized(xq, xs, out_dtype=F32))
+
+
+@pytest.mark.parametrize("T,H,I", [(6498, 128, 264), (4929, 1920, 16), (5014, 1792, 136), (4922, 136, 768), (2454, 16, 2432),
+                                   (289, 128, 7936)])
+def test_mlp_many_tokens_few_rows(S, T, H, I):
+    w1, w2, x, mlp = mlp_case(S, T, H, I, BF, "gelu", seed=90)
+    saved = torch.empty(T, 2 * I, device="cuda")
+    ref.check(mlp.forward(x, saved=saved), ref.forward(x, w1, w2, "gelu", BF))
+    dy = rand(T, H, seed=91, scale=0.1)
+    for got, w in zip(mlp.backward(dy, x, saved), ref.backward(dy, x, saved, w1, w2, "gelu", BF, BF)):
+        ref.check(got, w)
+
+
+def test_outputs_that_overlap_the_weights_are_refused(S):
+    B = S.binding
+    codes, scales = weights8(256, 256, seed=3)
+    kept = codes.clone()
+    lin = S.Fp8Linear(codes, scales, max_tokens=8)
+    x = rand(8, 256, seed=4)
+    xq, xs = ref.quantize_rows(x)
+    inside = codes.data_ptr() + 4096
+    assert status(B, B.moe_fp8_linear, lin.handle, x.data_ptr(), 256, 8, inside, 0, 0) == B.MOE_ERR_INVALID_ARG
+    assert status(B, B.moe_fp8_linear_quantized, lin.handle, xq.data_ptr(), xs.data_ptr(), 8, inside, 0,
+                  0) == B.MOE_ERR_INVALID_ARG
+    assert torch.equal(codes, kept)
+    w1, w2, xm, mlp = mlp_case(S, 8, 64, 32, BF, "silu", seed=5)
+    kept = w1.clone(), w2.clone()
+    saved, y = torch.zeros(8, 64, device="cuda"), torch.zeros(64, 64, dtype=BF, device="cuda")
+    for w in (w1, w2):
+        p = w.data_ptr()
+        assert status(B, B.moe_mlp_forward, mlp.handle, xm.data_ptr(), 64, 8, p, 0, 0, 0) == B.MOE_ERR_INVALID_ARG
+        assert status(B, B.moe_mlp_forward, mlp.handle, xm.data_ptr(), 64, 8, y.data_ptr(), p, 0, 0) == B.MOE_ERR_INVALID_ARG
+        for out in ((p, 0, 0), (0, p, 0), (0, 0, p)):
+            assert status(B, B.moe_mlp_backward, mlp.handle, xm.data_ptr(), 64, xm.data_ptr(), 64, saved.data_ptr(), 1, 8,
+                          *out, 0, 0, 0) == B.MOE_ERR_INVALID_ARG
+    assert torch.equal(w1, kept[0]) and torch.equal(w2, kept[1]) and mlp.read_status() == (0, 0)
