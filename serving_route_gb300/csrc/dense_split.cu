@@ -12,7 +12,7 @@
 // Two CTAs per SM overlap one's join with the other's stream.
 // FUSE (E4M3, up to 16 tokens): the tokens come in BF16 and the CTAs quantise what they need of
 // them themselves, a warp for each ring place, straight into it: a kernel less before the
-// stream (4096 x 7168, one token: 8.6 -> 7.2 us), for 16 x 256 bytes a K block from L2.
+// stream (4096 x 7168, one token: 8.6 -> 7.2 us, 6.2 with what came after), for 16 x 256 bytes a K block from L2.
 // Warps: 0 and 3 loads, 1 MMAs, 2 scales, 4-7 drain the accumulator (thread = weight row); all
 // eight finish tokens (a lane has consecutive columns, so stores are whole lines).
 #include "dense.cuh"
