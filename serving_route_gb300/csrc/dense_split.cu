@@ -275,10 +275,12 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     const uint32_t idesc0 = F8 ? idesc_mxf8_e4m3(128, 0) + ((uint32_t)(p.NT >> 3) << 17)
                                : idesc_16(128, 0, g.type == kBF16, BMN, false) + ((uint32_t)(p.NT >> 3) << 17);
     uint32_t sf = 0, slot = 0, group = 0;
-    // (the next place is probed between this one's MMAs and their commit)
+    // The next place is probed between this one's MMAs and their commit.  (In twos a K block takes
+    // 0.235 us, one by one 0.257, in fours 0.239: 128 x 7168 by one CTA.)
     int st = 0;
     uint32_t ph = 0;
     bool ready = mbar_test_wait(smem_u32(&full_bar[0]), 0);
+#pragma unroll 2
     for (int i = 0; i < n; ++i) {
       const uint32_t j = (uint32_t)(kb0 + i) & 3u;
       const bool fresh = F8 && !FUSE && (j == 0 || i == 0);
