@@ -810,8 +810,8 @@ cudaError_t dense_set_attributes() {
 // microseconds.  Fitted, as the split kernel's, to the times of 90 E4M3 products (1 to 8192
 // tokens, 64 to 8192 weight rows, K from 128 to 7168) in each width and split: one K block of 128
 // bytes 0.31 us with 64 columns, 0.35 with 256; start, first copies and last tile 4.2 and 5.4
-// us, 2.6 more with gate and gradient.  512 x 4096 x 2048 takes 9.3 us with 128 columns, 10.0
-// with 256; 1021 x 4096 x 7168 46 and 25; 8192 x 256 x 7168 26.6.
+// us, 2.6 more with gate and gradient.  512 x 4096 x 2048 takes 9.3 us with 128 columns, 10.3
+// with 256; 1021 x 4096 x 7168 44 and 25; 8192 x 256 x 7168 27 and 25 (20.3 by the split kernel).
 static double pair_columns(const DenseGemm* g, int count, int pairs, int* columns) {
   double least = 0;
   for (int BN = 256; BN >= 64; BN -= 64) {

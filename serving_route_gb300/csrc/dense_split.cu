@@ -498,8 +498,8 @@ cudaError_t dense_split_set_attributes() {
 // How a product is divided: tokens in equal tiles of at most 64 or 128, two CTAs per SM, K
 // in 1, 2, 4 or 8 shares (others did not do better: clusters of them fill the GPU's parts
 // unevenly).  By microseconds as measured (E4M3, 4096 x 7168, 32 tiles of 128 rows; K split by
-// 1 / 2 / 4 / 8): 1 token 18.4 / 11.1 / 7.4 / 6.8, 64 tokens 20.1 / 12.4 / 8.8 / 9.7, 128
-// tokens 22.5 / 14.2 / 11.1 / 14.0.  A K block of 128 bytes takes 0.25 us, 0.32 with 128
+// 1 / 2 / 4 / 8): 1 token 15.7 / 9.7 / 6.7 / 6.7, 64 tokens 16.4 / 10.5 / 7.9 / 9.2, 128
+// tokens 19.6 / 12.8 / 10.7 / 13.7.  A K block of 128 bytes takes 0.25 us, 0.32 with 128
 // tokens; start, drain and finish 2.8 us and 18 ns a token; the join through other CTAs'
 // shared memory 5 or 9 ns a token for 4 or 8 shares; where SMs have two CTAs each of
 // these takes longer, and so do joining and finishing gate and up.  Over 90 sizes
