@@ -822,10 +822,14 @@ static double pair_columns(const DenseGemm* g, int count, int pairs, int* column
       const int cols = g[i].epi == kEpiGate ? BN / 2 : BN;
       const int64_t n = (int64_t)((g[i].M + 255) / 256) * ((g[i].N + cols - 1) / cols);
       const int KB = (g[i].K + (g[i].type == kE4M3 ? 127 : 63)) / (g[i].type == kE4M3 ? 128 : 64);
-      // (an MN-major operand comes in boxes of 64: as many bytes for 192 columns as for 256, half for 128)
-      double us = KB * (block + (g[i].b.mn && BN > 128 ? 0.08 : 0.0));
-      // a tile of a gradient that sums few rows takes its stores' time
-      if (count > 1 && us < 0.7 + 2.2 * w) us = 0.7 + 2.2 * w;
+      double us = KB * block;
+      if (count > 1) {
+        // the gradients' MN-major operands come in boxes of 64: as many bytes for 192 columns as for
+        // 256, half for 128; and a tile that sums few rows takes its stores' time (25 tokens, 3224 x
+        // 1928: the step 45.8 us, by K alone 50.5)
+        if (BN > 128) us += KB * 0.08;
+        if (us < 0.7 + 2.2 * w) us = 0.7 + 2.2 * w;
+      }
       us += 0.4;
       units += n;
       sum += n * us;
