@@ -698,6 +698,7 @@ MOE_API moe_status moe_fp8_linear_create(int32_t rows, int32_t cols, uint32_t fl
  * elements apart, a multiple of 8; 16-byte aligned), each row rounded to E4M3 with one
  * power-of-two scale per 128 columns: the least 2^e with amax <= 448 * 2^e, e in
  * [-127, 127], 0 for an all-zero block, as moe_add_rms_norm's.
+ * A row that holds a NaN or an infinity gives a row of NaN.
  * moe_fp8_linear_quantized -- the same of rows that are so already: d_xq
  * E4M3 [num_tokens, cols], 16-byte aligned, d_xq_scale E8M0 bytes [num_tokens, cols / 128].
  * Products are exact, sums FP32, which the tensor cores truncate at every step (measured

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* x, i
       for (int o = 4; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
       if (c[i] >= kb) continue;
       const int e = pow2_scale_exp(m);
-      const float inv = pow2_neg(e);
+      const float inv = block_factor(m, e);
       uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)

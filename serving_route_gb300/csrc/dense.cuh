@@ -121,6 +121,14 @@ __device__ __forceinline__ void gradient_values(DenseAct act, float (&dh)[N], fl
     all(std::integral_constant<DenseAct, kGeluTanh>{});
 }
 
+// What a block of 128 values with the largest magnitude `amax` is multiplied by before its
+// rounding to E4M3 with the scale 2^e: 2^-e, or NaN where the block holds an infinity.  E4M3
+// has none, and the conversion's 448 would pass for a number; so all of the block's codes are
+// NaN, and with them the row of the product, as they are from a NaN.
+__device__ __forceinline__ float block_factor(float amax, int e) {
+  return __float_as_uint(amax) == 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : pow2_neg(e);
+}
+
 struct DenseArgs {
   int M, N, K;
   DenseAct act;

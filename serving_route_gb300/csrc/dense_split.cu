@@ -125,8 +125,9 @@ __device__ __forceinline__ void quantize_block(const uint16_t* x, int64_t ld, in
     for (int k = 0; k < 4; ++k) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[k] & 0x7FFF7FFFu));
   }
   asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(__shfl_xor_sync(0xFFFFFFFFu, m, 1)));
-  const int e = pow2_scale_exp(fmaxf(bf16_bits_to_float(m & 0xFFFFu), bf16_bits_to_float(m >> 16)));
-  const float inv = pow2_neg(e);
+  const float amax = fmaxf(bf16_bits_to_float(m & 0xFFFFu), bf16_bits_to_float(m >> 16));
+  const int e = pow2_scale_exp(amax);
+  const float inv = block_factor(amax, e);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint32_t q[4];
