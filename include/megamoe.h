@@ -738,7 +738,7 @@ typedef struct moe_mlp_handle moe_mlp_handle;
  * Read in place at every call: an optimiser may change them between calls.
  * hidden and inter are multiples of 8 up to 65536, else MOE_ERR_UNSUPPORTED.
  * The workspace holds h and the gradients of gate and up, 6 max_tokens inter
- * bytes.
+ * bytes.  Creating synchronises `stream`.
  */
 MOE_API moe_status moe_mlp_workspace_query(int32_t hidden, int32_t inter, int64_t max_tokens,
                                            size_t* workspace_bytes);

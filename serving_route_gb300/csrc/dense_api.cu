@@ -246,7 +246,9 @@ moe_status moe_mlp_create(int32_t hidden, int32_t inter, int32_t fp16, int32_t a
   if ((st = this_device(&dev, &sms)) != MOE_OK) return st;
   const MlpLayout l(inter, max_tokens);
   uint8_t* b = aligned(d_workspace);
-  if (cudaMemsetAsync(b, 0, kAlign, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  // (finished before the handle exists: its calls may be on other streams)
+  if (cudaMemsetAsync(b, 0, kAlign, stream) != cudaSuccess || cudaStreamSynchronize(stream) != cudaSuccess)
+    return MOE_ERR_CUDA;
   moe_mlp_handle* h = new (std::nothrow) moe_mlp_handle;
   if (!h) return MOE_ERR_INVALID_ARG;
   memset(h, 0, sizeof(*h));
