@@ -63,7 +63,7 @@ struct Span {
   uintptr_t a, b;
   Span(const void* p, int64_t rows, int64_t ld, int64_t cols, size_t size)
       : a((uintptr_t)p), b(p && rows ? a + ((rows - 1) * ld + cols) * size : a) {}
-  bool meets(const Span& o) const { return a < o.b && o.a < b; }
+  bool meets(const Span& o) const { return a < b && o.a < o.b && a < o.b && o.a < b; }  // (an empty one nothing)
 };
 
 moe_status read_word(const uint32_t* d_status, uint32_t* h_status, cudaStream_t stream) {
@@ -325,14 +325,8 @@ moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_
   const int H = h->hidden, I = h->inter, T = (int)num_tokens;
   const size_t ds = dw_float32 ? 4 : 2;
   if ((d_dw1 && off(d_dw1, 16)) || (d_dw2 && off(d_dw2, 16)) || elsewhere(h->device)) return MOE_ERR_INVALID_ARG;
-  if (T == 0) {  // the weights' gradients are sums over no rows
-    if (accumulate) return MOE_OK;
-    if (d_dw1 && cudaMemsetAsync(d_dw1, 0, 2 * ds * H * I, stream) != cudaSuccess) return MOE_ERR_CUDA;
-    if (d_dw2 && cudaMemsetAsync(d_dw2, 0, ds * H * I, stream) != cudaSuccess) return MOE_ERR_CUDA;
-    return MOE_OK;
-  }
-  if (off(d_dy, 16) || off(d_x, 16) || off(d_saved, 16) || (d_dx && off(d_dx, 16)) || dy_stride < H ||
-      dy_stride % 8 || x_stride < H || x_stride % 8)
+  if (T && (off(d_dy, 16) || off(d_x, 16) || off(d_saved, 16) || (d_dx && off(d_dx, 16)) || dy_stride < H ||
+            dy_stride % 8 || x_stride < H || x_stride % 8))
     return MOE_ERR_INVALID_ARG;
   const Span in[5] = {Span(d_dy, T, dy_stride, H, 2), Span(d_x, T, x_stride, H, 2),
                       Span(d_saved, T, 2 * I, 2 * I, saved_float32 ? 4 : 2), Span(h->w1, 2 * I, H, H, 2),
@@ -342,6 +336,12 @@ moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_
     for (const Span& s : in)
       if (out[i].meets(s)) return MOE_ERR_INVALID_ARG;
     if (out[i].meets(out[(i + 1) % 3])) return MOE_ERR_INVALID_ARG;
+  }
+  if (T == 0) {  // the weights' gradients are sums over no rows
+    if (accumulate) return MOE_OK;
+    if (d_dw1 && cudaMemsetAsync(d_dw1, 0, 2 * ds * H * I, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    if (d_dw2 && cudaMemsetAsync(d_dw2, 0, ds * H * I, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
   }
   // dh = dy W2 -> dg, du (and h)
   DenseGemm g = {};
