@@ -761,15 +761,16 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
 constexpr uint64_t kWithheldNs = 20000000ull;  // the limit under the watchdog's test
 
 static bool encode_map(CUtensorMap* map, const DenseOperand& o, int K, DenseType t, int box_rows) {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
+  // (looked up once, by whichever host thread comes first)
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return false;
-    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
+    const bool found = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                           cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(found ? p : nullptr);
+  }();
+  if (!fn) return false;
   const cuuint64_t es = t == kE4M3 ? 1 : 2;
   const cuuint64_t dims[2] = {(cuuint64_t)(o.mn ? o.rows : K), (cuuint64_t)(o.mn ? K : o.rows)};
   const cuuint64_t strides[1] = {(cuuint64_t)o.ld * es};

@@ -1,4 +1,4 @@
-"""Making a handle on one stream and using it on another, and what calls of no rows refuse."""
+"""Making a handle on one stream and using it on another."""
 import pytest
 import torch
 
