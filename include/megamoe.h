@@ -672,6 +672,20 @@ MOE_API void moe_fp4_destroy(moe_fp4_handle* h);
  * no-op (but see moe_mlp_backward); MOE_ERR_CAPACITY above max_tokens (at most 2^24).
  * ------------------------------------------------------------------------ */
 
+/*
+ * moe_fp8_linear_plan, moe_mlp_plan -- the launches that the calls of a handle
+ * make of num_tokens tokens: which kernel, and how the product is divided.
+ * Pure host arithmetic, no CUDA call; the same functions the calls use.
+ * num_tokens 0 gives zeros; MOE_ERR_INVALID_ARG for a NULL argument or
+ * num_tokens < 0, MOE_ERR_CAPACITY above max_tokens.
+ */
+typedef struct moe_dense_launch {
+  int32_t pairs; /* 1: CTA pairs on tiles of 256 rows; 0: K shared over clusters of CTAs */
+  int32_t width; /* a tile's columns (pairs: 64, 128, 192, 256, gate and up counted), or its tokens (16..128) */
+  int32_t split; /* CTAs that share a tile's K: 1 (pairs too), 2, 4, 8 */
+  int32_t tiles;
+} moe_dense_launch;
+
 typedef struct moe_fp8_linear_handle moe_fp8_linear_handle;
 
 /*
@@ -712,6 +726,10 @@ MOE_API moe_status moe_fp8_linear(moe_fp8_linear_handle* h, const uint16_t* d_x,
 MOE_API moe_status moe_fp8_linear_quantized(moe_fp8_linear_handle* h, const uint8_t* d_xq,
                                             const uint8_t* d_xq_scale, int64_t num_tokens, void* d_y,
                                             int32_t y_float32, struct CUstream_st* stream);
+
+/* of moe_fp8_linear, or (quantized != 0) of moe_fp8_linear_quantized */
+MOE_API moe_status moe_fp8_linear_plan(moe_fp8_linear_handle* h, int64_t num_tokens, int32_t quantized,
+                                       moe_dense_launch* out);
 
 /* moe_fp8_linear_read_status, moe_mlp_read_status -- the handle's device status
  * word since it was last read (synchronises `stream`): 0 and MOE_OK, or MOE_DEV_TIMEOUT
@@ -777,6 +795,8 @@ MOE_API moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int
                                     int32_t saved_float32, int64_t num_tokens, uint16_t* d_dx,
                                     void* d_dw1, void* d_dw2, int32_t dw_float32, int32_t accumulate,
                                     struct CUstream_st* stream);
+/* gate and up, down; the backward's dh, and dx, dW1 and dW2 (all three asked for) in one launch */
+MOE_API moe_status moe_mlp_plan(moe_mlp_handle* h, int64_t num_tokens, moe_dense_launch out[4]);
 MOE_API moe_status moe_mlp_read_status(moe_mlp_handle* h, uint32_t* h_status, struct CUstream_st* stream);
 MOE_API void moe_mlp_destroy(moe_mlp_handle* h);
 

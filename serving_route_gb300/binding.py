@@ -63,7 +63,7 @@ API_NAMES = ("moe_workspace_query", "moe_create", "moe_quantize_weights", "moe_q
              "moe_fp8_linear_workspace_query", "moe_fp8_linear_create", "moe_fp8_linear",
              "moe_fp8_linear_quantized", "moe_fp8_linear_read_status", "moe_fp8_linear_destroy",
              "moe_mlp_workspace_query", "moe_mlp_create", "moe_mlp_forward", "moe_mlp_backward",
-             "moe_mlp_read_status", "moe_mlp_destroy")
+             "moe_mlp_read_status", "moe_mlp_destroy", "moe_fp8_linear_plan", "moe_mlp_plan")
 
 
 class moe_dims(ctypes.Structure):
@@ -81,6 +81,11 @@ class moe_debug_view(ctypes.Structure):
                 ("rows_alloc", ctypes.c_int64), ("sf_atom_bytes", ctypes.c_int32),
                 ("gemm_pair", ctypes.c_int32), ("gemm_ctas", ctypes.c_int32),
                 ("pad_rows", ctypes.c_int32), ("route_coop_blocks", ctypes.c_int32)]
+
+
+class moe_dense_launch(ctypes.Structure):
+    _fields_ = [("pairs", ctypes.c_int32), ("width", ctypes.c_int32), ("split", ctypes.c_int32),
+                ("tiles", ctypes.c_int32)]
 
 
 class moe_plan(ctypes.Structure):
@@ -151,6 +156,8 @@ def lib() -> ctypes.CDLL:
                                      ctypes.POINTER(vp)]
         L.moe_mlp_forward.argtypes = [vp, vp, i64, i64, vp, vp, i32, vp]
         L.moe_mlp_backward.argtypes = [vp, vp, i64, vp, i64, vp, i32, i64, vp, vp, vp, i32, i32, vp]
+        L.moe_fp8_linear_plan.argtypes = [vp, i64, i32, ctypes.POINTER(moe_dense_launch)]
+        L.moe_mlp_plan.argtypes = [vp, i64, ctypes.POINTER(moe_dense_launch)]
         for n in ("fp8_linear", "mlp"):
             getattr(L, f"moe_{n}_read_status").argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
             getattr(L, f"moe_{n}_destroy").argtypes = [vp]
@@ -384,6 +391,12 @@ def moe_fp8_linear_quantized(h, d_xq, d_xq_scale, num_tokens, d_y, y_float32, st
         raise MoEError(s, "moe_fp8_linear_quantized")
 
 
+def moe_fp8_linear_plan(h, num_tokens, quantized) -> moe_dense_launch:
+    p = moe_dense_launch()
+    _check(lib().moe_fp8_linear_plan(h, num_tokens, quantized, ctypes.byref(p)), "moe_fp8_linear_plan")
+    return p
+
+
 def moe_fp8_linear_read_status(h, stream):
     """(status code, device status bits)"""
     bits = ctypes.c_uint32()
@@ -421,6 +434,13 @@ def moe_mlp_backward(*args) -> None:
     s = (_lib or lib()).moe_mlp_backward(*args)
     if s:
         raise MoEError(s, "moe_mlp_backward")
+
+
+def moe_mlp_plan(h, num_tokens):
+    """Four launches: gate and up, down, dh, the gradients."""
+    p = (moe_dense_launch * 4)()
+    _check(lib().moe_mlp_plan(h, num_tokens, p), "moe_mlp_plan")
+    return list(p)
 
 
 def moe_mlp_read_status(h, stream):

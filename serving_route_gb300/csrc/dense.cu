@@ -930,20 +930,57 @@ static cudaError_t split_gemm(const DenseGemm& g, DenseSplit p, cudaStream_t s) 
 }
 
 // Which kernel: the one that the measured times above say is faster.
+struct DenseChoice {
+  bool pairs;
+  int BN;          // of the pairs
+  DenseSplit split;
+};
+
+static DenseChoice choose(const DenseGemm& g, int sms) {
+  DenseChoice c = {};
+  const double pair_us = pair_columns(&g, 1, sms / 2, &c.BN);
+  c.split = dense_split_plan(g, sms);
+  c.pairs = !(c.split.us < pair_us || g.x);
+  return c;
+}
+
+// The longest K first.
+static void sort_products(DenseGemm* g, int count) {
+  for (int i = 1; i < count; ++i)
+    for (int j = i; j > 0 && g[j].K > g[j - 1].K; --j) std::swap(g[j], g[j - 1]);
+}
+
 cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s) {
-  int BN = 256;
-  const double pair_us = pair_columns(&g, 1, sms / 2, &BN);
-  const DenseSplit p = dense_split_plan(g, sms);
-  if (p.us < pair_us || g.x) return split_gemm(g, p, s);
-  return pair_gemm(&g, 1, BN, sms / 2, s);
+  const DenseChoice c = choose(g, sms);
+  return c.pairs ? pair_gemm(&g, 1, c.BN, sms / 2, s) : split_gemm(g, c.split, s);
 }
 
 cudaError_t dense_gemms(DenseGemm* g, int count, int sms, cudaStream_t s) {
-  for (int i = 1; i < count; ++i)  // the longest K first
-    for (int j = i; j > 0 && g[j].K > g[j - 1].K; --j) std::swap(g[j], g[j - 1]);
+  sort_products(g, count);
   int BN = 256;
   pair_columns(g, count, sms / 2, &BN);
   return pair_gemm(g, count, BN, sms / 2, s);
+}
+
+moe_dense_launch dense_choice(DenseGemm* g, int count, int sms) {
+  DenseChoice c = {};
+  if (count == 1) {
+    c = choose(*g, sms);
+  } else {
+    c.pairs = true;
+    sort_products(g, count);
+    pair_columns(g, count, sms / 2, &c.BN);
+  }
+  moe_dense_launch l = {};
+  l.pairs = c.pairs;
+  l.width = c.pairs ? c.BN : c.split.NT;
+  l.split = c.pairs ? 1 : c.split.split;
+  for (int i = 0; i < count && c.pairs; ++i) {
+    const int cols = g[i].epi == kEpiGate ? c.BN / 2 : c.BN;
+    l.tiles += (g[i].M + 255) / 256 * ((g[i].N + cols - 1) / cols);
+  }
+  if (!c.pairs) l.tiles = c.split.tt * c.split.rt;
+  return l;
 }
 
 }  // namespace mm

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/megamoe.h"
+
 namespace mm {
 
 constexpr int kFusedTokens = 16;
@@ -52,6 +54,8 @@ struct DenseGemm {
 
 cudaError_t dense_set_attributes();  // of the kernels, on the current device
 cudaError_t dense_gemm(const DenseGemm& g, int sms, cudaStream_t s);
+// What dense_gemm, and dense_gemms of `count` products, would launch (sorts them).
+moe_dense_launch dense_choice(DenseGemm* g, int count, int sms);
 // Up to three products of 16-bit operands (kEpiStore), of which none reads what another writes, in one launch
 // (sorts them).
 cudaError_t dense_gemms(DenseGemm* g, int count, int sms, cudaStream_t s);

@@ -118,6 +118,69 @@ DenseGemm linear_product(const moe_fp8_linear_handle* h, int64_t T, void* y, boo
   return g;
 }
 
+// The rows of x in BF16: rounded by the product itself, or before it.
+void linear_rows(DenseGemm& g, const moe_fp8_linear_handle* h, const uint16_t* x, int64_t stride) {
+  if (g.M <= kFusedTokens) {
+    g.x = x;
+    g.ldx = stride;
+  } else {
+    g.a = {h->xq, h->cols, g.M, false};
+    g.sa = h->xs;
+    g.sa_pitch = scale_pitch(h->cols);
+    g.early = true;
+  }
+}
+
+// The block's products, but for what the caller gives.
+DenseGemm mlp_product(const moe_mlp_handle* h, DenseEpi epi, DenseOperand a, DenseOperand b, int M, int N, int K) {
+  DenseGemm g = {};
+  g.a = a;
+  g.b = b;
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.type = h->type;
+  g.epi = epi;
+  g.act = h->act;
+  g.ld_out = N;
+  g.status = h->status;
+  g.withhold = h->withhold;
+  return g;
+}
+
+DenseGemm gate_product(const moe_mlp_handle* h, int T, const void* x, int64_t stride) {  // h, from x W1^T
+  DenseGemm g = mlp_product(h, kEpiGate, {x, stride, T, false}, {h->w1, h->hidden, 2 * h->inter, false}, T, h->inter, h->hidden);
+  g.out = h->h;
+  return g;
+}
+
+DenseGemm down_product(const moe_mlp_handle* h, int T) {  // h W2^T
+  DenseGemm g = mlp_product(h, kEpiStore, {h->h, h->inter, T, false}, {h->w2, h->inter, h->hidden, false}, T, h->hidden,
+                            h->inter);
+  g.early = true;
+  return g;
+}
+
+DenseGemm grad_product(const moe_mlp_handle* h, int T, const void* dy, int64_t stride) {  // dg, du (and h), from dy W2
+  DenseGemm g = mlp_product(h, kEpiGrad, {dy, stride, T, false}, {h->w2, h->inter, h->inter, true}, T, h->inter, h->hidden);
+  g.dgu = h->dgu;
+  return g;
+}
+
+DenseGemm dx_product(const moe_mlp_handle* h, int T) {  // (dg, du) W1
+  return mlp_product(h, kEpiStore, {h->dgu, 2 * h->inter, T, false}, {h->w1, h->hidden, h->hidden, true}, T, h->hidden,
+                     2 * h->inter);
+}
+
+DenseGemm dw1_product(const moe_mlp_handle* h, int T, const void* x, int64_t stride) {  // (dg, du)^T x
+  return mlp_product(h, kEpiStore, {h->dgu, 2 * h->inter, 2 * h->inter, true}, {x, stride, h->hidden, true}, 2 * h->inter,
+                     h->hidden, T);
+}
+
+DenseGemm dw2_product(const moe_mlp_handle* h, int T, const void* dy, int64_t stride) {  // dy^T h
+  return mlp_product(h, kEpiStore, {dy, stride, h->hidden, true}, {h->h, h->inter, h->inter, true}, h->hidden, h->inter, T);
+}
+
 bool mlp_dims_ok(int32_t hidden, int32_t inter) {
   return hidden % 8 == 0 && inter % 8 == 0 && hidden <= 65536 && inter <= 65536;
 }
@@ -185,17 +248,9 @@ moe_status moe_fp8_linear(moe_fp8_linear_handle* h, const uint16_t* d_x, int64_t
   if (y.meets(Span(d_x, num_tokens, x_stride, h->cols, 2)) || y.meets(Span(h->codes, h->rows, h->cols, h->cols, 1)))
     return MOE_ERR_INVALID_ARG;
   DenseGemm g = linear_product(h, num_tokens, d_y, y_float32 != 0);
-  if (num_tokens <= kFusedTokens) {
-    g.x = d_x;
-    g.ldx = x_stride;
-  } else {
-    if (dense_quantize_rows(d_x, x_stride, num_tokens, h->cols, h->xq, h->xs, stream) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    g.a = {h->xq, h->cols, (int)num_tokens, false};
-    g.sa = h->xs;
-    g.sa_pitch = scale_pitch(h->cols);
-    g.early = true;
-  }
+  linear_rows(g, h, d_x, x_stride);
+  if (!g.x && dense_quantize_rows(d_x, x_stride, num_tokens, h->cols, h->xq, h->xs, stream) != cudaSuccess)
+    return MOE_ERR_CUDA;
   return dense_gemm(g, h->sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -215,6 +270,18 @@ moe_status moe_fp8_linear_quantized(moe_fp8_linear_handle* h, const uint8_t* d_x
   g.sa = d_xq_scale;
   g.sa_pitch = h->cols / 128;
   return dense_gemm(g, h->sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status moe_fp8_linear_plan(moe_fp8_linear_handle* h, int64_t num_tokens, int32_t quantized, moe_dense_launch* out) {
+  if (!h || !out || num_tokens < 0) return MOE_ERR_INVALID_ARG;
+  if (num_tokens > h->max_tokens) return MOE_ERR_CAPACITY;
+  *out = moe_dense_launch{};
+  if (num_tokens == 0) return MOE_OK;
+  DenseGemm g = linear_product(h, num_tokens, nullptr, false);
+  const uint16_t row = 0;  // (some address: the choice reads none)
+  if (!quantized) linear_rows(g, h, &row, h->cols);
+  *out = dense_choice(&g, 1, h->sms);
+  return MOE_OK;
 }
 
 moe_status moe_fp8_linear_read_status(moe_fp8_linear_handle* h, uint32_t* h_status, struct CUstream_st* stream) {
@@ -284,35 +351,12 @@ moe_status moe_mlp_forward(moe_mlp_handle* h, const uint16_t* d_x, int64_t x_str
   if (saved.meets(x) || saved.meets(y) || (x.meets(y) && !(d_x == d_y && x_stride == H)) || y.meets(w1) || y.meets(w2) ||
       saved.meets(w1) || saved.meets(w2))
     return MOE_ERR_INVALID_ARG;
-  DenseGemm g = {};
-  g.a = {d_x, x_stride, (int)num_tokens, false};
-  g.b = {h->w1, H, 2 * I, false};
-  g.M = (int)num_tokens;
-  g.N = I;
-  g.K = H;
-  g.type = h->type;
-  g.epi = kEpiGate;
-  g.act = h->act;
-  g.out = h->h;
-  g.ld_out = I;
+  DenseGemm g = gate_product(h, (int)num_tokens, d_x, x_stride);
   g.saved = d_saved;
   g.saved_f32 = saved_float32 != 0;
-  g.status = h->status;
-  g.withhold = h->withhold;
   if (dense_gemm(g, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
-  DenseGemm d = {};
-  d.a = {h->h, I, (int)num_tokens, false};
-  d.b = {h->w2, I, H, false};
-  d.M = (int)num_tokens;
-  d.N = H;
-  d.K = I;
-  d.type = h->type;
-  d.epi = kEpiStore;
+  DenseGemm d = down_product(h, (int)num_tokens);
   d.out = d_y;
-  d.ld_out = H;
-  d.early = true;
-  d.status = h->status;
-  d.withhold = h->withhold;
   return dense_gemm(d, h->sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -343,47 +387,37 @@ moe_status moe_mlp_backward(moe_mlp_handle* h, const uint16_t* d_dy, int64_t dy_
     if (d_dw2 && cudaMemsetAsync(d_dw2, 0, ds * H * I, stream) != cudaSuccess) return MOE_ERR_CUDA;
     return MOE_OK;
   }
-  // dh = dy W2 -> dg, du (and h)
-  DenseGemm g = {};
-  g.a = {d_dy, dy_stride, T, false};
-  g.b = {h->w2, I, I, true};
-  g.M = T;
-  g.N = I;
-  g.K = H;
-  g.type = h->type;
-  g.epi = kEpiGrad;
-  g.act = h->act;
+  DenseGemm g = grad_product(h, T, d_dy, dy_stride);
   g.out = d_dw2 ? h->h : nullptr;
-  g.ld_out = I;
   g.saved = const_cast<void*>(d_saved);
   g.saved_f32 = saved_float32 != 0;
-  g.dgu = h->dgu;
-  g.status = h->status;
-  g.withhold = h->withhold;
   if (dense_gemm(g, h->sms, stream) != cudaSuccess) return MOE_ERR_CUDA;
   // what these read the product above has written, or the caller
   DenseGemm d[3] = {};
   int count = 0;
-  auto add = [&](DenseOperand a, DenseOperand b, int M, int N, int K, void* out, bool weights) {
-    DenseGemm& p = d[count++];
-    p.a = a;
-    p.b = b;
-    p.M = M;
-    p.N = N;
-    p.K = K;
-    p.type = h->type;
-    p.epi = kEpiStore;
-    p.out = out;
-    p.ld_out = N;
-    p.out_f32 = weights && dw_float32;
-    p.accumulate = weights && accumulate;
-    p.status = h->status;
-    p.withhold = h->withhold;
+  auto add = [&](const DenseGemm& p, void* to, bool weights) {
+    d[count] = p;
+    d[count].out = to;
+    d[count].out_f32 = weights && dw_float32;
+    d[count++].accumulate = weights && accumulate;
   };
-  if (d_dx) add({h->dgu, 2 * I, T, false}, {h->w1, H, H, true}, T, H, 2 * I, d_dx, false);            // dgu W1
-  if (d_dw1) add({h->dgu, 2 * I, 2 * I, true}, {d_x, x_stride, H, true}, 2 * I, H, T, d_dw1, true);   // dgu^T x
-  if (d_dw2) add({d_dy, dy_stride, H, true}, {h->h, I, I, true}, H, I, T, d_dw2, true);               // dy^T h
+  if (d_dx) add(dx_product(h, T), d_dx, false);
+  if (d_dw1) add(dw1_product(h, T, d_x, x_stride), d_dw1, true);
+  if (d_dw2) add(dw2_product(h, T, d_dy, dy_stride), d_dw2, true);
   return !count || dense_gemms(d, count, h->sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status moe_mlp_plan(moe_mlp_handle* h, int64_t num_tokens, moe_dense_launch out[4]) {
+  if (!h || !out || num_tokens < 0) return MOE_ERR_INVALID_ARG;
+  if (num_tokens > h->max_tokens) return MOE_ERR_CAPACITY;
+  memset(out, 0, 4 * sizeof(*out));
+  const int T = (int)num_tokens;
+  if (T == 0) return MOE_OK;
+  DenseGemm g[3] = {gate_product(h, T, nullptr, h->hidden), down_product(h, T), grad_product(h, T, nullptr, h->hidden)};
+  for (int i = 0; i < 3; ++i) out[i] = dense_choice(&g[i], 1, h->sms);
+  DenseGemm d[3] = {dx_product(h, T), dw1_product(h, T, nullptr, h->hidden), dw2_product(h, T, nullptr, h->hidden)};
+  out[3] = dense_choice(d, 3, h->sms);
+  return MOE_OK;
 }
 
 moe_status moe_mlp_read_status(moe_mlp_handle* h, uint32_t* h_status, struct CUstream_st* stream) {

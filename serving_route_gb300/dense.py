@@ -36,6 +36,10 @@ class _Handle:
             pass
 
 
+def _launch(p) -> dict:
+    return {n: getattr(p, n) for n, _ in p._fields_}
+
+
 def _rows(t: torch.Tensor, dtype, cols: int, dev: int) -> bool:
     """Whether t is [T, cols] of dtype, its rows contiguous (they may be strided)."""
     return (t.dtype is dtype and t.get_device() == dev and t.dim() == 2 and t.shape[1] == cols
@@ -102,6 +106,10 @@ class Fp8Linear(_Handle):
                                    out.dtype is _F32,
                                    _current_stream(dev) if stream is None else _given_stream(stream, dev))
         return out
+
+    def plan(self, num_tokens: int, quantized: bool = False) -> dict:
+        """How forward (or forward_quantized) divides num_tokens tokens: pairs, width, split, tiles."""
+        return _launch(B.moe_fp8_linear_plan(self.handle, num_tokens, quantized))
 
     def read_status(self, stream=None):
         """(status code, device status bits) since the last read; synchronises the stream."""
@@ -180,6 +188,11 @@ class GatedMlp(_Handle):
                            *(0 if t is None else t.data_ptr() for t in out), grad is _F32, accumulate,
                            _current_stream(dev) if stream is None else _given_stream(stream, dev))
         return dx, dw1, dw2
+
+    def plan(self, num_tokens: int) -> dict:
+        """The launches of forward ("gate", "down") and backward ("dh", "gradients") on num_tokens
+        tokens: pairs, width, split, tiles of each."""
+        return dict(zip(("gate", "down", "dh", "gradients"), map(_launch, B.moe_mlp_plan(self.handle, num_tokens))))
 
     def read_status(self, stream=None):
         """(status code, device status bits) since the last read; synchronises the stream."""
