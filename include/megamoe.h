@@ -151,6 +151,10 @@ typedef enum moe_status {
  * wave. */
 #define MOE_FLAG_COMBINE_IN_FC2 0x1000u
 
+/* Test only, of moe_mlp_create: MOE_FLAG_WATCHDOG_TEST for the last kernel of every call alone
+ * (down; the backward's gradients), whose timeout is then the only one. */
+#define MOE_FLAG_WATCHDOG_LAST_TEST 0x2000u
+
 typedef struct moe_dims {
   int32_t hidden;      /* H: multiple of 128, 128..16384 */
   int32_t inter;       /* I: expert intermediate size, multiple of 128, 128..16384 */
@@ -667,7 +671,8 @@ MOE_API void moe_fp4_destroy(moe_fp4_handle* h);
  * not overlap on the GPU, and a call on another device than the handle's is
  * refused with MOE_ERR_INVALID_ARG.  flags: 0, or MOE_FLAG_WATCHDOG_TEST (every wait
  * of the kernels is bounded by 1 s; here by 20 ms, and each kernel withholds one of its
- * copies, so that the calls record MOE_DEV_TIMEOUT).  Calls are asynchronous on `stream`,
+ * copies, so that the calls record MOE_DEV_TIMEOUT; a block also takes
+ * MOE_FLAG_WATCHDOG_LAST_TEST).  Calls are asynchronous on `stream`,
  * allocate nothing and can be captured in a CUDA graph.  num_tokens 0 is a
  * no-op (but see moe_mlp_backward); MOE_ERR_CAPACITY above max_tokens (at most 2^24).
  * ------------------------------------------------------------------------ */

@@ -45,6 +45,7 @@ MOE_FLAG_WATCHDOG_ROUTE_TEST = 0x200
 MOE_FLAG_PER_TENSOR = 0x400
 MOE_FLAG_NO_SWAP_AB = 0x800
 MOE_FLAG_COMBINE_IN_FC2 = 0x1000
+MOE_FLAG_WATCHDOG_LAST_TEST = 0x2000
 
 MOE_ACT_SILU = 0
 MOE_ACT_GELU_TANH = 1

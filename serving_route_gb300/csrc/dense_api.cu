@@ -24,7 +24,7 @@ struct moe_mlp_handle {
   DenseType type;
   DenseAct act;
   int64_t max_tokens;
-  bool withhold;
+  bool withhold, withhold_last;
   const void *w1, *w2;
   uint32_t* status;
   void* h;       // [max_tokens, inter]
@@ -144,7 +144,7 @@ DenseGemm mlp_product(const moe_mlp_handle* h, DenseEpi epi, DenseOperand a, Den
   g.act = h->act;
   g.ld_out = N;
   g.status = h->status;
-  g.withhold = h->withhold;
+  g.withhold = h->withhold || (h->withhold_last && epi == kEpiStore);  // (a call ends with these)
   return g;
 }
 
@@ -306,7 +306,9 @@ moe_status moe_mlp_create(int32_t hidden, int32_t inter, int32_t fp16, int32_t a
   size_t need = 0;
   moe_status st = moe_mlp_workspace_query(hidden, inter, max_tokens, &need);
   if (st != MOE_OK) return st;
-  if ((activation != MOE_ACT_SILU && activation != MOE_ACT_GELU_TANH) || (flags & ~MOE_FLAG_WATCHDOG_TEST)) return MOE_ERR_UNSUPPORTED;
+  if ((activation != MOE_ACT_SILU && activation != MOE_ACT_GELU_TANH) ||
+      (flags & ~(MOE_FLAG_WATCHDOG_TEST | MOE_FLAG_WATCHDOG_LAST_TEST)))
+    return MOE_ERR_UNSUPPORTED;
   if (off(d_w1, 16) || off(d_w2, 16) || off(d_workspace, 16)) return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
   int dev = 0, sms = 0;
@@ -327,6 +329,7 @@ moe_status moe_mlp_create(int32_t hidden, int32_t inter, int32_t fp16, int32_t a
   h->act = activation == MOE_ACT_SILU ? kSilu : kGeluTanh;
   h->max_tokens = max_tokens;
   h->withhold = (flags & MOE_FLAG_WATCHDOG_TEST) != 0;
+  h->withhold_last = (flags & MOE_FLAG_WATCHDOG_LAST_TEST) != 0;
   h->w1 = d_w1;
   h->w2 = d_w2;
   h->status = reinterpret_cast<uint32_t*>(b);

@@ -127,7 +127,7 @@ class GatedMlp(_Handle):
     _destroy = staticmethod(B.moe_mlp_destroy)
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, *, max_tokens: int, activation: str = "silu",
-                 watchdog_test: bool = False, stream=None):
+                 watchdog_test: bool = False, watchdog_last_test: bool = False, stream=None):
         H, I = w2.shape
         assert activation in _ACTS
         n = B.moe_mlp_workspace_query(H, I, max_tokens)
@@ -138,8 +138,9 @@ class GatedMlp(_Handle):
         self.weights = (w1, w2)
         self.workspace = torch.empty(n, dtype=_U8, device=w1.device)
         self.handle = B.moe_mlp_create(H, I, dtype is _F16, _ACTS[activation],
-                                       B.MOE_FLAG_WATCHDOG_TEST if watchdog_test else 0, max_tokens, w1.data_ptr(),
-                                       w2.data_ptr(), self.workspace.data_ptr(), n,
+                                       (B.MOE_FLAG_WATCHDOG_TEST if watchdog_test else 0)
+                                       | (B.MOE_FLAG_WATCHDOG_LAST_TEST if watchdog_last_test else 0),
+                                       max_tokens, w1.data_ptr(), w2.data_ptr(), self.workspace.data_ptr(), n,
                                        _current_stream(dev) if stream is None else _given_stream(stream, dev))
 
     def _saved(self, saved: torch.Tensor, T: int, dev: int) -> bool:

@@ -35,3 +35,14 @@ def test_plans_of_nothing(B):
     L, p = B.lib(), (B.moe_dense_launch * 4)()
     assert L.moe_fp8_linear_plan(None, 1, 0, p) == B.MOE_ERR_INVALID_ARG
     assert L.moe_mlp_plan(None, 1, p) == B.MOE_ERR_INVALID_ARG
+
+
+def test_flags_of_the_block(B):
+    A = 0x7000000000  # an address, not memory: refused before anything reads it
+    for flags in (B.MOE_FLAG_WATCHDOG_LAST_TEST << 1, B.MOE_FLAG_WATCHDOG_LAST_TEST | 1):
+        with pytest.raises(B.MoEError) as e:
+            B.moe_mlp_create(64, 32, 0, 0, flags, 4, A, A, A, 1 << 20, 0)
+        assert e.value.status == B.MOE_ERR_UNSUPPORTED
+    with pytest.raises(B.MoEError) as e:
+        B.moe_fp8_linear_create(64, 256, B.MOE_FLAG_WATCHDOG_LAST_TEST, 4, A, A, A, 1 << 20, 0)
+    assert e.value.status == B.MOE_ERR_UNSUPPORTED
