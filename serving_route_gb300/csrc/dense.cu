@@ -277,7 +277,8 @@ struct PairProblem {
   int M, N, K;
   int mt, nt, end;         // tiles of 256 rows, of columns; units of this product and those before
   bool amn, bmn;
-  bool out_f32, accumulate, vec;  // vec: columns in pieces of 8, rows on 16-byte boundaries
+  bool out_f32, accumulate;  // (accumulate: 16-bit operands)
+  bool vec;                  // columns in pieces of 8, rows on 16-byte boundaries: always, but in E4M3
   void* out;
   int64_t ld_out;
 };
@@ -638,9 +639,9 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
               put_f32(buf, lane, v);
               __syncwarp();
               uint8_t* dst = reinterpret_cast<uint8_t*>(out + 32 * h);
-              if (!p.vec)
+              if (F8 && !p.vec)
                 flush_elements(smem + epi, out + 32 * h, ld, rows, left, lane);
-              else if (p.accumulate)
+              else if (!F8 && p.accumulate)
                 flush<128, true>(buf, dst, ld * 4, rows, left * 4, lane);
               else
                 flush<128>(buf, dst, ld * 4, rows, left * 4, lane);
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(kDThreads, 1) dense_pair_kernel(const __grid_c
             }
             __syncwarp();
             uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + row0 * ld + col;
-            if (p.vec)
+            if (!F8 || p.vec)
               flush<128>(buf, reinterpret_cast<uint8_t*>(out), ld * 2, rows, cols * 2, lane);
             else
               flush_elements(smem + epi, out, ld, rows, cols, lane);

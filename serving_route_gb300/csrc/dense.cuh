@@ -139,7 +139,7 @@ struct DenseArgs {
   int64_t ldx;
   void* out;
   int64_t ld_out;
-  bool out_f32, vec;  // vec: columns in pieces of 8, rows on 16-byte boundaries
+  bool out_f32, vec;  // vec: columns in pieces of 8, rows on 16-byte boundaries (both of E4M3 products alone)
   void* saved;
   bool saved_f32;
   void* dgu;

@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         gate_values(g.act, gv, uv);
         store_few(g.out, o, col, g.N, uv, false, g.type, true);
       } else if constexpr (EPI == kEpiStore) {
-        store_few(g.out, o, col, g.N, v[j], g.out_f32, g.type, g.vec);
+        store_few(g.out, o, col, g.N, v[j], F8 && g.out_f32, g.type, !F8 || g.vec);
       } else {
         const float4 gs = load_four(g.saved, s, g.saved_f32, g.type);
         const float4 us = load_four(g.saved, s + g.N, g.saved_f32, g.type);
