@@ -66,11 +66,11 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint16_t* x, i
   }
 }
 
-cudaError_t dense_quantize_rows(const uint16_t* x, int64_t ld, int64_t T, int cols, uint8_t* q, uint8_t* s,
+cudaError_t dense_quantize_rows(const uint16_t* x, int64_t ld, int64_t T, int cols, uint8_t* q, uint8_t* s, int sms,
                                 cudaStream_t stream) {
   const uint32_t segs = (uint32_t)(cols / 128 + 3) / 4, units = (uint32_t)T * segs;  // (below 2^30)
-  const uint32_t ctas = (units + 7) / 8;
-  return launch_k(quantize_rows_kernel, dim3(ctas < 152 * 4 ? ctas : 152 * 4), dim3(256), 0, stream, true, nullptr, x, ld,
+  const uint32_t ctas = (units + 7) / 8, most = (uint32_t)sms * 4;
+  return launch_k(quantize_rows_kernel, dim3(ctas < most ? ctas : most), dim3(256), 0, stream, true, nullptr, x, ld,
                   units, segs, cols / 128, scale_pitch(cols), q, s);
 }
 

@@ -63,7 +63,7 @@ cudaError_t dense_gemms(DenseGemm* g, int count, int sms, cudaStream_t s);
 // Bytes from one row of E8M0 scales to the next where the library lays them out: whole words.
 constexpr int scale_pitch(int K) { return (K / 128 + 3) / 4 * 4; }
 // x BF16 [T, cols] (rows ld elements apart) -> E4M3 codes [T, cols] and E8M0 bytes [T, scale_pitch(cols)].
-cudaError_t dense_quantize_rows(const uint16_t* x, int64_t ld, int64_t T, int cols, uint8_t* q, uint8_t* s,
+cudaError_t dense_quantize_rows(const uint16_t* x, int64_t ld, int64_t T, int cols, uint8_t* q, uint8_t* s, int sms,
                                 cudaStream_t stream);
 // Power-of-two float scales [rows, cols] to E8M0 bytes (rows pitch apart); others set MOE_DEV_BAD_SCALE in *status.
 cudaError_t dense_scales_to_e8m0(const float* s, int64_t rows, int cols, int pitch, uint8_t* out, uint32_t* status,

@@ -249,7 +249,7 @@ moe_status moe_fp8_linear(moe_fp8_linear_handle* h, const uint16_t* d_x, int64_t
     return MOE_ERR_INVALID_ARG;
   DenseGemm g = linear_product(h, num_tokens, d_y, y_float32 != 0);
   linear_rows(g, h, d_x, x_stride);
-  if (!g.x && dense_quantize_rows(d_x, x_stride, num_tokens, h->cols, h->xq, h->xs, stream) != cudaSuccess)
+  if (!g.x && dense_quantize_rows(d_x, x_stride, num_tokens, h->cols, h->xq, h->xs, h->sms, stream) != cudaSuccess)
     return MOE_ERR_CUDA;
   return dense_gemm(g, h->sms, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
