@@ -814,6 +814,8 @@ cudaError_t dense_set_attributes() {
 // bytes 0.31 us with 64 columns, 0.35 with 256; start, first copies and last tile 4.2 and 5.4
 // us, 2.6 more with gate and gradient.  512 x 4096 x 2048 takes 9.3 us with 128 columns, 10.3
 // with 256; 1021 x 4096 x 7168 44 and 25; 8192 x 256 x 7168 27 and 25 (20.3 by the split kernel).
+// The outputs were BF16: float ones and rows off 16-byte boundaries take longer, which is not in
+// it (1021 x 10007 x 1408 into float: 17 us by this, 27 measured).
 static double pair_columns(const DenseGemm* g, int count, int pairs, int* columns) {
   double least = 0;
   for (int BN = 256; BN >= 64; BN -= 64) {

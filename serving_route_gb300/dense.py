@@ -84,7 +84,7 @@ class Fp8Linear(_Handle):
                 out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
         """x BF16 [T, cols] (rows may be strided by a multiple of 8), rounded to E4M3 with a
         power-of-two scale per 128 columns -> [T, rows] in out_dtype (bfloat16 or float32) or in
-        `out`'s type; `out` may not overlap x."""
+        `out`'s type; `out` may not overlap x.  A row with a NaN or an infinity gives NaN."""
         T = x.shape[0]
         dev = x.get_device()
         assert dev == _current_device() and _rows(x, _BF16, self.cols, dev)
@@ -117,12 +117,13 @@ class Fp8Linear(_Handle):
 
 
 class GatedMlp(_Handle):
-    """y = (act(x Wg^T) * (x Wu^T)) Wd^T for up to max_tokens rows, in BF16 or FP16, and its gradients.
+    """y = (act(x Wg^T) * (x Wu^T)) Wd^T for up to max_tokens rows, in BF16 or FP16, and its gradients
+    (by backward(): the calls take no part in autograd).
 
     w1 [2I, H] (gate rows, then up rows), w2 [H, I], of one type, on the GPU; H and I
     multiples of 8.  activation: "silu", or "gelu" in its tanh form.  The object keeps
     the weights, which every call reads where they are (an optimiser may change them in
-    place), and its own workspace of 6 max_tokens I bytes."""
+    place), and its own workspace of 6 max_tokens I bytes (2 of them are the forward's)."""
 
     _destroy = staticmethod(B.moe_mlp_destroy)
 
@@ -150,7 +151,8 @@ class GatedMlp(_Handle):
                 stream=None) -> torch.Tensor:
         """x [T, H] in the weights' type (rows may be strided by a multiple of 8) -> [T, H].
         `out` may be x.  saved: a buffer [T, 2I], float32 or in the weights' type, that
-        takes gate and up before the activation for backward()."""
+        takes gate and up before the activation for backward() (in FP16 what is beyond 65504 is
+        infinite, and its gradients infinite or NaN)."""
         T = x.shape[0]
         dev = x.get_device()
         assert dev == _current_device() and _rows(x, self.dtype, self.H, dev)
