@@ -688,7 +688,8 @@ typedef struct moe_dense_launch {
   int32_t pairs; /* 1: CTA pairs on tiles of 256 rows; 0: K shared over clusters of CTAs */
   int32_t width; /* a tile's columns (pairs: 64, 128, 192, 256, gate and up counted), or its tokens (16..128) */
   int32_t split; /* CTAs that share a tile's K: 1 (pairs too), 2, 4, 8 */
-  int32_t tiles;
+  int32_t reserved;
+  int64_t tiles; /* of all its products */
 } moe_dense_launch;
 
 typedef struct moe_fp8_linear_handle moe_fp8_linear_handle;

@@ -86,7 +86,7 @@ class moe_debug_view(ctypes.Structure):
 
 class moe_dense_launch(ctypes.Structure):
     _fields_ = [("pairs", ctypes.c_int32), ("width", ctypes.c_int32), ("split", ctypes.c_int32),
-                ("tiles", ctypes.c_int32)]
+                ("reserved", ctypes.c_int32), ("tiles", ctypes.c_int64)]
 
 
 class moe_plan(ctypes.Structure):

@@ -980,9 +980,9 @@ moe_dense_launch dense_choice(DenseGemm* g, int count, int sms) {
   l.split = c.pairs ? 1 : c.split.split;
   for (int i = 0; i < count && c.pairs; ++i) {
     const int cols = g[i].epi == kEpiGate ? c.BN / 2 : c.BN;
-    l.tiles += (g[i].M + 255) / 256 * ((g[i].N + cols - 1) / cols);
+    l.tiles += (int64_t)((g[i].M + 255) / 256) * ((g[i].N + cols - 1) / cols);
   }
-  if (!c.pairs) l.tiles = c.split.tt * c.split.rt;
+  if (!c.pairs) l.tiles = (int64_t)c.split.tt * c.split.rt;
   return l;
 }
 

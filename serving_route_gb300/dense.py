@@ -37,7 +37,7 @@ class _Handle:
 
 
 def _launch(p) -> dict:
-    return {n: getattr(p, n) for n, _ in p._fields_}
+    return {n: getattr(p, n) for n in ("pairs", "width", "split", "tiles")}
 
 
 def _rows(t: torch.Tensor, dtype, cols: int, dev: int) -> bool:

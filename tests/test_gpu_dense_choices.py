@@ -86,3 +86,14 @@ def test_linear_choices(S, row):
             ref.check(got, want)
             norms.check(got, want[0], norms.summed(cols) + (norms.rounded(BF) if dtype is BF else 0.0))
     assert lin.read_status() == (0, 0)
+
+
+def test_linear_plan_at_the_limits(S):
+    """2^24 tokens and rows: more tiles than 32 bits hold."""
+    n = 1 << 24
+    codes, scales = torch.zeros(n, 128, dtype=torch.uint8, device="cuda"), torch.ones(n // 128, 1, device="cuda")
+    lin = S.Fp8Linear(codes, scales, max_tokens=n)
+    for quantized in (False, True):
+        p = lin.plan(n, quantized)
+        area = 256 * p["width"] if p["pairs"] else 128 * p["width"]
+        assert p["tiles"] * area >= n * n and p["tiles"] >= 2 ** 32
